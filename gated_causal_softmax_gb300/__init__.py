@@ -9,6 +9,11 @@ Entry points (same names as the C ABI in include/gcs_attn.h):
     attn_fwd(q, k, v, cu_seqlens, ...)           -> (o, lse)
     attn_bwd(q, k, v, o, lse, dout, cu_seqlens, ...) -> (dq, dk, dv, dlog_gate, dsink)
     attn_decode_paged(q, k_cache, v_cache, ...)  -> out
+    attn_qk_norm_rope_fwd(q, k, cos_sin, positions, ...) -> (q_out, k_out)
+    attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, ...)     -> (dq, dk, dq_weight, dk_weight)
+    attn_cache_append(k, v, k_cache, v_cache, ...)       -> None (writes the cache)
+    attn_cache_append_rope(q, k, v, k_cache, v_cache, ...) -> q_out (and writes the cache)
+    attn_cache_gather(k_cache, v_cache, ...)             -> (k, v, log_gate)
 """
 from __future__ import annotations
 
@@ -27,6 +32,11 @@ __all__ = [
     "attn_decode_paged",
     "attn_decode_paged_noalloc",
     "attn_prefill_paged",
+    "attn_qk_norm_rope_fwd",
+    "attn_qk_norm_rope_bwd",
+    "attn_cache_append",
+    "attn_cache_append_rope",
+    "attn_cache_gather",
     "selftest_bounded_wait",
     "set_device_checks",
     "device_checks",
@@ -34,6 +44,8 @@ __all__ = [
     "check_paged_inputs",
     "PrefillArgs",
     "DecodeArgs",
+    "QkRopeArgs",
+    "CacheArgs",
     "GcsError",
     "get_device_status",
     "set_kernel_events",
@@ -123,6 +135,61 @@ class DecodeArgs(ctypes.Structure):
     ]
 
 
+class QkRopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("total_tokens", _c_int),
+        ("hq", _c_int),
+        ("hkv", _c_int),
+        ("d", _c_int),
+        ("rotary_dim", _c_int),
+        ("interleaved", _c_int),
+        ("norm", _c_int),
+        ("eps", _c_float),
+        ("q", _vp),
+        ("k", _vp),
+        ("q_weight", _vp),
+        ("k_weight", _vp),
+        ("cos_sin", _vp),
+        ("max_pos", _c_int),
+        ("positions", _vp),
+        ("q_stride", Strides),
+        ("k_stride", Strides),
+        ("q_out_stride", Strides),
+        ("k_out_stride", Strides),
+        ("dq_stride", Strides),
+        ("dk_stride", Strides),
+    ]
+
+
+class CacheArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", _c_int),
+        ("cu_rows", _vp),
+        ("total_rows", _c_int),
+        ("max_rows", _c_int),
+        ("seq_lens", _vp),
+        ("block_table", _vp),
+        ("max_blocks_per_req", _c_int),
+        ("k_cache", _vp),
+        ("v_cache", _vp),
+        ("k_scale", _vp),
+        ("v_scale", _vp),
+        ("num_blocks", _c_int),
+        ("block_size", _c_int),
+        ("hq", _c_int),
+        ("hkv", _c_int),
+        ("d", _c_int),
+        ("kv_format", _c_int),
+        ("scale_mode", _c_int),
+        ("g_cache", _vp),
+        ("kv_stride_block", _i64),
+        ("kv_stride_head", _i64),
+        ("kv_stride_slot", _i64),
+        ("k_stride", Strides),
+        ("v_stride", Strides),
+    ]
+
+
 KV_FP8_E4M3, KV_BF16 = 0, 1
 SCALE_PER_TOKEN, SCALE_PER_TENSOR = 0, 1
 
@@ -160,6 +227,20 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_prefill_paged_workspace.restype = ctypes.c_size_t
     lib.attn_prefill_paged.argtypes = [P(DecodeArgs), _vp, _vp, ctypes.c_size_t, _vp]
     lib.attn_prefill_paged.restype = _c_int
+    lib.attn_qk_norm_rope_fwd.argtypes = [P(QkRopeArgs), _vp, _vp, _vp]
+    lib.attn_qk_norm_rope_fwd.restype = _c_int
+    lib.attn_qk_norm_rope_bwd_workspace.argtypes = [P(QkRopeArgs)]
+    lib.attn_qk_norm_rope_bwd_workspace.restype = ctypes.c_size_t
+    lib.attn_qk_norm_rope_bwd.argtypes = [P(QkRopeArgs), _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_qk_norm_rope_bwd.restype = _c_int
+    lib.attn_cache_append_workspace.argtypes = [P(CacheArgs)]
+    lib.attn_cache_append_workspace.restype = ctypes.c_size_t
+    lib.attn_cache_append.argtypes = [P(CacheArgs), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_cache_append.restype = _c_int
+    lib.attn_cache_append_rope.argtypes = [P(CacheArgs), P(QkRopeArgs), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_cache_append_rope.restype = _c_int
+    lib.attn_cache_gather.argtypes = [P(CacheArgs), _vp, _vp, _vp, _vp]
+    lib.attn_cache_gather.restype = _c_int
     lib.gcs_get_device_status.argtypes = [P(_c_int), _c_int]
     lib.gcs_get_device_status.restype = _c_int
     lib.gcs_selftest_bounded_wait.argtypes = [_vp]
@@ -518,3 +599,222 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, k_scale, v_scale, block_table
     _check(L.attn_decode_paged_noalloc(ctypes.byref(a), out.data_ptr(), _stream()), "attn_decode_paged_noalloc")
     return out
 
+
+def _on_current_device(*tensors) -> None:
+    """The calls below launch on the current device's stream; their tensors have to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on device {t.get_device()}, the current device is {dev}")
+
+
+def _rows(t, name: str, tokens: int, heads: int, d: int) -> torch.Tensor:
+    """A bf16 [tokens, heads, d] tensor, heads and tokens at any strides the library takes."""
+    _need(t, torch.bfloat16, name, strided=True)
+    if tuple(t.shape) != (tokens, heads, d):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
+    return t
+
+
+def _row_strides(t: torch.Tensor) -> Strides:
+    """Strides of a [tokens, heads, dim] tensor; a dimension of one element has no stride of its
+    own, whatever torch says of it."""
+    n, heads, d = t.shape
+    head = t.stride(1) if heads > 1 else d
+    return Strides(t.stride(0) if n > 1 else heads * head, head)
+
+
+def _vector(t, dtype, name: str, shape) -> Optional[torch.Tensor]:
+    if t is not None:
+        _need(t, dtype, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved) -> QkRopeArgs:
+    """Marshals the arguments of the norm and rotation.  rotary_dim is the table's width."""
+    _need(q, torch.bfloat16, "q", strided=True)
+    if q.dim() != 3 or k is None or k.dim() != 3:
+        raise ValueError("expected [tokens, heads, dim] tensors q and k")
+    n, hq, d = q.shape
+    hkv = k.shape[1]
+    _rows(k, "k", n, hkv, d)
+    _vector(q_weight, torch.float32, "q_weight", (d,))
+    _vector(k_weight, torch.float32, "k_weight", (d,))
+    _vector(positions, torch.int32, "positions", (n,))
+    max_pos = rot = 0
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin")
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rotary_dim]")
+        max_pos, rot = cos_sin.shape
+    return QkRopeArgs(n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, q.data_ptr(), k.data_ptr(),
+                      _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), max_pos, _ptr(positions), _row_strides(q), _row_strides(k))
+
+
+def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
+                          interleaved=False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and rotation by position, one pass.  q bf16 [tot, hq,
+    d], k bf16 [tot, hkv, d] (last dim contiguous, e.g. views of a fused projection); weights
+    fp32 [d] or None (ones); cos_sin fp32 [max_pos, rotary_dim] (cosines, then sines) or None (no
+    rotation); positions int32 [tot], negative = padding (outputs left as they were).
+    norm=False: rotation only.  Returns q_out, k_out."""
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else _rows(q_out, "q_out", *q.shape)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else _rows(k_out, "k_out", *k.shape)
+    a.q_out_stride, a.k_out_stride = _row_strides(q_out), _row_strides(k_out)
+    _on_current_device(q, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
+    _check(load().attn_qk_norm_rope_fwd(ctypes.byref(a), q_out.data_ptr(), k_out.data_ptr(), _stream()),
+           "attn_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                          norm=True, interleaved=False, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                          workspace=None):
+    """Backward of attn_qk_norm_rope_fwd: dq_out, dk_out are the gradients of its outputs, the
+    rest its arguments.  Returns dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]; None without
+    the weight)."""
+    L = load()
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
+    _rows(dq_out, "dq_out", *q.shape)
+    _rows(dk_out, "dk_out", *k.shape)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _rows(dq, "dq", *q.shape)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else _rows(dk, "dk", *k.shape)
+    a.q_out_stride, a.k_out_stride, a.dq_stride, a.dk_stride = _row_strides(dq_out), _row_strides(dk_out), _row_strides(dq), _row_strides(dk)
+    if q_weight is not None:
+        dq_weight = torch.empty_like(q_weight) if dq_weight is None else dq_weight
+    if k_weight is not None:
+        dk_weight = torch.empty_like(k_weight) if dk_weight is None else dk_weight
+    _vector(dq_weight, torch.float32, "dq_weight", (q.shape[2],))
+    _vector(dk_weight, torch.float32, "dk_weight", (q.shape[2],))
+    if workspace is None:
+        ws_bytes = L.attn_qk_norm_rope_bwd_workspace(ctypes.byref(a))
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+    _on_current_device(q, k, dq_out, dk_out, cos_sin, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight,
+                       workspace)
+    _check(L.attn_qk_norm_rope_bwd(ctypes.byref(a), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+                                   dk.data_ptr(), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
+                                   workspace.numel() if workspace is not None else 0, _stream()),
+           "attn_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq=None,
+               g_cache=None) -> CacheArgs:
+    """Marshals the arguments of the cache calls: the caches, scales and index arrays are those of
+    decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes)."""
+    if k_cache is None or v_cache is None or k_cache.dim() != 4:
+        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache shapes or types differ")
+    if k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must share one layout")
+    nb, hkv, bs, d = k_cache.shape
+    fmt = k_cache.dtype
+    if fmt not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"caches must be bf16, uint8 or float8_e4m3fn, got {fmt}")
+    _need(k_cache, fmt, "k_cache", strided=True)
+    _need(v_cache, fmt, "v_cache", strided=True)
+    kv_format, scale_mode = KV_FP8_E4M3, SCALE_PER_TOKEN
+    if fmt == torch.bfloat16:
+        kv_format = KV_BF16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 KV cache takes no scales")
+    else:
+        _need(k_scale, torch.float32, "k_scale")
+        _need(v_scale, torch.float32, "v_scale")
+        if k_scale.shape == (nb, hkv, bs) and v_scale.shape == (nb, hkv, bs):
+            pass
+        elif k_scale.numel() == 1 and v_scale.numel() == 1:
+            scale_mode = SCALE_PER_TENSOR
+        else:
+            raise NotImplementedError("fp8 scales must have the page shape [num_blocks, num_kv_heads, block_size] "
+                                      "(per token) or hold one value (per tensor)")
+    _need(block_table, torch.int32, "block_table")
+    _need(seq_lens, torch.int32, "seq_lens")
+    _need(cu_rows, torch.int32, "cu_rows")
+    num_reqs = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != num_reqs or cu_rows.numel() != num_reqs + 1:
+        raise ValueError("block_table, seq_lens and cu_rows are [R, max_blocks], [R] and [R + 1]")
+    if g_cache is not None:
+        hq = g_cache.shape[1] if hq is None and g_cache.dim() == 3 else hq
+        _vector(g_cache, torch.float32, "g_cache", (nb, hq, bs))
+    return CacheArgs(num_reqs, cu_rows.data_ptr(), int(total_rows), int(max_rows), seq_lens.data_ptr(),
+                     block_table.data_ptr(), block_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                     _ptr(k_scale), _ptr(v_scale), nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
+                     _ptr(g_cache), *k_cache.stride()[:3])
+
+
+def _append_workspace(L, a, workspace, device):
+    if workspace is None:
+        ws_bytes = L.attn_cache_append_workspace(ctypes.byref(a))
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
+    return workspace
+
+
+def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, log_gate=None,
+                      g_cache=None, workspace=None) -> None:
+    """Writes k, v bf16 [tot, hkv, d] (and log_gate fp32 [tot, hq] into g_cache) into the paged
+    cache, as the last cu_q[r + 1] - cu_q[r] of the seq_lens[r] cached positions of request r:
+    the arrays that attn_decode_paged and attn_prefill_paged take.  A per-token fp8 cache gets its
+    scales written, a per-tensor one is quantised with the given scales."""
+    L = load()
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, k.shape[0], max_q_len, None,
+                   g_cache)
+    _rows(k, "k", a.total_rows, a.hkv, a.d)
+    _rows(v, "v", a.total_rows, a.hkv, a.d)
+    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
+    a.k_stride, a.v_stride = _row_strides(k), _row_strides(v)
+    workspace = _append_workspace(L, a, workspace, k.device)
+    _on_current_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, log_gate, g_cache,
+                       workspace)
+    _check(L.attn_cache_append(ctypes.byref(a), k.data_ptr(), v.data_ptr(), _ptr(log_gate), _ptr(workspace),
+                               workspace.numel() if workspace is not None else 0, _stream()), "attn_cache_append")
+
+
+def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len,
+                           cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
+                           interleaved=False, log_gate=None, g_cache=None, q_out=None, workspace=None):
+    """attn_qk_norm_rope_fwd and attn_cache_append in one launch: returns the normed and rotated
+    q, and writes the normed and rotated k (quantised without a rounding to bf16 in between) and
+    v into the cache.  positions None: the cached positions."""
+    L = load()
+    r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, q.shape[0], max_q_len, r.hq,
+                   g_cache)
+    _rows(k, "k", a.total_rows, a.hkv, a.d)
+    _rows(v, "v", a.total_rows, a.hkv, a.d)
+    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else _rows(q_out, "q_out", *q.shape)
+    r.q_out_stride, a.v_stride = _row_strides(q_out), _row_strides(v)
+    workspace = _append_workspace(L, a, workspace, q.device)
+    _on_current_device(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, cos_sin, positions,
+                       q_weight, k_weight, log_gate, g_cache, q_out, workspace)
+    _check(L.attn_cache_append_rope(ctypes.byref(a), ctypes.byref(r), v.data_ptr(), _ptr(log_gate), q_out.data_ptr(),
+                                    _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream()),
+           "attn_cache_append_rope")
+    return q_out
+
+
+def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, g_cache=None,
+                      k=None, v=None, log_gate=None):
+    """Reads the last cu_rows[r + 1] - cu_rows[r] of the seq_lens[r] cached positions of every
+    request back into packed k, v bf16 [total_rows, hkv, d] and, with g_cache, log_gate fp32
+    [total_rows, hq] (the differences of the cumulative gates): what attn_fwd takes.  total_rows
+    is cu_rows's last entry on the host.  Returns k, v, log_gate (None without g_cache)."""
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, total_rows),
+                   None, g_cache)
+    shape = (a.total_rows, a.hkv, a.d)
+    new = lambda s, t: torch.empty(s, dtype=t, device=k_cache.device)
+    k = new(shape, torch.bfloat16) if k is None else _rows(k, "k", *shape)
+    v = new(shape, torch.bfloat16) if v is None else _rows(v, "v", *shape)
+    if g_cache is not None and log_gate is None:
+        log_gate = new((a.total_rows, a.hq), torch.float32)
+    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
+    a.k_stride, a.v_stride = _row_strides(k), _row_strides(v)
+    _on_current_device(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, g_cache, k, v, log_gate)
+    _check(load().attn_cache_gather(ctypes.byref(a), k.data_ptr(), v.data_ptr(), _ptr(log_gate), _stream()),
+           "attn_cache_gather")
+    return k, v, log_gate

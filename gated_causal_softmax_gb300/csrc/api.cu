@@ -892,6 +892,368 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
   return cuda_status(launch_prefill_paged(p, maps, s, &timer.b, &timer.a));
 }
 
+// ------------------------------------------------------------------ norm and rotation of q and k
+
+static bool head_dim_supported(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// in_cache: positions may be missing (the cached positions are used).
+static int check_rope(const gcs_qk_rope_args* a, bool in_cache) {
+  if (!a) return GCS_ERR_INVALID_ARG;
+  if (a->total_tokens < 1 || a->hq < 1 || a->hkv < 1 || a->hq % a->hkv != 0) return GCS_ERR_INVALID_ARG;
+  if ((a->interleaved != 0 && a->interleaved != 1) || (a->norm != 0 && a->norm != 1)) return GCS_ERR_INVALID_ARG;
+  if (!a->q || !a->k || !aligned16(a->q) || !aligned16(a->k)) return GCS_ERR_INVALID_ARG;
+  if (!aligned16(a->q_weight) || !aligned16(a->k_weight) || !aligned16(a->cos_sin) || !aligned4(a->positions))
+    return GCS_ERR_INVALID_ARG;
+  if (a->norm) {
+    if (!(a->eps >= 0.f) || !std::isfinite(a->eps)) return GCS_ERR_INVALID_ARG;
+  } else if (a->q_weight || a->k_weight) {
+    return GCS_ERR_INVALID_ARG;
+  }
+  if ((a->rotary_dim == 0) != (a->cos_sin == nullptr) || a->rotary_dim < 0) return GCS_ERR_INVALID_ARG;
+  if (a->cos_sin && (a->max_pos < 1 || (!a->positions && !in_cache))) return GCS_ERR_INVALID_ARG;
+  if (!head_dim_supported(a->d)) return GCS_ERR_UNSUPPORTED;
+  if (a->rotary_dim > a->d) return GCS_ERR_INVALID_ARG;
+  if (a->rotary_dim % 16 != 0) return GCS_ERR_UNSUPPORTED;
+  // heads that fill the grid's warps many times over, and element counts of a token beyond 2^31
+  if ((double)a->hq * a->d > 2147483647.0) return GCS_ERR_UNSUPPORTED;
+  Layout l;
+  int st;
+  if ((st = resolve_layout(a->q_stride, a->hq, a->d, &l)) != GCS_OK) return st;
+  if ((st = resolve_layout(a->k_stride, a->hkv, a->d, &l)) != GCS_OK) return st;
+  if ((st = resolve_layout(a->q_out_stride, a->hq, a->d, &l)) != GCS_OK) return st;
+  if ((st = resolve_layout(a->k_out_stride, a->hkv, a->d, &l)) != GCS_OK) return st;
+  if ((st = resolve_layout(a->dq_stride, a->hq, a->d, &l)) != GCS_OK) return st;
+  return resolve_layout(a->dk_stride, a->hkv, a->d, &l);
+}
+
+struct RopeLayouts {
+  Layout q, k, q_out, k_out, dq, dk;
+};
+static RopeLayouts rope_layouts(const gcs_qk_rope_args* a) {
+  RopeLayouts l;
+  resolve_layout(a->q_stride, a->hq, a->d, &l.q);
+  resolve_layout(a->k_stride, a->hkv, a->d, &l.k);
+  resolve_layout(a->q_out_stride, a->hq, a->d, &l.q_out);
+  resolve_layout(a->k_out_stride, a->hkv, a->d, &l.k_out);
+  resolve_layout(a->dq_stride, a->hq, a->d, &l.dq);
+  resolve_layout(a->dk_stride, a->hkv, a->d, &l.dk);
+  return l;
+}
+
+static RopeParams rope_params(const gcs_qk_rope_args* a, const RopeLayouts& l) {
+  RopeParams p{};
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.q_ts = l.q.ts, p.q_hs = l.q.hs, p.k_ts = l.k.ts, p.k_hs = l.k.hs;
+  p.qo_ts = l.q_out.ts, p.qo_hs = l.q_out.hs, p.ko_ts = l.k_out.ts, p.ko_hs = l.k_out.hs;
+  p.dq_ts = l.dq.ts, p.dq_hs = l.dq.hs, p.dk_ts = l.dk.ts, p.dk_hs = l.dk.hs;
+  p.total = a->total_tokens;
+  p.hq = a->hq;
+  p.hkv = a->hkv;
+  p.d = a->d;
+  p.rotary_dim = a->rotary_dim;
+  p.interleaved = a->interleaved;
+  p.norm = a->norm;
+  p.eps = a->eps;
+  p.q_weight = a->q_weight;
+  p.k_weight = a->k_weight;
+  p.cos_sin = a->cos_sin;
+  p.max_pos = a->max_pos;
+  p.positions = a->positions;
+  return p;
+}
+
+// Byte ranges of a rope call's inputs: q, k, the weights, the table and the positions.
+struct RopeSpans {
+  TSpan q, k, qw, kw, table, pos;
+};
+static RopeSpans rope_spans(const gcs_qk_rope_args* a, const RopeLayouts& l) {
+  const int T = a->total_tokens;
+  return RopeSpans{tspan(a->q, T, a->hq, a->d, l.q, 2),
+                   tspan(a->k, T, a->hkv, a->d, l.k, 2),
+                   tspan(span(a->q_weight, (size_t)a->d * 4)),
+                   tspan(span(a->k_weight, (size_t)a->d * 4)),
+                   tspan(span(a->cos_sin, (size_t)a->max_pos * a->rotary_dim * 4)),
+                   tspan(span(a->positions, (size_t)T * 4))};
+}
+
+int attn_qk_norm_rope_fwd(const gcs_qk_rope_args* a, void* q_out, void* k_out, gcs_stream_t stream) {
+  const int st = check_rope(a, false);
+  if (st != GCS_OK) return st;
+  if (!q_out || !k_out || !aligned16(q_out) || !aligned16(k_out)) return GCS_ERR_INVALID_ARG;
+  const RopeLayouts l = rope_layouts(a);
+  const RopeSpans in = rope_spans(a, l);
+  const TSpan outs[] = {tspan(q_out, a->total_tokens, a->hq, a->d, l.q_out, 2),
+                        tspan(k_out, a->total_tokens, a->hkv, a->d, l.k_out, 2)};
+  const TSpan ins[] = {in.q, in.k, in.qw, in.kw, in.table, in.pos};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  RopeParams p = rope_params(a, l);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_norm_rope_fwd(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_qk_norm_rope_bwd_workspace(const gcs_qk_rope_args* a) {
+  if (check_rope(a, false) != GCS_OK || (!a->q_weight && !a->k_weight)) return 0;
+  return round_up(norm_rope_bwd_partials(rope_params(a, rope_layouts(a))) * sizeof(float));
+}
+
+int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                          float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                          gcs_stream_t stream) {
+  const int st = check_rope(a, false);
+  if (st != GCS_OK) return st;
+  if (!dq_out || !dk_out || !dq || !dk) return GCS_ERR_INVALID_ARG;
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned4(dq_weight) ||
+      !aligned4(dk_weight))
+    return GCS_ERR_INVALID_ARG;
+  if ((dq_weight && !a->q_weight) || (dk_weight && !a->k_weight)) return GCS_ERR_INVALID_ARG;
+  const RopeLayouts l = rope_layouts(a);
+  const RopeSpans in = rope_spans(a, l);
+  const int T = a->total_tokens;
+  const TSpan outs[] = {tspan(dq, T, a->hq, a->d, l.dq, 2), tspan(dk, T, a->hkv, a->d, l.dk, 2),
+                        tspan(span(dq_weight, (size_t)a->d * 4)), tspan(span(dk_weight, (size_t)a->d * 4))};
+  const TSpan ins[] = {in.q, in.k, in.qw, in.kw, in.table, in.pos, tspan(dq_out, T, a->hq, a->d, l.q_out, 2),
+                       tspan(dk_out, T, a->hkv, a->d, l.k_out, 2)};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  RopeParams p = rope_params(a, l);
+  if (dq_weight || dk_weight) {
+    const size_t need = norm_rope_bwd_partials(p) * sizeof(float);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return GCS_ERR_WORKSPACE;
+    p.partials = static_cast<float*>(workspace);
+  }
+  p.q_out = static_cast<uint16_t*>(const_cast<void*>(dq_out));
+  p.k_out = static_cast<uint16_t*>(const_cast<void*>(dk_out));
+  p.dq = static_cast<uint16_t*>(dq);
+  p.dk = static_cast<uint16_t*>(dk);
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_norm_rope_bwd(p, dq_weight, dk_weight, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ write and read of the paged cache
+
+// The cache strides by the rules of the paged attention calls.
+static int cache_args_layout(const gcs_cache_args* a, CacheLayout* l) {
+  gcs_decode_args d{};
+  d.kv_format = a->kv_format;
+  d.d = a->d;
+  d.hkv = a->hkv;
+  d.block_size = a->block_size;
+  d.kv_stride_block = a->kv_stride_block;
+  d.kv_stride_head = a->kv_stride_head;
+  d.kv_stride_slot = a->kv_stride_slot;
+  return cache_layout(&d, l);
+}
+
+static int check_cache(const gcs_cache_args* a) {
+  if (!a) return GCS_ERR_INVALID_ARG;
+  if (a->num_reqs < 1 || a->total_rows < 1 || a->max_rows < 1 || a->max_blocks_per_req < 1 || a->num_blocks < 1 ||
+      a->hq < 1 || a->hkv < 1 || a->hq % a->hkv != 0)
+    return GCS_ERR_INVALID_ARG;
+  if (!a->cu_rows || !a->seq_lens || !a->block_table || !a->k_cache || !a->v_cache) return GCS_ERR_INVALID_ARG;
+  if (!aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->g_cache) || !aligned4(a->cu_rows) ||
+      !aligned4(a->seq_lens) || !aligned4(a->block_table) || !aligned4(a->k_scale) || !aligned4(a->v_scale))
+    return GCS_ERR_INVALID_ARG;
+  if (a->kv_format == GCS_KV_BF16) {
+    if (a->k_scale || a->v_scale || a->scale_mode != GCS_SCALE_PER_TOKEN) return GCS_ERR_INVALID_ARG;
+  } else if (a->kv_format == GCS_KV_FP8_E4M3) {
+    if (!a->k_scale || !a->v_scale) return GCS_ERR_INVALID_ARG;
+    if (a->scale_mode != GCS_SCALE_PER_TOKEN && a->scale_mode != GCS_SCALE_PER_TENSOR) return GCS_ERR_INVALID_ARG;
+  } else {
+    return GCS_ERR_INVALID_ARG;
+  }
+  if (!head_dim_supported(a->d)) return GCS_ERR_UNSUPPORTED;
+  if (a->block_size < 16 || a->block_size > 4096 || (a->block_size & (a->block_size - 1)) != 0)
+    return GCS_ERR_UNSUPPORTED;
+  // heads, gate tiles and the gates' grid within 32 bits
+  if ((double)a->hq * a->d > 2147483647.0) return GCS_ERR_UNSUPPORTED;
+  if (((double)a->total_rows / 128 + 2.0 * a->num_reqs) * ((a->hq + 31) / 32) > 1073741824.0 ||
+      (a->hq + 31) / 32 > 65535)
+    return GCS_ERR_UNSUPPORTED;
+  if ((double)a->num_blocks * a->hkv * a->block_size * a->d > 9.0e15) return GCS_ERR_UNSUPPORTED;
+  CacheLayout cl;
+  int st = cache_args_layout(a, &cl);
+  if (st != GCS_OK) return st;
+  Layout l;
+  if ((st = resolve_layout(a->k_stride, a->hkv, a->d, &l)) != GCS_OK) return st;
+  return resolve_layout(a->v_stride, a->hkv, a->d, &l);
+}
+
+struct CacheSpans {
+  TSpan k, v, ks, vs, g, table, lens, cu;
+};
+static CacheSpans cache_spans(const gcs_cache_args* a, const CacheLayout& cl) {
+  const size_t elt = a->kv_format == GCS_KV_BF16 ? 2 : 1;
+  const size_t rows = (size_t)a->num_blocks * a->hkv * a->block_size;
+  const size_t sc = a->scale_mode == GCS_SCALE_PER_TENSOR ? 4 : rows * 4;
+  const size_t bytes = (size_t)(a->num_blocks - 1) * cl.bs + (size_t)(a->hkv - 1) * cl.hs +
+                       (size_t)(a->block_size - 1) * cl.ss + (size_t)a->d * elt;
+  return CacheSpans{tspan(span(a->k_cache, bytes)),
+                    tspan(span(a->v_cache, bytes)),
+                    tspan(span(a->k_scale, sc)),
+                    tspan(span(a->v_scale, sc)),
+                    tspan(span(a->g_cache, (size_t)a->num_blocks * a->hq * a->block_size * 4)),
+                    tspan(span(a->block_table, (size_t)a->num_reqs * a->max_blocks_per_req * 4)),
+                    tspan(span(a->seq_lens, (size_t)a->num_reqs * 4)),
+                    tspan(span(a->cu_rows, ((size_t)a->num_reqs + 1) * 4))};
+}
+
+// True when the K and V caches (same strides) share a byte.  Apart, or side by side within every
+// period of one of the strides that the wider strides are multiples of, they do not.
+static bool caches_meet(const gcs_cache_args* a, const CacheLayout& l, const CacheSpans& s) {
+  if (!(s.k.a < s.v.b && s.v.a < s.k.b)) return false;
+  const long long row = (long long)a->d * (a->kv_format == GCS_KV_BF16 ? 2 : 1);
+  const bool hi = l.head_inner();
+  const long long inner = hi ? l.hs : l.ss, outer = hi ? l.ss : l.hs;
+  const long long n_inner = hi ? a->hkv : a->block_size, n_outer = hi ? a->block_size : a->hkv;
+  const unsigned long long off = s.k.a < s.v.a ? s.v.a - s.k.a : s.k.a - s.v.a;
+  auto beside = [&](long long period, long long width) {
+    const long long d = (long long)(off % (unsigned long long)period);
+    return d >= width && d + width <= period;
+  };
+  const long long w_outer = (n_inner - 1) * inner + row;              // bytes within an outer period
+  const long long w_block = (n_outer - 1) * outer + w_outer;          // and within a block
+  if (beside(l.bs, w_block)) return false;
+  if (l.bs % outer == 0 && beside(outer, w_outer)) return false;
+  return !(l.bs % inner == 0 && outer % inner == 0 && beside(inner, row));
+}
+
+static CacheParams cache_params(const gcs_cache_args* a, const CacheLayout& cl) {
+  CacheParams p{};
+  p.num_reqs = a->num_reqs;
+  p.total = a->total_rows;
+  p.hq = a->hq;
+  p.hkv = a->hkv;
+  p.d = a->d;
+  p.cu = a->cu_rows;
+  p.seq_lens = a->seq_lens;
+  p.block_table = a->block_table;
+  p.max_blocks = a->max_blocks_per_req;
+  p.num_blocks = a->num_blocks;
+  p.block_size = a->block_size;
+  while ((1 << p.log2_block) < a->block_size) ++p.log2_block;
+  p.capacity = (long long)a->max_blocks_per_req * a->block_size;
+  p.format = a->kv_format == GCS_KV_BF16 ? kCacheBf16
+             : a->scale_mode == GCS_SCALE_PER_TENSOR ? kCachePerTensor : kCachePerToken;
+  p.k_cache = static_cast<uint8_t*>(a->k_cache);
+  p.v_cache = static_cast<uint8_t*>(a->v_cache);
+  p.kv_bs = cl.bs, p.kv_hs = cl.hs, p.kv_ss = cl.ss;
+  p.k_scale = a->k_scale;
+  p.v_scale = a->v_scale;
+  p.g_cache = a->g_cache;
+  Layout lk, lv;
+  resolve_layout(a->k_stride, a->hkv, a->d, &lk);
+  resolve_layout(a->v_stride, a->hkv, a->d, &lv);
+  p.k_ts = lk.ts, p.k_hs = lk.hs, p.v_ts = lv.ts, p.v_hs = lv.hs;
+  return p;
+}
+
+// Bytes of the gates' tile sums.
+static size_t append_ws(const gcs_cache_args* a) {
+  if (!a->g_cache || !cache_gates_need_sums(a->max_rows)) return 0;
+  return round_up((size_t)cache_gate_slots(a->total_rows, a->num_reqs) * a->hq * sizeof(float));
+}
+
+size_t attn_cache_append_workspace(const gcs_cache_args* a) { return check_cache(a) == GCS_OK ? append_ws(a) : 0; }
+
+// Both appends: r and q_out are null without the rotation, k is null with it.
+static int cache_append(const gcs_cache_args* a, const gcs_qk_rope_args* r, const void* k, const void* v,
+                        const float* log_gate, void* q_out, void* workspace, size_t workspace_bytes,
+                        gcs_stream_t stream) {
+  int st = check_cache(a);
+  if (st != GCS_OK) return st;
+  if (r) {
+    if ((st = check_rope(r, true)) != GCS_OK) return st;
+    if (r->total_tokens != a->total_rows || r->hq != a->hq || r->hkv != a->hkv || r->d != a->d)
+      return GCS_ERR_INVALID_ARG;
+    if (!q_out || !aligned16(q_out)) return GCS_ERR_INVALID_ARG;
+  } else if (!k || !aligned16(k)) {
+    return GCS_ERR_INVALID_ARG;
+  }
+  if (!v || !aligned16(v) || !aligned4(log_gate)) return GCS_ERR_INVALID_ARG;
+  if ((log_gate == nullptr) != (a->g_cache == nullptr)) return GCS_ERR_INVALID_ARG;
+  CacheLayout cl;
+  cache_args_layout(a, &cl);
+  const CacheSpans cs = cache_spans(a, cl);
+  if (caches_meet(a, cl, cs)) return GCS_ERR_INVALID_ARG;
+  CacheParams p = cache_params(a, cl);
+  RopeParams q{};
+  const TSpan none = tspan(Span{0, 0});
+  RopeSpans rs{none, none, none, none, none, none};
+  const int T = a->total_rows;
+  const Layout lk{p.k_ts, p.k_hs}, lv{p.v_ts, p.v_hs};
+  TSpan qo = none;
+  if (r) {
+    const RopeLayouts rl = rope_layouts(r);
+    q = rope_params(r, rl);
+    rs = rope_spans(r, rl);
+    qo = tspan(q_out, T, a->hq, a->d, rl.q_out, 2);
+    q.q_out = static_cast<uint16_t*>(q_out);
+    p.k = q.k, p.k_ts = q.k_ts, p.k_hs = q.k_hs;
+  } else {
+    rs.k = tspan(k, T, a->hkv, a->d, lk, 2);
+    p.k = static_cast<const uint16_t*>(k);
+  }
+  p.v = static_cast<const uint16_t*>(v);
+  p.log_gate = log_gate;
+  const bool per_token = p.format == kCachePerToken;
+  // K against V was checked above; here each against everything else
+  const TSpan ins[] = {rs.q, rs.k, rs.qw, rs.kw, rs.table, rs.pos, tspan(v, T, a->hkv, a->d, lv, 2),
+                       tspan(span(log_gate, (size_t)T * a->hq * 4)), cs.table, cs.lens, cs.cu,
+                       per_token ? none : cs.ks, per_token ? none : cs.vs};
+  const TSpan outs_k[] = {cs.k, per_token ? cs.ks : none, per_token ? cs.vs : none, cs.g, qo};
+  const TSpan outs_v[] = {cs.v, per_token ? cs.ks : none, per_token ? cs.vs : none, cs.g, qo};
+  if (outputs_overlap(outs_k, ins) || outputs_overlap(outs_v, ins)) return GCS_ERR_INVALID_ARG;
+  const size_t need = append_ws(a);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+      return GCS_ERR_WORKSPACE;
+    p.tile_sums = static_cast<float*>(workspace);
+  }
+  p.status = q.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_cache_append(p, r ? &q : nullptr, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_append(const gcs_cache_args* a, const void* k, const void* v, const float* log_gate, void* workspace,
+                      size_t workspace_bytes, gcs_stream_t stream) {
+  return cache_append(a, nullptr, k, v, log_gate, nullptr, workspace, workspace_bytes, stream);
+}
+
+int attn_cache_append_rope(const gcs_cache_args* a, const gcs_qk_rope_args* r, const void* v, const float* log_gate,
+                           void* q_out, void* workspace, size_t workspace_bytes, gcs_stream_t stream) {
+  if (!r) return GCS_ERR_INVALID_ARG;
+  return cache_append(a, r, nullptr, v, log_gate, q_out, workspace, workspace_bytes, stream);
+}
+
+int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate, gcs_stream_t stream) {
+  const int st = check_cache(a);
+  if (st != GCS_OK) return st;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned4(log_gate)) return GCS_ERR_INVALID_ARG;
+  if ((log_gate == nullptr) != (a->g_cache == nullptr)) return GCS_ERR_INVALID_ARG;
+  CacheLayout cl;
+  cache_args_layout(a, &cl);
+  const CacheSpans cs = cache_spans(a, cl);
+  CacheParams p = cache_params(a, cl);
+  const int T = a->total_rows;
+  const TSpan outs[] = {tspan(k, T, a->hkv, a->d, Layout{p.k_ts, p.k_hs}, 2),
+                        tspan(v, T, a->hkv, a->d, Layout{p.v_ts, p.v_hs}, 2),
+                        tspan(span(log_gate, (size_t)T * a->hq * 4))};
+  const TSpan ins[] = {cs.k, cs.v, cs.ks, cs.vs, cs.g, cs.table, cs.lens, cs.cu};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  p.k_out = static_cast<uint16_t*>(k);
+  p.v_out = static_cast<uint16_t*>(v);
+  p.log_gate_out = log_gate;
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_cache_gather(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int gcs_set_device_checks(int enable) {
   if (enable != 0 && enable != 1) return GCS_ERR_INVALID_ARG;
   g_device_checks.store(enable, std::memory_order_relaxed);

@@ -198,6 +198,60 @@ cudaError_t launch_check_paged(const int32_t* cu_q, const int32_t* seq_lens, con
                                int block_size, int window, const PagedOperandCheck& fp8, int32_t* cu_out,
                                int* status, cudaStream_t s);
 
+// Norm and rotation of query and key rows ([tokens, heads, d] bf16, element strides (token, head)).
+struct RopeParams {
+  const uint16_t *q, *k;
+  long long q_ts, q_hs, k_ts, k_hs;
+  uint16_t *q_out, *k_out;  // the outputs (backward: their gradients, read)
+  long long qo_ts, qo_hs, ko_ts, ko_hs;
+  uint16_t *dq, *dk;        // backward
+  long long dq_ts, dq_hs, dk_ts, dk_hs;
+  int total, hq, hkv, d;
+  int rotary_dim, interleaved, norm;
+  float eps;
+  const float *q_weight, *k_weight;  // [d] or null (ones)
+  const float* cos_sin;              // [max_pos, rotary_dim] or null
+  int max_pos;
+  const int32_t* positions;          // [total] or null
+  float* partials;                   // backward: norm_rope_bwd_partials() floats, or null (no weight gradients)
+  int* status;
+};
+cudaError_t launch_norm_rope_fwd(const RopeParams& p, cudaStream_t s);
+// dq, dk, then (with p.partials) d q_weight and d k_weight, each where not null.
+size_t norm_rope_bwd_partials(const RopeParams& p);
+cudaError_t launch_norm_rope_bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStream_t s);
+
+// Rows between packed tensors and the paged cache.
+constexpr int kCachePerToken = 0, kCachePerTensor = 1, kCacheBf16 = 2;
+struct CacheParams {
+  int num_reqs, total, hq, hkv, d;
+  const int32_t* cu;           // [num_reqs + 1]
+  const int32_t* seq_lens;     // [num_reqs]
+  const int32_t* block_table;  // [num_reqs, max_blocks]
+  int max_blocks, num_blocks, block_size, log2_block;
+  long long capacity;          // max_blocks * block_size
+  int format;                  // kCache...
+  uint8_t *k_cache, *v_cache;
+  long long kv_bs, kv_hs, kv_ss;  // byte strides (block, kv head, slot)
+  float *k_scale, *v_scale;    // per token [num_blocks, hkv, block_size], per tensor [1], or null
+  float* g_cache;              // [num_blocks, hq, block_size] or null
+  const uint16_t *k, *v;       // append: rows to write
+  uint16_t *k_out, *v_out;     // gather: rows read
+  long long k_ts, k_hs, v_ts, v_hs;
+  const float* log_gate;       // append: [total, hq] or null
+  float* log_gate_out;         // gather: [total, hq] or null
+  float* tile_sums;            // append: [cache_gate_slots()][hq], or null (every tile sums what is before it)
+  int n_gate, gate_groups;     // set by the launchers: blocks of the gate role, groups of 32 query heads
+  int* status;
+};
+// Tile slots of the gates of `total` rows in num_reqs requests.
+int cache_gate_slots(int total, int num_reqs);
+// Whether appends of up to max_rows rows with gates take the tile sums.
+bool cache_gates_need_sums(int max_rows);
+// rope: queries and keys go through the norm and rotation first (rope->k, rope->q; p.k unused).
+cudaError_t launch_cache_append(const CacheParams& p, const RopeParams* rope, cudaStream_t s);
+cudaError_t launch_cache_gather(const CacheParams& p, cudaStream_t s);
+
 // Size of the static scratch behind attn_decode_paged_noalloc (64 MiB).
 constexpr size_t kNoAllocScratchBytes = size_t(64) << 20;
 

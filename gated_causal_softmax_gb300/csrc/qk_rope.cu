@@ -1,0 +1,252 @@
+// Norm of every query and key head with the rotation by position in the same pass, and its
+// backward.  For a row x of token t (one head), weights w and the angles of position p_t:
+//
+//   forward    r = (mean(x^2) + eps)^(-1/2),  y = x r w,  out = R(p_t) y
+//   backward   g = R(p_t)^T dout,  dw = sum over tokens and heads of g x r,  u = g w,
+//              dx = r (u - x r mean(u x r))
+//
+// R turns the first rotary_dim elements in pairs; both sums of a row's backward (x^2 and u x)
+// are reduced side by side, as mean(u x r) = r mean(u x).
+//
+// Both are bound by HBM: each element is read once (twice in the backward: x and dout) and
+// written once, all arithmetic in fp32 between one load and one rounding to bf16.
+#include <algorithm>
+
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace gcs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxBlocks = 152 * 4;  // warps take further tokens beyond this many blocks
+
+// A warp's share: heads [h0, h1) of the queries or of the keys, and every step-th token.
+struct Share {
+  bool is_k;
+  int h0, h1;
+  uint32_t t, step;
+};
+template <int H>  // heads of a share
+__device__ __forceinline__ bool warp_share(int total, int hq, int hkv, Share& s) {
+  const int q_segs = (hq + H - 1) / H, segs = q_segs + (hkv + H - 1) / H;
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
+  s.step = warps / segs;
+  if (w >= s.step * segs) return false;
+  const int seg = w % segs;
+  s.is_k = seg >= q_segs;
+  s.h0 = (s.is_k ? seg - q_segs : seg) * H;
+  s.h1 = min(s.h0 + H, s.is_k ? hkv : hq);
+  s.t = w / segs;
+  return true;
+}
+int blocks_for(int total, int hq, int hkv, int H) {
+  const int segs = (hq + H - 1) / H + (hkv + H - 1) / H;
+  const long long blocks = ((long long)total * segs + kWarps - 1) / kWarps;
+  // at least one warp for each share of heads
+  return (int)std::max<long long>(std::min<long long>(blocks, kMaxBlocks), (segs + kWarps - 1) / kWarps);
+}
+
+// The token's position: false for a row to leave out (negative: padding; past the table: an error).
+__device__ __forceinline__ bool token_position(const RopeParams& p, uint32_t t, int& pos) {
+  pos = p.positions ? __ldg(p.positions + t) : 0;
+  if (pos < 0) return false;
+  if (p.cos_sin && pos >= p.max_pos) {
+    if ((threadIdx.x & 31) == 0) atomicCAS(p.status, kDevOk, kDevInvalidArg);
+    return false;
+  }
+  return true;
+}
+
+template <int D, int U>
+__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const RopeParams p) {
+  constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
+  Share s;
+  if (!warp_share<R * U>(p.total, p.hq, p.hkv, s)) return;
+  const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
+  const RowRuns runs = row_runs(sub, p.rotary_dim, p.interleaved);
+  const uint16_t* in = s.is_k ? p.k : p.q;
+  uint16_t* out = s.is_k ? p.k_out : p.q_out;
+  const long long its = s.is_k ? p.k_ts : p.q_ts, ihs = s.is_k ? p.k_hs : p.q_hs;
+  const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
+  float w[16];
+  load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
+  for (uint32_t t = s.t; t < (uint32_t)p.total; t += s.step) {
+    RawRow raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = s.h0 + u * R + grp;
+      raw[u] = h < s.h1 ? load_row(in + t * its + h * ihs, runs) : zero_row();
+    }
+    int pos;
+    if (!token_position(p, t, pos)) continue;
+    Angles ang;
+    load_angles(p.cos_sin, pos, p.rotary_dim, sub, runs, ang);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = s.h0 + u * R + grp;
+      float x[16];
+      unpack_row(raw[u], x);
+      if (p.norm) {
+        const float r = row_rstd<D>(x, p.eps);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+      }
+      rotate_row<false>(x, runs, ang, p.interleaved);
+      if (h < s.h1) store_row(out + t * ots + h * ohs, runs, x);
+    }
+  }
+}
+
+// Also the gradients of the weights: every lane sums g x r of its 16 elements over its rows, the
+// lanes of a block with the same elements are added in a fixed order, and the block writes its
+// part of d q_weight and d k_weight to p.partials [blocks][2][D]; weight_grad_kernel adds those.
+template <int D>
+__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeParams p) {
+  constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
+  __shared__ float part[kWarps][D];
+  __shared__ int part_is_k[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = threadIdx.x & (L - 1), grp = lane / L;
+  const RowRuns runs = row_runs(sub, p.rotary_dim, p.interleaved);
+  Share s;
+  float dw[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  const bool works = warp_share<R>(p.total, p.hq, p.hkv, s);
+  if (works) {
+    const uint16_t* in = s.is_k ? p.k : p.q;
+    const uint16_t* dout = s.is_k ? p.k_out : p.q_out;
+    uint16_t* dx = s.is_k ? p.dk : p.dq;
+    const long long its = s.is_k ? p.k_ts : p.q_ts, ihs = s.is_k ? p.k_hs : p.q_hs;
+    const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
+    const long long dts = s.is_k ? p.dk_ts : p.dq_ts, dhs = s.is_k ? p.dk_hs : p.dq_hs;
+    float w[16];
+    load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
+    const int h = s.h0 + grp;
+    const bool valid = h < s.h1;
+    for (uint32_t t = s.t; t < (uint32_t)p.total; t += s.step) {
+      RawRow rx = zero_row(), rg = zero_row();
+      if (valid) {
+        rg = load_row(dout + t * ots + h * ohs, runs);
+        if (p.norm) rx = load_row(in + t * its + h * ihs, runs);
+      }
+      int pos;
+      float g[16];
+      if (!token_position(p, t, pos)) {  // the row's output does not depend on it
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = 0.f;
+      } else {
+        Angles ang;
+        load_angles(p.cos_sin, pos, p.rotary_dim, sub, runs, ang);
+        unpack_row(rg, g);
+        rotate_row<true>(g, runs, ang, p.interleaved);
+        if (p.norm) {
+          float x[16], ss = 0.f, su = 0.f;
+          unpack_row(rx, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            ss = fmaf(x[i], x[i], ss);
+            su = fmaf(g[i] * w[i], x[i], su);
+          }
+          ss = row_sum<L>(ss);
+          su = row_sum<L>(su);
+          const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+          const float m = su * r * r * (1.f / D);  // r mean(u x r)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            dw[i] = fmaf(g[i] * r, x[i], dw[i]);
+            g[i] = r * fmaf(-x[i], m, g[i] * w[i]);
+          }
+        }
+      }
+      if (valid) store_row(dx + t * dts + h * dhs, runs, g);
+    }
+  }
+  if (!p.partials) return;
+#pragma unroll
+  for (int off = L; off < 32; off <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dw[i] += __shfl_xor_sync(kFullMask, dw[i], off);
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[warp][runs.a + i] = dw[i];
+      part[warp][runs.b + i] = dw[8 + i];
+    }
+  }
+  if (lane == 0) part_is_k[warp] = works ? (s.is_k ? 1 : 0) : 2;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+    const int is_k = c / D;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i)
+      if (part_is_k[i] == is_k) sum += part[i][c % D];
+    p.partials[(size_t)blockIdx.x * 2 * D + c] = sum;
+  }
+}
+
+// dw of 32 columns a block: 32 threads a column add every 32nd block's part, then their sums.
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restrict__ partials, int blocks, int d,
+                                                           float* __restrict__ dq_weight,
+                                                           float* __restrict__ dk_weight) {
+  __shared__ float sm[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float sum = 0.f;
+  for (int b = threadIdx.y; b < blocks; b += 32) sum += __ldg(partials + (size_t)b * 2 * d + c);
+  sm[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  float x = sm[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  if (threadIdx.x == 0) {
+    const int col = blockIdx.x * 32 + threadIdx.y;
+    float* dst = col < d ? dq_weight : dk_weight;
+    if (dst) dst[col < d ? col : col - d] = x;
+  }
+}
+
+template <int D>
+cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
+  constexpr int U = 2;
+  norm_rope_fwd_kernel<D, U><<<blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows * U), kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStream_t s) {
+  const int blocks = blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows);
+  norm_rope_bwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.partials) return e;
+  weight_grad_kernel<<<2 * D / 32, dim3(32, 32), 0, s>>>(p.partials, blocks, D, dq_weight, dk_weight);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t norm_rope_bwd_partials(const RopeParams& p) {
+  return (size_t)blocks_for(p.total, p.hq, p.hkv, 512 / p.d) * 2 * p.d;
+}
+
+cudaError_t launch_norm_rope_fwd(const RopeParams& p, cudaStream_t s) {
+  switch (p.d) {
+    case 64: return fwd<64>(p, s);
+    case 128: return fwd<128>(p, s);
+    case 256: return fwd<256>(p, s);
+    default: return fwd<512>(p, s);
+  }
+}
+
+cudaError_t launch_norm_rope_bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStream_t s) {
+  switch (p.d) {
+    case 64: return bwd<64>(p, dq_weight, dk_weight, s);
+    case 128: return bwd<128>(p, dq_weight, dk_weight, s);
+    case 256: return bwd<256>(p, dq_weight, dk_weight, s);
+    default: return bwd<512>(p, dq_weight, dk_weight, s);
+  }
+}
+
+}  // namespace gcs

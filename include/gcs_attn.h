@@ -6,6 +6,10 @@
  *   attn_bwd           prefill backward (dQ, dK, dV, d log_gate, d sink)
  *   attn_decode_paged  paged single-query / short-query decode over an fp8 e4m3 KV cache
  *   attn_prefill_paged paged chunked prefill (query chunks of any length) over the same cache
+ * and these make what the four read (library calls with no counterpart in the pages):
+ *   attn_qk_norm_rope_fwd, attn_qk_norm_rope_bwd   per-head norm and rotation of q and k
+ *   attn_cache_append, attn_cache_append_rope      write of k, v and log gates into the paged cache
+ *   attn_cache_gather                              read of the paged cache into packed tensors
  *
  * Sources for what each call computes (page title, section):
  *   [FLA] fla-org/flash-linear-attention issue #1322 "[Perf] Gluon attention backend with
@@ -41,7 +45,8 @@
  *   - Device-side contents (cu_seqlens monotone and ending at total_tokens, page-table
  *     entries in [0, num_blocks), seq_lens >= q_len) are preconditions; they are not
  *     checked on the host because reading them would synchronise.  gcs_set_device_checks
- *     makes every call check them on the device first (see "device-content checks").
+ *     makes every attention call check them on the device first (see "device-content
+ *     checks"); the norm, rotation and cache calls always check what they index with.
  *   - Every wait inside a kernel is bounded (2 s).  A kernel that gives up records
  *     GCS_ERR_DEVICE_TIMEOUT in a per-device status word, releases its resources and
  *     returns; read it with gcs_get_device_status().
@@ -274,6 +279,123 @@ size_t attn_prefill_paged_workspace(const gcs_decode_args* a);
 int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, size_t workspace_bytes,
                        gcs_stream_t stream);
 
+/* ------------------------------------------------------------------ norm and rotation of q and k
+ * Between the projections and the attention calls: each query and key head goes through an
+ * RMS norm over its d elements and a rotation by its token's position, in one pass:
+ *     r = (mean(x^2) + eps)^(-1/2),   y = x * r * weight          (norm = 0: y = x)
+ *     pairs (a, b) of y's first rotary_dim elements, i < m = rotary_dim / 2:
+ *         interleaved = 0: (y_i, y_{i+m});   interleaved = 1: (y_{2i}, y_{2i+1})
+ *         a' = a c - b s,  b' = b c + a s,   c = cos_sin[p][i], s = cos_sin[p][m + i], p = positions[t]
+ *     elements from rotary_dim on are passed through.
+ * All in fp32 with one rounding to bf16.  The table is the caller's (computed in 64 bits for far
+ * positions, with whatever frequency scaling the model uses).
+ * A token with a negative position is padding: its outputs are left as they were, and its
+ * gradients are 0.  A position of max_pos or more is not read: the token is treated as padding
+ * and GCS_ERR_INVALID_ARG is recorded in the device status word (in every mode; checked mode
+ * adds nothing to these calls).
+ * Supported: d 64, 128, 256 or 512; rotary_dim a multiple of 16, <= d.
+ */
+typedef struct {
+  int total_tokens;            /* rows of q and k, >= 1                                   */
+  int hq, hkv, d;              /* hq % hkv == 0                                           */
+  int rotary_dim;              /* 0 (exactly when cos_sin is NULL), or a multiple of 16   */
+  int interleaved;             /* 0: halves, 1: neighbouring pairs                        */
+  int norm;                    /* 1: RMS norm, 0: rotation only (weights must be NULL)    */
+  float eps;                   /* >= 0                                                    */
+  const void* q;               /* bf16 [total_tokens, hq, d]                              */
+  const void* k;               /* bf16 [total_tokens, hkv, d]                             */
+  const float* q_weight;       /* fp32 [d], 16-byte aligned, or NULL: ones                */
+  const float* k_weight;       /* fp32 [d], 16-byte aligned, or NULL: ones                */
+  const float* cos_sin;        /* fp32 [max_pos, rotary_dim], cosines then sines; or NULL */
+  int max_pos;                 /* rows of cos_sin (>= 1 with cos_sin)                     */
+  const int32_t* positions;    /* int32 [total_tokens]; NULL only without cos_sin, and in
+                                  attn_cache_append_rope (there: the cached positions)    */
+  gcs_strides q_stride, k_stride;          /* layouts of q and k                          */
+  gcs_strides q_out_stride, k_out_stride;  /* of q_out and k_out (backward: dq_out, dk_out) */
+  gcs_strides dq_stride, dk_stride;        /* backward: of dq and dk                      */
+} gcs_qk_rope_args;
+
+/* Forward.  q_out bf16 [total_tokens, hq, d] (q_out_stride), k_out bf16 [total_tokens, hkv, d]
+ * (k_out_stride).  No workspace. */
+int attn_qk_norm_rope_fwd(const gcs_qk_rope_args* a, void* q_out, void* k_out, gcs_stream_t stream);
+
+/* Backward of L = sum(q_out * dq_out) + sum(k_out * dk_out): dq, dk (bf16) and, with the norm,
+ * dq_weight and dk_weight (fp32 [d], summed over tokens and heads; each may be NULL when it is
+ * not wanted, and must be NULL when its weight is NULL).  Reads the forward's q and k (with
+ * norm = 0 they are not read).  Every gradient is summed in a fixed order, so repeated calls
+ * give the same bits.  The workspace (256-byte aligned) holds the blocks' parts of the weights'
+ * gradients; none is needed when neither is wanted. */
+size_t attn_qk_norm_rope_bwd_workspace(const gcs_qk_rope_args* a);
+int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                          float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                          gcs_stream_t stream);
+
+/* ------------------------------------------------------------------ write and read of the paged cache
+ * The cache is the one attn_decode_paged and attn_prefill_paged read.  Packed row t belongs to
+ * request r with cu_rows[r] <= t < cu_rows[r + 1]; with len = cu_rows[r + 1] - cu_rows[r] it is
+ * cached position p = seq_lens[r] - len + t - cu_rows[r], like the paged calls' query rows: the
+ * same cu_q, seq_lens and block_table serve an append and the attention call after it.  Rows
+ * from cu_rows[num_reqs] on (a padded batch) are left out.
+ *   fp8, per token:  scale = max|x| / 448 over the d elements of (token, kv head), written to
+ *                    k_scale / v_scale; code = e4m3(x / scale), nearest even.  A row of zeros
+ *                    has scale 0 and codes 0.  An infinity gives scale inf, a NaN scale NaN.
+ *   fp8, per tensor: code = e4m3(x / scale) saturating at +-448, with the caller's scale (read).
+ *   bf16:            the elements.
+ *   gates:           g_cache at p = (g_cache at p - 1, or 0 before the first) + log_gate, in fp32,
+ *                    running on through the request's rows.
+ * Slots outside the rows' positions are not touched.
+ * Preconditions: no two rows share a slot (blocks that are written belong to one request), and
+ * cu_rows is sorted from 0.  A row whose position or block-table entry lies outside the cache
+ * (0 <= p < max_blocks_per_req * block_size, entry in [0, num_blocks)) is left out, as are the
+ * gates of a request whose preceding cached gate lies outside, and GCS_ERR_INVALID_ARG is recorded
+ * in the device status word: in every mode; checked mode adds nothing to these calls.
+ * Supported: d 64, 128, 256 or 512; any hq, hkv with hq % hkv == 0; block_size 16 x 2^k, 16..4096;
+ * the cache strides of gcs_decode_args.  K and V may interleave within one buffer (block by block,
+ * slot by slot or head by head) as long as no byte belongs to both. */
+typedef struct {
+  int num_reqs;                /* >= 1                                                    */
+  const int32_t* cu_rows;      /* device int32 [num_reqs + 1]                            */
+  int total_rows;              /* rows of the packed tensors, >= 1                        */
+  int max_rows;                /* host upper bound on the rows of a request, >= 1 (it chooses
+                                  how the gates are summed; nothing else depends on it)   */
+  const int32_t* seq_lens;     /* device int32 [num_reqs]: cached tokens, these rows included */
+  const int32_t* block_table;  /* device int32 [num_reqs, max_blocks_per_req]            */
+  int max_blocks_per_req;
+  void* k_cache;               /* fp8 e4m3 or bf16 [num_blocks, hkv, block_size, d]      */
+  void* v_cache;               /* same format and strides                                 */
+  float* k_scale;              /* fp32 [num_blocks, hkv, block_size], or [1], or NULL    */
+  float* v_scale;
+  int num_blocks, block_size;
+  int hq, hkv, d;              /* hq: heads of the gates and of the rotated queries       */
+  int kv_format, scale_mode;   /* as in gcs_decode_args                                   */
+  float* g_cache;              /* fp32 [num_blocks, hq, block_size], or NULL              */
+  int64_t kv_stride_block, kv_stride_head, kv_stride_slot;  /* as in gcs_decode_args      */
+  gcs_strides k_stride, v_stride;  /* layouts of the packed k and v                       */
+} gcs_cache_args;
+
+/* Workspace bytes of the two append calls (0 without g_cache and for short appends). */
+size_t attn_cache_append_workspace(const gcs_cache_args* a);
+
+/* Write k, v (bf16 [total_rows, hkv, d]) and, with g_cache, log_gate (fp32 [total_rows, hq]; NULL
+ * exactly when g_cache is) into the cache. */
+int attn_cache_append(const gcs_cache_args* a, const void* k, const void* v, const float* log_gate, void* workspace,
+                      size_t workspace_bytes, gcs_stream_t stream);
+
+/* attn_qk_norm_rope_fwd and attn_cache_append in one launch: r->q goes through norm and rotation
+ * into q_out (r->q_out_stride), r->k straight into the cache (quantised from fp32, without the
+ * rounding to bf16 in between), v as it is.  r's total_tokens, hq, hkv and d are those of a;
+ * a->k_stride is not used.  r->positions NULL: the cached positions; otherwise a row with a
+ * negative position is padding and left out of q_out and of the cache (not of the gates). */
+int attn_cache_append_rope(const gcs_cache_args* a, const gcs_qk_rope_args* r, const void* v, const float* log_gate,
+                           void* q_out, void* workspace, size_t workspace_bytes, gcs_stream_t stream);
+
+/* Read the rows back: k, v bf16 [total_rows, hkv, d] (a->k_stride, a->v_stride), each value
+ * bf16(code * scale); log_gate (with g_cache; NULL exactly when g_cache is) fp32 [total_rows, hq],
+ * g_cache at p minus g_cache at p - 1 (or 0).  With cu_rows the cumulated seq_lens the whole cache is
+ * read, as attn_fwd takes it; with fewer rows the last ones of each request.  The caches, scales
+ * and g_cache are only read.  No workspace. */
+int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate, gcs_stream_t stream);
+
 /* ------------------------------------------------------------------ status
  * Per-device status word written by kernels that gave up on a bounded wait.
  * Copies the word for the current device into *status (synchronous) and, if clear != 0,
@@ -303,9 +425,9 @@ int gcs_selftest_bounded_wait(gcs_stream_t stream);
  * writer wins, like a timeout); read it with gcs_get_device_status.
  *
  * gcs_set_device_checks(1) turns on checked mode for every later call of this process (0
- * turns it off; other values return GCS_ERR_INVALID_ARG).  In checked mode each attn_* call
- * first launches one single-CTA kernel on its stream that checks its arrays and writes a copy
- * of cu_seqlens (or cu_q) to the end of the call's workspace; the call's kernels read that
+ * turns it off; other values return GCS_ERR_INVALID_ARG).  In checked mode each attention call
+ * (attn_fwd, attn_bwd, attn_decode_paged, attn_prefill_paged) first launches one single-CTA
+ * kernel on its stream that checks its arrays and writes a copy of cu_seqlens (or cu_q) to the end of the call's workspace; the call's kernels read that
  * copy.  When a check fails the copy is all zeros, an empty batch: no kernel then reads
  * through an index taken from these arrays, so a broken array cannot send a kernel outside a
  * buffer.
@@ -327,7 +449,8 @@ int gcs_check_paged_inputs(const gcs_decode_args* a, gcs_stream_t stream);
 
 /* ------------------------------------------------------------------ instrumentation
  * Arms two caller-created CUDA events (cudaEvent_t, passed as void*) for the next attn_fwd,
- * attn_bwd, attn_decode_paged or attn_prefill_paged call made by this host thread: `before`
+ * attn_bwd, attn_decode_paged or attn_prefill_paged call made by this host thread (the norm,
+ * rotation and cache calls leave them armed): `before`
  * is recorded on the call's stream immediately before its main attention kernels (the
  * prefill forward kernel; the backward's attention kernels -- dQ pass + dK/dV pass, or the
  * wide-head role kernels; the split-K decode kernel; the paged prefill kernel) and `after`

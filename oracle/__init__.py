@@ -8,7 +8,8 @@ Parity pins: every function here is checked in ``tests/test_oracle_pins.py`` aga
 library routines (fp64 ``scaled_dot_product_attention``, ``torch.autograd``,
 ``torch.float8_e4m3fn`` / ``torch.bfloat16`` conversions), closed forms, finite
 differences, invariants and hand-derived fixtures (``tests/golden/``), and on random small
-cases in ``tests/test_oracle_properties.py``.  No function is "parity unpinned".
+cases in ``tests/test_oracle_properties.py`` (the functions of ``rows.py`` in
+``tests/test_oracle_rows.py``).  No function is "parity unpinned".
 """
 from .formats import bf16_round, e4m3_decode  # noqa: F401
 from .attention import (  # noqa: F401
@@ -21,4 +22,13 @@ from .attention import (  # noqa: F401
     decode_paged_splitk,
     gather_kv,
     rel_rms,
+)
+from .rows import (  # noqa: F401
+    cache_gates,
+    cache_gather,
+    e4m3_round,
+    norm_rope,
+    norm_rope_backward,
+    quantise_row,
+    row_places,
 )
