@@ -600,57 +600,67 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, k_scale, v_scale, block_table
     return out
 
 
-def _on_current_device(*tensors) -> None:
-    """The calls below launch on the current device's stream; their tensors have to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on device {t.get_device()}, the current device is {dev}")
+# ------------------------------------------------------------------ norm, rotation and cache rows
+# These calls run once a layer in a decoding step, where the host's time is what counts, so every
+# tensor is looked at once: type, shape, device and layout in one test, the reason only if it fails.
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(dev).cuda_stream without the object
 
 
-def _rows(t, name: str, tokens: int, heads: int, d: int) -> torch.Tensor:
-    """A bf16 [tokens, heads, d] tensor, heads and tokens at any strides the library takes."""
-    _need(t, torch.bfloat16, name, strided=True)
-    if tuple(t.shape) != (tokens, heads, d):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}], got {list(t.shape)}")
-    return t
+def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:
+    _need(t, dtype, name, strided)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    # the library launches on the current device's stream
+    raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
 
 
-def _row_strides(t: torch.Tensor) -> Strides:
-    """Strides of a [tokens, heads, dim] tensor; a dimension of one element has no stride of its
-    own, whatever torch says of it."""
-    n, heads, d = t.shape
-    head = t.stride(1) if heads > 1 else d
-    return Strides(t.stride(0) if n > 1 else heads * head, head)
+def _vector(t, dtype, name: str, shape, dev: int) -> Optional[int]:
+    """Address of a contiguous tensor, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, name, shape, dev, False)
+    return t.data_ptr()
 
 
-def _vector(t, dtype, name: str, shape) -> Optional[torch.Tensor]:
-    if t is not None:
-        _need(t, dtype, name)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+def _rows(t, name: str, shape, dev: int):
+    """(address, (token stride, head stride)) of a bf16 [tokens, heads, d] tensor.  A dimension of one
+    element has no stride of its own, whatever torch says of it."""
+    if t is None or t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        _refuse(t, _BF16, name, shape, dev, True)
+    token, head, last = t.stride()
+    if last != 1:
+        _refuse(t, _BF16, name, shape, dev, True)
+    n, heads, d = shape
+    if heads == 1:
+        head = d
+    return t.data_ptr(), (token if n > 1 else heads * head, head)
 
 
-def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved) -> QkRopeArgs:
-    """Marshals the arguments of the norm and rotation.  rotary_dim is the table's width."""
-    _need(q, torch.bfloat16, "q", strided=True)
-    if q.dim() != 3 or k is None or k.dim() != 3:
+def _new_rows(like, shape):
+    return torch.empty(shape, dtype=_BF16, device=like.device)
+
+
+def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int) -> QkRopeArgs:
+    """Marshals the arguments of the norm and rotation (rotary_dim is the table's width); the strides
+    of the outputs are set by the callers."""
+    if q is None or k is None or q.dim() != 3 or k.dim() != 3:
         raise ValueError("expected [tokens, heads, dim] tensors q and k")
-    n, hq, d = q.shape
+    shape = q.shape
+    n, hq, d = shape
     hkv = k.shape[1]
-    _rows(k, "k", n, hkv, d)
-    _vector(q_weight, torch.float32, "q_weight", (d,))
-    _vector(k_weight, torch.float32, "k_weight", (d,))
-    _vector(positions, torch.int32, "positions", (n,))
+    qp, qs = _rows(q, "q", shape, dev)
+    kp, ks = _rows(k, "k", (n, hkv, d), dev)
     max_pos = rot = 0
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin")
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_pos, rotary_dim]")
         max_pos, rot = cos_sin.shape
-    return QkRopeArgs(n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, q.data_ptr(), k.data_ptr(),
-                      _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), max_pos, _ptr(positions), _row_strides(q), _row_strides(k))
+    return QkRopeArgs(n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, qp, kp,
+                      _vector(q_weight, _F32, "q_weight", (d,), dev), _vector(k_weight, _F32, "k_weight", (d,), dev),
+                      _vector(cos_sin, _F32, "cos_sin", (max_pos, rot), dev), max_pos,
+                      _vector(positions, _I32, "positions", (n,), dev), qs, ks)
 
 
 def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
@@ -660,13 +670,15 @@ def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_w
     fp32 [d] or None (ones); cos_sin fp32 [max_pos, rotary_dim] (cosines, then sines) or None (no
     rotation); positions int32 [tot], negative = padding (outputs left as they were).
     norm=False: rotation only.  Returns q_out, k_out."""
-    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else _rows(q_out, "q_out", *q.shape)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else _rows(k_out, "k_out", *k.shape)
-    a.q_out_stride, a.k_out_stride = _row_strides(q_out), _row_strides(k_out)
-    _on_current_device(q, k, cos_sin, positions, q_weight, k_weight, q_out, k_out)
-    _check(load().attn_qk_norm_rope_fwd(ctypes.byref(a), q_out.data_ptr(), k_out.data_ptr(), _stream()),
-           "attn_qk_norm_rope_fwd")
+    dev = torch.cuda.current_device()
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
+    if q_out is None:
+        q_out = _new_rows(q, q.shape)
+    if k_out is None:
+        k_out = _new_rows(k, k.shape)
+    qp, a.q_out_stride = _rows(q_out, "q_out", q.shape, dev)
+    kp, a.k_out_stride = _rows(k_out, "k_out", k.shape, dev)
+    _check(load().attn_qk_norm_rope_fwd(a, qp, kp, _raw_stream(dev)), "attn_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -677,81 +689,85 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_
     rest its arguments.  Returns dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]; None without
     the weight)."""
     L = load()
-    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
-    _rows(dq_out, "dq_out", *q.shape)
-    _rows(dk_out, "dk_out", *k.shape)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _rows(dq, "dq", *q.shape)
-    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else _rows(dk, "dk", *k.shape)
-    a.q_out_stride, a.k_out_stride, a.dq_stride, a.dk_stride = _row_strides(dq_out), _row_strides(dk_out), _row_strides(dq), _row_strides(dk)
-    if q_weight is not None:
-        dq_weight = torch.empty_like(q_weight) if dq_weight is None else dq_weight
-    if k_weight is not None:
-        dk_weight = torch.empty_like(k_weight) if dk_weight is None else dk_weight
-    _vector(dq_weight, torch.float32, "dq_weight", (q.shape[2],))
-    _vector(dk_weight, torch.float32, "dk_weight", (q.shape[2],))
-    if workspace is None:
-        ws_bytes = L.attn_qk_norm_rope_bwd_workspace(ctypes.byref(a))
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
-    _on_current_device(q, k, dq_out, dk_out, cos_sin, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight,
-                       workspace)
-    _check(L.attn_qk_norm_rope_bwd(ctypes.byref(a), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
-                                   dk.data_ptr(), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace),
-                                   workspace.numel() if workspace is not None else 0, _stream()),
-           "attn_qk_norm_rope_bwd")
+    dev = torch.cuda.current_device()
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
+    qs, ks, w = q.shape, k.shape, (a.d,)
+    if dq is None:
+        dq = _new_rows(q, qs)
+    if dk is None:
+        dk = _new_rows(k, ks)
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty_like(q_weight)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty_like(k_weight)
+    gqp, a.q_out_stride = _rows(dq_out, "dq_out", qs, dev)
+    gkp, a.k_out_stride = _rows(dk_out, "dk_out", ks, dev)
+    dqp, a.dq_stride = _rows(dq, "dq", qs, dev)
+    dkp, a.dk_stride = _rows(dk, "dk", ks, dev)
+    ws, ws_bytes = _workspace(workspace, L.attn_qk_norm_rope_bwd_workspace(a), dev)
+    _check(L.attn_qk_norm_rope_bwd(a, gqp, gkp, dqp, dkp, _vector(dq_weight, _F32, "dq_weight", w, dev),
+                                   _vector(dk_weight, _F32, "dk_weight", w, dev), _ptr(ws), ws_bytes,
+                                   _raw_stream(dev)), "attn_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
 
-def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq=None,
-               g_cache=None) -> CacheArgs:
+def _workspace(workspace, need: int, dev: int):
+    """The caller's workspace, or a new one when one is needed, and its bytes."""
+    if workspace is None:
+        if not need:
+            return None, 0
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq, g_cache,
+               dev: int) -> CacheArgs:
     """Marshals the arguments of the cache calls: the caches, scales and index arrays are those of
-    decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes)."""
+    decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes); hq None:
+    g_cache's heads."""
     if k_cache is None or v_cache is None or k_cache.dim() != 4:
         raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    shape, fmt, strides = k_cache.shape, k_cache.dtype, k_cache.stride()
+    if shape != v_cache.shape or fmt is not v_cache.dtype:
         raise ValueError("k_cache and v_cache shapes or types differ")
-    if k_cache.stride() != v_cache.stride():
+    if strides != v_cache.stride():
         raise ValueError("k_cache and v_cache must share one layout")
-    nb, hkv, bs, d = k_cache.shape
-    fmt = k_cache.dtype
-    if fmt not in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn):
+    if fmt not in (_BF16, _U8, _E4M3):
         raise ValueError(f"caches must be bf16, uint8 or float8_e4m3fn, got {fmt}")
-    _need(k_cache, fmt, "k_cache", strided=True)
-    _need(v_cache, fmt, "v_cache", strided=True)
-    kv_format, scale_mode = KV_FP8_E4M3, SCALE_PER_TOKEN
-    if fmt == torch.bfloat16:
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if strides[3] != 1 or t.get_device() != dev:
+            _refuse(t, fmt, name, shape, dev, True)
+    nb, hkv, bs, d = shape
+    kv_format, scale_mode, ks, vs = KV_FP8_E4M3, SCALE_PER_TOKEN, None, None
+    if fmt is _BF16:
         kv_format = KV_BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 KV cache takes no scales")
     else:
-        _need(k_scale, torch.float32, "k_scale")
-        _need(v_scale, torch.float32, "v_scale")
-        if k_scale.shape == (nb, hkv, bs) and v_scale.shape == (nb, hkv, bs):
-            pass
-        elif k_scale.numel() == 1 and v_scale.numel() == 1:
+        if k_scale is None or v_scale is None:
+            raise ValueError("k_scale and v_scale are required")
+        page = (nb, hkv, bs)
+        if k_scale.shape != page or v_scale.shape != page:
+            if k_scale.numel() != 1 or v_scale.numel() != 1:
+                raise NotImplementedError("fp8 scales must have the page shape [num_blocks, num_kv_heads, block_size] "
+                                          "(per token) or hold one value (per tensor)")
             scale_mode = SCALE_PER_TENSOR
-        else:
-            raise NotImplementedError("fp8 scales must have the page shape [num_blocks, num_kv_heads, block_size] "
-                                      "(per token) or hold one value (per tensor)")
-    _need(block_table, torch.int32, "block_table")
-    _need(seq_lens, torch.int32, "seq_lens")
-    _need(cu_rows, torch.int32, "cu_rows")
-    num_reqs = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != num_reqs or cu_rows.numel() != num_reqs + 1:
+        ks = _vector(k_scale, _F32, "k_scale", k_scale.shape, dev)
+        vs = _vector(v_scale, _F32, "v_scale", v_scale.shape, dev)
+    if block_table is None or seq_lens is None or cu_rows is None or block_table.dim() != 2:
         raise ValueError("block_table, seq_lens and cu_rows are [R, max_blocks], [R] and [R + 1]")
-    if g_cache is not None:
-        hq = g_cache.shape[1] if hq is None and g_cache.dim() == 3 else hq
-        _vector(g_cache, torch.float32, "g_cache", (nb, hq, bs))
-    return CacheArgs(num_reqs, cu_rows.data_ptr(), int(total_rows), int(max_rows), seq_lens.data_ptr(),
-                     block_table.data_ptr(), block_table.shape[1], k_cache.data_ptr(), v_cache.data_ptr(),
-                     _ptr(k_scale), _ptr(v_scale), nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
-                     _ptr(g_cache), *k_cache.stride()[:3])
-
-
-def _append_workspace(L, a, workspace, device):
-    if workspace is None:
-        ws_bytes = L.attn_cache_append_workspace(ctypes.byref(a))
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
-    return workspace
+    num_reqs, max_blocks = block_table.shape
+    if g_cache is not None and hq is None:
+        if g_cache.dim() != 3:
+            raise ValueError("g_cache must be [num_blocks, num_q_heads, block_size]")
+        hq = g_cache.shape[1]
+    return CacheArgs(num_reqs, _vector(cu_rows, _I32, "cu_rows", (num_reqs + 1,), dev), total_rows, max_rows,
+                     _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev),
+                     _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(),
+                     v_cache.data_ptr(), ks, vs, nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
+                     _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), strides[0], strides[1], strides[2])
 
 
 def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, log_gate=None,
@@ -761,17 +777,15 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     the arrays that attn_decode_paged and attn_prefill_paged take.  A per-token fp8 cache gets its
     scales written, a per-tensor one is quantised with the given scales."""
     L = load()
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, k.shape[0], max_q_len, None,
-                   g_cache)
-    _rows(k, "k", a.total_rows, a.hkv, a.d)
-    _rows(v, "v", a.total_rows, a.hkv, a.d)
-    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
-    a.k_stride, a.v_stride = _row_strides(k), _row_strides(v)
-    workspace = _append_workspace(L, a, workspace, k.device)
-    _on_current_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, log_gate, g_cache,
-                       workspace)
-    _check(L.attn_cache_append(ctypes.byref(a), k.data_ptr(), v.data_ptr(), _ptr(log_gate), _ptr(workspace),
-                               workspace.numel() if workspace is not None else 0, _stream()), "attn_cache_append")
+    dev = torch.cuda.current_device()
+    n = 0 if k is None else k.shape[0]
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev)
+    shape = (n, a.hkv, a.d)
+    kp, a.k_stride = _rows(k, "k", shape, dev)
+    vp, a.v_stride = _rows(v, "v", shape, dev)
+    lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
+    ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
+    _check(L.attn_cache_append(a, kp, vp, lg, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append")
 
 
 def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len,
@@ -781,20 +795,17 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     q, and writes the normed and rotated k (quantised without a rounding to bf16 in between) and
     v into the cache.  positions None: the cached positions."""
     L = load()
-    r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved)
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, q.shape[0], max_q_len, r.hq,
-                   g_cache)
-    _rows(k, "k", a.total_rows, a.hkv, a.d)
-    _rows(v, "v", a.total_rows, a.hkv, a.d)
-    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else _rows(q_out, "q_out", *q.shape)
-    r.q_out_stride, a.v_stride = _row_strides(q_out), _row_strides(v)
-    workspace = _append_workspace(L, a, workspace, q.device)
-    _on_current_device(q, k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, cos_sin, positions,
-                       q_weight, k_weight, log_gate, g_cache, q_out, workspace)
-    _check(L.attn_cache_append_rope(ctypes.byref(a), ctypes.byref(r), v.data_ptr(), _ptr(log_gate), q_out.data_ptr(),
-                                    _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream()),
-           "attn_cache_append_rope")
+    dev = torch.cuda.current_device()
+    r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
+    n, hq = r.total_tokens, r.hq
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev)
+    if q_out is None:
+        q_out = _new_rows(q, q.shape)
+    qp, r.q_out_stride = _rows(q_out, "q_out", q.shape, dev)
+    vp, a.v_stride = _rows(v, "v", (n, a.hkv, a.d), dev)
+    lg = _vector(log_gate, _F32, "log_gate", (n, hq), dev)
+    ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
+    _check(L.attn_cache_append_rope(a, r, vp, lg, qp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append_rope")
     return q_out
 
 
@@ -804,17 +815,18 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     request back into packed k, v bf16 [total_rows, hkv, d] and, with g_cache, log_gate fp32
     [total_rows, hq] (the differences of the cumulative gates): what attn_fwd takes.  total_rows
     is cu_rows's last entry on the host.  Returns k, v, log_gate (None without g_cache)."""
+    dev = torch.cuda.current_device()
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, total_rows),
-                   None, g_cache)
-    shape = (a.total_rows, a.hkv, a.d)
-    new = lambda s, t: torch.empty(s, dtype=t, device=k_cache.device)
-    k = new(shape, torch.bfloat16) if k is None else _rows(k, "k", *shape)
-    v = new(shape, torch.bfloat16) if v is None else _rows(v, "v", *shape)
+                   None, g_cache, dev)
+    shape = (max(0, total_rows), a.hkv, a.d)
+    if k is None:
+        k = _new_rows(k_cache, shape)
+    if v is None:
+        v = _new_rows(k_cache, shape)
     if g_cache is not None and log_gate is None:
-        log_gate = new((a.total_rows, a.hq), torch.float32)
-    _vector(log_gate, torch.float32, "log_gate", (a.total_rows, a.hq))
-    a.k_stride, a.v_stride = _row_strides(k), _row_strides(v)
-    _on_current_device(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, g_cache, k, v, log_gate)
-    _check(load().attn_cache_gather(ctypes.byref(a), k.data_ptr(), v.data_ptr(), _ptr(log_gate), _stream()),
-           "attn_cache_gather")
+        log_gate = torch.empty((shape[0], a.hq), dtype=_F32, device=k_cache.device)
+    kp, a.k_stride = _rows(k, "k", shape, dev)
+    vp, a.v_stride = _rows(v, "v", shape, dev)
+    lg = _vector(log_gate, _F32, "log_gate", (shape[0], a.hq), dev)
+    _check(load().attn_cache_gather(a, kp, vp, lg, _raw_stream(dev)), "attn_cache_gather")
     return k, v, log_gate

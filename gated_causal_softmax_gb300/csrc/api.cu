@@ -915,7 +915,7 @@ static int check_rope(const gcs_qk_rope_args* a, bool in_cache) {
   if (!head_dim_supported(a->d)) return GCS_ERR_UNSUPPORTED;
   if (a->rotary_dim > a->d) return GCS_ERR_INVALID_ARG;
   if (a->rotary_dim % 16 != 0) return GCS_ERR_UNSUPPORTED;
-  // heads that fill the grid's warps many times over, and element counts of a token beyond 2^31
+  // elements of a token within 32 bits
   if ((double)a->hq * a->d > 2147483647.0) return GCS_ERR_UNSUPPORTED;
   Layout l;
   int st;
@@ -1070,9 +1070,9 @@ static int check_cache(const gcs_cache_args* a) {
   if (!head_dim_supported(a->d)) return GCS_ERR_UNSUPPORTED;
   if (a->block_size < 16 || a->block_size > 4096 || (a->block_size & (a->block_size - 1)) != 0)
     return GCS_ERR_UNSUPPORTED;
-  // heads, gate tiles and the gates' grid within 32 bits
-  if ((double)a->hq * a->d > 2147483647.0) return GCS_ERR_UNSUPPORTED;
-  if (((double)a->total_rows / 128 + 2.0 * a->num_reqs) * ((a->hq + 31) / 32) > 1073741824.0 ||
+  // rows (with the few that a warp looks ahead), heads and the gates' grid within 32 bits
+  if (a->total_rows > 1 << 30 || (double)a->hq * a->d > 2147483647.0) return GCS_ERR_UNSUPPORTED;
+  if (((double)a->total_rows / 64 + 2.0 * a->num_reqs) * ((a->hq + 31) / 32) > 1073741824.0 ||
       (a->hq + 31) / 32 > 65535)
     return GCS_ERR_UNSUPPORTED;
   if ((double)a->num_blocks * a->hkv * a->block_size * a->d > 9.0e15) return GCS_ERR_UNSUPPORTED;

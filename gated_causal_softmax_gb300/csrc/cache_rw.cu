@@ -25,9 +25,10 @@
 namespace gcs {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 152 * 8;
+// Blocks of an SM: beyond 152 SMs full, warps take longer runs of tokens.
+constexpr int kAppendBlocks = 4, kGatherBlocks = 8;
 constexpr float kE4m3Max = 448.f;
 
 __device__ __forceinline__ void record_bad(int* status) { atomicCAS(status, kDevOk, kDevInvalidArg); }
@@ -59,28 +60,63 @@ __device__ __forceinline__ int block_of(const CacheParams& p, int r, long long p
   return -1;
 }
 
-// The place of packed row t; blk < 0: left out.
+// Where packed row t is cached: blk < 0: left out.
 struct Place {
   int blk, slot;
   long long pos;
 };
-__device__ __forceinline__ Place place_of(const CacheParams& p, int t) {
+// A warp goes through neighbouring rows, so it looks the request up again only past its end, and
+// the block only past the block's.
+struct Cursor {
+  int r = -1, a = 0, b = 0;  // the request of the rows [a, b)
+  long long shift = 0;       // position - row
+  long long page = -1;
+  int blk = -1;
+};
+__device__ __forceinline__ Place place_of(const CacheParams& p, int t, Cursor& c) {
   Place w{-1, 0, 0};
-  const int r = warp_last_le(p.num_reqs + 1, t, [&](int i) { return __ldg(p.cu + i); });
-  if (r >= p.num_reqs) return w;  // behind the last request
-  long long a = 0, b = 0;
-  if (r >= 0) {
-    a = __ldg(p.cu + r);
-    b = __ldg(p.cu + r + 1);
+  if (t < c.a || t >= c.b) {
+    c.a = c.b = 0;
+    const int r = warp_last_le(p.num_reqs + 1, t, [&](int i) { return __ldg(p.cu + i); });
+    if (r >= p.num_reqs) return w;  // behind the last request
+    if (r >= 0) {
+      c.a = __ldg(p.cu + r);
+      c.b = __ldg(p.cu + r + 1);
+    }
+    if (t < c.a || t >= c.b) {  // cu does not start at 0 or is not sorted
+      if ((threadIdx.x & 31) == 0) record_bad(p.status);
+      return w;
+    }
+    c.r = r;
+    c.shift = (long long)__ldg(p.seq_lens + r) - c.b;
+    c.page = -1;
+    c.blk = -1;
   }
-  if (!(r >= 0 && a <= t && t < b)) {  // cu does not start at 0 or is not sorted
-    if ((threadIdx.x & 31) == 0) record_bad(p.status);
-    return w;
+  w.pos = t + c.shift;
+  const long long page = w.pos >> p.log2_block;
+  if (page != c.page || w.pos < 0) {
+    c.page = page;
+    c.blk = block_of(p, c.r, w.pos);
   }
-  w.pos = __ldg(p.seq_lens + r) - (b - a) + (t - a);
-  w.blk = block_of(p, r, w.pos);
+  w.blk = c.blk;
   w.slot = (int)(w.pos & (p.block_size - 1));
   return w;
+}
+
+// A warp's share of the rows: one of `segs` groups of heads, and a run of tokens [t, t1).
+struct Run {
+  int seg, t, t1;
+};
+__device__ __forceinline__ Run warp_run(const CacheParams& p, int segs) {
+  const long long w = (long long)(blockIdx.x - p.n_gate) * kWarps + (threadIdx.x >> 5);
+  const long long runs = (long long)(gridDim.x - p.n_gate) * kWarps / segs;  // of a group of heads
+  Run x{(int)(w % segs), 0, 0};
+  const long long i = w / segs;
+  if (i < runs) {
+    x.t = (int)(p.total * i / runs);
+    x.t1 = (int)(p.total * (i + 1) / runs);
+  }
+  return x;
 }
 
 // ------------------------------------------------------------------------- e4m3
@@ -150,11 +186,11 @@ __device__ __forceinline__ void write_cache_row(const CacheParams& p, uint8_t* c
 }
 
 // ------------------------------------------------------------------------- gates
-// A tile is 128 positions of one request x 32 query heads: a warp holds 16 positions (aligned, so
+// A tile is 64 positions of one request x 32 query heads: a warp holds 16 positions (aligned, so
 // they lie in one block and their cached values are 64 contiguous bytes of a head), a lane one
-// head.  Tile slots of request r start at cu[r] / 128 + 2 r; at most floor(len / 128) + 2 are used.
-constexpr int kTile = 128;
+// head.  Tile slots of request r start at cu[r] / 64 + 2 r; at most floor(len / 64) + 2 are used.
 constexpr int kStrip = 16;
+constexpr int kTile = kStrip * kWarps;
 // Up to this many positions a tile adds up the log gates before it by itself; for longer
 // appends gate_sums_kernel adds up every tile first.
 constexpr int kDirectRows = 512;
@@ -301,61 +337,98 @@ __device__ __forceinline__ void read_gates(const CacheParams& p, int slot, int h
 }
 
 // ------------------------------------------------------------------------- append
-// Blocks [0, n_gate): a gate tile each; the rest: rows.  A warp takes one row of all heads of a
-// share (queries, keys or values) of every step-th token.
+// Blocks [0, n_gate): a gate tile each; the rest: rows.  A warp takes either the queries of 2 R
+// heads or the keys and values of R heads (R rows to a warp), of one token a step, with the copies
+// of the next token under way.
 template <int D, int FMT, bool ROPE>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const CacheParams p, const RopeParams q) {
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) cache_append_kernel(const CacheParams p, const RopeParams q) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
-  __shared__ float sums[2][kWarps][32];
+  __shared__ union {
+    WarpStage<D, 2> ring[kWarps][2];
+    float sums[2][kWarps][32];
+  } sm;
   if ((int)blockIdx.x < p.n_gate) {
-    write_gates(p, blockIdx.x / p.gate_groups, blockIdx.x % p.gate_groups, sums);
+    write_gates(p, blockIdx.x / p.gate_groups, blockIdx.x % p.gate_groups, sm.sums);
     return;
   }
-  const int q_segs = ROPE ? (p.hq + R - 1) / R : 0, kv_segs = (p.hkv + R - 1) / R, segs = q_segs + 2 * kv_segs;
-  const uint32_t w = (blockIdx.x - p.n_gate) * kWarps + (threadIdx.x >> 5);
-  const uint32_t step = (gridDim.x - p.n_gate) * kWarps / segs;
-  if (w >= step * segs) return;
-  const int seg = w % segs;
-  const bool is_q = seg < q_segs, is_v = seg >= q_segs + kv_segs;
+  const int q_segs = ROPE ? (p.hq + 2 * R - 1) / (2 * R) : 0;
+  const Run run = warp_run(p, q_segs + (p.hkv + R - 1) / R);
+  if (run.t >= run.t1) return;
+  WarpStage<D, 2>* ring = sm.ring[threadIdx.x >> 5];
+  const bool is_q = run.seg < q_segs;
   const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
-  const int h = (is_q ? seg : is_v ? seg - q_segs - kv_segs : seg - q_segs) * R + grp;
-  const bool valid = h < (is_q ? p.hq : p.hkv);
-  const bool turns = ROPE && !is_v;
-  const RowRuns runs = row_runs(sub, turns ? q.rotary_dim : 0, turns && q.interleaved);
-  const uint16_t* in = is_q ? q.q : is_v ? p.v : p.k;
-  const long long ts = is_q ? q.q_ts : is_v ? p.v_ts : p.k_ts, hs = is_q ? q.q_hs : is_v ? p.v_hs : p.k_hs;
+  const RowRuns plain = row_runs<D>(sub, 0, false);
+  const RowRuns turned = ROPE ? row_runs<D>(sub, q.rotary_dim, q.interleaved) : plain;
+  // the lane's two rows of a token: two query heads, or the key and the value of one head
+  const int h = is_q ? run.seg * 2 * R + grp : (run.seg - q_segs) * R + grp;
+  const int heads = is_q ? p.hq : p.hkv;
+  const bool valid0 = h < heads, valid1 = is_q ? h + R < heads : valid0;
+  const uint16_t* row0 = is_q ? q.q + (valid0 ? h : 0) * q.q_hs : p.k + (valid0 ? h : 0) * p.k_hs;
+  const uint16_t* row1 = is_q ? q.q + (valid1 ? h + R : 0) * q.q_hs : p.v + (valid1 ? h : 0) * p.v_hs;
+  const long long ts0 = is_q ? q.q_ts : p.k_ts, ts1 = is_q ? q.q_ts : p.v_ts;
+  const RowRuns runs1 = is_q ? turned : plain;
   float wt[16];
-  if (turns) load_weights(is_q ? q.q_weight : q.k_weight, runs, wt);
-  for (uint32_t t = w / segs; t < (uint32_t)p.total; t += step) {
-    const RawRow raw = valid ? load_row(in + t * ts + h * hs, runs) : zero_row();
-    const Place pl = place_of(p, t);
-    if (pl.blk < 0) continue;
-    float x[16];
-    unpack_row(raw, x);
-    if (ROPE) {
-      long long pos = pl.pos;
-      if (q.positions) pos = __ldg(q.positions + t);
-      if (pos < 0) continue;
-      if (q.cos_sin && pos >= q.max_pos) {
-        if ((threadIdx.x & 31) == 0) record_bad(p.status);
-        continue;
-      }
-      if (turns) {
-        Angles ang;
-        load_angles(q.cos_sin, pos, q.rotary_dim, sub, runs, ang);
-        if (q.norm) {
-          const float r = row_rstd<D>(x, q.eps);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = x[i] * r * wt[i];
-        }
-        rotate_row<false>(x, runs, ang, q.interleaved);
-        if (is_q) {
-          if (valid) store_row(q.q_out + t * q.qo_ts + h * q.qo_hs, runs, x);
-          continue;
+  if (ROPE) load_weights(is_q ? q.q_weight : q.k_weight, turned, wt);
+
+  Cursor cursor;
+  // starts the copies of row t; its place (left out: blk < 0)
+  auto fetch = [&](WarpStage<D, 2>& st, int t) {
+    fetch_row(st, 0, row0 + t * ts0, turned, valid0);
+    fetch_row(st, 1, row1 + t * ts1, runs1, valid1);
+    Place w = place_of(p, t, cursor);
+    if (ROPE && w.blk >= 0) {
+      const long long pos = q.positions ? __ldg(q.positions + t) : w.pos;
+      if (pos < 0) {
+        w.blk = -1;
+      } else if (q.cos_sin) {
+        if (pos < q.max_pos) {
+          fetch_angles(st, q.cos_sin, pos, q.rotary_dim);
+        } else {
+          if ((threadIdx.x & 31) == 0) record_bad(p.status);
+          w.blk = -1;
         }
       }
     }
-    write_cache_row<D, FMT>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, pl, h, valid, sub, runs, x);
+    return w;
+  };
+  auto norm_turn = [&](float* x, const Angles& ang) {
+    if (q.norm) {
+      const float r = row_rstd<D>(x, q.eps);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * r * wt[i];
+    }
+    rotate_row<false>(x, turned, ang, q.interleaved);
+  };
+  auto use = [&](const WarpStage<D, 2>& st, int t, const Place& w) {
+    if (w.blk < 0) return;
+    float x[16];
+    Angles ang;
+    if (ROPE) read_angles(st.angles, q.rotary_dim, turned, ang);
+    unpack_row(fetched_row(st, 0), x);
+    if (ROPE) norm_turn(x, ang);
+    if (ROPE && is_q) {
+      uint16_t* out = q.q_out + t * q.qo_ts;
+      if (valid0) store_row(out + h * q.qo_hs, turned, x);
+      unpack_row(fetched_row(st, 1), x);
+      norm_turn(x, ang);
+      if (valid1) store_row(out + (h + R) * q.qo_hs, turned, x);
+    } else {
+      write_cache_row<D, FMT>(p, p.k_cache, p.k_scale, w, h, valid0, sub, turned, x);
+      unpack_row(fetched_row(st, 1), x);
+      write_cache_row<D, FMT>(p, p.v_cache, p.v_scale, w, h, valid0, sub, plain, x);
+    }
+  };
+
+  Place now = fetch(ring[0], run.t), next = now;
+  copy_commit();
+  for (int t = run.t, slot = 0; t < run.t1; ++t, slot ^= 1) {
+    if (t + 1 < run.t1) next = fetch(ring[slot ^ 1], t + 1);
+    copy_commit();
+    copy_wait<1>();
+    __syncwarp();
+    use(ring[slot], t, now);
+    __syncwarp();
+    now = next;
   }
 }
 
@@ -375,51 +448,91 @@ __device__ __forceinline__ uint2 from_e4m3x4(uint32_t code, float scale) {
   return make_uint2(pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale));
 }
 
+// The codes (or bf16 elements) and scales of a warp's steps ahead; codes and scales are copied and
+// read by the same lane.
+constexpr int kGatherStages = 4;
+template <int FMT>
+struct alignas(16) GatherStage {
+  static constexpr int kRun = FMT == kCacheBf16 ? 16 : 8;  // bytes of a run of 8 elements
+  uint8_t raw[2][2][32][kRun];                             // keys, values; the lane's two runs
+  float scale[2][32];
+};
+
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads) cache_gather_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(kThreads, kGatherBlocks) cache_gather_kernel(const CacheParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
+  using Stage = GatherStage<FMT>;
+  __shared__ Stage rings[kWarps][kGatherStages];
   if ((int)blockIdx.x < p.n_gate) {
     read_gates(p, blockIdx.x / p.gate_groups, blockIdx.x % p.gate_groups);
     return;
   }
-  const int kv_segs = (p.hkv + R - 1) / R, segs = 2 * kv_segs;
-  const uint32_t w = (blockIdx.x - p.n_gate) * kWarps + (threadIdx.x >> 5);
-  const uint32_t step = (gridDim.x - p.n_gate) * kWarps / segs;
-  if (w >= step * segs) return;
-  const int seg = w % segs;
-  const bool is_v = seg >= kv_segs;
-  const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
-  const int h = (is_v ? seg - kv_segs : seg) * R + grp;
+  const Run run = warp_run(p, (p.hkv + R - 1) / R);
+  if (run.t >= run.t1) return;
+  Stage* ring = rings[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, sub = lane & (L - 1), h = run.seg * R + lane / L;
   const bool valid = h < p.hkv;
-  const uint8_t* cache = is_v ? p.v_cache : p.k_cache;
-  const float* scales = is_v ? p.v_scale : p.k_scale;
-  uint16_t* out = is_v ? p.v_out : p.k_out;
-  const long long ts = is_v ? p.v_ts : p.k_ts, hs = is_v ? p.v_hs : p.k_hs;
-  for (uint32_t t = w / segs; t < (uint32_t)p.total; t += step) {
-    const Place pl = place_of(p, t);
-    if (pl.blk < 0 || !valid) continue;
-    const uint8_t* row = cache + (long long)pl.blk * p.kv_bs + (long long)h * p.kv_hs + (long long)pl.slot * p.kv_ss;
-    uint4* dst = reinterpret_cast<uint4*>(out + t * ts + h * hs + 16 * sub);
-    if (FMT == kCacheBf16) {
-      const uint4* src = reinterpret_cast<const uint4*>(row) + 2 * sub;
-      const uint4 u = __ldg(src), v = __ldg(src + 1);
-      dst[0] = u;
-      dst[1] = v;
-    } else {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(row) + sub);
-      const float sc =
-          __ldg(FMT == kCachePerToken ? scales + ((size_t)pl.blk * p.hkv + h) * p.block_size + pl.slot : scales);
-      const uint2 u0 = from_e4m3x4(c.x, sc), u1 = from_e4m3x4(c.y, sc), u2 = from_e4m3x4(c.z, sc),
-                  u3 = from_e4m3x4(c.w, sc);
-      dst[0] = make_uint4(u0.x, u0.y, u1.x, u1.y);
-      dst[1] = make_uint4(u2.x, u2.y, u3.x, u3.y);
+  const RowRuns runs = row_runs<D>(sub, 0, false);
+  const float ks = FMT == kCachePerTensor ? __ldg(p.k_scale) : 1.f, vs = FMT == kCachePerTensor ? __ldg(p.v_scale) : 1.f;
+  Cursor cursor;
+  uint32_t there = 0;  // bit i: the row i steps back from the last fetched one is in the cache
+  auto fetch = [&](Stage& st, int t) {
+    there <<= 1;
+    const Place w = place_of(p, t, cursor);
+    if (w.blk < 0) return;
+    there |= 1;
+    if (!valid) return;
+    const long long row = (long long)w.blk * p.kv_bs + h * p.kv_hs + (long long)w.slot * p.kv_ss;
+    constexpr int B = Stage::kRun;
+    copy_async<B>(st.raw[0][0][lane], p.k_cache + row + runs.a * (B / 8));
+    copy_async<B>(st.raw[0][1][lane], p.k_cache + row + runs.b * (B / 8));
+    copy_async<B>(st.raw[1][0][lane], p.v_cache + row + runs.a * (B / 8));
+    copy_async<B>(st.raw[1][1][lane], p.v_cache + row + runs.b * (B / 8));
+    if (FMT == kCachePerToken) {
+      const size_t s = ((size_t)w.blk * p.hkv + h) * p.block_size + w.slot;
+      copy_async<4>(&st.scale[0][lane], p.k_scale + s);
+      copy_async<4>(&st.scale[1][lane], p.v_scale + s);
     }
+  };
+  auto write = [&](const Stage& st, int i, float scale, uint16_t* row) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint4* dst = reinterpret_cast<uint4*>(row + (r ? runs.b : runs.a));
+      if (FMT == kCacheBf16) {
+        *dst = *reinterpret_cast<const uint4*>(st.raw[i][r][lane]);
+      } else {
+        const uint2 c = *reinterpret_cast<const uint2*>(st.raw[i][r][lane]);
+        const uint2 u = from_e4m3x4(c.x, scale), v = from_e4m3x4(c.y, scale);
+        *dst = make_uint4(u.x, u.y, v.x, v.y);
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kGatherStages - 1; ++i) {
+    if (run.t + i < run.t1) fetch(ring[i], run.t + i);
+    else there <<= 1;
+    copy_commit();
+  }
+  int slot = 0;
+  for (int t = run.t; t < run.t1; ++t) {
+    if (t + kGatherStages - 1 < run.t1) fetch(ring[(slot + kGatherStages - 1) % kGatherStages], t + kGatherStages - 1);
+    else there <<= 1;
+    copy_commit();
+    copy_wait<kGatherStages - 1>();
+    if ((there >> (kGatherStages - 1) & 1) && valid) {
+      const Stage& st = ring[slot];
+      const bool per_token = FMT == kCachePerToken;
+      write(st, 0, per_token ? st.scale[0][lane] : ks, p.k_out + t * p.k_ts + h * p.k_hs);
+      write(st, 1, per_token ? st.scale[1][lane] : vs, p.v_out + t * p.v_ts + h * p.v_hs);
+    }
+    slot = (slot + 1) % kGatherStages;
   }
 }
 
-int row_blocks(int total, int segs) {
+int row_blocks(int total, int segs, int most) {
   const long long blocks = ((long long)total * segs + kWarps - 1) / kWarps;
-  return (int)std::max<long long>(std::min<long long>(blocks, kMaxBlocks), (segs + kWarps - 1) / kWarps);
+  // at least one warp for each group of heads
+  return (int)std::max<long long>(std::min<long long>(blocks, most), (segs + kWarps - 1) / kWarps);
 }
 
 void plan_gates(CacheParams& p, bool gates) {
@@ -430,8 +543,9 @@ void plan_gates(CacheParams& p, bool gates) {
 template <int D, int FMT, bool ROPE>
 cudaError_t append(const CacheParams& p, const RopeParams& q, cudaStream_t s) {
   constexpr int R = RowLanes<D>::kRows;
-  const int segs = (ROPE ? (p.hq + R - 1) / R : 0) + 2 * ((p.hkv + R - 1) / R);
-  cache_append_kernel<D, FMT, ROPE><<<p.n_gate + row_blocks(p.total, segs), kThreads, 0, s>>>(p, q);
+  const int segs = (ROPE ? (p.hq + 2 * R - 1) / (2 * R) : 0) + (p.hkv + R - 1) / R;
+  cache_append_kernel<D, FMT, ROPE>
+      <<<p.n_gate + row_blocks(p.total, segs, 152 * kAppendBlocks), kThreads, 0, s>>>(p, q);
   return cudaGetLastError();
 }
 template <int D, int FMT>
@@ -448,7 +562,8 @@ cudaError_t append(const CacheParams& p, const RopeParams* q, cudaStream_t s) {
 template <int D, int FMT>
 cudaError_t gather(const CacheParams& p, cudaStream_t s) {
   constexpr int R = RowLanes<D>::kRows;
-  cache_gather_kernel<D, FMT><<<p.n_gate + row_blocks(p.total, 2 * ((p.hkv + R - 1) / R)), kThreads, 0, s>>>(p);
+  cache_gather_kernel<D, FMT>
+      <<<p.n_gate + row_blocks(p.total, (p.hkv + R - 1) / R, 152 * kGatherBlocks), kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <int D>

@@ -18,9 +18,11 @@
 namespace gcs {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBlocks = 152 * 4;  // warps take further tokens beyond this many blocks
+// Blocks of an SM, and rows of a lane group in a step: warps take further tokens beyond 152 SMs full.
+constexpr int kFwdBlocks = 4, kFwdRows = 2;
+constexpr int kBwdBlocks = 3;
 
 // A warp's share: heads [h0, h1) of the queries or of the keys, and every step-th token.
 struct Share {
@@ -41,16 +43,19 @@ __device__ __forceinline__ bool warp_share(int total, int hq, int hkv, Share& s)
   s.t = w / segs;
   return true;
 }
-int blocks_for(int total, int hq, int hkv, int H) {
+int blocks_for(int total, int hq, int hkv, int H, int most) {
   const int segs = (hq + H - 1) / H + (hkv + H - 1) / H;
   const long long blocks = ((long long)total * segs + kWarps - 1) / kWarps;
   // at least one warp for each share of heads
-  return (int)std::max<long long>(std::min<long long>(blocks, kMaxBlocks), (segs + kWarps - 1) / kWarps);
+  return (int)std::max<long long>(std::min<long long>(blocks, most), (segs + kWarps - 1) / kWarps);
 }
 
-// The token's position: false for a row to leave out (negative: padding; past the table: an error).
-__device__ __forceinline__ bool token_position(const RopeParams& p, uint32_t t, int& pos) {
-  pos = p.positions ? __ldg(p.positions + t) : 0;
+// Positions of the steps ahead.
+__device__ __forceinline__ int position_of(const RopeParams& p, uint32_t t) {
+  return p.positions && t < (uint32_t)p.total ? __ldg(p.positions + t) : 0;
+}
+// False for a token to leave out (negative: padding; past the table: an error).
+__device__ __forceinline__ bool token_used(const RopeParams& p, int pos) {
   if (pos < 0) return false;
   if (p.cos_sin && pos >= p.max_pos) {
     if ((threadIdx.x & 31) == 0) atomicCAS(p.status, kDevOk, kDevInvalidArg);
@@ -59,35 +64,71 @@ __device__ __forceinline__ bool token_position(const RopeParams& p, uint32_t t, 
   return true;
 }
 
-template <int D, int U>
-__global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const RopeParams p) {
-  constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
+// Runs through a warp's tokens with the copies of the next kStages - 1 of them under way:
+// fetch(stage, t, h) starts the copies of a token's rows, use(stage, t, used) works on them.
+template <int D, int ROWS, typename Fetch, typename Use>
+__device__ __forceinline__ void for_tokens(const RopeParams& p, const Share& s, WarpStage<D, ROWS>* ring, Fetch fetch,
+                                           Use use) {
+  const uint32_t total = p.total;
+  auto start = [&](int slot, uint32_t t, int pos) {
+    if (t < total) {
+      fetch(ring[slot], t);
+      if (p.cos_sin && pos >= 0 && pos < p.max_pos) fetch_angles(ring[slot], p.cos_sin, pos, p.rotary_dim);
+    }
+    copy_commit();
+  };
+  int ahead[kStages];  // positions of this token and of those after it
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) ahead[i] = position_of(p, s.t + i * s.step);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) start(i, s.t + i * s.step, ahead[i]);
+  int slot = 0;
+  for (uint32_t t = s.t; t < total; t += s.step) {
+    const int free = slot == 0 ? kStages - 1 : slot - 1;  // the slot used last
+    start(free, t + (kStages - 1) * s.step, ahead[kStages - 1]);
+    const int next = position_of(p, t + kStages * s.step);
+    copy_wait<kStages - 1>();
+    __syncwarp();
+    use(ring[slot], t, token_used(p, ahead[0]));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ahead[i] = ahead[i + 1];
+    ahead[kStages - 1] = next;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(const RopeParams p) {
+  constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows, U = kFwdRows;
+  __shared__ WarpStage<D, U> ring[kWarps][kStages];
   Share s;
   if (!warp_share<R * U>(p.total, p.hq, p.hkv, s)) return;
   const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
-  const RowRuns runs = row_runs(sub, p.rotary_dim, p.interleaved);
+  const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
   const uint16_t* in = s.is_k ? p.k : p.q;
   uint16_t* out = s.is_k ? p.k_out : p.q_out;
   const long long its = s.is_k ? p.k_ts : p.q_ts, ihs = s.is_k ? p.k_hs : p.q_hs;
   const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
   float w[16];
   load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
-  for (uint32_t t = s.t; t < (uint32_t)p.total; t += s.step) {
-    RawRow raw[U];
+  auto fetch = [&](WarpStage<D, U>& st, uint32_t t) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = s.h0 + u * R + grp;
-      raw[u] = h < s.h1 ? load_row(in + t * its + h * ihs, runs) : zero_row();
+      const bool valid = h < s.h1;
+      fetch_row(st, u, in + t * its + (valid ? h : s.h0) * ihs, runs, valid);
     }
-    int pos;
-    if (!token_position(p, t, pos)) continue;
+  };
+  auto use = [&](const WarpStage<D, U>& st, uint32_t t, bool used) {
+    if (!used) return;
     Angles ang;
-    load_angles(p.cos_sin, pos, p.rotary_dim, sub, runs, ang);
+    read_angles(st.angles, p.rotary_dim, runs, ang);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = s.h0 + u * R + grp;
       float x[16];
-      unpack_row(raw[u], x);
+      unpack_row(fetched_row(st, u), x);
       if (p.norm) {
         const float r = row_rstd<D>(x, p.eps);
 #pragma unroll
@@ -96,20 +137,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope_fwd_kernel(const RopeParam
       rotate_row<false>(x, runs, ang, p.interleaved);
       if (h < s.h1) store_row(out + t * ots + h * ohs, runs, x);
     }
-  }
+  };
+  for_tokens(p, s, ring[threadIdx.x >> 5], fetch, use);
 }
 
 // Also the gradients of the weights: every lane sums g x r of its 16 elements over its rows, the
 // lanes of a block with the same elements are added in a fixed order, and the block writes its
 // part of d q_weight and d k_weight to p.partials [blocks][2][D]; weight_grad_kernel adds those.
 template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const RopeParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
-  __shared__ float part[kWarps][D];
+  __shared__ union {
+    WarpStage<D, 2> ring[kWarps][kStages];
+    float part[kWarps][D];  // after the last step
+  } sm;
   __shared__ int part_is_k[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x & (L - 1), grp = lane / L;
-  const RowRuns runs = row_runs(sub, p.rotary_dim, p.interleaved);
+  const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
   Share s;
   float dw[16];
 #pragma unroll
@@ -124,27 +169,25 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeParam
     const long long dts = s.is_k ? p.dk_ts : p.dq_ts, dhs = s.is_k ? p.dk_hs : p.dq_hs;
     float w[16];
     load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
-    const int h = s.h0 + grp;
-    const bool valid = h < s.h1;
-    for (uint32_t t = s.t; t < (uint32_t)p.total; t += s.step) {
-      RawRow rx = zero_row(), rg = zero_row();
-      if (valid) {
-        rg = load_row(dout + t * ots + h * ohs, runs);
-        if (p.norm) rx = load_row(in + t * its + h * ihs, runs);
-      }
-      int pos;
+    const bool valid = s.h0 + grp < s.h1;
+    const int h = valid ? s.h0 + grp : s.h0;
+    auto fetch = [&](WarpStage<D, 2>& st, uint32_t t) {
+      fetch_row(st, 0, dout + t * ots + h * ohs, runs, valid);
+      if (p.norm) fetch_row(st, 1, in + t * its + h * ihs, runs, valid);
+    };
+    auto use = [&](const WarpStage<D, 2>& st, uint32_t t, bool used) {
       float g[16];
-      if (!token_position(p, t, pos)) {  // the row's output does not depend on it
+      if (!used) {  // the row's output does not depend on it
 #pragma unroll
         for (int i = 0; i < 16; ++i) g[i] = 0.f;
       } else {
         Angles ang;
-        load_angles(p.cos_sin, pos, p.rotary_dim, sub, runs, ang);
-        unpack_row(rg, g);
+        read_angles(st.angles, p.rotary_dim, runs, ang);
+        unpack_row(fetched_row(st, 0), g);
         rotate_row<true>(g, runs, ang, p.interleaved);
         if (p.norm) {
           float x[16], ss = 0.f, su = 0.f;
-          unpack_row(rx, x);
+          unpack_row(fetched_row(st, 1), x);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             ss = fmaf(x[i], x[i], ss);
@@ -162,18 +205,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeParam
         }
       }
       if (valid) store_row(dx + t * dts + h * dhs, runs, g);
-    }
+    };
+    for_tokens(p, s, sm.ring[warp], fetch, use);
   }
   if (!p.partials) return;
 #pragma unroll
   for (int off = L; off < 32; off <<= 1)
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[i] += __shfl_xor_sync(kFullMask, dw[i], off);
+  __syncthreads();  // the ring is done with
   if (grp == 0) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      part[warp][runs.a + i] = dw[i];
-      part[warp][runs.b + i] = dw[8 + i];
+      sm.part[warp][runs.a + i] = dw[i];
+      sm.part[warp][runs.b + i] = dw[8 + i];
     }
   }
   if (lane == 0) part_is_k[warp] = works ? (s.is_k ? 1 : 0) : 2;
@@ -183,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const RopeParam
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i)
-      if (part_is_k[i] == is_k) sum += part[i][c % D];
+      if (part_is_k[i] == is_k) sum += sm.part[i][c % D];
     p.partials[(size_t)blockIdx.x * 2 * D + c] = sum;
   }
 }
@@ -208,16 +253,18 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restri
   }
 }
 
+int bwd_blocks(const RopeParams& p) { return blocks_for(p.total, p.hq, p.hkv, 512 / p.d, 152 * kBwdBlocks); }
+
 template <int D>
 cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
-  constexpr int U = 2;
-  norm_rope_fwd_kernel<D, U><<<blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows * U), kThreads, 0, s>>>(p);
+  const int blocks = blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows * kFwdRows, 152 * kFwdBlocks);
+  norm_rope_fwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStream_t s) {
-  const int blocks = blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows);
+  const int blocks = bwd_blocks(p);
   norm_rope_bwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partials) return e;
@@ -228,7 +275,7 @@ cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStr
 }  // namespace
 
 size_t norm_rope_bwd_partials(const RopeParams& p) {
-  return (size_t)blocks_for(p.total, p.hq, p.hkv, 512 / p.d) * 2 * p.d;
+  return (size_t)bwd_blocks(p) * 2 * p.d;
 }
 
 cudaError_t launch_norm_rope_fwd(const RopeParams& p, cudaStream_t s) {

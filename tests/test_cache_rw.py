@@ -20,7 +20,7 @@ import torch
 
 import oracle
 from helpers import DECODE_RTOL, PREFILL_RTOL, assert_close, f64
-from test_qk_rope import HALF_BF16, FP32_ROW, TINY, check_fwd, pair_magnitude, rope, table
+from test_qk_rope import FP32_ROW, HALF_BF16, OnGpu, TINY, check_fwd, pair_magnitude, rope, table
 
 SENTINEL = 0x5A  # byte of every cache before an append
 
@@ -708,30 +708,25 @@ def test_long_gates_need_a_workspace(L):
 def test_binding_refuses_wrong_shapes():
     import gated_causal_softmax_gb300 as gcs
 
-    class OnGpu:
-        is_cuda = True
-
-        def __init__(self, t):
-            self.t = t
-
-        def __getattr__(self, name):
-            return getattr(self.t, name)
-
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
     ok = dict(k_cache=torch.zeros(4, 2, 16, 64, dtype=torch.uint8), v_cache=torch.zeros(4, 2, 16, 64, dtype=torch.uint8),
               k_scale=torch.zeros(4, 2, 16), v_scale=torch.zeros(4, 2, 16), block_table=i32(3, 2), seq_lens=i32(3),
               cu_rows=i32(4))
 
-    def call(**over):
-        kw = {n: None if t is None else OnGpu(t) for n, t in dict(ok, **over).items() if n not in ("g", "hq")}
-        return gcs.cache_args(*[kw[n] for n in ok], 5, 5, over.get("hq"), None if "g" not in over else OnGpu(over["g"]))
+    def call(dev={}, hq=None, g=None, **over):
+        kw = {n: None if t is None else OnGpu(t, dev.get(n, 0)) for n, t in dict(ok, **over).items()}
+        return gcs.cache_args(*[kw[n] for n in ok], 5, 5, hq, None if g is None else OnGpu(g, dev.get("g", 0)), 0)
 
-    assert call().num_blocks == 4
+    assert call().num_blocks == 4 and call(g=torch.zeros(4, 4, 16)).hq == 4
     for over in (dict(v_cache=torch.zeros(4, 2, 16, 128, dtype=torch.uint8)), dict(k_cache=torch.zeros(4, 2, 16, 64)),
                  dict(cu_rows=i32(3)), dict(block_table=i32(2, 2)), dict(seq_lens=torch.zeros(3)), dict(k_scale=None),
-                 dict(g=torch.zeros(4, 4, 32)), dict(g=torch.zeros(4, 4, 16), hq=8),
+                 dict(g=torch.zeros(4, 4, 32)), dict(g=torch.zeros(4, 4, 16), hq=8), dict(g=torch.zeros(4, 4)),
+                 dict(block_table=None), dict(cu_rows=i32(8)[::2]), dict(k_cache=None),
                  dict(v_cache=torch.zeros(4, 16, 2, 64, dtype=torch.uint8).permute(0, 2, 1, 3))):
         with pytest.raises(ValueError):
             call(**over)
+    for name in (*ok, "g"):
+        with pytest.raises(ValueError, match="device 1"):
+            call(dev={name: 1}, g=torch.zeros(4, 4, 16))
     with pytest.raises(NotImplementedError):
         call(k_scale=torch.zeros(4, 2), v_scale=torch.zeros(4, 2))

@@ -426,45 +426,40 @@ def test_refused_outputs(L):
     assert L.attn_qk_norm_rope_bwd_workspace(None) == 0
 
 
-def test_binding_refuses_host_tensors_and_wrong_shapes():
+class OnGpu:
+    """What the binding reads of a tensor on GPU `dev`, without a GPU."""
+    is_cuda = True
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev = t, dev
+
+    def get_device(self):
+        return self.dev
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes(monkeypatch):
     import gated_causal_softmax_gb300 as gcs
 
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     c = make(4, 2, 1, 64, 64, seed=0, dev="cpu")
     with pytest.raises(ValueError, match="CUDA"):
         gcs.attn_qk_norm_rope_fwd(c["q"], c["k"], c["tab"], c["pos"], c["qw"], c["kw"])
 
-    class OnGpu:  # what the binding reads of a tensor, without a GPU
-        is_cuda = True
+    def call(dev={}, **over):
+        b = {n: None if t is None else OnGpu(t, dev.get(n, 0)) for n, t in dict(c, **over).items()}
+        return gcs.qk_rope_args(b["q"], b["k"], b["tab"], b["pos"], b["qw"], b["kw"], 1e-6, True, False, 0)
 
-        def __init__(self, t, dev=0):
-            self.t, self.dev = t, dev
-
-        def get_device(self):
-            return self.dev
-
-        def __getattr__(self, name):
-            return getattr(self.t, name)
-
-    g = lambda t: OnGpu(t)
+    assert call().rotary_dim == 64
     for over in (dict(k=c["k"][:3]), dict(k=c["k"][..., :32]), dict(qw=c["qw"][:32]), dict(pos=c["pos"][:3]),
                  dict(pos=c["pos"].long()), dict(q=c["q"].float()), dict(tab=c["tab"].double()), dict(tab=c["tab"][0]),
-                 dict(q=c["q"][..., ::2])):
-        b = {k: None if v is None else g(v) for k, v in dict(c, **over).items()}
+                 dict(q=c["q"].repeat(1, 1, 2)[..., ::2]), dict(q=None), dict(tab=c["tab"].repeat(1, 2)[:, ::2])):
         with pytest.raises(ValueError):
-            gcs.qk_rope_args(b["q"], b["k"], b["tab"], b["pos"], b["qw"], b["kw"], 1e-6, True, False)
-
-
-def test_binding_refuses_tensors_of_another_device(monkeypatch):
-    import gated_causal_softmax_gb300 as gcs
-
-    class On:
-        def __init__(self, dev):
-            self.dev = dev
-
-        def get_device(self):
-            return self.dev
-
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    gcs._on_current_device(On(0), None, On(0))
+            call(**over)
+    for name in ("q", "k", "tab", "pos", "qw", "kw"):  # on another device than the current one
+        with pytest.raises(ValueError, match="device 1"):
+            call(dev={name: 1})
     with pytest.raises(ValueError, match="device 1"):
-        gcs._on_current_device(On(0), None, On(1))
+        gcs._workspace(OnGpu(torch.zeros(4), 1), 0, 0)
