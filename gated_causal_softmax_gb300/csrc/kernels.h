@@ -241,7 +241,10 @@ struct CacheParams {
   const float* log_gate;       // append: [total, hq] or null
   float* log_gate_out;         // gather: [total, hq] or null
   float* tile_sums;            // append: [cache_gate_slots()][hq], or null (every tile sums what is before it)
-  int n_gate, gate_groups;     // set by the launchers: blocks of the gate role, groups of 32 query heads
+  // set by the launchers: the blocks that take rows (the grid's last), gate tiles (over all blocks),
+  // groups of 32 query heads,
+  int row_blocks, n_gate, gate_groups;
+  int log2_step;               // log2 of the rows of a warp's step (of the keys and values)
   int* status;
 };
 // Tile slots of the gates of `total` rows in num_reqs requests.

@@ -20,9 +20,13 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// Blocks of an SM, and rows of a lane group in a step: warps take further tokens beyond 152 SMs full.
-constexpr int kFwdBlocks = 4, kFwdRows = 2;
-constexpr int kBwdBlocks = 3;
+// Rows of a lane group in a step of the forward, and blocks of an SM: warps take further tokens beyond
+// 152 SMs full.  16384 x 36 heads of 512 forward: 179 us with 3, 193 with 4; 8192 x 40 of 128: 28.9 and
+// 27.6, 38 with 5 (spills); backward 47.0 with 3, 45.1 with 4.
+constexpr int kFwdRows = 2;
+template <int D>
+constexpr int kFwdBlocks = D == 512 ? 3 : 4;
+constexpr int kBwdBlocks = 4;
 
 // A warp's share: heads [h0, h1) of the queries or of the keys, and every step-th token.
 struct Share {
@@ -64,8 +68,8 @@ __device__ __forceinline__ bool token_used(const RopeParams& p, int pos) {
   return true;
 }
 
-// Runs through a warp's tokens with the copies of the next kStages - 1 of them under way:
-// fetch(stage, t, h) starts the copies of a token's rows, use(stage, t, used) works on them.
+// Runs through a warp's tokens with the copies of the next one under way: fetch(stage, t) starts the
+// copies of a token's rows, use(stage, t, used) works on them.
 template <int D, int ROWS, typename Fetch, typename Use>
 __device__ __forceinline__ void for_tokens(const RopeParams& p, const Share& s, WarpStage<D, ROWS>* ring, Fetch fetch,
                                            Use use) {
@@ -73,45 +77,41 @@ __device__ __forceinline__ void for_tokens(const RopeParams& p, const Share& s, 
   auto start = [&](int slot, uint32_t t, int pos) {
     if (t < total) {
       fetch(ring[slot], t);
-      if (p.cos_sin && pos >= 0 && pos < p.max_pos) fetch_angles(ring[slot], p.cos_sin, pos, p.rotary_dim);
+      if (p.cos_sin && pos >= 0 && pos < p.max_pos) fetch_angles(ring[slot].angles[0], p.cos_sin, pos, p.rotary_dim);
     }
     copy_commit();
   };
-  int ahead[kStages];  // positions of this token and of those after it
-#pragma unroll
-  for (int i = 0; i < kStages; ++i) ahead[i] = position_of(p, s.t + i * s.step);
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) start(i, s.t + i * s.step, ahead[i]);
+  int pos = position_of(p, s.t), next = position_of(p, s.t + s.step);
+  start(0, s.t, pos);
   int slot = 0;
-  for (uint32_t t = s.t; t < total; t += s.step) {
-    const int free = slot == 0 ? kStages - 1 : slot - 1;  // the slot used last
-    start(free, t + (kStages - 1) * s.step, ahead[kStages - 1]);
-    const int next = position_of(p, t + kStages * s.step);
-    copy_wait<kStages - 1>();
+  for (uint32_t t = s.t; t < total; t += s.step, slot ^= 1) {
+    start(slot ^ 1, t + s.step, next);
+    const int after = position_of(p, t + 2 * s.step);
+    copy_wait<1>();
     __syncwarp();
-    use(ring[slot], t, token_used(p, ahead[0]));
+    use(ring[slot], t, token_used(p, pos));
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) ahead[i] = ahead[i + 1];
-    ahead[kStages - 1] = next;
-    slot = slot == kStages - 1 ? 0 : slot + 1;
+    pos = next;
+    next = after;
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(const RopeParams p) {
+// BACK: the gradient without the norm, which is the rotation back of dout (p.q_out, p.k_out) into dx.
+template <int D, bool BACK>
+__global__ void __launch_bounds__(kThreads, kFwdBlocks<D>) norm_rope_fwd_kernel(const RopeParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows, U = kFwdRows;
-  __shared__ WarpStage<D, U> ring[kWarps][kStages];
+  __shared__ WarpStage<D, U> ring[kWarps][2];
   Share s;
   if (!warp_share<R * U>(p.total, p.hq, p.hkv, s)) return;
   const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
   const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
-  const uint16_t* in = s.is_k ? p.k : p.q;
-  uint16_t* out = s.is_k ? p.k_out : p.q_out;
-  const long long its = s.is_k ? p.k_ts : p.q_ts, ihs = s.is_k ? p.k_hs : p.q_hs;
-  const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
-  float w[16];
-  load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
+  const uint16_t* in = BACK ? s.is_k ? p.k_out : p.q_out : s.is_k ? p.k : p.q;
+  uint16_t* out = BACK ? s.is_k ? p.dk : p.dq : s.is_k ? p.k_out : p.q_out;
+  const long long its = BACK ? s.is_k ? p.ko_ts : p.qo_ts : s.is_k ? p.k_ts : p.q_ts;
+  const long long ihs = BACK ? s.is_k ? p.ko_hs : p.qo_hs : s.is_k ? p.k_hs : p.q_hs;
+  const long long ots = BACK ? s.is_k ? p.dk_ts : p.dq_ts : s.is_k ? p.ko_ts : p.qo_ts;
+  const long long ohs = BACK ? s.is_k ? p.dk_hs : p.dq_hs : s.is_k ? p.ko_hs : p.qo_hs;
+  const Row w = load_weights(s.is_k ? p.k_weight : p.q_weight, runs);
   auto fetch = [&](WarpStage<D, U>& st, uint32_t t) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -121,34 +121,32 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) norm_rope_fwd_kernel(con
     }
   };
   auto use = [&](const WarpStage<D, U>& st, uint32_t t, bool used) {
-    if (!used) return;
-    Angles ang;
-    read_angles(st.angles, p.rotary_dim, runs, ang);
+    if (!used && !BACK) return;
+    const Angles ang = read_angles<BACK>(st.angles[0], p.rotary_dim, runs);
+    Row x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = BACK && !used ? zero_row() : unpack_row(fetched_row(st, u));
+    if (!BACK)
+      norm_rotate_rows<D>(x, w, runs, ang, p.norm, p.eps, p.interleaved);
+    else if (used)  // else the row's output does not depend on it
+      rotate_rows(x, runs, ang, p.interleaved);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int h = s.h0 + u * R + grp;
-      float x[16];
-      unpack_row(fetched_row(st, u), x);
-      if (p.norm) {
-        const float r = row_rstd<D>(x, p.eps);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
-      }
-      rotate_row<false>(x, runs, ang, p.interleaved);
-      if (h < s.h1) store_row(out + t * ots + h * ohs, runs, x);
+      if (h < s.h1) store_row(out + t * ots + h * ohs, runs, x[u]);
     }
   };
   for_tokens(p, s, ring[threadIdx.x >> 5], fetch, use);
 }
 
-// Also the gradients of the weights: every lane sums g x r of its 16 elements over its rows, the
+// The backward with the norm, and the gradients of its weights: every lane sums g x r of its 16 elements over its rows, the
 // lanes of a block with the same elements are added in a fixed order, and the block writes its
 // part of d q_weight and d k_weight to p.partials [blocks][2][D]; weight_grad_kernel adds those.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const RopeParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
   __shared__ union {
-    WarpStage<D, 2> ring[kWarps][kStages];
+    WarpStage<D, 2> ring[kWarps][2];
     float part[kWarps][D];  // after the last step
   } sm;
   __shared__ int part_is_k[kWarps];
@@ -156,9 +154,7 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
   const int sub = threadIdx.x & (L - 1), grp = lane / L;
   const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
   Share s;
-  float dw[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+  Row dw = zero_row();
   const bool works = warp_share<R>(p.total, p.hq, p.hkv, s);
   if (works) {
     const uint16_t* in = s.is_k ? p.k : p.q;
@@ -167,41 +163,36 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const long long its = s.is_k ? p.k_ts : p.q_ts, ihs = s.is_k ? p.k_hs : p.q_hs;
     const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
     const long long dts = s.is_k ? p.dk_ts : p.dq_ts, dhs = s.is_k ? p.dk_hs : p.dq_hs;
-    float w[16];
-    load_weights(s.is_k ? p.k_weight : p.q_weight, runs, w);
+    const Row w = load_weights(s.is_k ? p.k_weight : p.q_weight, runs);
     const bool valid = s.h0 + grp < s.h1;
     const int h = valid ? s.h0 + grp : s.h0;
     auto fetch = [&](WarpStage<D, 2>& st, uint32_t t) {
       fetch_row(st, 0, dout + t * ots + h * ohs, runs, valid);
-      if (p.norm) fetch_row(st, 1, in + t * its + h * ihs, runs, valid);
+      fetch_row(st, 1, in + t * its + h * ihs, runs, valid);
     };
     auto use = [&](const WarpStage<D, 2>& st, uint32_t t, bool used) {
-      float g[16];
-      if (!used) {  // the row's output does not depend on it
+      Row gs[1] = {zero_row()}, &g = gs[0];
+      if (used) {
+        g = unpack_row(fetched_row(st, 0));
+        rotate_rows(gs, runs, read_angles<true>(st.angles[0], p.rotary_dim, runs), p.interleaved);
+        Row x = unpack_row(fetched_row(st, 1)), u;
+        float2 xx = both(0.f), ux = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = 0.f;
-      } else {
-        Angles ang;
-        read_angles(st.angles, p.rotary_dim, runs, ang);
-        unpack_row(fetched_row(st, 0), g);
-        rotate_row<true>(g, runs, ang, p.interleaved);
-        if (p.norm) {
-          float x[16], ss = 0.f, su = 0.f;
-          unpack_row(fetched_row(st, 1), x);
+        for (int i = 0; i < 8; ++i) {
+          u.e[i] = mul2(g.e[i], w.e[i]);
+          xx = fma2(x.e[i], x.e[i], xx);
+          ux = fma2(u.e[i], x.e[i], ux);
+        }
+        float sums[2] = {xx.x + xx.y, ux.x + ux.y};
+        row_sums<L>(sums);
+        const float r = rsqrtf(fmaf(sums[0], 1.f / D, p.eps));
+        const float m = sums[1] * r * (1.f / D);  // mean(u x r)
+        const float2 r2 = both(r), m2 = both(-m * r);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            ss = fmaf(x[i], x[i], ss);
-            su = fmaf(g[i] * w[i], x[i], su);
-          }
-          ss = row_sum<L>(ss);
-          su = row_sum<L>(su);
-          const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-          const float m = su * r * r * (1.f / D);  // r mean(u x r)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            dw[i] = fmaf(g[i] * r, x[i], dw[i]);
-            g[i] = r * fmaf(-x[i], m, g[i] * w[i]);
-          }
+        for (int i = 0; i < 8; ++i) {
+          x.e[i] = mul2(x.e[i], r2);
+          dw.e[i] = fma2(g.e[i], x.e[i], dw.e[i]);
+          g.e[i] = fma2(x.e[i], m2, mul2(u.e[i], r2));
         }
       }
       if (valid) store_row(dx + t * dts + h * dhs, runs, g);
@@ -209,16 +200,20 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     for_tokens(p, s, sm.ring[warp], fetch, use);
   }
   if (!p.partials) return;
+  grid_release();
 #pragma unroll
   for (int off = L; off < 32; off <<= 1)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[i] += __shfl_xor_sync(kFullMask, dw[i], off);
+    for (int i = 0; i < 8; ++i) {
+      dw.e[i].x += __shfl_xor_sync(kFullMask, dw.e[i].x, off);
+      dw.e[i].y += __shfl_xor_sync(kFullMask, dw.e[i].y, off);
+    }
   __syncthreads();  // the ring is done with
   if (grp == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sm.part[warp][runs.a + i] = dw[i];
-      sm.part[warp][runs.b + i] = dw[8 + i];
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<float2*>(&sm.part[warp][runs.a + 2 * i]) = dw.e[i];
+      *reinterpret_cast<float2*>(&sm.part[warp][runs.b + 2 * i]) = dw.e[4 + i];
     }
   }
   if (lane == 0) part_is_k[warp] = works ? (s.is_k ? 1 : 0) : 2;
@@ -234,13 +229,13 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
 }
 
 // dw of 32 columns a block: 32 threads a column add every 32nd block's part, then their sums.
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restrict__ partials, int blocks, int d,
-                                                           float* __restrict__ dq_weight,
-                                                           float* __restrict__ dk_weight) {
+__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials, int blocks, int d,
+                                                           float* dq_weight, float* dk_weight) {
   __shared__ float sm[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float sum = 0.f;
-  for (int b = threadIdx.y; b < blocks; b += 32) sum += __ldg(partials + (size_t)b * 2 * d + c);
+  grid_wait();
+  for (int b = threadIdx.y; b < blocks; b += 32) sum += __ldcg(partials + (size_t)b * 2 * d + c);
   sm[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
   float x = sm[threadIdx.x][threadIdx.y];
@@ -255,21 +250,21 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const float* __restri
 
 int bwd_blocks(const RopeParams& p) { return blocks_for(p.total, p.hq, p.hkv, 512 / p.d, 152 * kBwdBlocks); }
 
-template <int D>
+template <int D, bool BACK>
 cudaError_t fwd(const RopeParams& p, cudaStream_t s) {
-  const int blocks = blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows * kFwdRows, 152 * kFwdBlocks);
-  norm_rope_fwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
+  const int blocks = blocks_for(p.total, p.hq, p.hkv, RowLanes<D>::kRows * kFwdRows, 152 * kFwdBlocks<D>);
+  norm_rope_fwd_kernel<D, BACK><<<blocks, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStream_t s) {
+  if (!p.norm) return fwd<D, true>(p, s);
   const int blocks = bwd_blocks(p);
   norm_rope_bwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partials) return e;
-  weight_grad_kernel<<<2 * D / 32, dim3(32, 32), 0, s>>>(p.partials, blocks, D, dq_weight, dk_weight);
-  return cudaGetLastError();
+  return launch_behind(weight_grad_kernel, 2 * D / 32, dim3(32, 32), s, p.partials, blocks, D, dq_weight, dk_weight);
 }
 
 }  // namespace
@@ -280,10 +275,10 @@ size_t norm_rope_bwd_partials(const RopeParams& p) {
 
 cudaError_t launch_norm_rope_fwd(const RopeParams& p, cudaStream_t s) {
   switch (p.d) {
-    case 64: return fwd<64>(p, s);
-    case 128: return fwd<128>(p, s);
-    case 256: return fwd<256>(p, s);
-    default: return fwd<512>(p, s);
+    case 64: return fwd<64, false>(p, s);
+    case 128: return fwd<128, false>(p, s);
+    case 256: return fwd<256, false>(p, s);
+    default: return fwd<512, false>(p, s);
   }
 }
 

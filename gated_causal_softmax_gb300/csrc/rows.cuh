@@ -12,11 +12,32 @@
 // sector: the forward of 16384 tokens of 36 heads of 512 took 270 us that way and took 202 so.)
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <cstdint>
 
 #include "sm103_ptx.cuh"
 
 namespace gcs {
+
+// A kernel that needs what the one before it on the stream wrote, launched while that one still
+// runs: it waits for its end and for its writes before it reads them (grid_wait).  Where the first
+// kernel says so (grid_release, by all blocks), or when its blocks have ended, the second may start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.stream = s;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, Params(args)...);
+}
 
 constexpr unsigned kFullMask = 0xffffffffu;
 
@@ -60,15 +81,14 @@ struct RawRow {
   uint4 a, b;
 };
 
-// The rows of a warp's steps ahead, in shared memory: ROWS rows of every lane group and the table's
-// row of the step's token.  Copies go in asynchronously, one step ahead of their use (two steps
-// ahead measured the same or slower), so the bytes in flight do not depend on how many registers
-// the arithmetic leaves for occupancy.
-constexpr int kStages = 2;
-template <int D, int ROWS>
+// The rows of a warp's next step, in shared memory: ROWS rows of every lane group and the table's
+// row of the step's token (or the rows of its tokens, at most one for each lane group).  Copies go in asynchronously a step ahead of their use (two and three
+// steps ahead measured the same, and slower at d = 512), so the bytes in flight do not depend on how
+// many registers the arithmetic leaves for occupancy.
+template <int D, int ROWS, int TOKENS = 1>
 struct WarpStage {
   uint4 raw[ROWS][2][32];  // a lane's two runs of each row: read by the lane that copied them
-  float angles[D];         // read by the whole warp
+  float angles[TOKENS][D]; // read by the whole warp
 };
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src, bool valid) {
@@ -89,118 +109,188 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // Starts the copy of the lane's part of a row (zeros where not valid: nothing is read).
-template <int D, int ROWS>
-__device__ __forceinline__ void fetch_row(WarpStage<D, ROWS>& st, int i, const uint16_t* row, const RowRuns& r,
-                                          bool valid) {
+template <typename Stage>
+__device__ __forceinline__ void fetch_row(Stage& st, int i, const uint16_t* row, const RowRuns& r, bool valid) {
   const int lane = threadIdx.x & 31;
   copy_async16(&st.raw[i][0][lane], row + r.a, valid);
   copy_async16(&st.raw[i][1][lane], row + r.b, valid);
 }
 // Starts the copy of a table row, by the whole warp.
-template <int D, int ROWS>
-__device__ __forceinline__ void fetch_angles(WarpStage<D, ROWS>& st, const float* table, long long pos, int rot) {
-  for (int i = (threadIdx.x & 31) * 4; i < rot; i += 128) copy_async16(&st.angles[i], table + pos * rot + i, true);
+template <int D>
+__device__ __forceinline__ void fetch_angles(float (&angles)[D], const float* table, int pos, int rot) {
+  const float* row = table + (long long)pos * rot;
+#pragma unroll
+  for (int i = 0; i < D; i += 128) {
+    const int j = i + (threadIdx.x & 31) * 4;
+    if (j < rot) copy_async<16>(&angles[j], row + j);
+  }
 }
-template <int D, int ROWS>
-__device__ __forceinline__ RawRow fetched_row(const WarpStage<D, ROWS>& st, int i) {
+template <typename Stage>
+__device__ __forceinline__ RawRow fetched_row(const Stage& st, int i) {
   const int lane = threadIdx.x & 31;
   return RawRow{st.raw[i][0][lane], st.raw[i][1][lane]};
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+// Two fp32 operations in one instruction, each rounded as usual.
+__device__ __forceinline__ float2 as_f2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
 }
-__device__ __forceinline__ void unpack_row(const RawRow& w, float* x) {
-  unpack8(w.a, x);
-  unpack8(w.b, x + 8);
+__device__ __forceinline__ unsigned long long as_u64(const float2& a) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a.x), "f"(a.y));
+  return v;
 }
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg2(const float2& a) { return make_float2(-a.x, -a.y); }
 
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-// The one rounding of a row to bf16 (nearest even).
-__device__ __forceinline__ void store_row(uint16_t* row, const RowRuns& r, const float* x) {
-  *reinterpret_cast<uint4*>(row + r.a) = pack8(x);
-  *reinterpret_cast<uint4*>(row + r.b) = pack8(x + 8);
-}
-
-// Sum over the lanes of a row.
-template <int L>
-__device__ __forceinline__ float row_sum(float x) {
+// A lane's 16 elements in fp32: e[0..3] are run a, e[4..7] run b.
+struct Row {
+  float2 e[8];
+};
+__device__ __forceinline__ Row zero_row() {
+  Row x;
 #pragma unroll
-  for (int off = L / 2; off; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
+  for (int i = 0; i < 8; ++i) x.e[i] = both(0.f);
   return x;
 }
+__device__ __forceinline__ Row unpack_row(const RawRow& w) {
+  const uint32_t u[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
+  Row x;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x.e[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+  return x;
+}
+// The one rounding of a row to bf16 (nearest even).
+__device__ __forceinline__ uint4 pack_run(const float2* e) {
+  return make_uint4(pack_bf16x2(e[0].x, e[0].y), pack_bf16x2(e[1].x, e[1].y), pack_bf16x2(e[2].x, e[2].y),
+                    pack_bf16x2(e[3].x, e[3].y));
+}
+__device__ __forceinline__ void store_row(uint16_t* row, const RowRuns& r, const Row& x) {
+  *reinterpret_cast<uint4*>(row + r.a) = pack_run(x.e);
+  *reinterpret_cast<uint4*>(row + r.b) = pack_run(x.e + 4);
+}
 
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 u = __ldg(reinterpret_cast<const float4*>(p)), v = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+// Sums over the lanes of a row, of N values side by side.
+template <int L, int N>
+__device__ __forceinline__ void row_sums(float (&x)[N]) {
+#pragma unroll
+  for (int off = L / 2; off; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] += __shfl_xor_sync(kFullMask, x[i], off);
+}
+
+__device__ __forceinline__ void read4(const float* p, float2* x) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  x[0] = make_float2(u.x, u.y);
+  x[1] = make_float2(u.z, u.w);
 }
 
 // The norm's weights of the lane's elements; ones without weights.
-__device__ __forceinline__ void load_weights(const float* w, const RowRuns& r, float* x) {
+__device__ __forceinline__ Row load_weights(const float* w, const RowRuns& r) {
+  Row x;
   if (w) {
-    load8(w + r.a, x);
-    load8(w + r.b, x + 8);
+    read4(w + r.a, x.e);
+    read4(w + r.a + 4, x.e + 2);
+    read4(w + r.b, x.e + 4);
+    read4(w + r.b + 4, x.e + 6);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 1.f;
+    for (int i = 0; i < 8; ++i) x.e[i] = both(1.f);
   }
+  return x;
 }
 
-// Cosines and sines of the lane's 8 pairs, from a row of the table (cosines, then sines).
+// Cosines c and sines s of the lane's 8 pairs, from a row of the table (cosines, then sines), and
+// n = -s; BACK: of the opposite angle.
 struct Angles {
-  float c[8], s[8];
+  float2 c[4], s[4], n[4];
 };
-__device__ __forceinline__ void read4(const float* p, float* x) {
-  const float4 u = *reinterpret_cast<const float4*>(p);
-  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-}
-__device__ __forceinline__ void read_angles(const float* row, int rot, const RowRuns& r, Angles& t) {
+template <bool BACK>
+__device__ __forceinline__ Angles read_angles(const float* row, int rot, const RowRuns& r) {
   const float* sines = row + (rot >> 1);
+  Angles t;
   if (r.turn_a) {
     read4(row + r.angle_a, t.c);
-    read4(sines + r.angle_a, t.s);
+    read4(sines + r.angle_a, BACK ? t.n : t.s);
   }
   if (r.turn_b) {
-    read4(row + r.angle_b, t.c + 4);
-    read4(sines + r.angle_b, t.s + 4);
+    read4(row + r.angle_b, t.c + 2);
+    read4(sines + r.angle_b, (BACK ? t.n : t.s) + 2);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BACK)
+      t.s[i] = neg2(t.n[i]);
+    else
+      t.n[i] = neg2(t.s[i]);
+  }
+  return t;
 }
 
-// (a, b) -> (a c - b s, b c + a s) for the lane's pairs; BACK: by the opposite angle.
-__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
-  const float x = fmaf(a, c, -b * s), y = fmaf(b, c, a * s);
-  a = x, b = y;
-}
-template <bool BACK>
-__device__ __forceinline__ void rotate_row(float* x, const RowRuns& r, const Angles& t, bool interleaved) {
+// Pairs (a, b) -> (a c - b s, b c + a s), of U rows side by side.
+template <int U>
+__device__ __forceinline__ void rotate_rows(Row (&x)[U], const RowRuns& r, const Angles& t, bool interleaved) {
   if (interleaved) {
+    auto turn = [](float2& p, float c, float s, float n) { p = make_float2(fmaf(p.y, n, p.x * c), fmaf(p.x, s, p.y * c)); };
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < 4 ? r.turn_a : r.turn_b) rotate_pair(x[2 * i], x[2 * i + 1], t.c[i], BACK ? -t.s[i] : t.s[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (i < 2 ? r.turn_a : r.turn_b) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          turn(x[u].e[2 * i], t.c[i].x, t.s[i].x, t.n[i].x);
+          turn(x[u].e[2 * i + 1], t.c[i].y, t.s[i].y, t.n[i].y);
+        }
+      }
+    }
   } else if (r.turn_a) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rotate_pair(x[i], x[8 + i], t.c[i], BACK ? -t.s[i] : t.s[i]);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float2 a = x[u].e[i], b = x[u].e[4 + i];
+        x[u].e[i] = fma2(b, t.n[i], mul2(a, t.c[i]));
+        x[u].e[4 + i] = fma2(a, t.s[i], mul2(b, t.c[i]));
+      }
   }
 }
 
-// (mean(x^2) + eps)^(-1/2) over the row; the sum in fp32.
-template <int D>
-__device__ __forceinline__ float row_rstd(const float* x, float eps) {
-  float s0 = 0.f, s1 = 0.f;
+// x = R (x w) r with r = (mean(x^2) + eps)^(-1/2) over the row, the sum in fp32; without the norm
+// w = 1 and r = 1.  The products and the rotation do not wait for the sum over the lanes.
+template <int D, int U>
+__device__ __forceinline__ void norm_rotate_rows(Row (&x)[U], const Row& w, const RowRuns& runs, const Angles& t,
+                                                 bool norm, float eps, bool interleaved) {
+  float r[U];
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    s0 = fmaf(x[i], x[i], s0);
-    s1 = fmaf(x[i + 1], x[i + 1], s1);
+  for (int u = 0; u < U; ++u) {
+    float2 s = mul2(x[u].e[0], x[u].e[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s = fma2(x[u].e[i], x[u].e[i], s);
+    r[u] = s.x + s.y;
   }
-  return rsqrtf(fmaf(row_sum<RowLanes<D>::kLanes>(s0 + s1), 1.f / D, eps));
+  row_sums<RowLanes<D>::kLanes>(r);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    r[u] = norm ? rsqrtf(fmaf(r[u], 1.f / D, eps)) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[u].e[i] = mul2(x[u].e[i], w.e[i]);
+  }
+  rotate_rows(x, runs, t, interleaved);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[u].e[i] = mul2(x[u].e[i], both(r[u]));
 }
 
 }  // namespace gcs

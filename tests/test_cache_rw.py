@@ -225,6 +225,35 @@ def test_many_requests(gcs_lib):
     check_read(c, gcs_lib)
 
 
+NARROW = [dict(rows=[7001, 1, 0, 9003, 6000], lens=[7010, 1, 4, 9003, 6100], hq=2, hkv=1, d=64, block=16, pad=3),
+          dict(rows=[6000] + [1, 2, 3] * 40 + [7000], lens=[6003] + [20, 16, 3] * 40 + [7000], hq=2, hkv=2, d=128, block=32),
+          dict(rows=[11000], lens=[11001], hq=4, hkv=1, d=256, block=64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["token", "tensor", "bf16"])
+@pytest.mark.parametrize("shape", range(len(NARROW)))
+def test_few_heads_many_rows(gcs_lib, shape, fmt):
+    """With few kv heads a warp takes several rows at a time: over page ends, request ends, the last
+    rows, and rows that lie outside."""
+    c = Cache(**NARROW[shape], fmt=fmt, gates=False, seed=50 + shape)
+    append_and_check(gcs_lib, c)
+    check_read(c, gcs_lib)
+    if shape == 0:  # a block in the middle of request 0, and what lies behind its 100th page
+        whole = c.gather(gcs_lib)[0]
+        c.idx["block_table"][0, 57] = -1
+        c.idx["block_table"][3, 100:] = c.nb
+        out = torch.full_like(whole, 3.0)
+        gcs_lib.attn_cache_gather(c.kc, c.vc, c.ks, c.vs, c.idx["block_table"], c.idx["seq_lens"], c.dcu, len(whole), k=out)
+        assert gcs_lib.get_device_status() == 1
+        first = 7010 - 7001  # position of request 0's first row
+        lost = set(range(57 * 16 - first, 58 * 16 - first)) | set(range(7002 + 1600, 7002 + 9003))
+        lost = torch.tensor(sorted(lost), device="cuda")
+        keep = torch.ones(len(whole), dtype=torch.bool, device="cuda")
+        keep[lost] = False
+        assert bool((out[lost] == 3.0).all()) and torch.equal(out[keep], whole[keep])
+
+
 @pytest.mark.gpu
 def test_appends_in_pieces_equal_one(gcs_lib):
     """A prompt written at once, and in pieces of 1, 15, 16, 100 tokens: the same cache (the gates
@@ -352,7 +381,22 @@ def append_rope(gcs, c, tab, w, positions=None, inter=False, **kw):
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt,d,rot,inter,explicit", ROPE)
 def test_append_rope(gcs_lib, fmt, d, rot, inter, explicit):
-    c = Cache([5, 1, 0, 40], [300, 17, 4, 40], 12, 3, d, fmt=fmt, seed=20 + d, pad=2)
+    check_append_rope(gcs_lib, Cache([5, 1, 0, 40], [300, 17, 4, 40], 12, 3, d, fmt=fmt, seed=20 + d, pad=2), rot, inter,
+                      explicit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,d,hkv,rot,inter,explicit", [("token", 64, 1, 64, False, True), ("token", 128, 2, 64, True, False),
+                                                         ("bf16", 128, 1, 128, False, True)])
+def test_append_rope_of_few_heads(gcs_lib, fmt, d, hkv, rot, inter, explicit):
+    """Several rows at a time, each with its own angles."""
+    rows = [9000] + [1, 2, 3] * 20 + [5001]
+    check_append_rope(gcs_lib, Cache(rows, [n + 9 for n in rows], hkv, hkv, d, fmt=fmt, seed=60 + d, pad=2), rot, inter,
+                      explicit)
+
+
+def check_append_rope(gcs_lib, c, rot, inter, explicit):
+    d, fmt = c.d, c.fmt
     w, tab = rope_inputs(c, rot, 21)
     pos = np.zeros(c.total, np.int32)
     for t, _, p, _, _ in c.places():
