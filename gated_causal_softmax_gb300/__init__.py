@@ -638,13 +638,15 @@ def _rows(t, name: str, shape, dev: int):
     return t.data_ptr(), (token if n > 1 else heads * head, head)
 
 
-def _new_rows(like, shape):
-    return torch.empty(shape, dtype=_BF16, device=like.device)
+def _new(like):
+    """An uninitialised contiguous tensor of the same shape, type and device."""
+    return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int) -> QkRopeArgs:
-    """Marshals the arguments of the norm and rotation (rotary_dim is the table's width); the strides
-    of the outputs are set by the callers."""
+def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int,
+                 *strides) -> QkRopeArgs:
+    """Marshals the arguments of the norm and rotation (rotary_dim is the table's width); strides:
+    those of q_out, k_out, dq and dk, as far as the call has them."""
     if q is None or k is None or q.dim() != 3 or k.dim() != 3:
         raise ValueError("expected [tokens, heads, dim] tensors q and k")
     shape = q.shape
@@ -660,7 +662,7 @@ def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interl
     return QkRopeArgs(n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, qp, kp,
                       _vector(q_weight, _F32, "q_weight", (d,), dev), _vector(k_weight, _F32, "k_weight", (d,), dev),
                       _vector(cos_sin, _F32, "cos_sin", (max_pos, rot), dev), max_pos,
-                      _vector(positions, _I32, "positions", (n,), dev), qs, ks)
+                      _vector(positions, _I32, "positions", (n,), dev), qs, ks, *strides)
 
 
 def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
@@ -671,13 +673,13 @@ def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_w
     rotation); positions int32 [tot], negative = padding (outputs left as they were).
     norm=False: rotation only.  Returns q_out, k_out."""
     dev = torch.cuda.current_device()
-    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
     if q_out is None:
-        q_out = _new_rows(q, q.shape)
+        q_out = _new(q)
     if k_out is None:
-        k_out = _new_rows(k, k.shape)
-    qp, a.q_out_stride = _rows(q_out, "q_out", q.shape, dev)
-    kp, a.k_out_stride = _rows(k_out, "k_out", k.shape, dev)
+        k_out = _new(k)
+    qp, qs = _rows(q_out, "q_out", q.shape, dev)
+    kp, ks = _rows(k_out, "k_out", k.shape, dev)
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs, ks)
     _check(load().attn_qk_norm_rope_fwd(a, qp, kp, _raw_stream(dev)), "attn_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -690,20 +692,21 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_
     the weight)."""
     L = load()
     dev = torch.cuda.current_device()
-    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
-    qs, ks, w = q.shape, k.shape, (a.d,)
     if dq is None:
-        dq = _new_rows(q, qs)
+        dq = _new(q)
     if dk is None:
-        dk = _new_rows(k, ks)
+        dk = _new(k)
     if q_weight is not None and dq_weight is None:
         dq_weight = torch.empty_like(q_weight)
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty_like(k_weight)
-    gqp, a.q_out_stride = _rows(dq_out, "dq_out", qs, dev)
-    gkp, a.k_out_stride = _rows(dk_out, "dk_out", ks, dev)
-    dqp, a.dq_stride = _rows(dq, "dq", qs, dev)
-    dkp, a.dk_stride = _rows(dk, "dk", ks, dev)
+    qs, ks = q.shape, k.shape
+    gqp, gqs = _rows(dq_out, "dq_out", qs, dev)
+    gkp, gks = _rows(dk_out, "dk_out", ks, dev)
+    dqp, dqs = _rows(dq, "dq", qs, dev)
+    dkp, dks = _rows(dk, "dk", ks, dev)
+    a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, gqs, gks, dqs, dks)
+    w = (a.d,)
     ws, ws_bytes = _workspace(workspace, L.attn_qk_norm_rope_bwd_workspace(a), dev)
     _check(L.attn_qk_norm_rope_bwd(a, gqp, gkp, dqp, dkp, _vector(dq_weight, _F32, "dq_weight", w, dev),
                                    _vector(dk_weight, _F32, "dk_weight", w, dev), _ptr(ws), ws_bytes,
@@ -723,21 +726,21 @@ def _workspace(workspace, need: int, dev: int):
 
 
 def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq, g_cache,
-               dev: int) -> CacheArgs:
+               dev: int, *strides) -> CacheArgs:
     """Marshals the arguments of the cache calls: the caches, scales and index arrays are those of
     decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes); hq None:
-    g_cache's heads."""
+    g_cache's heads; strides: those of the packed k and v."""
     if k_cache is None or v_cache is None or k_cache.dim() != 4:
         raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
-    shape, fmt, strides = k_cache.shape, k_cache.dtype, k_cache.stride()
+    shape, fmt, cs = k_cache.shape, k_cache.dtype, k_cache.stride()
     if shape != v_cache.shape or fmt is not v_cache.dtype:
         raise ValueError("k_cache and v_cache shapes or types differ")
-    if strides != v_cache.stride():
+    if cs != v_cache.stride():
         raise ValueError("k_cache and v_cache must share one layout")
     if fmt not in (_BF16, _U8, _E4M3):
         raise ValueError(f"caches must be bf16, uint8 or float8_e4m3fn, got {fmt}")
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if strides[3] != 1 or t.get_device() != dev:
+        if cs[3] != 1 or t.get_device() != dev:
             _refuse(t, fmt, name, shape, dev, True)
     nb, hkv, bs, d = shape
     kv_format, scale_mode, ks, vs = KV_FP8_E4M3, SCALE_PER_TOKEN, None, None
@@ -763,11 +766,18 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
         if g_cache.dim() != 3:
             raise ValueError("g_cache must be [num_blocks, num_q_heads, block_size]")
         hq = g_cache.shape[1]
-    return CacheArgs(num_reqs, _vector(cu_rows, _I32, "cu_rows", (num_reqs + 1,), dev), total_rows, max_rows,
+    return CacheArgs(num_reqs, _vector(cu_rows, _I32, "cu_rows", (num_reqs + 1,), dev), int(total_rows), int(max_rows),
                      _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev),
                      _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(),
                      v_cache.data_ptr(), ks, vs, nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
-                     _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), strides[0], strides[1], strides[2])
+                     _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), cs[0], cs[1], cs[2], *strides)
+
+
+def _packed_shape(rows, k_cache):
+    """[tokens, kv heads, d] of the packed tensors of a cache."""
+    if rows is None or k_cache is None or k_cache.dim() != 4:
+        raise ValueError("expected packed rows and a cache [num_blocks, num_kv_heads, block_size, d]")
+    return rows.shape[0], k_cache.shape[1], k_cache.shape[3]
 
 
 def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, log_gate=None,
@@ -778,11 +788,12 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     scales written, a per-tensor one is quantised with the given scales."""
     L = load()
     dev = torch.cuda.current_device()
-    n = 0 if k is None else k.shape[0]
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev)
-    shape = (n, a.hkv, a.d)
-    kp, a.k_stride = _rows(k, "k", shape, dev)
-    vp, a.v_stride = _rows(v, "v", shape, dev)
+    shape = _packed_shape(k, k_cache)
+    kp, ks = _rows(k, "k", shape, dev)
+    vp, vs = _rows(v, "v", shape, dev)
+    n = shape[0]
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev, ks,
+                   vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
     ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
     _check(L.attn_cache_append(a, kp, vp, lg, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append")
@@ -796,13 +807,15 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     v into the cache.  positions None: the cached positions."""
     L = load()
     dev = torch.cuda.current_device()
-    r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev)
-    n, hq = r.total_tokens, r.hq
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev)
+    shape = _packed_shape(q, k_cache)
     if q_out is None:
-        q_out = _new_rows(q, q.shape)
-    qp, r.q_out_stride = _rows(q_out, "q_out", q.shape, dev)
-    vp, a.v_stride = _rows(v, "v", (n, a.hkv, a.d), dev)
+        q_out = _new(q)
+    qp, qs = _rows(q_out, "q_out", q.shape, dev)
+    r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs)
+    n, hq = shape[0], r.hq
+    vp, vs = _rows(v, "v", shape, dev)
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev, (0, 0),
+                   vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, hq), dev)
     ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
     _check(L.attn_cache_append_rope(a, r, vp, lg, qp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append_rope")
@@ -816,17 +829,20 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     [total_rows, hq] (the differences of the cumulative gates): what attn_fwd takes.  total_rows
     is cu_rows's last entry on the host.  Returns k, v, log_gate (None without g_cache)."""
     dev = torch.cuda.current_device()
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, total_rows),
-                   None, g_cache, dev)
-    shape = (max(0, total_rows), a.hkv, a.d)
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
+    n = max(0, int(total_rows))
+    shape = (n, k_cache.shape[1], k_cache.shape[3])
     if k is None:
-        k = _new_rows(k_cache, shape)
+        k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
     if v is None:
-        v = _new_rows(k_cache, shape)
+        v = _new(k)
+    kp, ks = _rows(k, "k", shape, dev)
+    vp, vs = _rows(v, "v", shape, dev)
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, n), None,
+                   g_cache, dev, ks, vs)
     if g_cache is not None and log_gate is None:
-        log_gate = torch.empty((shape[0], a.hq), dtype=_F32, device=k_cache.device)
-    kp, a.k_stride = _rows(k, "k", shape, dev)
-    vp, a.v_stride = _rows(v, "v", shape, dev)
-    lg = _vector(log_gate, _F32, "log_gate", (shape[0], a.hq), dev)
+        log_gate = torch.empty((n, a.hq), dtype=_F32, device=k_cache.device)
+    lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
     _check(load().attn_cache_gather(a, kp, vp, lg, _raw_stream(dev)), "attn_cache_gather")
     return k, v, log_gate

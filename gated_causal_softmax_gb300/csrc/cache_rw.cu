@@ -10,9 +10,9 @@
 //   gates            G_p = G_{p-1} + log_gate_p per query head, G_{-1} = 0
 //   read             bf16(code * scale); log_gate_p = G_p - G_{p-1}
 //
-// e4m3() rounds to nearest even and saturates at +-448.  A row of zeros has scale 0 and codes 0;
-// a row with an infinity or a NaN has that for its scale, and reads back as NaN wherever the
-// products say so.
+// e4m3() rounds to nearest even and saturates at +-448.  A scale that is not above 0 (a row of zeros,
+// or a NaN in the row) has codes 0; a row with an infinity has scale inf.  Both read back as the
+// products say.
 //
 // All of it is bound by HBM, or by latency when there are few rows.  Every index that comes from
 // a device array is checked against its buffer before it is used: a row whose place is not in
@@ -305,8 +305,10 @@ __device__ __forceinline__ void write_cache_rows(const CacheParams& p, const Cac
 // head.  Tile slots of request r start at cu[r] / 64 + 2 r; at most floor(len / 64) + 2 are used.
 constexpr int kStrip = 16;
 constexpr int kTile = kStrip * kWarps;
-// Up to this many positions a tile adds up the log gates before it by itself; for longer
-// appends gate_sums_kernel adds up every tile first.
+// Up to this many positions a tile adds up the log gates before it by itself; for longer appends
+// the kernel that writes the rows adds up every tile, and the gates are a kernel behind it.  8
+// requests of 256 rows: 7.3 us alone, 5.4 with the sums; of 128: 6.2 and 5.0, but a second launch
+// costs the host 5.
 constexpr int kDirectRows = 128;
 
 struct GateStrip {
@@ -345,12 +347,10 @@ __device__ __forceinline__ void load_log_gates(const CacheParams& p, const GateS
   }
 }
 
-// Sum of every tile's log gates, [tile slot][hq].
-__global__ void __launch_bounds__(kThreads) gate_sums_kernel(const CacheParams p) {
-  __shared__ float sums[kWarps][32];
+// The sum of a tile's log gates, to p.tile_sums [tile slot][hq].
+__device__ __forceinline__ void sum_gates(const CacheParams& p, int slot, int hgroup, float (*sums)[32]) {
   GateStrip g;
-  grid_release();
-  if (!gate_strip(p, blockIdx.x, blockIdx.y, g)) return;
+  if (!gate_strip(p, slot, hgroup, g)) return;
   float v[kStrip], sum = 0.f;
   load_log_gates(p, g, v);
 #pragma unroll
@@ -362,12 +362,13 @@ __global__ void __launch_bounds__(kThreads) gate_sums_kernel(const CacheParams p
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) sum += sums[i][lane];
-    p.tile_sums[(size_t)blockIdx.x * p.hq + g.h] = sum;
+    p.tile_sums[(size_t)slot * p.hq + g.h] = sum;
   }
 }
 
-// A tile is all latency, so its loads go out together: the table's entries and the log gates, then the
-// gate to continue from, and last, behind the wait, the sums of the tiles before.
+// Writes a tile's gates.  It is all latency, so its loads go out together: the table's entries and the
+// log gates, then the gate to continue from, and last, behind the wait for the kernel that sums the
+// tiles, the sums of the tiles before.
 __device__ __forceinline__ void write_gates(const CacheParams& p, int slot, int hgroup, float (*sums)[kWarps][32]) {
   GateStrip g;
   if (!gate_strip(p, slot, hgroup, g)) return;
@@ -387,7 +388,7 @@ __device__ __forceinline__ void write_gates(const CacheParams& p, int slot, int 
   // the rows of the request before this tile, split over the warps
   float before = 0.f;
   if (p.tile_sums) {
-    grid_wait();  // for gate_sums_kernel
+    grid_wait();
     const float* ts = p.tile_sums + (size_t)(slot - g.tile) * p.hq + h;
 #pragma unroll 16
     for (int j = warp; j < g.tile; j += kWarps) before += __ldcg(ts + (size_t)j * p.hq);
@@ -580,11 +581,18 @@ __device__ __forceinline__ void append_rows(const CacheParams& p, const RopePara
     append_keys_values<D, FMT, ROPE>(p, q, run, run.seg - q_segs, ring);
 }
 
-// Rows in the last row_blocks blocks; gate tiles in all of them, from the first on.  Few of both run
-// side by side; where a block has both, its rows come first, so that they overlap gate_sums_kernel,
-// which only the tiles wait for.
+// Blocks of an SM; beyond 152 SMs full, warps take longer runs of tokens.  Four chunks of 1024 with the
+// rotation 28 us with 4, 34 with 5 (spills); prompts of 36K tokens without it 42 with 4, 39 with 5.
 template <bool ROPE>
-constexpr int kAppendBlocks = ROPE ? 4 : 5;  // of an SM: beyond 152 SMs full, warps take longer runs of tokens
+constexpr int kAppendBlocks = ROPE ? 4 : 5;
+
+// Rows in the last row_blocks blocks; gate tiles (their sums alone, with p.tile_sums) in all of
+// them, from the first on: few of both run side by side.
+//
+// The rows are bound by HBM as far as the warps can issue: a step of 4 keys and 4 values of 128 is
+// 3 KB of traffic and about 330 instructions.  Prompts of 36K tokens and 8 kv heads (231 MB) take
+// 39 us, 5.9 TB/s, 87% of the measured copy rate, and 8 us more with the gates of 32 heads (10 MB), which
+// are latency: two rounds over the tiles, of which only the first overlaps the rows.
 template <int D, int FMT, bool ROPE>
 __global__ void __launch_bounds__(kThreads, kAppendBlocks<ROPE>)
     cache_append_kernel(const CacheParams p, const RopeParams q) {
@@ -592,12 +600,27 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks<ROPE>)
     AppendStage<D> ring[kWarps][2];
     float sums[2][kWarps][32];
   } sm;
-  append_rows<D, FMT, ROPE>(p, q, sm.ring[threadIdx.x >> 5]);
-  for (int i = blockIdx.x; i < p.n_gate; i += gridDim.x) {
-    __syncthreads();
-    write_gates(p, i / p.gate_groups, i % p.gate_groups, sm.sums);
+  if (p.tile_sums) {
+    grid_release();
+    for (int i = blockIdx.x; i < p.n_gate; i += gridDim.x) {
+      sum_gates(p, i / p.gate_groups, i % p.gate_groups, sm.sums[0]);
+      __syncthreads();
+    }
   }
-  if (p.tile_sums) grid_wait();  // the call ends when both of its kernels have
+  append_rows<D, FMT, ROPE>(p, q, sm.ring[threadIdx.x >> 5]);
+  if (!p.tile_sums) {
+    for (int i = blockIdx.x; i < p.n_gate; i += gridDim.x) {
+      __syncthreads();
+      write_gates(p, i / p.gate_groups, i % p.gate_groups, sm.sums);
+    }
+  }
+}
+
+// Behind the kernel with the tile sums.
+__global__ void __launch_bounds__(kThreads) gate_tiles_kernel(const CacheParams p) {
+  __shared__ float sums[2][kWarps][32];
+  write_gates(p, blockIdx.x, blockIdx.y, sums);
+  grid_wait();  // the call ends when both of its kernels have
 }
 
 // ------------------------------------------------------------------------- gather
@@ -618,6 +641,11 @@ __device__ __forceinline__ uint2 from_e4m3x4(uint32_t code, float scale) {
 
 // The codes (or bf16 elements) and scales of a warp's steps ahead; codes and scales are copied and
 // read by the same lane.
+//
+// Bound by the load / store unit more than by HBM: each of a lane's 8 codes are an 8-byte copy, an
+// 8-byte read and a 16-byte store.  82K tokens of 4 kv heads of 128 (188 MB) take 34 us, 5.5 TB/s, 81%
+// of the measured copy rate.  (16 neighbouring codes a lane with 32-byte stores 36 us, with two
+// 16-byte stores 40; 2, 3 and 6 stages ahead the same.)
 constexpr int kGatherStages = 4;
 template <int FMT>
 struct alignas(16) GatherStage {
@@ -724,14 +752,10 @@ cudaError_t append(CacheParams p, const RopeParams& q, cudaStream_t s) {
   const int segs = (ROPE ? (p.hq + 2 * R - 1) / (2 * R) : 0) + (p.hkv + R - 1) / R;
   const int blocks = plan(p, p.log_gate != nullptr, segs, 152 * kAppendBlocks<ROPE>);
   p.log2_step = log2_step<R>(p, 152 * kAppendBlocks<ROPE> / segs);
-  if (p.tile_sums) {
-    gate_sums_kernel<<<dim3(p.n_gate / p.gate_groups, p.gate_groups), kThreads, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_behind(cache_append_kernel<D, FMT, ROPE>, blocks, kThreads, s, p, q);
-  }
   cache_append_kernel<D, FMT, ROPE><<<blocks, kThreads, 0, s>>>(p, q);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.tile_sums) return e;
+  return launch_behind(gate_tiles_kernel, dim3(p.n_gate / p.gate_groups, p.gate_groups), kThreads, s, p);
 }
 template <int D, int FMT>
 cudaError_t append(const CacheParams& p, const RopeParams* q, cudaStream_t s) {

@@ -324,7 +324,8 @@ int attn_qk_norm_rope_fwd(const gcs_qk_rope_args* a, void* q_out, void* k_out, g
  * not wanted, and must be NULL when its weight is NULL).  Reads the forward's q and k (with
  * norm = 0 they are not read).  Every gradient is summed in a fixed order, so repeated calls
  * give the same bits.  The workspace (256-byte aligned) holds the blocks' parts of the weights'
- * gradients; none is needed when neither is wanted. */
+ * gradients; none is needed when neither is wanted.  Calls that may run at the same time (two
+ * streams, two graphs) need one each. */
 size_t attn_qk_norm_rope_bwd_workspace(const gcs_qk_rope_args* a);
 int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const void* dk_out, void* dq, void* dk,
                           float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
@@ -338,8 +339,10 @@ int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const v
  * from cu_rows[num_reqs] on (a padded batch) are left out.
  *   fp8, per token:  scale = max|x| / 448 over the d elements of (token, kv head), written to
  *                    k_scale / v_scale; code = e4m3(x / scale), nearest even.  A row of zeros
- *                    has scale 0 and codes 0.  An infinity gives scale inf, a NaN scale NaN.
- *   fp8, per tensor: code = e4m3(x / scale) saturating at +-448, with the caller's scale (read).
+ *                    has scale 0 and codes 0.  An infinity gives scale inf, a NaN scale NaN
+ *                    (and the row reads back as NaN).
+ *   fp8, per tensor: code = e4m3(x / scale) saturating at +-448, with the caller's scale (read;
+ *                    codes 0 where it is not above 0).
  *   bf16:            the elements.
  *   gates:           g_cache at p = (g_cache at p - 1, or 0 before the first) + log_gate, in fp32,
  *                    running on through the request's rows.
@@ -373,7 +376,8 @@ typedef struct {
   gcs_strides k_stride, v_stride;  /* layouts of the packed k and v                       */
 } gcs_cache_args;
 
-/* Workspace bytes of the two append calls (0 without g_cache and for short appends). */
+/* Workspace bytes of the two append calls (256-byte aligned; 0 without g_cache and for short
+ * appends).  Calls that may run at the same time (two streams, two graphs) need one each. */
 size_t attn_cache_append_workspace(const gcs_cache_args* a);
 
 /* Write k, v (bf16 [total_rows, hkv, d]) and, with g_cache, log_gate (fp32 [total_rows, hq]; NULL

@@ -358,6 +358,40 @@ def test_strided_rows(gcs_lib):
     assert torch.equal(k, want[0]) and torch.equal(v, want[1]) and bool((out[:, 2] == 3.0).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("nhd", [False, True])
+def test_offsets_beyond_32_bits(gcs_lib, nhd):
+    """Caches of 5 GB each (and scales and gates at the same blocks), rows at both ends and past 2^31
+    and 2^32 bytes."""
+    hkv, d, bs, hq = 8, 128, 16, 8
+    nb = (5 << 30) // (hkv * d * bs)
+    shape = (nb, bs, hkv, d) if nhd else (nb, hkv, bs, d)
+    kc, vc = (torch.empty(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    if nhd:
+        kc, vc = kc.permute(0, 2, 1, 3), vc.permute(0, 2, 1, 3)
+    ks, vs = (torch.empty((nb, hkv, bs), device="cuda") for _ in range(2))
+    g = torch.empty((nb, hq, bs), device="cuda")
+    at = [0, nb - 1, (1 << 31) // (hkv * d * bs), (1 << 32) // (hkv * d * bs) - 1, (1 << 32) // (hkv * d * bs) + 1]
+    lens, rows = [16 * len(at), 7], [16 * len(at), 7]
+    bt = torch.tensor([at, [nb - 2] * len(at)], dtype=torch.int32, device="cuda")
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, rows[0], sum(rows)], dtype=torch.int32, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(1)
+    k, v = (torch.randn((sum(rows), hkv, d), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    lg = -torch.rand((sum(rows), hq), generator=gen, device="cuda")
+    gcs_lib.attn_cache_append(k, v, kc, vc, ks, vs, bt, sl, cu, max(rows), lg, g)
+    got = gcs_lib.attn_cache_gather(kc, vc, ks, vs, bt, sl, cu, sum(rows), g)
+    assert gcs_lib.get_device_status() == 0
+    # the same rows through a small cache
+    small = dict(kc=torch.empty((8, hkv, bs, d), dtype=torch.uint8, device="cuda"), ks=torch.empty((8, hkv, bs), device="cuda"))
+    small.update(vc=torch.empty_like(small["kc"]), vs=torch.empty_like(small["ks"]), g=torch.empty((8, hq, bs), device="cuda"))
+    bt2 = torch.tensor([[0, 1, 2, 3, 4], [5] * 5], dtype=torch.int32, device="cuda")
+    gcs_lib.attn_cache_append(k, v, small["kc"], small["vc"], small["ks"], small["vs"], bt2, sl, cu, max(rows), lg, small["g"])
+    want = gcs_lib.attn_cache_gather(small["kc"], small["vc"], small["ks"], small["vs"], bt2, sl, cu, sum(rows), small["g"])
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert torch.equal(kc[at], small["kc"][:5]) and torch.equal(vs[at], small["vs"][:5]) and torch.equal(g[at], small["g"][:5])
+
+
 # ------------------------------------------------------------------------------ with norm and rotation
 ROPE = [(fmt, d, rot, inter, explicit) for fmt, d, rot, inter, explicit in (
     ("token", 128, 128, False, False), ("token", 64, 32, True, True), ("tensor", 256, 256, False, False),

@@ -135,6 +135,25 @@ def test_many_tokens_share_a_warp(gcs_lib):
 
 
 @pytest.mark.gpu
+def test_more_than_2_31_elements(gcs_lib):
+    """Tensors of 4.5 GB: the last tokens give the same bits as a call of their own."""
+    n, hq, d = 140000, 128, 128
+    q = torch.empty((n, hq, d), dtype=torch.bfloat16, device="cuda")
+    c = make(40, hq, 1, d, d, seed=21)
+    q[-40:] = c["q"]
+    q[:-40] = c["q"][:1]
+    k, pos = c["k"][:1].repeat(n, 1, 1), torch.zeros(n, dtype=torch.int32, device="cuda")
+    k[-40:], pos[-40:] = c["k"], c["pos"]
+    big, _ = gcs_lib.attn_qk_norm_rope_fwd(q, k, c["tab"], pos, c["qw"], c["kw"])
+    (ref, _), (gref, *_) = run(gcs_lib, c)
+    assert torch.equal(big[-40:], ref)
+    big[:-40], big[-40:] = c["dq"][:1], c["dq"]
+    dq, dk, _, _ = gcs_lib.attn_qk_norm_rope_bwd(big, k, q, k, c["tab"], pos, c["qw"], c["kw"])
+    assert gcs_lib.get_device_status() == 0
+    assert torch.equal(dq[-40:], gref) and bool(torch.isfinite(dk).all())
+
+
+@pytest.mark.gpu
 def test_only_one_weight(gcs_lib):
     c = make(9, 4, 2, 64, 64, seed=7)
     c["kw"] = None
