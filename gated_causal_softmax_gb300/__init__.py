@@ -604,7 +604,10 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, k_scale, v_scale, block_table
 # These calls run once a layer in a decoding step, where the host's time is what counts, so every
 # tensor is looked at once: type, shape, device and layout in one test, the reason only if it fails.
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
-_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(dev).cuda_stream without the object
+# torch.cuda.current_device() and torch.cuda.current_stream(dev).cuda_stream, without the set-up that a
+# CUDA tensor's existence already proves
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:
@@ -672,7 +675,7 @@ def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_w
     fp32 [d] or None (ones); cos_sin fp32 [max_pos, rotary_dim] (cosines, then sines) or None (no
     rotation); positions int32 [tot], negative = padding (outputs left as they were).
     norm=False: rotation only.  Returns q_out, k_out."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if q_out is None:
         q_out = _new(q)
     if k_out is None:
@@ -691,7 +694,7 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_
     rest its arguments.  Returns dq, dk (bf16) and dq_weight, dk_weight (fp32 [d]; None without
     the weight)."""
     L = load()
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if dq is None:
         dq = _new(q)
     if dk is None:
@@ -723,6 +726,12 @@ def _workspace(workspace, need: int, dev: int):
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {dev}")
     return workspace, workspace.numel() * workspace.element_size()
+
+
+def _append_workspace(L, a, workspace, max_q_len, dev: int):
+    # a decoding step's few rows never need one
+    need = 0 if workspace is not None or a.g_cache is None or max_q_len <= 16 else L.attn_cache_append_workspace(a)
+    return _workspace(workspace, need, dev)
 
 
 def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq, g_cache,
@@ -787,7 +796,7 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     the arrays that attn_decode_paged and attn_prefill_paged take.  A per-token fp8 cache gets its
     scales written, a per-tensor one is quantised with the given scales."""
     L = load()
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     shape = _packed_shape(k, k_cache)
     kp, ks = _rows(k, "k", shape, dev)
     vp, vs = _rows(v, "v", shape, dev)
@@ -795,7 +804,7 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev, ks,
                    vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
-    ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
+    ws, ws_bytes = _append_workspace(L, a, workspace, max_q_len, dev)
     _check(L.attn_cache_append(a, kp, vp, lg, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append")
 
 
@@ -806,7 +815,7 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     q, and writes the normed and rotated k (quantised without a rounding to bf16 in between) and
     v into the cache.  positions None: the cached positions."""
     L = load()
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     shape = _packed_shape(q, k_cache)
     if q_out is None:
         q_out = _new(q)
@@ -817,7 +826,7 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev, (0, 0),
                    vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, hq), dev)
-    ws, ws_bytes = _workspace(workspace, L.attn_cache_append_workspace(a) if g_cache is not None else 0, dev)
+    ws, ws_bytes = _append_workspace(L, a, workspace, max_q_len, dev)
     _check(L.attn_cache_append_rope(a, r, vp, lg, qp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append_rope")
     return q_out
 
@@ -828,7 +837,7 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     request back into packed k, v bf16 [total_rows, hkv, d] and, with g_cache, log_gate fp32
     [total_rows, hq] (the differences of the cumulative gates): what attn_fwd takes.  total_rows
     is cu_rows's last entry on the host.  Returns k, v, log_gate (None without g_cache)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if k_cache is None or k_cache.dim() != 4:
         raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
     n = max(0, int(total_rows))

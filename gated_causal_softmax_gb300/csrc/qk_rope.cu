@@ -231,24 +231,27 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
   }
 }
 
-// dw of 32 columns a block: 32 threads a column add every 32nd block's part, then their sums.
-__global__ void __launch_bounds__(1024) weight_grad_kernel(const float* partials, int blocks, int d,
-                                                           float* dq_weight, float* dk_weight) {
-  __shared__ float sm[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+// dw of 16 columns a block: 64 threads a column add every 64th block's part, then their sums.
+constexpr int kGradCols = 16, kGradRows = 64;
+__global__ void __launch_bounds__(kGradCols * kGradRows) weight_grad_kernel(const float* partials, int blocks, int d,
+                                                                             float* dq_weight, float* dk_weight) {
+  __shared__ float sm[kGradRows][kGradCols + 1];
+  const int x = threadIdx.x % kGradCols, y = threadIdx.x / kGradCols;
   float sum = 0.f;
   grid_wait();
-#pragma unroll 8
-  for (int b = threadIdx.y; b < blocks; b += 32) sum += __ldcg(partials + (size_t)b * 2 * d + c);
-  sm[threadIdx.y][threadIdx.x] = sum;
+#pragma unroll 5
+  for (int b = y; b < blocks; b += kGradRows) sum += __ldcg(partials + (size_t)b * 2 * d + blockIdx.x * kGradCols + x);
+  sm[y][x] = sum;
   __syncthreads();
-  float x = sm[threadIdx.x][threadIdx.y];
+  const int lane = threadIdx.x & 31, c = threadIdx.x >> 5;  // a warp a column
+  if (c >= kGradCols) return;
+  sum = sm[lane][c] + sm[lane + 32][c];
 #pragma unroll
-  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kFullMask, x, off);
-  if (threadIdx.x == 0) {
-    const int col = blockIdx.x * 32 + threadIdx.y;
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
+  if (lane == 0) {
+    const int col = blockIdx.x * kGradCols + c;
     float* dst = col < d ? dq_weight : dk_weight;
-    if (dst) dst[col < d ? col : col - d] = x;
+    if (dst) dst[col < d ? col : col - d] = sum;
   }
 }
 
@@ -268,7 +271,7 @@ cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStr
   norm_rope_bwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partials) return e;
-  return launch_behind(weight_grad_kernel, 2 * D / 32, dim3(32, 32), s, p.partials, blocks, D, dq_weight, dk_weight);
+  return launch_behind(weight_grad_kernel, 2 * D / kGradCols, kGradCols * kGradRows, s, p.partials, blocks, D, dq_weight, dk_weight);
 }
 
 }  // namespace

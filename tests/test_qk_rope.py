@@ -462,7 +462,7 @@ class OnGpu:
 def test_binding_refuses_host_tensors_and_wrong_shapes(monkeypatch):
     import gated_causal_softmax_gb300 as gcs
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(gcs, "_current_device", lambda: 0)
     c = make(4, 2, 1, 64, 64, seed=0, dev="cpu")
     with pytest.raises(ValueError, match="CUDA"):
         gcs.attn_qk_norm_rope_fwd(c["q"], c["k"], c["tab"], c["pos"], c["qw"], c["kw"])
