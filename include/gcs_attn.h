@@ -349,9 +349,10 @@ int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const v
  * Slots outside the rows' positions are not touched.
  * Preconditions: no two rows share a slot (blocks that are written belong to one request), and
  * cu_rows is sorted from 0.  A row whose position or block-table entry lies outside the cache
- * (0 <= p < max_blocks_per_req * block_size, entry in [0, num_blocks)) is left out, as are the
- * gates of a request whose preceding cached gate lies outside, and GCS_ERR_INVALID_ARG is recorded
- * in the device status word: in every mode; checked mode adds nothing to these calls.
+ * (0 <= p < max_blocks_per_req * block_size, entry in [0, num_blocks)) is left out, and
+ * GCS_ERR_INVALID_ARG is recorded in the device status word: in every mode; checked mode adds nothing
+ * to these calls.  So are the gates of a request with any position outside, and those that have no
+ * cached gate inside to continue from.
  * Supported: d 64, 128, 256 or 512; any hq, hkv with hq % hkv == 0; block_size 16 x 2^k, 16..4096;
  * the cache strides of gcs_decode_args.  K and V may interleave within one buffer (block by block,
  * slot by slot or head by head) as long as no byte belongs to both. */

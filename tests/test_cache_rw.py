@@ -122,7 +122,7 @@ def check_written(c, cache, scale, x, before_cache, before_scale):
                 assert np.array_equal(gs[blk, h, slot], sc, equal_nan=True), (t, h)
             else:
                 with np.errstate(all="ignore"):
-                    want = oracle.e4m3_round(row / gs[0])
+                    want = oracle.e4m3_round(row / gs[0]) if gs[0] > 0 else np.zeros(c.d)
             assert np.array_equal(oracle.e4m3_decode(got[blk, h, slot]), want, equal_nan=True), (t, h)
     if got.dtype == np.uint8:
         assert np.array_equal(got[~touched], want_other[~touched])
@@ -131,7 +131,7 @@ def check_written(c, cache, scale, x, before_cache, before_scale):
     if c.fmt == "token":
         assert np.array_equal(gs[~touched], before_scale.cpu().numpy()[~touched])
     elif c.fmt == "tensor":
-        assert np.array_equal(gs, before_scale.cpu().numpy())
+        assert np.array_equal(gs, before_scale.cpu().numpy(), equal_nan=True)
 
 
 def check_gates(c, before):
@@ -184,6 +184,7 @@ SHAPES = [
     dict(rows=[130, 31], lens=[130, 95], hq=48, hkv=3, d=128, block=32),
     dict(rows=[70], lens=[4200], hq=4, hkv=2, d=256, block=64),
     dict(rows=[17, 64], lens=[40, 64], hq=33, hkv=11, d=512, block=128, pad=1),
+    dict(rows=[20, 3], lens=[4100, 8], hq=2, hkv=1, d=64, block=4096),
 ]
 
 
@@ -313,6 +314,50 @@ def test_rows_of_zeros_nan_and_infinity(gcs_lib):
             assert bool(torch.isnan(k[3, 0]).all())  # 0 * inf, NaN * inf
         # their neighbours are whole
         assert bool(torch.isfinite(k[2, 0]).all()) and bool(torch.isfinite(k[3, 1]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.0, -1.0, float("nan"), float("inf"), 1e-30, 1e30, 3e38, 1e-42])
+def test_odd_scales_of_a_cache(gcs_lib, scale):
+    """A caller's scale that is not above 0 gives codes 0; the ends of the range divide."""
+    c = Cache([9], [9], 2, 2, 64, fmt="tensor", gates=False, seed=16)
+    c.ks.fill_(scale)
+    c.vs.fill_(scale)
+    c.v = (c.v.float() * min(abs(scale), 1e30) if 0 < abs(scale) < 1e38 else c.v.float()).to(torch.bfloat16)
+    append_and_check(gcs_lib, c)
+
+
+@pytest.mark.gpu
+def test_checked_mode_adds_nothing(gcs_lib):
+    a, b = (Cache([200, 3], [260, 3], 8, 2, 128, seed=17) for _ in range(2))
+    append_and_check(gcs_lib, a)
+    gcs_lib.set_device_checks(True)
+    try:
+        append_and_check(gcs_lib, b)
+        assert all(torch.equal(x, y) for x, y in zip(a.gather(gcs_lib), b.gather(gcs_lib)))
+    finally:
+        gcs_lib.set_device_checks(False)
+    assert torch.equal(a.kc, b.kc) and torch.equal(a.g, b.g)
+
+
+@pytest.mark.gpu
+def test_more_heads_than_the_grid_has_warps(gcs_lib):
+    c = Cache([2, 1], [5, 1], 1, 1, 64, gates=False, seed=18)
+    n, hkv = 3, 45000
+    kc, vc = (torch.zeros((3, hkv, 16, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((3, hkv, 16), device="cuda") for _ in range(2))
+    bt = torch.tensor([[2], [0]], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((n, hkv, 64), device="cuda").to(torch.bfloat16) for _ in range(2))
+    tab = torch.from_numpy(table(8, 64)).cuda()
+    q = gcs_lib.attn_cache_append_rope(k, k, v, kc, vc, ks, vs, bt, c.idx["seq_lens"], c.dcu, 2, tab, norm=False)
+    back = gcs_lib.attn_cache_gather(kc, vc, ks, vs, bt, c.idx["seq_lens"], c.dcu, n)
+    assert gcs_lib.get_device_status() == 0
+    pos = torch.tensor([3, 4, 0], dtype=torch.int32, device="cuda")
+    want, _ = gcs_lib.attn_qk_norm_rope_fwd(k, k, tab, pos, norm=False)
+    assert torch.equal(q, want)
+    for x, y in ((back[0], want), (back[1], v)):  # one e4m3 step of each row's scale, and bf16's
+        err, amax = (x.float() - y.float()).abs(), y.float().abs().amax(-1, keepdim=True)
+        assert bool((err <= torch.maximum(2.0 ** -4 * y.float().abs(), amax / 448 * 2.0 ** -10) * 1.02 + 2.0 ** -7 * y.float().abs()).all())
 
 
 @pytest.mark.gpu
@@ -481,6 +526,31 @@ def test_bf16_append_rope_is_the_two_calls(gcs_lib):
     b.append(gcs_lib)
     for x, y in ((q, q2), (a.kc, b.kc), (a.vc, b.vc), (a.g, b.g)):
         assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["token", "bf16"])
+@pytest.mark.parametrize("norm,rotate", [(False, True), (True, False), (False, False)])
+def test_append_rope_in_parts(gcs_lib, fmt, norm, rotate):
+    """Rotation alone, norm alone, and neither (then it is the plain append and a copy)."""
+    c, e = (Cache([30, 2], [30, 50], 8, 2, 128, fmt=fmt, seed=27) for _ in range(2))
+    w, tab = rope_inputs(c, 128, 28)
+    if not norm:
+        w = [None, None]
+    q = gcs_lib.attn_cache_append_rope(c.q, c.k, c.v, c.kc, c.vc, c.ks, c.vs, c.idx["block_table"], c.idx["seq_lens"], c.dcu,
+                                       30, tab if rotate else None, None, w[0], w[1], norm=norm, log_gate=c.lg, g_cache=c.g)
+    pos = torch.tensor([p for _, _, p, _, _ in c.places()], dtype=torch.int32, device="cuda")
+    q2, e.k = gcs_lib.attn_qk_norm_rope_fwd(e.q, e.k, tab if rotate else None, pos, w[0], w[1], norm=norm)
+    assert torch.equal(q, q2)
+    if fmt == "bf16" or not (norm or rotate):
+        e.append(gcs_lib)
+        assert torch.equal(c.kc.contiguous().view(torch.uint8), e.kc.contiguous().view(torch.uint8))
+        assert torch.equal(c.vc.contiguous().view(torch.uint8), e.vc.contiguous().view(torch.uint8)) and torch.equal(c.g, e.g)
+    k, _, _ = c.gather(gcs_lib)
+    # at most half a step of e4m3 (of the value, or of its smallest steps) and bf16's own, twice
+    err, y = (k.float() - e.k.float()).abs(), e.k.float().abs()
+    assert bool((err <= torch.maximum(2.0 ** -4 * y, y.amax(-1, keepdim=True) / 448 * 2.0 ** -10) * 1.02 + 2.0 ** -7 * y).all())
+    assert gcs_lib.get_device_status() == 0
 
 
 @pytest.mark.gpu

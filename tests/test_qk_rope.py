@@ -224,6 +224,28 @@ def test_padding_and_positions_outside(gcs_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("norm", [True, False])
+def test_padding_without_a_rotation(gcs_lib, norm):
+    """Positions without a table only say which tokens are padding."""
+    c = make(20, 4, 2, 64, 0, seed=22, weights=norm)
+    c["pos"] = torch.full((20,), 10 ** 9, dtype=torch.int32, device="cuda")
+    c["pos"][3::5] = -1
+    out = [torch.full_like(c["q"], 3.0), torch.full_like(c["k"], 3.0)]
+    gcs_lib.attn_qk_norm_rope_fwd(c["q"], c["k"], None, c["pos"], c["qw"], c["kw"], norm=norm, q_out=out[0], k_out=out[1])
+    grads = gcs_lib.attn_qk_norm_rope_bwd(c["dq"], c["dk"], c["q"], c["k"], None, c["pos"], c["qw"], c["kw"], norm=norm)
+    assert gcs_lib.get_device_status() == 0
+    assert bool((out[0][3::5] == 3.0).all()) and bool((out[1][3::5] == 3.0).all())
+    check_fwd(out[0], c["q"], c["qw"], None, c["pos"], 1e-6, norm, False)
+    check_bwd(grads[0], grads[2], c["dq"], c["q"], c["qw"], None, c["pos"], 1e-6, norm, False)
+    check_bwd(grads[1], grads[3], c["dk"], c["k"], c["kw"], None, c["pos"], 1e-6, norm, False)
+
+
+@pytest.mark.gpu
+def test_more_heads_than_the_grid_has_warps(gcs_lib):
+    check_all(gcs_lib, make(2, 45000, 45000, 64, 64, seed=23))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 256])
 def test_strided_views(gcs_lib, d):
     """q and k as views of one projection, outputs as views of another buffer; bit-equal to the
