@@ -11,7 +11,7 @@
 // Both are bound by HBM: each element is read once (twice in the backward: x and dout) and
 // written once, all arithmetic in fp32 between one load and one rounding to bf16.  Forward of 8192
 // tokens of 40 heads of 128 (172 MB): 27.6 us, 6.2 TB/s, 92% of the measured copy rate; of 16384 of 36
-// heads of 512 (1.2 GB): 179 us, 100%.  Backward of the first (256 MB): 45.1 us, 84%, of which 2.5 are
+// heads of 512 (1.2 GB): 179 us, 100%.  Backward of the first (256 MB): 41.5 us, 91%, of which 2.5 are
 // the kernel that adds up the weights' gradients.
 #include <algorithm>
 
@@ -23,13 +23,14 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// Rows of a lane group in a step of the forward, and blocks of an SM: warps take further tokens beyond
+// Rows of a lane group in a step, and blocks of an SM: warps take further tokens beyond
 // 152 SMs full.  16384 x 36 heads of 512 forward: 179 us with 3, 193 with 4; 8192 x 40 of 128: 28.9 and
-// 27.6, 38 with 5 (spills); backward 47.0 with 3, 45.1 with 4.
-constexpr int kFwdRows = 2;
+// 27.6, 38 with 5 (spills).  Backward of the latter with 1 row: 47.0 with 3 blocks, 45.1 with 4; with 2
+// rows 41.5 with 3, 46.4 with 4 (spills).
+constexpr int kFwdRows = 2, kBwdRows = 2;
 template <int D>
 constexpr int kFwdBlocks = D == 512 ? 3 : 4;
-constexpr int kBwdBlocks = 4;
+constexpr int kBwdBlocks = 3;
 
 // A warp's share: heads [h0, h1) of the queries or of the keys, and every step-th token.
 struct Share {
@@ -38,7 +39,7 @@ struct Share {
   uint32_t t, step;
 };
 template <int H>  // heads of a share
-__device__ __forceinline__ bool warp_share(int total, int hq, int hkv, Share& s) {
+__device__ __forceinline__ bool warp_share(int hq, int hkv, Share& s) {
   const int q_segs = (hq + H - 1) / H, segs = q_segs + (hkv + H - 1) / H;
   const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
   s.step = warps / segs;
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<D>) norm_rope_fwd_kernel(
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows, U = kFwdRows;
   __shared__ WarpStage<D, U> ring[kWarps][2];
   Share s;
-  if (!warp_share<R * U>(p.total, p.hq, p.hkv, s)) return;
+  if (!warp_share<R * U>(p.hq, p.hkv, s)) return;
   const int sub = threadIdx.x & (L - 1), grp = (threadIdx.x & 31) / L;
   const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
   const uint16_t* in = BACK ? s.is_k ? p.k_out : p.q_out : s.is_k ? p.k : p.q;
@@ -148,17 +149,21 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<D>) norm_rope_fwd_kernel(
 template <int D>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const RopeParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
+  constexpr int U = kBwdRows;
+  using Stage = WarpStage<D, 2 * U>;
   __shared__ union {
-    WarpStage<D, 2> ring[kWarps][2];
-    float part[kWarps][D];  // after the last step
+    Stage ring[kWarps][2];
+    struct {
+      float dw[kWarps][D];
+      int of[kWarps];  // of the queries 0, the keys 1, none 2
+    } part;  // after the last step
   } sm;
-  __shared__ int part_is_k[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x & (L - 1), grp = lane / L;
   const RowRuns runs = row_runs<D>(sub, p.rotary_dim, p.interleaved);
   Share s;
   Row dw = zero_row();
-  const bool works = warp_share<R>(p.total, p.hq, p.hkv, s);
+  const bool works = warp_share<R * U>(p.hq, p.hkv, s);
   if (works) {
     const uint16_t* in = s.is_k ? p.k : p.q;
     const uint16_t* dout = s.is_k ? p.k_out : p.q_out;
@@ -167,38 +172,49 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
     const long long ots = s.is_k ? p.ko_ts : p.qo_ts, ohs = s.is_k ? p.ko_hs : p.qo_hs;
     const long long dts = s.is_k ? p.dk_ts : p.dq_ts, dhs = s.is_k ? p.dk_hs : p.dq_hs;
     const Row w = load_weights(s.is_k ? p.k_weight : p.q_weight, runs);
-    const bool valid = s.h0 + grp < s.h1;
-    const int h = valid ? s.h0 + grp : s.h0;
-    auto fetch = [&](WarpStage<D, 2>& st, uint32_t t) {
-      fetch_row(st, 0, dout + t * ots + h * ohs, runs, valid);
-      fetch_row(st, 1, in + t * its + h * ihs, runs, valid);
-    };
-    auto use = [&](const WarpStage<D, 2>& st, uint32_t t, bool used) {
-      Row gs[1] = {zero_row()}, &g = gs[0];
-      if (used) {
-        g = unpack_row(fetched_row(st, 0));
-        rotate_rows(gs, runs, read_angles<true>(st.angles[0], p.rotary_dim, runs), p.interleaved);
-        Row x = unpack_row(fetched_row(st, 1)), u;
-        float2 xx = both(0.f), ux = both(0.f);
+    auto fetch = [&](Stage& st, uint32_t t) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u.e[i] = mul2(g.e[i], w.e[i]);
-          xx = fma2(x.e[i], x.e[i], xx);
-          ux = fma2(u.e[i], x.e[i], ux);
-        }
-        float sums[2] = {xx.x + xx.y, ux.x + ux.y};
-        row_sums<L>(sums);
-        const float r = rsqrtf(fmaf(sums[0], 1.f / D, p.eps));
-        const float m = sums[1] * r * (1.f / D);  // mean(u x r)
-        const float2 r2 = both(r), m2 = both(-m * r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x.e[i] = mul2(x.e[i], r2);
-          dw.e[i] = fma2(g.e[i], x.e[i], dw.e[i]);
-          g.e[i] = fma2(x.e[i], m2, mul2(u.e[i], r2));
-        }
+      for (int n = 0; n < U; ++n) {
+        const int head = s.h0 + n * R + grp;
+        const bool valid = head < s.h1;
+        const int h = valid ? head : s.h0;
+        fetch_row(st, 2 * n, dout + t * ots + h * ohs, runs, valid);
+        fetch_row(st, 2 * n + 1, in + t * its + h * ihs, runs, valid);
       }
-      if (valid) store_row(dx + t * dts + h * dhs, runs, g);
+    };
+    auto use = [&](const Stage& st, uint32_t t, bool used) {
+      const Angles ang = read_angles<true>(st.angles[0], p.rotary_dim, runs);
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int h = s.h0 + n * R + grp;
+        const bool valid = h < s.h1;
+        Row gs[1] = {zero_row()}, &g = gs[0];
+        if (used) {
+          g = unpack_row(fetched_row(st, 2 * n));
+          rotate_rows(gs, runs, ang, p.interleaved);
+          Row x = unpack_row(fetched_row(st, 2 * n + 1)), u;
+          float2 xx = both(0.f), ux = both(0.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            u.e[i] = mul2(g.e[i], w.e[i]);
+            xx = fma2(x.e[i], x.e[i], xx);
+            ux = fma2(u.e[i], x.e[i], ux);
+          }
+          float sums[2] = {xx.x + xx.y, ux.x + ux.y};
+          row_sums<L>(sums);
+          // the idle lanes' rows of zeros would have r = inf with eps = 0, and be a NaN in the sum
+          const float r = valid ? rsqrtf(fmaf(sums[0], 1.f / D, p.eps)) : 0.f;
+          const float m = sums[1] * r * (1.f / D);  // mean(u x r)
+          const float2 r2 = both(r), m2 = both(-m * r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x.e[i] = mul2(x.e[i], r2);
+            dw.e[i] = fma2(g.e[i], x.e[i], dw.e[i]);
+            g.e[i] = fma2(x.e[i], m2, mul2(u.e[i], r2));
+          }
+        }
+        if (valid) store_row(dx + t * dts + h * dhs, runs, g);
+      }
     };
     for_tokens(p, s, sm.ring[warp], fetch, use);
   }
@@ -215,18 +231,18 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(con
   if (grp == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<float2*>(&sm.part[warp][runs.a + 2 * i]) = dw.e[i];
-      *reinterpret_cast<float2*>(&sm.part[warp][runs.b + 2 * i]) = dw.e[4 + i];
+      *reinterpret_cast<float2*>(&sm.part.dw[warp][runs.a + 2 * i]) = dw.e[i];
+      *reinterpret_cast<float2*>(&sm.part.dw[warp][runs.b + 2 * i]) = dw.e[4 + i];
     }
   }
-  if (lane == 0) part_is_k[warp] = works ? (s.is_k ? 1 : 0) : 2;
+  if (lane == 0) sm.part.of[warp] = works ? (s.is_k ? 1 : 0) : 2;
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-    const int is_k = c / D;
+    const int of = c / D;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i)
-      if (part_is_k[i] == is_k) sum += sm.part[i][c % D];
+      if (sm.part.of[i] == of) sum += sm.part.dw[i][c % D];
     p.partials[(size_t)blockIdx.x * 2 * D + c] = sum;
   }
 }
@@ -255,7 +271,9 @@ __global__ void __launch_bounds__(kGradCols * kGradRows) weight_grad_kernel(cons
   }
 }
 
-int bwd_blocks(const RopeParams& p) { return blocks_for(p.total, p.hq, p.hkv, 512 / p.d, 152 * kBwdBlocks); }
+int bwd_blocks(const RopeParams& p) {
+  return blocks_for(p.total, p.hq, p.hkv, 512 / p.d * kBwdRows, 152 * kBwdBlocks);
+}
 
 template <int D, bool BACK>
 cudaError_t fwd(const RopeParams& p, cudaStream_t s) {

@@ -128,6 +128,14 @@ def test_parts(gcs_lib, norm, weights, rot, eps):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,d", [(6, 3, 64), (5, 1, 128), (3, 1, 256)])
+def test_no_eps_with_idle_lanes(gcs_lib, hq, hkv, d):
+    """eps 0, weights, and head counts that leave lane groups without a row: only rows that there are
+    count in the weights' gradients."""
+    check_all(gcs_lib, make(11, hq, hkv, d, d, seed=24), eps=0.0)
+
+
+@pytest.mark.gpu
 def test_many_tokens_share_a_warp(gcs_lib):
     """More rows than the grid has warps: each warp goes through several tokens.  2048 tokens of 21
     shares of 4 heads give a warp at most 2048 * 21 / 4845 + 1 = 9 rows."""
