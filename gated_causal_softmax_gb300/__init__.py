@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -159,6 +160,8 @@ class QkRopeArgs(ctypes.Structure):
         ("dq_stride", Strides),
         ("dk_stride", Strides),
     ]
+    # the same fields in one call (a constructor with nested strides takes six times as long)
+    _pack = struct.Struct("@7if5PiP12q").pack
 
 
 class CacheArgs(ctypes.Structure):
@@ -188,6 +191,7 @@ class CacheArgs(ctypes.Structure):
         ("k_stride", Strides),
         ("v_stride", Strides),
     ]
+    _pack = struct.Struct("@iPiiPPi4P7iP7q").pack
 
 
 KV_FP8_E4M3, KV_BF16 = 0, 1
@@ -618,17 +622,17 @@ def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:
     raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
 
 
-def _vector(t, dtype, name: str, shape, dev: int) -> Optional[int]:
-    """Address of a contiguous tensor, None for None."""
+def _vector(t, dtype, name: str, shape, dev: int) -> int:
+    """Address of a contiguous tensor, 0 for None."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _refuse(t, dtype, name, shape, dev, False)
     return t.data_ptr()
 
 
 def _rows(t, name: str, shape, dev: int):
-    """(address, (token stride, head stride)) of a bf16 [tokens, heads, d] tensor.  A dimension of one
+    """(address, token stride, head stride) of a bf16 [tokens, heads, d] tensor.  A dimension of one
     element has no stride of its own, whatever torch says of it."""
     if t is None or t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
         _refuse(t, _BF16, name, shape, dev, True)
@@ -638,7 +642,7 @@ def _rows(t, name: str, shape, dev: int):
     n, heads, d = shape
     if heads == 1:
         head = d
-    return t.data_ptr(), (token if n > 1 else heads * head, head)
+    return t.data_ptr(), token if n > 1 else heads * head, head
 
 
 def _new(like):
@@ -646,26 +650,27 @@ def _new(like):
     return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int,
-                 *strides) -> QkRopeArgs:
-    """Marshals the arguments of the norm and rotation (rotary_dim is the table's width); strides:
-    those of q_out, k_out, dq and dk, as far as the call has them."""
+def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int, out=(0, 0),
+                 k_out=(0, 0), dq=(0, 0), dk=(0, 0)) -> QkRopeArgs:
+    """Marshals the arguments of the norm and rotation (rotary_dim is the table's width); the last
+    four: (token, head) strides of q_out, k_out, dq and dk."""
     if q is None or k is None or q.dim() != 3 or k.dim() != 3:
         raise ValueError("expected [tokens, heads, dim] tensors q and k")
     shape = q.shape
     n, hq, d = shape
     hkv = k.shape[1]
-    qp, qs = _rows(q, "q", shape, dev)
-    kp, ks = _rows(k, "k", (n, hkv, d), dev)
+    qp, q_token, q_head = _rows(q, "q", shape, dev)
+    kp, k_token, k_head = _rows(k, "k", (n, hkv, d), dev)
     max_pos = rot = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_pos, rotary_dim]")
         max_pos, rot = cos_sin.shape
-    return QkRopeArgs(n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, qp, kp,
-                      _vector(q_weight, _F32, "q_weight", (d,), dev), _vector(k_weight, _F32, "k_weight", (d,), dev),
-                      _vector(cos_sin, _F32, "cos_sin", (max_pos, rot), dev), max_pos,
-                      _vector(positions, _I32, "positions", (n,), dev), qs, ks, *strides)
+    return QkRopeArgs.from_buffer_copy(QkRopeArgs._pack(
+        n, hq, hkv, d, rot, 1 if interleaved else 0, 1 if norm else 0, eps, qp, kp,
+        _vector(q_weight, _F32, "q_weight", (d,), dev), _vector(k_weight, _F32, "k_weight", (d,), dev),
+        _vector(cos_sin, _F32, "cos_sin", (max_pos, rot), dev), max_pos,
+        _vector(positions, _I32, "positions", (n,), dev), q_token, q_head, k_token, k_head, *out, *k_out, *dq, *dk))
 
 
 def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
@@ -680,8 +685,8 @@ def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_w
         q_out = _new(q)
     if k_out is None:
         k_out = _new(k)
-    qp, qs = _rows(q_out, "q_out", q.shape, dev)
-    kp, ks = _rows(k_out, "k_out", k.shape, dev)
+    qp, *qs = _rows(q_out, "q_out", q.shape, dev)
+    kp, *ks = _rows(k_out, "k_out", k.shape, dev)
     a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs, ks)
     _check(load().attn_qk_norm_rope_fwd(a, qp, kp, _raw_stream(dev)), "attn_qk_norm_rope_fwd")
     return q_out, k_out
@@ -704,10 +709,10 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty_like(k_weight)
     qs, ks = q.shape, k.shape
-    gqp, gqs = _rows(dq_out, "dq_out", qs, dev)
-    gkp, gks = _rows(dk_out, "dk_out", ks, dev)
-    dqp, dqs = _rows(dq, "dq", qs, dev)
-    dkp, dks = _rows(dk, "dk", ks, dev)
+    gqp, *gqs = _rows(dq_out, "dq_out", qs, dev)
+    gkp, *gks = _rows(dk_out, "dk_out", ks, dev)
+    dqp, *dqs = _rows(dq, "dq", qs, dev)
+    dkp, *dks = _rows(dk, "dk", ks, dev)
     a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, gqs, gks, dqs, dks)
     w = (a.d,)
     ws, ws_bytes = _workspace(workspace, L.attn_qk_norm_rope_bwd_workspace(a), dev)
@@ -735,10 +740,10 @@ def _append_workspace(L, a, workspace, max_q_len, dev: int):
 
 
 def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq, g_cache,
-               dev: int, *strides) -> CacheArgs:
+               dev: int, k_stride=(0, 0), v_stride=(0, 0)) -> CacheArgs:
     """Marshals the arguments of the cache calls: the caches, scales and index arrays are those of
     decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes); hq None:
-    g_cache's heads; strides: those of the packed k and v."""
+    g_cache's heads; the last two: (token, head) strides of the packed k and v."""
     if k_cache is None or v_cache is None or k_cache.dim() != 4:
         raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
     shape, fmt, cs = k_cache.shape, k_cache.dtype, k_cache.stride()
@@ -752,7 +757,7 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
         if cs[3] != 1 or t.get_device() != dev:
             _refuse(t, fmt, name, shape, dev, True)
     nb, hkv, bs, d = shape
-    kv_format, scale_mode, ks, vs = KV_FP8_E4M3, SCALE_PER_TOKEN, None, None
+    kv_format, scale_mode, ks, vs = KV_FP8_E4M3, SCALE_PER_TOKEN, 0, 0
     if fmt is _BF16:
         kv_format = KV_BF16
         if k_scale is not None or v_scale is not None:
@@ -775,11 +780,12 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
         if g_cache.dim() != 3:
             raise ValueError("g_cache must be [num_blocks, num_q_heads, block_size]")
         hq = g_cache.shape[1]
-    return CacheArgs(num_reqs, _vector(cu_rows, _I32, "cu_rows", (num_reqs + 1,), dev), int(total_rows), int(max_rows),
-                     _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev),
-                     _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(),
-                     v_cache.data_ptr(), ks, vs, nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
-                     _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), cs[0], cs[1], cs[2], *strides)
+    return CacheArgs.from_buffer_copy(CacheArgs._pack(
+        num_reqs, _vector(cu_rows, _I32, "cu_rows", (num_reqs + 1,), dev), total_rows, max_rows,
+        _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev),
+        _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(),
+        v_cache.data_ptr(), ks, vs, nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
+        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), cs[0], cs[1], cs[2], *k_stride, *v_stride))
 
 
 def _packed_shape(rows, k_cache):
@@ -798,8 +804,8 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     L = load()
     dev = _current_device()
     shape = _packed_shape(k, k_cache)
-    kp, ks = _rows(k, "k", shape, dev)
-    vp, vs = _rows(v, "v", shape, dev)
+    kp, *ks = _rows(k, "k", shape, dev)
+    vp, *vs = _rows(v, "v", shape, dev)
     n = shape[0]
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev, ks,
                    vs)
@@ -819,10 +825,10 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     shape = _packed_shape(q, k_cache)
     if q_out is None:
         q_out = _new(q)
-    qp, qs = _rows(q_out, "q_out", q.shape, dev)
+    qp, *qs = _rows(q_out, "q_out", q.shape, dev)
     r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs)
     n, hq = shape[0], r.hq
-    vp, vs = _rows(v, "v", shape, dev)
+    vp, *vs = _rows(v, "v", shape, dev)
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev, (0, 0),
                    vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, hq), dev)
@@ -846,8 +852,8 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
         k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
     if v is None:
         v = _new(k)
-    kp, ks = _rows(k, "k", shape, dev)
-    vp, vs = _rows(v, "v", shape, dev)
+    kp, *ks = _rows(k, "k", shape, dev)
+    vp, *vs = _rows(v, "v", shape, dev)
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, n), None,
                    g_cache, dev, ks, vs)
     if g_cache is not None and log_gate is None:

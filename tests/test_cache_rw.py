@@ -866,6 +866,17 @@ def test_binding_refuses_wrong_shapes():
         return gcs.cache_args(*[kw[n] for n in ok], 5, 5, hq, None if g is None else OnGpu(g, dev.get("g", 0)), 0)
 
     assert call().num_blocks == 4 and call(g=torch.zeros(4, 4, 16)).hq == 4
+    # every field at its place
+    g = torch.zeros(4, 6, 16)
+    a = gcs.cache_args(*[OnGpu(t) for t in ok.values()], 5, 7, None, OnGpu(g), 0, (11, 12), (13, 14))
+    want = dict(num_reqs=3, total_rows=5, max_rows=7, max_blocks_per_req=2, num_blocks=4, block_size=16, hq=6, hkv=2, d=64,
+                kv_format=0, scale_mode=0, g_cache=g.data_ptr(), kv_stride_block=2048, kv_stride_head=1024,
+                kv_stride_slot=64, **{n: t.data_ptr() for n, t in ok.items()})
+    assert {n: getattr(a, n) for n in want} == want
+    assert [a.k_stride.token, a.k_stride.head, a.v_stride.token, a.v_stride.head] == [11, 12, 13, 14]
+    bf16 = [OnGpu(t.to(torch.bfloat16)) for t in (ok["k_cache"], ok["v_cache"])]
+    b = gcs.cache_args(*bf16, None, None, *[OnGpu(ok[n]) for n in ("block_table", "seq_lens", "cu_rows")], 5, 5, None, None, 0)
+    assert (b.kv_format, b.k_scale, b.v_scale, b.g_cache, b.hq) == (1, None, None, None, 2)
     for over in (dict(v_cache=torch.zeros(4, 2, 16, 128, dtype=torch.uint8)), dict(k_cache=torch.zeros(4, 2, 16, 64)),
                  dict(cu_rows=i32(3)), dict(block_table=i32(2, 2)), dict(seq_lens=torch.zeros(3)), dict(k_scale=None),
                  dict(g=torch.zeros(4, 4, 32)), dict(g=torch.zeros(4, 4, 16), hq=8), dict(g=torch.zeros(4, 4)),

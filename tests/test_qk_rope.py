@@ -502,6 +502,18 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(monkeypatch):
         return gcs.qk_rope_args(b["q"], b["k"], b["tab"], b["pos"], b["qw"], b["kw"], 1e-6, True, False, 0)
 
     assert call().rotary_dim == 64
+    # every field at its place
+    x = torch.zeros(4, 7, 64, dtype=torch.bfloat16)
+    a = gcs.qk_rope_args(OnGpu(x[:, :2]), OnGpu(x[:, 2:3]), OnGpu(c["tab"]), OnGpu(c["pos"]), OnGpu(c["qw"]), OnGpu(c["kw"]),
+                         0.25, False, True, 0, (1, 2), (3, 4), (5, 6), (7, 8))
+    want = dict(total_tokens=4, hq=2, hkv=1, d=64, rotary_dim=64, interleaved=1, norm=0, eps=0.25, q=x.data_ptr(),
+                k=x[:, 2:].data_ptr(), q_weight=c["qw"].data_ptr(), k_weight=c["kw"].data_ptr(),
+                cos_sin=c["tab"].data_ptr(), max_pos=64, positions=c["pos"].data_ptr())
+    assert {n: getattr(a, n) for n in want} == want
+    strides = [getattr(a, n + "_stride") for n in ("q", "k", "q_out", "k_out", "dq", "dk")]
+    assert [(t.token, t.head) for t in strides] == [(448, 64), (448, 64), (1, 2), (3, 4), (5, 6), (7, 8)]
+    none = gcs.qk_rope_args(OnGpu(x[:, :2]), OnGpu(x[:, 2:3]), None, None, None, None, 1e-6, True, False, 0)
+    assert [none.q_weight, none.k_weight, none.cos_sin, none.positions, none.rotary_dim] == [None] * 4 + [0]
     for over in (dict(k=c["k"][:3]), dict(k=c["k"][..., :32]), dict(qw=c["qw"][:32]), dict(pos=c["pos"][:3]),
                  dict(pos=c["pos"].long()), dict(q=c["q"].float()), dict(tab=c["tab"].double()), dict(tab=c["tab"][0]),
                  dict(q=c["q"].repeat(1, 1, 2)[..., ::2]), dict(q=None), dict(tab=c["tab"].repeat(1, 2)[:, ::2])):
