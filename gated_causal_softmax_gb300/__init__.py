@@ -610,8 +610,8 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, k_scale, v_scale, block_table
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 # torch.cuda.current_device() and torch.cuda.current_stream(dev).cuda_stream, without the set-up that a
 # CUDA tensor's existence already proves
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:

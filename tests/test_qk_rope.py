@@ -171,6 +171,27 @@ def test_only_one_weight(gcs_lib):
 
 
 @pytest.mark.gpu
+def test_weight_gradients_that_are_not_wanted(gcs_lib):
+    """Through the C ABI: either gradient, or both with the workspace, left out; the rest as ever."""
+    c = make(33, 6, 3, 128, 64, seed=25)
+    _, ref = run(gcs_lib, c)
+    L, stream = gcs_lib.load(), torch.cuda.current_stream().cuda_stream
+    a = gcs_lib.qk_rope_args(c["q"], c["k"], c["tab"], c["pos"], c["qw"], c["kw"], 1e-6, True, False, 0)
+    ws = torch.empty(L.attn_qk_norm_rope_bwd_workspace(ctypes.byref(a)), dtype=torch.uint8, device="cuda")
+    for want in ((True, False), (False, True), (False, False)):
+        got = [torch.full_like(x, 3.0) for x in ref]
+        w = [g.data_ptr() if on else None for g, on in zip(got[2:], want)]
+        assert L.attn_qk_norm_rope_bwd(ctypes.byref(a), c["dq"].data_ptr(), c["dk"].data_ptr(), got[0].data_ptr(),
+                                       got[1].data_ptr(), w[0], w[1], ws.data_ptr() if any(want) else None,
+                                       ws.numel() if any(want) else 0, stream) == 0
+        torch.cuda.synchronize()
+        assert gcs_lib.get_device_status() == 0
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+        for g, r, on in zip(got[2:], ref[2:], want):
+            assert torch.equal(g, r) if on else bool((g == 3.0).all())
+
+
+@pytest.mark.gpu
 def test_far_positions_come_from_the_table(gcs_lib):
     """A table of 300000 positions (an element offset beyond 2^25) and its last row."""
     c = make(5, 2, 1, 128, 128, seed=8)
