@@ -645,9 +645,16 @@ def _rows(t, name: str, shape, dev: int):
     return t.data_ptr(), token if n > 1 else heads * head, head
 
 
-def _new(like):
-    """An uninitialised contiguous tensor of the same shape, type and device."""
-    return torch.empty_like(like, memory_format=torch.contiguous_format)
+def _output(t, like, name: str, dev: int):
+    """An output shaped like the input `like`, the caller's or a new one: (tensor, address, strides)."""
+    if like is None or like.dim() != 3:
+        raise ValueError("expected [tokens, heads, dim] tensors")
+    if t is None:  # as good as `like`, which is checked as an input
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        _, heads, d = like.shape
+        return t, t.data_ptr(), (heads * d, d)
+    p, *strides = _rows(t, name, like.shape, dev)
+    return t, p, strides
 
 
 def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev: int, out=(0, 0),
@@ -681,12 +688,8 @@ def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_w
     rotation); positions int32 [tot], negative = padding (outputs left as they were).
     norm=False: rotation only.  Returns q_out, k_out."""
     dev = _current_device()
-    if q_out is None:
-        q_out = _new(q)
-    if k_out is None:
-        k_out = _new(k)
-    qp, *qs = _rows(q_out, "q_out", q.shape, dev)
-    kp, *ks = _rows(k_out, "k_out", k.shape, dev)
+    q_out, qp, qs = _output(q_out, q, "q_out", dev)
+    k_out, kp, ks = _output(k_out, k, "k_out", dev)
     a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs, ks)
     _check(load().attn_qk_norm_rope_fwd(a, qp, kp, _raw_stream(dev)), "attn_qk_norm_rope_fwd")
     return q_out, k_out
@@ -700,19 +703,14 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, cos_sin=None, positions=None, q_
     the weight)."""
     L = load()
     dev = _current_device()
-    if dq is None:
-        dq = _new(q)
-    if dk is None:
-        dk = _new(k)
+    dq, dqp, dqs = _output(dq, q, "dq", dev)
+    dk, dkp, dks = _output(dk, k, "dk", dev)
     if q_weight is not None and dq_weight is None:
         dq_weight = torch.empty_like(q_weight)
     if k_weight is not None and dk_weight is None:
         dk_weight = torch.empty_like(k_weight)
-    qs, ks = q.shape, k.shape
-    gqp, *gqs = _rows(dq_out, "dq_out", qs, dev)
-    gkp, *gks = _rows(dk_out, "dk_out", ks, dev)
-    dqp, *dqs = _rows(dq, "dq", qs, dev)
-    dkp, *dks = _rows(dk, "dk", ks, dev)
+    gqp, *gqs = _rows(dq_out, "dq_out", q.shape, dev)
+    gkp, *gks = _rows(dk_out, "dk_out", k.shape, dev)
     a = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, gqs, gks, dqs, dks)
     w = (a.d,)
     ws, ws_bytes = _workspace(workspace, L.attn_qk_norm_rope_bwd_workspace(a), dev)
@@ -807,8 +805,8 @@ def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq
     kp, *ks = _rows(k, "k", shape, dev)
     vp, *vs = _rows(v, "v", shape, dev)
     n = shape[0]
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev, ks,
-                   vs)
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, None, g_cache, dev,
+                   ks, vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
     ws, ws_bytes = _append_workspace(L, a, workspace, max_q_len, dev)
     _check(L.attn_cache_append(a, kp, vp, lg, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append")
@@ -823,14 +821,12 @@ def attn_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, block_ta
     L = load()
     dev = _current_device()
     shape = _packed_shape(q, k_cache)
-    if q_out is None:
-        q_out = _new(q)
-    qp, *qs = _rows(q_out, "q_out", q.shape, dev)
+    q_out, qp, qs = _output(q_out, q, "q_out", dev)
     r = qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interleaved, dev, qs)
     n, hq = shape[0], r.hq
     vp, *vs = _rows(v, "v", shape, dev)
-    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev, (0, 0),
-                   vs)
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, n, max_q_len, hq, g_cache, dev,
+                   (0, 0), vs)
     lg = _vector(log_gate, _F32, "log_gate", (n, hq), dev)
     ws, ws_bytes = _append_workspace(L, a, workspace, max_q_len, dev)
     _check(L.attn_cache_append_rope(a, r, vp, lg, qp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_append_rope")
@@ -851,7 +847,7 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     if k is None:
         k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
     if v is None:
-        v = _new(k)
+        v = torch.empty_like(k, memory_format=torch.contiguous_format)
     kp, *ks = _rows(k, "k", shape, dev)
     vp, *vs = _rows(v, "v", shape, dev)
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max(1, n), None,

@@ -450,7 +450,8 @@ __device__ __forceinline__ void read_gates(const CacheParams& p, int slot, int h
 #pragma unroll
   for (int i = 0; i < kStrip; ++i) {
     const long long pos = g.s0 + i;
-    if (pos >= g.p0 && pos < g.p1) p.log_gate_out[(size_t)(g.a + (pos - g.p0)) * p.hq + g.h] = v[i] - (i ? v[i - 1] : prev);
+    if (pos >= g.p0 && pos < g.p1)
+      p.log_gate_out[(size_t)(g.a + (pos - g.p0)) * p.hq + g.h] = v[i] - (i ? v[i - 1] : prev);
   }
 }
 
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(kThreads, kGatherBlocks) cache_gather_kernel(c
   const int lane = threadIdx.x & 31, sub = lane & (L - 1), h = run.seg * R + s.head;
   const bool has_head = h < p.hkv;
   const RowRuns runs = row_runs<D>(sub, 0, false);
-  const float ks = FMT == kCachePerTensor ? __ldg(p.k_scale) : 1.f, vs = FMT == kCachePerTensor ? __ldg(p.v_scale) : 1.f;
+  const float ks = FMT == kCachePerTensor ? __ldg(p.k_scale) : 1.f;
+  const float vs = FMT == kCachePerTensor ? __ldg(p.v_scale) : 1.f;
   Cursor cursor;
   uint32_t there = 0;  // bit i: this lane's row i steps back from the last fetched one is in the cache
   auto fetch = [&](Stage& st, int t) {

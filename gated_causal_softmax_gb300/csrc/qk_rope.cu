@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks<D>) norm_rope_fwd_kernel(
   for_tokens(p, s, ring[threadIdx.x >> 5], fetch, use);
 }
 
-// The backward with the norm, and the gradients of its weights: every lane sums g x r of its 16 elements over its rows, the
-// lanes of a block with the same elements are added in a fixed order, and the block writes its
-// part of d q_weight and d k_weight to p.partials [blocks][2][D]; weight_grad_kernel adds those.
+// The backward with the norm, and the gradients of its weights: every lane sums g x r of its 16
+// elements over its rows, the lanes of a block with the same elements are added in a fixed order, and
+// the block writes its part of d q_weight and d k_weight to p.partials [blocks][2][D];
+// weight_grad_kernel adds those.
 template <int D>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) norm_rope_bwd_kernel(const RopeParams p) {
   constexpr int L = RowLanes<D>::kLanes, R = RowLanes<D>::kRows;
@@ -289,7 +290,8 @@ cudaError_t bwd(const RopeParams& p, float* dq_weight, float* dk_weight, cudaStr
   norm_rope_bwd_kernel<D><<<blocks, kThreads, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.partials) return e;
-  return launch_behind(weight_grad_kernel, 2 * D / kGradCols, kGradCols * kGradRows, s, p.partials, blocks, D, dq_weight, dk_weight);
+  return launch_behind(weight_grad_kernel, 2 * D / kGradCols, kGradCols * kGradRows, s, p.partials, blocks, D,
+                       dq_weight, dk_weight);
 }
 
 }  // namespace

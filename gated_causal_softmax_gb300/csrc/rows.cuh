@@ -81,10 +81,11 @@ struct RawRow {
   uint4 a, b;
 };
 
-// The rows of a warp's next step, in shared memory: ROWS rows of every lane group and the table's
-// row of the step's token (or the rows of its tokens, at most one for each lane group).  Copies go in asynchronously a step ahead of their use (two and three
-// steps ahead measured the same, and slower at d = 512), so the bytes in flight do not depend on how
-// many registers the arithmetic leaves for occupancy.
+// The rows of a warp's next step, in shared memory: ROWS rows of every lane group and the table's row
+// of the step's token (or the rows of its tokens, at most one for each lane group).  Copies go in
+// asynchronously a step ahead of their use (two and three steps ahead measured the same, and slower at
+// d = 512), so the bytes in flight do not depend on how many registers the arithmetic leaves for
+// occupancy.
 template <int D, int ROWS, int TOKENS = 1>
 struct WarpStage {
   uint4 raw[ROWS][2][32];  // a lane's two runs of each row: read by the lane that copied them
@@ -243,7 +244,9 @@ __device__ __forceinline__ Angles read_angles(const float* row, int rot, const R
 template <int U>
 __device__ __forceinline__ void rotate_rows(Row (&x)[U], const RowRuns& r, const Angles& t, bool interleaved) {
   if (interleaved) {
-    auto turn = [](float2& p, float c, float s, float n) { p = make_float2(fmaf(p.y, n, p.x * c), fmaf(p.x, s, p.y * c)); };
+    auto turn = [](float2& p, float c, float s, float n) {
+      p = make_float2(fmaf(p.y, n, p.x * c), fmaf(p.x, s, p.y * c));
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i < 2 ? r.turn_a : r.turn_b) {

@@ -432,8 +432,8 @@ int gcs_selftest_bounded_wait(gcs_stream_t stream);
  * gcs_set_device_checks(1) turns on checked mode for every later call of this process (0
  * turns it off; other values return GCS_ERR_INVALID_ARG).  In checked mode each attention call
  * (attn_fwd, attn_bwd, attn_decode_paged, attn_prefill_paged) first launches one single-CTA
- * kernel on its stream that checks its arrays and writes a copy of cu_seqlens (or cu_q) to the end of the call's workspace; the call's kernels read that
- * copy.  When a check fails the copy is all zeros, an empty batch: no kernel then reads
+ * kernel on its stream that checks its arrays and writes a copy of cu_seqlens (or cu_q) to the
+ * end of the call's workspace; the call's kernels read that copy.  When a check fails the copy is all zeros, an empty batch: no kernel then reads
  * through an index taken from these arrays, so a broken array cannot send a kernel outside a
  * buffer.
  * The outputs of such a call are unspecified.  The copy takes ((num_seqs or num_reqs) + 1)

@@ -515,8 +515,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(monkeypatch):
 
     monkeypatch.setattr(gcs, "_current_device", lambda: 0)
     c = make(4, 2, 1, 64, 64, seed=0, dev="cpu")
-    with pytest.raises(ValueError, match="CUDA"):
+    with pytest.raises(ValueError, match="q must be a CUDA"):
         gcs.attn_qk_norm_rope_fwd(c["q"], c["k"], c["tab"], c["pos"], c["qw"], c["kw"])
+    for bad in (None, c["q"][0]):
+        with pytest.raises(ValueError, match="tokens, heads, dim"):
+            gcs.attn_qk_norm_rope_fwd(bad, c["k"], c["tab"], c["pos"], c["qw"], c["kw"])
+    with pytest.raises(ValueError, match="q_out must be a CUDA"):
+        gcs.attn_qk_norm_rope_fwd(c["q"], c["k"], c["tab"], c["pos"], c["qw"], c["kw"], q_out=c["q"])
 
     def call(dev={}, **over):
         b = {n: None if t is None else OnGpu(t, dev.get(n, 0)) for n, t in dict(c, **over).items()}
