@@ -622,6 +622,10 @@ def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:
     raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
 
 
+def _refuse_broadcast(name: str) -> None:
+    raise NotImplementedError(f"{name} is a broadcast view (its elements share memory), not a layout of the library")
+
+
 def _vector(t, dtype, name: str, shape, dev: int) -> int:
     """Address of a contiguous tensor, 0 for None."""
     if t is None:
@@ -642,6 +646,8 @@ def _rows(t, name: str, shape, dev: int):
     n, heads, d = shape
     if heads == 1:
         head = d
+    elif not head:
+        _refuse_broadcast(name)  # the pair (0, 0) would say "contiguous" to the library
     return t.data_ptr(), token if n > 1 else heads * head, head
 
 
@@ -683,10 +689,11 @@ def qk_rope_args(q, k, cos_sin, positions, q_weight, k_weight, eps, norm, interl
 def attn_qk_norm_rope_fwd(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6, norm=True,
                           interleaved=False, q_out=None, k_out=None):
     """RMS norm of every query and key head and rotation by position, one pass.  q bf16 [tot, hq,
-    d], k bf16 [tot, hkv, d] (last dim contiguous, e.g. views of a fused projection); weights
-    fp32 [d] or None (ones); cos_sin fp32 [max_pos, rotary_dim] (cosines, then sines) or None (no
-    rotation); positions int32 [tot], negative = padding (outputs left as they were).
-    norm=False: rotation only.  Returns q_out, k_out."""
+    d], k bf16 [tot, hkv, d] (last dim contiguous, e.g. views of a fused projection; broadcast
+    views are refused, here and in the calls below); weights fp32 [d] or None (ones); cos_sin
+    fp32 [max_pos, rotary_dim] (cosines, then sines) or None (no rotation); positions int32
+    [tot], negative = padding (outputs left as they were).  norm=False: rotation only.  Returns
+    q_out, k_out."""
     dev = _current_device()
     q_out, qp, qs = _output(q_out, q, "q_out", dev)
     k_out, kp, ks = _output(k_out, k, "k_out", dev)
@@ -754,6 +761,8 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if cs[3] != 1 or t.get_device() != dev:
             _refuse(t, fmt, name, shape, dev, True)
+    if not (cs[0] or cs[1] or cs[2]):  # would say "contiguous" to the library
+        _refuse_broadcast("k_cache")
     nb, hkv, bs, d = shape
     kv_format, scale_mode, ks, vs = KV_FP8_E4M3, SCALE_PER_TOKEN, 0, 0
     if fmt is _BF16:
