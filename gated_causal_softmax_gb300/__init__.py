@@ -322,7 +322,14 @@ def _st(t: Optional[torch.Tensor]) -> Strides:
         return Strides(0, 0)
     if t.dim() != 3:
         raise ValueError("expected a [tokens, heads, dim] tensor")
-    return Strides(t.stride(0), t.stride(1))
+    token, head = t.stride(0), t.stride(1)
+    if not (token or head) and (t.shape[0] > 1 or t.shape[1] > 1):
+        _refuse_broadcast("a [tokens, heads, dim] tensor")  # (0, 0) would say "contiguous" to the library
+    return Strides(token, head)
+
+
+def _refuse_broadcast(name: str) -> None:
+    raise NotImplementedError(f"{name} is a broadcast view (its elements share memory), not a layout of the library")
 
 
 def set_kernel_events(before: Optional[torch.cuda.Event], after: Optional[torch.cuda.Event]) -> None:
@@ -487,6 +494,8 @@ def decode_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu
         raise ValueError("k_cache and v_cache shapes differ")
     if k_cache.stride() != v_cache.stride():
         raise ValueError("k_cache and v_cache must share one layout")
+    if not any(k_cache.stride()[:3]):  # would say "contiguous" to the library
+        _refuse_broadcast("k_cache")
     nb, hkv, bs, d = k_cache.shape
     if k_cache.dtype == torch.bfloat16:
         _need(k_cache, torch.bfloat16, "k_cache", strided=True)
@@ -620,10 +629,6 @@ def _refuse(t, dtype, name: str, shape, dev: int, strided: bool) -> None:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     # the library launches on the current device's stream
     raise ValueError(f"{name} is on device {t.get_device()}, the current device is {dev}")
-
-
-def _refuse_broadcast(name: str) -> None:
-    raise NotImplementedError(f"{name} is a broadcast view (its elements share memory), not a layout of the library")
 
 
 def _vector(t, dtype, name: str, shape, dev: int) -> int:

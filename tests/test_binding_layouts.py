@@ -42,6 +42,7 @@ def binding(monkeypatch):
     monkeypatch.setattr(gcs, "load", lambda *a: lib)
     monkeypatch.setattr(gcs, "_current_device", lambda: 0)
     monkeypatch.setattr(gcs, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(gcs, "_stream", lambda: 0)
     return gcs
 
 
@@ -139,3 +140,53 @@ def test_partly_broadcast_rows_are_the_library_s_to_refuse():
     t = torch.zeros(8, 1, 64, dtype=BF16).expand(8, 4, 64)  # heads broadcast: the binding refuses it by name
     with pytest.raises(NotImplementedError, match="x"):
         gcs._rows(OnGpu(t), "x", t.shape, 0)
+
+
+# ------------------------------------------------------------------------------ the attention calls
+# (the attention's marshalling passes a stride of its own for one token or head on to the library, which
+# refuses those that are no layout)
+ZEROS = {"all": broadcast(8, 4, 64), **{name: torch.as_strided(torch.zeros(64, dtype=BF16), shape, (0, 0, 1))
+                                       for name, shape in (("heads_of_one_token", (1, 4, 64)), ("tokens_of_one_head", (8, 1, 64)))}}
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "out"])
+@pytest.mark.parametrize("bad", ZEROS.values(), ids=ZEROS)
+def test_prefill_refuses_broadcast_rows(binding, bad, which):
+    n, heads, _ = bad.shape
+    kw = {x: rows(n, heads) for x in ("q", "k", "v", "out")}
+    kw[which] = OnGpu(bad)
+    with pytest.raises(NotImplementedError, match="broadcast"):
+        binding.attn_fwd(cu_seqlens=OnGpu(torch.zeros(2, dtype=torch.int32)), max_seqlen=n, lse=OnGpu(torch.zeros(heads, n)),
+                         **kw)
+
+
+@pytest.mark.parametrize("which", ["q", "k", "v", "o", "dout", "dq", "dk", "dv"])
+@pytest.mark.parametrize("bad", ZEROS.values(), ids=ZEROS)
+def test_prefill_backward_refuses_broadcast_rows(binding, bad, which):
+    n, heads, _ = bad.shape
+    kw = {x: rows(n, heads) for x in ("q", "k", "v", "o", "dout", "dq", "dk", "dv")}
+    kw[which] = OnGpu(bad)
+    with pytest.raises(NotImplementedError, match="broadcast"):
+        binding.attn_bwd(cu_seqlens=OnGpu(torch.zeros(2, dtype=torch.int32)), max_seqlen=n, lse=OnGpu(torch.zeros(heads, n)),
+                         workspace=OnGpu(torch.zeros(256, dtype=torch.uint8)), **kw)
+
+
+@pytest.mark.parametrize("which", ["q", "out", "cache"])
+@pytest.mark.parametrize("call", ["attn_decode_paged", "attn_prefill_paged", "attn_decode_paged_noalloc"])
+def test_paged_calls_refuse_broadcast_rows_and_caches(binding, call, which):
+    kw = paged(*(OnGpu(torch.zeros(64, dtype=torch.uint8).expand(4, 4, 16, 64)) for _ in range(2 if which == "cache" else 0)))
+    kw.update(cu_q=OnGpu(torch.zeros(2, dtype=torch.int32)), max_q_len=3, max_seq_len=16, q=rows(8, 4), out=rows(8, 4))
+    if call != "attn_decode_paged_noalloc":
+        kw["workspace"] = OnGpu(torch.zeros(256, dtype=torch.uint8))
+    if which != "cache":
+        kw[which] = OnGpu(SHARED["all"])
+    with pytest.raises(NotImplementedError, match="broadcast"):
+        getattr(binding, call)(**kw)
+
+
+def test_single_rows_of_the_attention_keep_their_layout():
+    """One token of one head: any strides."""
+    st = gcs._st(OnGpu(torch.as_strided(torch.zeros(64, dtype=BF16), (1, 1, 64), (0, 0, 1))))
+    assert (st.token, st.head) == (0, 0)
+    st = gcs._st(OnGpu(torch.zeros(8, 6, 64, dtype=BF16)[:, 1:3]))
+    assert (st.token, st.head) == (384, 64)
