@@ -740,6 +740,8 @@ def _workspace(workspace, need: int, dev: int):
         workspace = torch.empty(need, dtype=_U8, device=dev)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace is on device {workspace.get_device()}, the current device is {dev}")
+    elif not workspace.is_contiguous():  # its bytes would not be its storage's
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.numel() * workspace.element_size()
 
 

@@ -190,3 +190,12 @@ def test_single_rows_of_the_attention_keep_their_layout():
     assert (st.token, st.head) == (0, 0)
     st = gcs._st(OnGpu(torch.zeros(8, 6, 64, dtype=BF16)[:, 1:3]))
     assert (st.token, st.head) == (384, 64)
+
+
+# ------------------------------------------------------------------------------ workspaces
+def test_a_broadcast_workspace_is_refused():
+    """Its size is not the size of its storage."""
+    assert gcs._workspace(OnGpu(torch.zeros(512, dtype=torch.uint8)), 0, 0)[1] == 512
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(512, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            gcs._workspace(OnGpu(ws), 0, 0)
