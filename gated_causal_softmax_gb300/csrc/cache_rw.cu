@@ -15,10 +15,11 @@
 // products say.
 //
 // All of it is bound by HBM, or by latency when there are few rows.  Every index that comes from
-// a device array is checked against its buffer before it is used: a row whose place is not in
-// the cache is left out and recorded in the status word.
+// a device array is checked against its buffer before it is used (cache_places.h): a row whose place
+// is not in the cache is left out and recorded in the status word.
 #include <algorithm>
 
+#include "cache_places.h"
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -32,111 +33,10 @@ constexpr float kE4m3Max = 448.f;
 
 __device__ __forceinline__ void record_bad(int* status) { atomicCAS(status, kDevOk, kDevInvalidArg); }
 
-// The last i in [0, n) with f(i) <= t, by the whole warp, for f that does not decrease; -1 if
-// there is none.  Whatever f returns, i stays in [-1, n).
-template <typename F>
-__device__ __forceinline__ int warp_last_le(int n, int t, F f) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, left = n;
-  while (true) {
-    const int stride = (left + 31) / 32;
-    const int i = lane * stride;
-    const int c = __popc(__ballot_sync(kFullMask, i < left && f(lo + i) <= t));
-    if (c == 0) return lo - 1;
-    if (stride == 1) return lo + c - 1;
-    lo += (c - 1) * stride;
-    left = min(stride, left - (c - 1) * stride);
-  }
-}
-
-// The table's entry for position pos of request r, -1 for a position outside the table: to be
-// checked before its use.
-__device__ __forceinline__ int table_entry(const CacheParams& p, int r, long long pos) {
-  return pos >= 0 && pos < p.capacity ? __ldg(p.block_table + (size_t)r * p.max_blocks + (pos >> p.log2_block)) : -1;
-}
-// The entry if it is a block of the cache; -1, and a record, if not.
-__device__ __forceinline__ int checked_block(const CacheParams& p, int entry) {
-  if (entry >= 0 && entry < p.num_blocks) return entry;
-  if ((threadIdx.x & 31) == 0) record_bad(p.status);
-  return -1;
-}
-__device__ __forceinline__ int block_of(const CacheParams& p, int r, long long pos) {
-  return checked_block(p, table_entry(p, r, pos));
-}
-
-// Where packed row t is cached: blk < 0: left out.
-struct Place {
-  int blk, slot, pos;
-};
-// A warp goes through neighbouring rows, so it looks the request up again only past its end, and
-// the block only past the block's.
-struct Cursor {
-  int r = -1, a = 0, b = 0;  // the request of the rows [a, b)
-  int shift = 0;             // position - row
-  int page = -1, blk = -1;
-};
-__device__ __forceinline__ bool find_request(const CacheParams& p, int t, Cursor& c) {
-  c.a = c.b = 0;
-  const int r = warp_last_le(p.num_reqs + 1, t, [&](int i) { return __ldg(p.cu + i); });
-  if (r >= p.num_reqs) return false;  // behind the last request
-  if (r >= 0) {
-    c.a = __ldg(p.cu + r);
-    c.b = __ldg(p.cu + r + 1);
-  }
-  if (t < c.a || t >= c.b) {  // cu does not start at 0 or is not sorted
-    if ((threadIdx.x & 31) == 0) record_bad(p.status);
-    return false;
-  }
-  c.r = r;
-  // rows stay below 2^30: a position below that is negative with either shift
-  c.shift = (int)max((long long)__ldg(p.seq_lens + r) - c.b, -(1LL << 30) - 1);
-  c.page = -1;
-  c.blk = -1;
-  return true;
-}
-__device__ __forceinline__ Place place_of(const CacheParams& p, int t, Cursor& c) {
-  Place w{-1, 0, 0};
-  if ((t < c.a || t >= c.b) && !find_request(p, t, c)) return w;
-  w.pos = t + c.shift;
-  const int page = w.pos >> p.log2_block;
-  if (page != c.page || w.pos < 0) {
-    c.page = page;
-    c.blk = block_of(p, c.r, w.pos);
-  }
-  w.blk = c.blk;
-  w.slot = w.pos & (p.block_size - 1);
-  return w;
-}
-
-// A step of a warp takes `tokens` rows of the packed tensors: one, or with few kv heads as many as
-// its lane groups have room for (powers of two).  This lane's group works on row t + off.
-struct Step {
-  int tokens, off, head;  // head: of the group, from the share's first on
-  int lanes;              // of one row's heads
-};
 template <int D>
 __device__ __forceinline__ Step narrow_step(int log2_tokens) {
   const int lane = threadIdx.x & 31, lanes = 32 >> log2_tokens;
   return Step{1 << log2_tokens, lane >> (5 - log2_tokens), (lane & (lanes - 1)) / RowLanes<D>::kLanes, lanes};
-}
-// This lane's place; the same block for all rows of the step in the middle of a block, and one by
-// one over the ends.
-__device__ __forceinline__ Place place_of(const CacheParams& p, int t, int t1, const Step& s, Cursor& c) {
-  if (s.tokens == 1) return place_of(p, t, c);
-  const int n = min(s.tokens, t1 - t);
-  if (n > 1 && t >= c.a && t + n <= c.b && t + c.shift >= 0 && (t + c.shift) >> p.log2_block == c.page &&
-      (t + n - 1 + c.shift) >> p.log2_block == c.page) {
-    Place w{s.off < n ? c.blk : -1, 0, t + s.off + c.shift};
-    w.slot = w.pos & (p.block_size - 1);
-    return w;
-  }
-  Place w = place_of(p, t, c);
-  for (int i = 1; i < n; ++i) {
-    const Place x = place_of(p, t + i, c);
-    if (s.off == i) w = x;
-  }
-  if (s.off >= n) w.blk = -1;
-  return w;
 }
 
 // A warp's share of the rows, which the last row_blocks blocks take: one of `segs` groups of heads,
