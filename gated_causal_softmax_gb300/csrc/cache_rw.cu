@@ -333,10 +333,12 @@ __device__ __forceinline__ void read_gates(const CacheParams& p, int slot, int h
   if (blk < 0) return;
   const size_t row = ((size_t)blk * p.hq + g.h) * p.block_size;
   const int s = (int)(g.s0 & (p.block_size - 1));
+  // the gate before the strip, where the strip's first position is a row: the other rows have theirs inside
+  const bool reaches_back = g.s0 >= g.p0 && g.s0 > 0;
   float prev = 0.f;
-  if (s > 0) {
+  if (reaches_back && s > 0) {
     if (head) prev = __ldg(p.g_cache + row + s - 1);
-  } else if (g.s0 > 0) {
+  } else if (reaches_back) {
     const int b1 = block_of(p, g.r, g.s0 - 1);
     if (b1 >= 0 && head) prev = __ldg(p.g_cache + ((size_t)b1 * p.hq + g.h) * p.block_size + p.block_size - 1);
   }
