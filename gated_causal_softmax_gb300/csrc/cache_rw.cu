@@ -333,14 +333,17 @@ __device__ __forceinline__ void read_gates(const CacheParams& p, int slot, int h
   if (blk < 0) return;
   const size_t row = ((size_t)blk * p.hq + g.h) * p.block_size;
   const int s = (int)(g.s0 & (p.block_size - 1));
-  // the gate before the strip, where the strip's first position is a row: the other rows have theirs inside
+  // the gate before the strip, where the strip's first position is a row: the other rows have theirs
+  // inside.  Without it (its page is not in the cache) that row's log gate is left out.
   const bool reaches_back = g.s0 >= g.p0 && g.s0 > 0;
+  bool has_first = true;
   float prev = 0.f;
   if (reaches_back && s > 0) {
     if (head) prev = __ldg(p.g_cache + row + s - 1);
   } else if (reaches_back) {
     const int b1 = block_of(p, g.r, g.s0 - 1);
-    if (b1 >= 0 && head) prev = __ldg(p.g_cache + ((size_t)b1 * p.hq + g.h) * p.block_size + p.block_size - 1);
+    has_first = b1 >= 0;
+    if (has_first && head) prev = __ldg(p.g_cache + ((size_t)b1 * p.hq + g.h) * p.block_size + p.block_size - 1);
   }
   if (!head) return;
   float v[kStrip];
@@ -352,7 +355,7 @@ __device__ __forceinline__ void read_gates(const CacheParams& p, int slot, int h
 #pragma unroll
   for (int i = 0; i < kStrip; ++i) {
     const long long pos = g.s0 + i;
-    if (pos >= g.p0 && pos < g.p1)
+    if (pos >= g.p0 && pos < g.p1 && (i || has_first))
       p.log_gate_out[(size_t)(g.a + (pos - g.p0)) * p.hq + g.h] = v[i] - (i ? v[i - 1] : prev);
   }
 }

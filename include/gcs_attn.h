@@ -397,8 +397,10 @@ int attn_cache_append_rope(const gcs_cache_args* a, const gcs_qk_rope_args* r, c
 /* Read the rows back: k, v bf16 [total_rows, hkv, d] (a->k_stride, a->v_stride), each value
  * bf16(code * scale); log_gate (with g_cache; NULL exactly when g_cache is) fp32 [total_rows, hq],
  * g_cache at p minus g_cache at p - 1 (or 0).  With cu_rows the cumulated seq_lens the whole cache is
- * read, as attn_fwd takes it; with fewer rows the last ones of each request.  The caches, scales
- * and g_cache are only read.  No workspace. */
+ * read, as attn_fwd takes it; with fewer rows the last ones of each request.  A log gate whose
+ * g_cache at p - 1 lies in a block outside the cache is left out (and recorded); blocks that hold
+ * neither the rows nor the gate before the first are not looked at.  The caches, scales and g_cache
+ * are only read.  No workspace. */
 int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate, gcs_stream_t stream);
 
 /* ------------------------------------------------------------------ status

@@ -33,3 +33,32 @@ def test_a_page_in_front_of_the_rows_is_not_looked_at(gcs_lib, n, hq):
     got, want, status = last_rows(gcs_lib, c, n, slice(0, (40 - n) // 16))
     assert status == 0
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq", [2, 40])
+@pytest.mark.parametrize("n,block", [(24, 16), (8, 16), (8, 32)])  # of 40: from the first position of a page
+def test_a_gate_without_the_one_before_it_is_left_out(gcs_lib, n, block, hq):
+    """Its page is there and the one before is not: the difference of two gates has only one.  The row's
+    key and value, and all later gates, are as ever."""
+    c = Cache([40], [40], hq, 1, 64, block=block, seed=71)
+    c.append(gcs_lib)
+    (k, v, lg), want, status = last_rows(gcs_lib, c, n, slice(0, (40 - n) // block))
+    assert status == 1
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    assert bool((lg[0] == 3.0).all()) and torch.equal(lg[1:], want[2][1:])
+
+
+@pytest.mark.gpu
+def test_gates_behind_a_page_that_is_missing(gcs_lib):
+    """A hole in the middle: its rows are left out, and the first gate behind it."""
+    c = Cache([100], [100], 33, 3, 64, seed=72)
+    c.append(gcs_lib)
+    (k, v, lg), want, status = last_rows(gcs_lib, c, 100, slice(2, 4))
+    assert status == 1
+    rows = torch.ones(100, dtype=torch.bool, device="cuda")
+    rows[32:64] = False
+    for x, y in ((k, want[0]), (v, want[1])):
+        assert torch.equal(x[rows], y[rows]) and bool((x[~rows] == 3.0).all())
+    rows[64] = False
+    assert torch.equal(lg[rows], want[2][rows]) and bool((lg[~rows] == 3.0).all())
