@@ -95,7 +95,8 @@ __device__ __forceinline__ void pack_codes(const Row& q, uint32_t* code) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) code[i] = to_e4m3x4(q.e[2 * i], q.e[2 * i + 1]);
 }
-// Codes of x / scale; zeros where the scale is not above 0.  With a caller's scale (CUT) a quotient
+// Codes of x / scale; all bits 0 where the scale is not above 0 (the products with it would leave NaN, and
+// the signs of zeros).  With a caller's scale (CUT) a quotient
 // can be far beyond +-448, up to infinity, where the correction has no meaning: it saturates
 // without.
 template <bool CUT>
@@ -112,6 +113,9 @@ __device__ __forceinline__ void quantise_row(const Row& x, float scale, uint32_t
     }
   }
   pack_codes(q, code);
+  const uint32_t keep = scale > 0.f ? 0xffffffffu : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) code[i] &= keep;
 }
 // The same by divisions, for the scales that quantise_row is not for.
 __device__ __noinline__ uint4 divide_row(Row x, float scale) {

@@ -62,3 +62,45 @@ def test_gates_behind_a_page_that_is_missing(gcs_lib):
         assert torch.equal(x[rows], y[rows]) and bool((x[~rows] == 3.0).all())
     rows[64] = False
     assert torch.equal(lg[rows], want[2][rows]) and bool((lg[~rows] == 3.0).all())
+
+
+def zero_codes_inputs(c):
+    inf = float("inf")
+    for x in (c.k, c.v):
+        x[0, 0, :6] = torch.tensor([inf, -inf, float("nan"), -1.0, -0.0, -3e38], device="cuda").to(x.dtype)
+        x[1] = -x[1].abs()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,hkv", [(64, 1), (128, 2), (256, 2), (512, 1)])
+@pytest.mark.parametrize("scale", [0.0, -0.0, -1.0, float("nan"), float("-inf")])
+def test_codes_of_a_given_scale_that_is_not_above_0(gcs_lib, scale, d, hkv):
+    """All of them are the byte 0: of infinities, NaN and negative elements too."""
+    c = Cache([9], [9], hkv, hkv, d, fmt="tensor", gates=False, seed=73)
+    zero_codes_inputs(c)
+    c.ks.fill_(scale)
+    c.append(gcs_lib)
+    assert gcs_lib.get_device_status() == 0
+    for _, _, _, blk, slot in c.places():
+        assert not c.kc[blk, :, slot].any()
+        assert bool((c.vc[blk, 0, slot] != 0).any())  # V's scale is as ever
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_codes_of_rows_of_zeros(gcs_lib, d):
+    """Scale 0 and the byte 0, whatever the zeros' signs; rows of NaN have codes 0 too."""
+    c = Cache([9], [9], 2, 2, d, gates=False, seed=74)
+    c.k[0], c.k[3, 1] = -0.0, 0.0
+    c.k[5, 0, ::2], c.k[5, 0, 1::2] = 0.0, -0.0
+    c.v[2] = -0.0
+    c.v[4, 1, 7] = float("nan")
+    c.append(gcs_lib)
+    assert gcs_lib.get_device_status() == 0
+    at = {t: (blk, slot) for t, _, _, blk, slot in c.places()}
+    for cache, scale, rows in ((c.kc, c.ks, ((0, 0), (0, 1), (3, 1), (5, 0))), (c.vc, c.vs, ((2, 0), (2, 1)))):
+        for t, h in rows:
+            blk, slot = at[t]
+            assert not cache[blk, h, slot].any() and float(scale[blk, h, slot]) == 0.0
+    blk, slot = at[4]
+    assert not c.vc[blk, 1, slot].any() and bool(torch.isnan(c.vs[blk, 1, slot]))
