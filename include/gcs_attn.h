@@ -293,7 +293,11 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
  * gradients are 0.  A position of max_pos or more is not read: the token is treated as padding
  * and GCS_ERR_INVALID_ARG is recorded in the device status word (in every mode; checked mode
  * adds nothing to these calls).
- * Supported: d 64, 128, 256 or 512; rotary_dim a multiple of 16, <= d.
+ * The sum of squares is held in fp32: it overflows from one element of about 1.8e19 on (128 of
+ * 1.6e18), and such a row's outputs and gradients are 0 or NaN; with eps = 0 it also underflows, for
+ * rows of elements below about 1e-19, whose outputs lose bits and become infinite or NaN.
+ * Supported: d 64, 128, 256 or 512; rotary_dim a multiple of 16, <= d; q_out and k_out (dq and dk)
+ * apart from q and k.
  */
 typedef struct {
   int total_tokens;            /* rows of q and k, >= 1                                   */
@@ -332,7 +336,10 @@ int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const v
                           gcs_stream_t stream);
 
 /* ------------------------------------------------------------------ write and read of the paged cache
- * The cache is the one attn_decode_paged and attn_prefill_paged read.  Packed row t belongs to
+ * The cache has the layout that attn_decode_paged and attn_prefill_paged read.  They attend over it
+ * where they support its shape: d 128 with 8 or 16 query heads a kv head, and for
+ * attn_prefill_paged an fp8 cache.  These calls take more (d 64, 256 and 512, any group, bf16 in
+ * chunks): over such a cache the way on is attn_cache_gather and attn_fwd.  Packed row t belongs to
  * request r with cu_rows[r] <= t < cu_rows[r + 1]; with len = cu_rows[r + 1] - cu_rows[r] it is
  * cached position p = seq_lens[r] - len + t - cu_rows[r], like the paged calls' query rows: the
  * same cu_q, seq_lens and block_table serve an append and the attention call after it.  Rows
@@ -345,7 +352,8 @@ int attn_qk_norm_rope_bwd(const gcs_qk_rope_args* a, const void* dq_out, const v
  *                    codes 0 where it is not above 0).
  *   bf16:            the elements.
  *   gates:           g_cache at p = (g_cache at p - 1, or 0 before the first) + log_gate, in fp32,
- *                    running on through the request's rows.
+ *                    running on through the request's rows.  (Each 64 positions add up the sums of
+ *                    all before them: a part of the work grows with the square of a request's rows.)
  * Slots outside the rows' positions are not touched.
  * Preconditions: no two rows share a slot (blocks that are written belong to one request), and
  * cu_rows is sorted from 0.  A row whose position or block-table entry lies outside the cache
