@@ -74,9 +74,13 @@ __device__ __forceinline__ float reciprocal(float x) {  // within an ulp
   return r;
 }
 
-// x / y rounded to fp32 for quotients away from the ends of the exponent range: the product with
-// 1 / y corrected once by its exact remainder (P. Markstein, "Computation of elementary functions
-// on the IBM RISC System/6000 processor", 1990), three multiply-adds in place of a division.
+// x / y for quotients away from the ends of the exponent range: the product with 1 / y corrected once by
+// its exact remainder (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), three multiply-adds in place of a division.  It is x / y rounded to
+// fp32 where inv is the rounded reciprocal, as in scale_of; with reciprocal(), which may be an ulp off,
+// that is not proven for every quotient.  Only codes are made of those: a quotient that is an e4m3 value or
+// the middle of two comes out exactly (its remainder corrects the product to it), and the codes are
+// tested bit by bit against those of the rounded quotients.
 __device__ __forceinline__ float2 quotient2(const float2& x, const float2& y, const float2& inv) {
   const float2 q = mul2(x, inv);
   return fma2(fma2(neg2(q), y, x), inv, q);
@@ -499,10 +503,15 @@ constexpr int kAppendBlocks = ROPE ? 4 : 5;
 // Rows in the last row_blocks blocks; gate tiles (their sums alone, with p.tile_sums) in all of
 // them, from the first on: few of both run side by side.
 //
-// The rows are bound by HBM as far as the warps can issue: a step of 4 keys and 4 values of 128 is
-// 3 KB of traffic and about 330 instructions.  Prompts of 36K tokens and 8 kv heads (231 MB) take
+// The rows are bound by HBM and by the latency of a step's chain (row maximum over the lanes, scale,
+// quotients, conversion) at the few warps that their registers leave: 16 to 20 an SM, of which one issues
+// in 54% of the cycles with the rotation and in 67% without.  A step of 4 keys and 4 values of 128 is 3 KB
+// of traffic and about 330 instructions; shares of queries and of keys and values get the same number
+// of warps, though theirs is not the same work.  Prompts of 36K tokens and 8 kv heads (231 MB) take
 // 39 us, 5.9 TB/s, 87% of the measured copy rate, and 8 us more with the gates of 32 heads (10 MB), which
-// are latency: two rounds over the tiles, of which only the first overlaps the rows.
+// are latency: two rounds over the tiles, of which only the first overlaps the rows.  Each tile adds up
+// the sums of all before it: one request of 16K rows takes 0.35 ns a row more with 32 gate heads and 0.49
+// with 64, one of 128K rows 0.34 and 0.60.
 template <int D, int FMT, bool ROPE>
 __global__ void __launch_bounds__(kThreads, kAppendBlocks<ROPE>)
     cache_append_kernel(const CacheParams p, const RopeParams q) {
@@ -552,10 +561,10 @@ __device__ __forceinline__ uint2 from_e4m3x4(uint32_t code, float scale) {
 // The codes (or bf16 elements) and scales of a warp's steps ahead; codes and scales are copied and
 // read by the same lane.
 //
-// Bound by the load / store unit more than by HBM: each of a lane's 8 codes are an 8-byte copy, an
-// 8-byte read and a 16-byte store.  82K tokens of 4 kv heads of 128 (188 MB) take 34 us, 5.5 TB/s, 81%
-// of the measured copy rate.  (16 neighbouring codes a lane with 32-byte stores 36 us, with two
-// 16-byte stores 40; 2, 3 and 6 stages ahead the same.)
+// Bound by its writes, and by the load / store unit: each of a lane's 8 codes are an 8-byte copy, an
+// 8-byte read and a 16-byte store.  60K tokens of 4 kv heads of 128 (188 MB) take 34.5 us, 5.4 TB/s, 80%
+// of the measured copy rate; a fill of the 124 MB that it writes takes 32.  (16 neighbouring codes a
+// lane with 32-byte stores 36 us, with two 16-byte stores 40; 2, 3 and 6 stages ahead the same.)
 constexpr int kGatherStages = 4;
 template <int FMT>
 struct alignas(16) GatherStage {
