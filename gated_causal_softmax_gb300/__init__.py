@@ -9,11 +9,15 @@ Entry points (same names as the C ABI in include/gcs_attn.h):
     attn_fwd(q, k, v, cu_seqlens, ...)           -> (o, lse)
     attn_bwd(q, k, v, o, lse, dout, cu_seqlens, ...) -> (dq, dk, dv, dlog_gate, dsink)
     attn_decode_paged(q, k_cache, v_cache, ...)  -> out
+    attn_decode_paged_shared(q, k_cache, v_cache, ...)   -> out (requests that share a prefix)
     attn_qk_norm_rope_fwd(q, k, cos_sin, positions, ...) -> (q_out, k_out)
     attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, ...)     -> (dq, dk, dq_weight, dk_weight)
     attn_cache_append(k, v, k_cache, v_cache, ...)       -> None (writes the cache)
     attn_cache_append_rope(q, k, v, k_cache, v_cache, ...) -> q_out (and writes the cache)
     attn_cache_gather(k_cache, v_cache, ...)             -> (k, v, log_gate)
+    attn_cache_weights(q, k_cache, k_scale, ..., w_cache) -> w_cache (gathered attention weights)
+    attn_cache_select(w_cache, block_table, ...)         -> (kept, kept_lens)
+    attn_cache_compact(k_cache, v_cache, ..., kept, kept_lens) -> None (moves the kept tokens)
 """
 from __future__ import annotations
 
@@ -32,12 +36,16 @@ __all__ = [
     "attn_bwd",
     "attn_decode_paged",
     "attn_decode_paged_noalloc",
+    "attn_decode_paged_shared",
     "attn_prefill_paged",
     "attn_qk_norm_rope_fwd",
     "attn_qk_norm_rope_bwd",
     "attn_cache_append",
     "attn_cache_append_rope",
     "attn_cache_gather",
+    "attn_cache_weights",
+    "attn_cache_select",
+    "attn_cache_compact",
     "selftest_bounded_wait",
     "set_device_checks",
     "device_checks",
@@ -47,6 +55,8 @@ __all__ = [
     "DecodeArgs",
     "QkRopeArgs",
     "CacheArgs",
+    "PrefixArgs",
+    "SelectArgs",
     "GcsError",
     "get_device_status",
     "set_kernel_events",
@@ -134,6 +144,18 @@ class DecodeArgs(ctypes.Structure):
         ("kv_stride_head", _i64),
         ("kv_stride_slot", _i64),
     ]
+    _pack = struct.Struct("@iPiiPiPiPPPPiiiiifiPiiPPi7q").pack
+
+
+class PrefixArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_groups", _c_int),
+        ("cu_groups", _vp),
+        ("prefix_lens", _vp),
+        ("max_group_q", _c_int),
+        ("max_prefix_len", _c_int),
+        ("max_suffix_len", _c_int),
+    ]
 
 
 class QkRopeArgs(ctypes.Structure):
@@ -194,6 +216,25 @@ class CacheArgs(ctypes.Structure):
     _pack = struct.Struct("@iPiiPPi4P7iP7q").pack
 
 
+class SelectArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", _c_int),
+        ("seq_lens", _vp),
+        ("max_seq_len", _c_int),
+        ("block_table", _vp),
+        ("max_blocks_per_req", _c_int),
+        ("num_blocks", _c_int),
+        ("block_size", _c_int),
+        ("hkv", _c_int),
+        ("w_cache", _vp),
+        ("budgets", _vp),
+        ("first_lens", _vp),
+        ("recent", _c_int),
+        ("max_keep", _c_int),
+    ]
+    _pack = struct.Struct("@iPiPiiiiPPPii").pack
+
+
 KV_FP8_E4M3, KV_BF16 = 0, 1
 SCALE_PER_TOKEN, SCALE_PER_TENSOR = 0, 1
 
@@ -227,6 +268,10 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_decode_paged.restype = _c_int
     lib.attn_decode_paged_noalloc.argtypes = [P(DecodeArgs), _vp, _vp]
     lib.attn_decode_paged_noalloc.restype = _c_int
+    lib.attn_decode_paged_shared_workspace.argtypes = [P(DecodeArgs), P(PrefixArgs)]
+    lib.attn_decode_paged_shared_workspace.restype = ctypes.c_size_t
+    lib.attn_decode_paged_shared.argtypes = [P(DecodeArgs), P(PrefixArgs), _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_decode_paged_shared.restype = _c_int
     lib.attn_prefill_paged_workspace.argtypes = [P(DecodeArgs)]
     lib.attn_prefill_paged_workspace.restype = ctypes.c_size_t
     lib.attn_prefill_paged.argtypes = [P(DecodeArgs), _vp, _vp, ctypes.c_size_t, _vp]
@@ -245,6 +290,14 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_cache_append_rope.restype = _c_int
     lib.attn_cache_gather.argtypes = [P(CacheArgs), _vp, _vp, _vp, _vp]
     lib.attn_cache_gather.restype = _c_int
+    lib.attn_cache_weights_workspace.argtypes = [P(DecodeArgs), _c_int]
+    lib.attn_cache_weights_workspace.restype = ctypes.c_size_t
+    lib.attn_cache_weights.argtypes = [P(DecodeArgs), _vp, _c_float, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_cache_weights.restype = _c_int
+    lib.attn_cache_select.argtypes = [P(SelectArgs), _vp, _vp, _vp]
+    lib.attn_cache_select.restype = _c_int
+    lib.attn_cache_compact.argtypes = [P(CacheArgs), _vp, _vp, _c_int, _vp, _vp]
+    lib.attn_cache_compact.restype = _c_int
     lib.gcs_get_device_status.argtypes = [P(_c_int), _c_int]
     lib.gcs_get_device_status.restype = _c_int
     lib.gcs_selftest_bounded_wait.argtypes = [_vp]
@@ -613,6 +666,49 @@ def attn_decode_paged_noalloc(q, k_cache, v_cache, k_scale, v_scale, block_table
     return out
 
 
+def attn_decode_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len,
+                             cu_groups, prefix_lens, max_group_q, max_prefix_len, max_suffix_len, scale=None,
+                             segment_len=0, out=None, workspace=None, g_cache=None, sink=None, window=0):
+    """attn_decode_paged for requests that share a prefix, which is read once for each group of
+    them: cu_groups int32 [groups + 1], the first request of each group and the end; prefix_lens
+    int32 [groups], its shared tokens (read through the block table of the group's first request).
+    Host bounds: max_group_q on the query rows of a group, max_prefix_len on the prefixes,
+    max_suffix_len on the tokens behind them.  segment_len: of those, 0 = the library's choice."""
+    L = load()
+    dev = _current_device()
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (block_table, "block_table"),
+                    (seq_lens, "seq_lens"), (cu_q, "cu_q"), (k_scale, "k_scale"), (v_scale, "v_scale"),
+                    (g_cache, "g_cache"), (sink, "sink"), (out, "out")):
+        if t is not None and t.get_device() != dev:
+            _refuse(t, t.dtype, name, t.shape, dev, True)
+    if k_cache is None or k_cache.dim() != 4 or v_cache is None or q is None or q.dim() != 3:
+        raise ValueError("expected q [tokens, heads, dim] and caches [num_blocks, num_kv_heads, block_size, d]")
+    if v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache types differ")
+    if block_table is None or block_table.dim() != 2 or seq_lens is None or cu_q is None or cu_groups is None:
+        raise ValueError("block_table, seq_lens, cu_q and cu_groups are [R, max_blocks], [R], [R + 1] and [groups + 1]")
+    num_reqs = block_table.shape[0]
+    if seq_lens.shape != (num_reqs,) or cu_q.shape != (num_reqs + 1,) or q.shape[2] != k_cache.shape[3]:
+        raise ValueError("seq_lens must be [R], cu_q [R + 1], and q and the caches of one head dim")
+    if sink is not None and sink.shape != (q.shape[1],):
+        raise ValueError("sink must be [num_q_heads]")
+    a = decode_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len,
+                    scale, segment_len, g_cache, sink, window)
+    groups = cu_groups.numel() - 1
+    x = PrefixArgs(groups, _vector(cu_groups, _I32, "cu_groups", (groups + 1,), dev) or None,
+                   _vector(prefix_lens, _I32, "prefix_lens", (groups,), dev) or None, int(max_group_q),
+                   int(max_prefix_len), int(max_suffix_len))
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _, token, head = _rows(out, "out", q.shape, dev)
+    a.out_stride = Strides(token, head)
+    need = 0 if workspace is not None else L.attn_decode_paged_shared_workspace(ctypes.byref(a), ctypes.byref(x))
+    ws, ws_bytes = _workspace(workspace, need, dev)
+    _check(L.attn_decode_paged_shared(ctypes.byref(a), ctypes.byref(x), out.data_ptr(), _ptr(ws), ws_bytes,
+                                      _raw_stream(dev)), "attn_decode_paged_shared")
+    return out
+
+
 # ------------------------------------------------------------------ norm, rotation and cache rows
 # These calls run once a layer in a decoding step, where the host's time is what counts, so every
 # tensor is looked at once: type, shape, device and layout in one test, the reason only if it fails.
@@ -752,10 +848,11 @@ def _append_workspace(L, a, workspace, max_q_len, dev: int):
 
 
 def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_rows, total_rows, max_rows, hq, g_cache,
-               dev: int, k_stride=(0, 0), v_stride=(0, 0)) -> CacheArgs:
+               dev: int, k_stride=(0, 0), v_stride=(0, 0), rows=True) -> CacheArgs:
     """Marshals the arguments of the cache calls: the caches, scales and index arrays are those of
     decode_args (fp8 per token, fp8 per tensor or bf16, any strides the library takes); hq None:
-    g_cache's heads; the last two: (token, head) strides of the packed k and v."""
+    g_cache's heads; k_stride, v_stride: (token, head) strides of the packed k and v; rows False: a call
+    without packed rows (cu_rows None)."""
     if k_cache is None or v_cache is None or k_cache.dim() != 4:
         raise ValueError("caches must be [num_blocks, num_kv_heads, block_size, d]")
     shape, fmt, cs = k_cache.shape, k_cache.dtype, k_cache.stride()
@@ -787,7 +884,7 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
             scale_mode = SCALE_PER_TENSOR
         ks = _vector(k_scale, _F32, "k_scale", k_scale.shape, dev)
         vs = _vector(v_scale, _F32, "v_scale", v_scale.shape, dev)
-    if block_table is None or seq_lens is None or cu_rows is None or block_table.dim() != 2:
+    if block_table is None or seq_lens is None or block_table.dim() != 2 or (cu_rows is None and rows):
         raise ValueError("block_table, seq_lens and cu_rows are [R, max_blocks], [R] and [R + 1]")
     num_reqs, max_blocks = block_table.shape
     if g_cache is not None and hq is None:
@@ -873,3 +970,120 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     lg = _vector(log_gate, _F32, "log_gate", (n, a.hq), dev)
     _check(load().attn_cache_gather(a, kp, vp, lg, _raw_stream(dev)), "attn_cache_gather")
     return k, v, log_gate
+
+
+# ------------------------------------------------------------------ eviction from the paged cache
+def _cache_scales(k_cache, k_scale, dev: int):
+    """(kv_format, scale_mode, address of the scales) of one cache and its scales, by decode_args'
+    rules."""
+    if k_cache.dtype is _BF16:
+        if k_scale is not None:
+            raise ValueError("a bf16 KV cache takes no scales")
+        return KV_BF16, SCALE_PER_TOKEN, 0
+    if k_scale is None:
+        raise ValueError("k_scale is required")
+    page = k_cache.shape[:3]
+    if k_scale.shape != page and k_scale.numel() != 1:
+        raise NotImplementedError("fp8 scales must have the page shape [num_blocks, num_kv_heads, block_size] "
+                                  "(per token) or hold one value (per tensor)")
+    mode = SCALE_PER_TOKEN if k_scale.shape == page else SCALE_PER_TENSOR
+    return KV_FP8_E4M3, mode, _vector(k_scale, _F32, "k_scale", k_scale.shape, dev)
+
+
+def _one_cache(t, name: str, dev: int):
+    """Checks one paged cache [num_blocks, hkv, block_size, d] of any layout the library may take."""
+    if t is None or t.dim() != 4:
+        raise ValueError(f"{name} must be [num_blocks, num_kv_heads, block_size, d]")
+    if t.dtype not in (_BF16, _U8, _E4M3):
+        raise ValueError(f"{name} must be bf16, uint8 or float8_e4m3fn, got {t.dtype}")
+    cs = t.stride()
+    if cs[3] != 1 or t.get_device() != dev:
+        _refuse(t, t.dtype, name, t.shape, dev, True)
+    if not (cs[0] or cs[1] or cs[2]):  # would say "contiguous" to the library
+        _refuse_broadcast(name)
+    return cs
+
+
+def attn_cache_weights(q, k_cache, k_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len, w_cache, decay=1.0,
+                       lse=None, scale=None, g_cache=None, sink=None, window=0, workspace=None):
+    """Adds the attention weight that every cached token gets from the query rows (summed over the
+    rows and the kv head's query heads) to w_cache fp32 [num_blocks, hkv, block_size], whose old
+    values are multiplied by `decay`; the rows' own tokens, and all with decay 0, start from 0.  The
+    other arguments are those of attn_decode_paged; q bf16 [total_q, hq, d] with d 64, 128, 256 or
+    512 and any group, any q_len.  lse fp32 [hq, total_q] (as attn_fwd gives it) saves one of two
+    reads of the keys.  Returns w_cache."""
+    L = load()
+    dev = _current_device()
+    cs = _one_cache(k_cache, "k_cache", dev)
+    nb, hkv, bs, d = k_cache.shape
+    if q is None or q.dim() != 3:
+        raise ValueError("expected a [tokens, heads, dim] tensor q")
+    n, hq = q.shape[0], q.shape[1]
+    qp, q_token, q_head = _rows(q, "q", (n, hq, d), dev)
+    fmt, mode, ks = _cache_scales(k_cache, k_scale, dev)
+    if block_table is None or seq_lens is None or cu_q is None or block_table.dim() != 2:
+        raise ValueError("block_table, seq_lens and cu_q are [R, max_blocks], [R] and [R + 1]")
+    num_reqs, max_blocks = block_table.shape
+    if w_cache is None:
+        raise ValueError("w_cache is required")
+    a = DecodeArgs.from_buffer_copy(DecodeArgs._pack(
+        num_reqs, _vector(cu_q, _I32, "cu_q", (num_reqs + 1,), dev), n, max_q_len,
+        _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev), max_seq_len,
+        _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(), 0, ks, 0,
+        nb, bs, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, 0, qp, fmt, mode,
+        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), _vector(sink, _F32, "sink", (hq,), dev), window, q_token,
+        q_head, 0, 0, cs[0], cs[1], cs[2]))
+    wp = _vector(w_cache, _F32, "w_cache", (nb, hkv, bs), dev)
+    lp = _vector(lse, _F32, "lse", (hq, n), dev)
+    need = 0 if workspace is not None else L.attn_cache_weights_workspace(a, 1 if lp else 0)
+    ws, ws_bytes = _workspace(workspace, need, dev)
+    _check(L.attn_cache_weights(a, lp, decay, wp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_weights")
+    return w_cache
+
+
+def attn_cache_select(w_cache, block_table, seq_lens, max_seq_len, budgets, max_keep, first_lens=None, recent=0,
+                      kept=None, kept_lens=None):
+    """Chooses the cached tokens that stay: of each request min(budgets[r], seq_lens[r], max_keep),
+    for every kv head on its own: the last `recent`, the first first_lens[r], then the largest weights
+    in w_cache fp32 [num_blocks, hkv, block_size] (equal ones: the lowest position).  budgets,
+    first_lens int32 [R].  Returns kept int32 [R, hkv, max_keep] (ascending positions, -1 behind
+    them) and kept_lens int32 [R]."""
+    dev = _current_device()
+    if w_cache is None or w_cache.dim() != 3:
+        raise ValueError("w_cache must be [num_blocks, num_kv_heads, block_size]")
+    if block_table is None or seq_lens is None or budgets is None or block_table.dim() != 2:
+        raise ValueError("block_table, seq_lens and budgets are [R, max_blocks], [R] and [R]")
+    nb, hkv, bs = w_cache.shape
+    num_reqs, max_blocks = block_table.shape
+    a = SelectArgs.from_buffer_copy(SelectArgs._pack(
+        num_reqs, _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev), max_seq_len,
+        _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, nb, bs, hkv,
+        _vector(w_cache, _F32, "w_cache", w_cache.shape, dev), _vector(budgets, _I32, "budgets", (num_reqs,), dev),
+        _vector(first_lens, _I32, "first_lens", (num_reqs,), dev), recent, max_keep))
+    if kept is None:
+        kept = torch.empty((num_reqs, hkv, max(0, max_keep)), dtype=_I32, device=w_cache.device)
+    if kept_lens is None:
+        kept_lens = torch.empty((num_reqs,), dtype=_I32, device=w_cache.device)
+    _check(load().attn_cache_select(a, _vector(kept, _I32, "kept", (num_reqs, hkv, max(0, max_keep)), dev),
+                                    _vector(kept_lens, _I32, "kept_lens", (num_reqs,), dev), _raw_stream(dev)),
+           "attn_cache_select")
+    return kept, kept_lens
+
+
+def attn_cache_compact(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, kept, kept_lens, g_cache=None,
+                       w_cache=None) -> None:
+    """Moves the kept tokens of every request and kv head to the front of its pages, in place: cached
+    position i takes what position kept[r, h, i] >= i holds (K, V, per-token scales, and the gates and
+    weights where given), i < kept_lens[r].  kept int32 [R, hkv, max_keep], as attn_cache_select gives
+    it.  kept_lens are the seq_lens of the calls after it."""
+    dev = _current_device()
+    a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, 1, 1, None, g_cache, dev,
+                   rows=False)
+    if kept is None or kept_lens is None or kept.dim() != 3:
+        raise ValueError("kept and kept_lens are [R, num_kv_heads, max_keep] and [R]")
+    nb, hkv, bs, _ = k_cache.shape
+    num_reqs, max_keep = block_table.shape[0], kept.shape[2]
+    kp = _vector(kept, _I32, "kept", (num_reqs, hkv, max_keep), dev)
+    lp = _vector(kept_lens, _I32, "kept_lens", (num_reqs,), dev)
+    wp = _vector(w_cache, _F32, "w_cache", (nb, hkv, bs), dev)
+    _check(load().attn_cache_compact(a, kp, lp, max_keep, wp, _raw_stream(dev)), "attn_cache_compact")

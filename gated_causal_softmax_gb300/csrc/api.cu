@@ -115,6 +115,22 @@ bool make_page_map_u8(CUtensorMap* m, const void* base, int num_blocks, int hkv,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same of a bf16 cache with head dim 128: one box is 64 dims of a page (16 rows of 128 bytes).
+bool make_page_map_bf16(CUtensorMap* m, const void* base, int num_blocks, int hkv, int block_size,
+                        const CacheLayout& l) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const bool hi = l.head_inner();
+  cuuint64_t dims[4] = {128, (cuuint64_t)(hi ? hkv : block_size), (cuuint64_t)(hi ? block_size : hkv),
+                        (cuuint64_t)num_blocks};
+  cuuint64_t strides[3] = {(cuuint64_t)(hi ? l.hs : l.ss), (cuuint64_t)(hi ? l.ss : l.hs), (cuuint64_t)l.bs};
+  cuuint32_t box[4] = {64, hi ? 1u : 16u, hi ? 16u : 1u, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t round_up(size_t x) { return (x + 255) & ~size_t(255); }
@@ -892,6 +908,139 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
   return cuda_status(launch_prefill_paged(p, maps, s, &timer.b, &timer.a));
 }
 
+// ------------------------------------------------------------------ decoding behind shared prefixes
+
+static int current_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+}
+
+static int check_shared(const gcs_decode_args* a, const gcs_prefix_args* x) {
+  if (!a || !x || a->segment_len < 0) return GCS_ERR_INVALID_ARG;
+  gcs_decode_args b = *a;
+  if (b.segment_len == 0) b.segment_len = 16;  // the library's choice
+  const int st = check_decode(&b);
+  if (st != GCS_OK) return st;
+  if (x->num_groups < 1 || x->max_group_q < 1 || x->max_group_q > a->total_q || x->max_prefix_len < 0 ||
+      x->max_prefix_len > a->max_seq_len || x->max_suffix_len < 0 || x->max_suffix_len > a->max_seq_len)
+    return GCS_ERR_INVALID_ARG;
+  if (!x->cu_groups || !x->prefix_lens || (reinterpret_cast<uintptr_t>(x->cu_groups) & 3u) ||
+      (reinterpret_cast<uintptr_t>(x->prefix_lens) & 3u))
+    return GCS_ERR_INVALID_ARG;
+  // the launch grids, and positions with a tile ahead
+  if (a->num_reqs > 65535 || x->num_groups > 65535 || a->hkv > 65535 || a->max_seq_len > 1 << 30)
+    return GCS_ERR_UNSUPPORTED;
+  return GCS_OK;
+}
+
+struct SharedPlan {
+  int pre_segs = 0, pre_seg_keys = 128;  // of the prefixes
+  int max_segs = 0, seg_pages = 0;       // of what lies behind them
+  size_t acc = 0, ml = 0, part = 0;      // bytes: the prefixes' partials, the others'
+  size_t ws = 0;                         // + the checked copies of cu_q and cu_groups
+};
+// Segments: of a prefix, enough for one CTA an SM with the groups' row tiles and kv heads; behind
+// it (segment_len 0), enough for the three CTAs of an SM, of 128 to 2048 tokens.
+static bool plan_shared(const gcs_decode_args* a, const gcs_prefix_args* x, bool chk, SharedPlan* pl) {
+  const int sms = current_sms();
+  if (!sms) return false;
+  if (x->max_prefix_len > 0) {
+    const int rows = 256 / (a->hq / a->hkv);
+    const long long base = (long long)x->num_groups * ((x->max_group_q + rows - 1) / rows) * a->hkv;
+    const long long tiles = (x->max_prefix_len + 127) / 128;
+    long long want = sms / base;
+    want = want < 1 ? 1 : want > tiles ? tiles : want;
+    pl->pre_seg_keys = (int)((tiles + want - 1) / want) * 128;
+    pl->pre_segs = (x->max_prefix_len + pl->pre_seg_keys - 1) / pl->pre_seg_keys;
+  }
+  if (x->max_suffix_len > 0) {
+    const int pages = (x->max_suffix_len + 30) / 16;  // the first may be the prefix's last
+    if (a->segment_len > 0) {
+      pl->seg_pages = a->segment_len / 16;
+    } else {
+      const long long units = (long long)a->num_reqs * a->hkv, want = (3LL * sms + units - 1) / units;
+      const long long sp = (pages + want - 1) / want;
+      pl->seg_pages = (int)(sp < 8 ? 8 : sp > 128 ? 128 : sp);
+    }
+    pl->max_segs = (pages + pl->seg_pages - 1) / pl->seg_pages;
+    pl->part = partials_ws(a, pl->max_segs);
+  }
+  const size_t rows = (size_t)pl->pre_segs * a->total_q * a->hq;
+  pl->acc = round_up(rows * 128 * sizeof(float));
+  pl->ml = round_up(rows * sizeof(float2));
+  pl->ws = pl->part + pl->acc + pl->ml + cu_q_copy_ws(a, chk) +
+           (chk ? round_up(((size_t)x->num_groups + 1) * sizeof(int32_t)) : 0);
+  return true;
+}
+
+size_t attn_decode_paged_shared_workspace(const gcs_decode_args* a, const gcs_prefix_args* x) {
+  SharedPlan pl;
+  return check_shared(a, x) == GCS_OK && plan_shared(a, x, device_checks_on(), &pl) ? pl.ws : 0;
+}
+
+int attn_decode_paged_shared(const gcs_decode_args* a, const gcs_prefix_args* x, void* out, void* workspace,
+                             size_t workspace_bytes, gcs_stream_t stream) {
+  int st = check_shared(a, x);
+  if (st != GCS_OK) return st;
+  if (!out || !aligned16(out)) return GCS_ERR_INVALID_ARG;
+  if (paged_out_overlaps(a, out)) return GCS_ERR_INVALID_ARG;
+  CacheLayout cl;
+  Layout lo;
+  cache_layout(a, &cl);
+  resolve_layout(a->out_stride, a->hq, a->d, &lo);
+  const TSpan outs[] = {tspan(out, a->total_q, a->hq, a->d, lo, 2)};
+  const TSpan ins[] = {tspan(span(x->cu_groups, ((size_t)x->num_groups + 1) * 4)),
+                       tspan(span(x->prefix_lens, (size_t)x->num_groups * 4))};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  SharedPlan pl;
+  const bool chk = device_checks_on();
+  if (!plan_shared(a, x, chk, &pl)) return GCS_ERR_CUDA;
+  if (pl.ws > 0 && (!workspace || workspace_bytes < pl.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return GCS_ERR_WORKSPACE;
+  int* status = device_status_ptr();
+  if (!status) return GCS_ERR_CUDA;
+  DecodeParams p{};
+  fill_paged_params(a, out, status, p);
+  p.max_segs = pl.max_segs;
+  p.seg_pages = pl.seg_pages > 0 ? pl.seg_pages : 1;
+  p.num_groups = x->num_groups;
+  p.cu_groups = x->cu_groups;
+  p.prefix_lens = x->prefix_lens;
+  p.max_prefix = x->max_prefix_len;
+  p.total_q = a->total_q;
+  p.max_group_q = x->max_group_q;
+  p.pre_segs = pl.pre_segs;
+  p.pre_seg_keys = pl.pre_seg_keys;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t units = (size_t)a->num_reqs * pl.max_segs * a->hkv;
+  p.part_acc = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + round_up(units * a->max_q_len * 16 * 128 * sizeof(float)));
+  p.pre_acc = reinterpret_cast<float*>(ws + pl.part);
+  p.pre_ml = reinterpret_cast<float2*>(ws + pl.part + pl.acc);
+  DecodeMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  auto map = [&](CUtensorMap* m, const void* base) {
+    return a->kv_format == GCS_KV_BF16 ? make_page_map_bf16(m, base, a->num_blocks, a->hkv, a->block_size, cl)
+                                       : make_page_map_u8(m, base, a->num_blocks, a->hkv, a->block_size, cl);
+  };
+  if (!map(&maps.k, a->k_cache) || !map(&maps.v, a->v_cache)) return GCS_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (chk) {
+    const size_t off = pl.part + pl.acc + pl.ml;
+    st = paged_checks(a, workspace, off, p, s);
+    if (st != GCS_OK) return st;
+    int32_t* groups = reinterpret_cast<int32_t*>(ws + off + cu_q_copy_ws(a, true));
+    st = cuda_status(launch_check_groups(x->cu_groups, x->prefix_lens, x->num_groups, a->seq_lens, a->block_table,
+                                         a->num_reqs, a->max_blocks_per_req, a->num_blocks, a->block_size, a->total_q,
+                                         x->max_group_q, x->max_prefix_len, x->max_suffix_len,
+                                         const_cast<int32_t*>(p.cu_q), groups, status, s));
+    if (st != GCS_OK) return st;
+    p.cu_groups = groups;
+  }
+  return cuda_status(launch_decode_shared(p, maps, s));
+}
+
 // ------------------------------------------------------------------ norm and rotation of q and k
 
 static bool head_dim_supported(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
@@ -1252,6 +1401,228 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
   p.status = device_status_ptr();
   if (!p.status) return GCS_ERR_CUDA;
   return cuda_status(launch_cache_gather(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ eviction from the paged cache
+
+static int log2_of(int block_size) {
+  int n = 0;
+  while ((1 << n) < block_size) ++n;
+  return n;
+}
+static bool block_size_supported(int n) { return n >= 16 && n <= 4096 && (n & (n - 1)) == 0; }
+
+// The arguments of the weights: those of the paged attention calls, without its limits on shapes and
+// without the values.
+static int check_weights(const gcs_decode_args* a) {
+  if (!a) return GCS_ERR_INVALID_ARG;
+  if (a->num_reqs < 1 || a->total_q < 1 || a->max_q_len < 1 || a->max_seq_len < 1 || a->max_blocks_per_req < 1 ||
+      a->num_blocks < 1 || a->hq < 1 || a->hkv < 1 || a->hq % a->hkv != 0 || a->window < 0)
+    return GCS_ERR_INVALID_ARG;
+  if (!a->cu_q || !a->seq_lens || !a->block_table || !a->k_cache || !a->q) return GCS_ERR_INVALID_ARG;
+  if (!std::isfinite(a->scale) || a->max_q_len > a->max_seq_len) return GCS_ERR_INVALID_ARG;
+  if (!aligned16(a->k_cache) || !aligned16(a->q) || !aligned16(a->g_cache) || !aligned4(a->k_scale) ||
+      !aligned4(a->sink) || !aligned4(a->cu_q) || !aligned4(a->seq_lens) || !aligned4(a->block_table))
+    return GCS_ERR_INVALID_ARG;
+  if (a->kv_format == GCS_KV_BF16) {
+    if (a->k_scale || a->scale_mode != GCS_SCALE_PER_TOKEN) return GCS_ERR_INVALID_ARG;
+  } else if (a->kv_format == GCS_KV_FP8_E4M3) {
+    if (!a->k_scale) return GCS_ERR_INVALID_ARG;
+    if (a->scale_mode != GCS_SCALE_PER_TOKEN && a->scale_mode != GCS_SCALE_PER_TENSOR) return GCS_ERR_INVALID_ARG;
+  } else {
+    return GCS_ERR_INVALID_ARG;
+  }
+  if (!head_dim_supported(a->d) || !block_size_supported(a->block_size)) return GCS_ERR_UNSUPPORTED;
+  if ((long long)a->max_blocks_per_req * a->block_size < a->max_seq_len) return GCS_ERR_INVALID_ARG;
+  // positions with a step ahead, rows x heads of a request and the launch grids within 32 bits
+  if (a->max_seq_len > 1 << 30 || a->total_q > 1 << 30 || a->num_reqs > 65535 || a->hkv > 65535 ||
+      (double)a->max_q_len * (a->hq / a->hkv) > 1073741824.0 || (double)a->hq * a->d > 2147483647.0)
+    return GCS_ERR_UNSUPPORTED;
+  if ((double)a->num_blocks * a->hkv * a->block_size * a->d > 9.0e15) return GCS_ERR_UNSUPPORTED;
+  CacheLayout cl;
+  const int st = cache_layout(a, &cl);
+  if (st != GCS_OK) return st;
+  Layout lq;
+  return resolve_layout(a->q_stride, a->hq, a->d, &lq);
+}
+
+struct WeightsPlan {
+  int seg_len = 0, segs = 0;
+  size_t ws = 0;
+};
+static bool plan_weights(const gcs_decode_args* a, bool with_lse, WeightsPlan* pl) {
+  const int sms = current_sms();
+  if (!sms) return false;
+  pl->seg_len = cache_weights_segment(a->max_seq_len, (long long)a->num_reqs * a->hkv, sms);
+  pl->segs = (a->max_seq_len + pl->seg_len - 1) / pl->seg_len;
+  pl->ws = with_lse ? 0 : round_up((size_t)pl->segs * a->total_q * a->hq * sizeof(float2));
+  return true;
+}
+
+size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse) {
+  WeightsPlan pl;
+  return check_weights(a) == GCS_OK && plan_weights(a, with_lse != 0, &pl) ? pl.ws : 0;
+}
+
+int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, float* w_cache, void* workspace,
+                       size_t workspace_bytes, gcs_stream_t stream) {
+  const int st = check_weights(a);
+  if (st != GCS_OK) return st;
+  if (!w_cache || !aligned16(w_cache) || !aligned4(lse) || !std::isfinite(decay)) return GCS_ERR_INVALID_ARG;
+  CacheLayout cl;
+  Layout lq;
+  cache_layout(a, &cl);
+  resolve_layout(a->q_stride, a->hq, a->d, &lq);
+  const size_t rows = (size_t)a->num_blocks * a->hkv * a->block_size;
+  const size_t elt = a->kv_format == GCS_KV_BF16 ? 2 : 1;
+  const size_t cache_bytes = (size_t)(a->num_blocks - 1) * cl.bs + (size_t)(a->hkv - 1) * cl.hs +
+                             (size_t)(a->block_size - 1) * cl.ss + (size_t)a->d * elt;
+  const TSpan outs[] = {tspan(span(w_cache, rows * 4))};
+  const TSpan ins[] = {tspan(a->q, a->total_q, a->hq, a->d, lq, 2),
+                       tspan(span(a->k_cache, cache_bytes)),
+                       tspan(span(a->k_scale, a->scale_mode == GCS_SCALE_PER_TENSOR ? 4 : rows * 4)),
+                       tspan(span(a->block_table, (size_t)a->num_reqs * a->max_blocks_per_req * 4)),
+                       tspan(span(a->seq_lens, (size_t)a->num_reqs * 4)),
+                       tspan(span(a->cu_q, ((size_t)a->num_reqs + 1) * 4)),
+                       tspan(span(a->g_cache, (size_t)a->num_blocks * a->hq * a->block_size * 4)),
+                       tspan(span(a->sink, (size_t)a->hq * 4)),
+                       tspan(span(lse, (size_t)a->hq * a->total_q * 4))};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  WeightsPlan pl;
+  if (!plan_weights(a, lse != nullptr, &pl)) return GCS_ERR_CUDA;
+  if (pl.ws > 0 && (!workspace || workspace_bytes < pl.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return GCS_ERR_WORKSPACE;
+  WeightsParams p{};
+  p.cu_q = a->cu_q;
+  p.seq_lens = a->seq_lens;
+  p.block_table = a->block_table;
+  p.max_blocks = a->max_blocks_per_req;
+  p.num_blocks = a->num_blocks;
+  p.block_size = a->block_size;
+  p.log2_block = log2_of(a->block_size);
+  p.num_reqs = a->num_reqs;
+  p.total_q = a->total_q;
+  p.max_q_len = a->max_q_len;
+  p.max_seq_len = a->max_seq_len;
+  p.hq = a->hq;
+  p.hkv = a->hkv;
+  p.group = a->hq / a->hkv;
+  p.d = a->d;
+  p.format = a->kv_format == GCS_KV_BF16 ? kCacheBf16
+             : a->scale_mode == GCS_SCALE_PER_TENSOR ? kCachePerTensor : kCachePerToken;
+  p.k_cache = static_cast<const uint8_t*>(a->k_cache);
+  p.kv_bs = cl.bs, p.kv_hs = cl.hs, p.kv_ss = cl.ss;
+  p.k_scale = a->k_scale;
+  p.g_cache = a->g_cache;
+  p.sink = a->sink;
+  p.window = a->window;
+  p.scale = a->scale;
+  p.decay = decay;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_ts = lq.ts, p.q_hs = lq.hs;
+  p.lse = lse;
+  p.w_cache = w_cache;
+  p.part = static_cast<float2*>(workspace);
+  p.seg_len = pl.seg_len;
+  p.segs = pl.segs;
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_cache_weights(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_select(const gcs_select_args* a, int32_t* kept, int32_t* kept_lens, gcs_stream_t stream) {
+  if (!a || a->num_reqs < 1 || a->hkv < 1 || a->max_seq_len < 1 || a->max_blocks_per_req < 1 || a->num_blocks < 1 ||
+      a->recent < 0 || a->max_keep < 1)
+    return GCS_ERR_INVALID_ARG;
+  if (!a->w_cache || !a->block_table || !a->seq_lens || !a->budgets || !kept || !kept_lens) return GCS_ERR_INVALID_ARG;
+  if (!aligned16(a->w_cache) || !aligned4(a->block_table) || !aligned4(a->seq_lens) || !aligned4(a->budgets) ||
+      !aligned4(a->first_lens) || !aligned4(kept) || !aligned4(kept_lens))
+    return GCS_ERR_INVALID_ARG;
+  if (!block_size_supported(a->block_size)) return GCS_ERR_UNSUPPORTED;
+  if ((long long)a->max_blocks_per_req * a->block_size < a->max_seq_len) return GCS_ERR_INVALID_ARG;
+  // positions, and the grid of up to 16 blocks a (request, kv head)
+  if (a->max_seq_len > 1 << 30 || a->max_keep > 1 << 30 || (double)a->num_reqs * a->hkv > 134217727.0)
+    return GCS_ERR_UNSUPPORTED;
+  const size_t R = (size_t)a->num_reqs;
+  const TSpan outs[] = {tspan(span(kept, R * a->hkv * a->max_keep * 4)), tspan(span(kept_lens, R * 4))};
+  const TSpan ins[] = {tspan(span(a->w_cache, (size_t)a->num_blocks * a->hkv * a->block_size * 4)),
+                       tspan(span(a->block_table, R * a->max_blocks_per_req * 4)), tspan(span(a->seq_lens, R * 4)),
+                       tspan(span(a->budgets, R * 4)), tspan(span(a->first_lens, R * 4))};
+  if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
+  SelectParams p{};
+  p.num_reqs = a->num_reqs;
+  p.hkv = a->hkv;
+  p.seq_lens = a->seq_lens;
+  p.block_table = a->block_table;
+  p.max_blocks = a->max_blocks_per_req;
+  p.num_blocks = a->num_blocks;
+  p.block_size = a->block_size;
+  p.log2_block = log2_of(a->block_size);
+  p.max_seq_len = a->max_seq_len;
+  p.w_cache = a->w_cache;
+  p.budgets = a->budgets;
+  p.first_lens = a->first_lens;
+  p.recent = a->recent;
+  p.max_keep = a->max_keep;
+  p.kept = kept;
+  p.kept_lens = kept_lens;
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_cache_select(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32_t* kept_lens, int max_keep,
+                       float* w_cache, gcs_stream_t stream) {
+  if (!a) return GCS_ERR_INVALID_ARG;
+  gcs_cache_args b = *a;  // no packed rows here
+  b.cu_rows = b.seq_lens;
+  b.total_rows = b.max_rows = 1;
+  b.k_stride = b.v_stride = gcs_strides{0, 0};
+  const int st = check_cache(&b);
+  if (st != GCS_OK) return st;
+  if (!kept || !kept_lens || max_keep < 1 || !aligned4(kept) || !aligned4(kept_lens) || !aligned4(w_cache))
+    return GCS_ERR_INVALID_ARG;
+  // positions, and the grid of up to 8 blocks a (request, kv head) and eight vectors
+  if (max_keep > 1 << 30 || (double)a->num_reqs * a->hkv > 268435455.0 || a->hq / a->hkv > 1 << 18)
+    return GCS_ERR_UNSUPPORTED;
+  CacheLayout cl;
+  cache_args_layout(&b, &cl);
+  const CacheSpans cs = cache_spans(&b, cl);
+  if (caches_meet(&b, cl, cs)) return GCS_ERR_INVALID_ARG;
+  const CacheParams c = cache_params(&b, cl);
+  const bool per_token = c.format == kCachePerToken;
+  const TSpan none = tspan(Span{0, 0});
+  const size_t R = (size_t)a->num_reqs, rows = (size_t)a->num_blocks * a->hkv * a->block_size;
+  const TSpan ks = per_token ? cs.ks : none, vs = per_token ? cs.vs : none, w = tspan(span(w_cache, rows * 4));
+  const TSpan ins[] = {cs.table, cs.lens, tspan(span(kept, R * a->hkv * max_keep * 4)), tspan(span(kept_lens, R * 4))};
+  // K against V was checked above
+  const TSpan outs_k[] = {cs.k, ks, vs, cs.g, w}, outs_v[] = {cs.v, ks, vs, cs.g, w};
+  if (outputs_overlap(outs_k, ins) || outputs_overlap(outs_v, ins)) return GCS_ERR_INVALID_ARG;
+  MoveParams p{};
+  p.num_reqs = a->num_reqs;
+  p.hkv = a->hkv;
+  p.group = a->hq / a->hkv;
+  p.seq_lens = a->seq_lens;
+  p.block_table = a->block_table;
+  p.kept = kept;
+  p.kept_lens = kept_lens;
+  p.max_blocks = c.max_blocks;
+  p.num_blocks = c.num_blocks;
+  p.block_size = c.block_size;
+  p.log2_block = c.log2_block;
+  p.max_keep = max_keep;
+  p.capacity = c.capacity;
+  p.k_cache = c.k_cache;
+  p.v_cache = c.v_cache;
+  p.kv_bs = c.kv_bs, p.kv_hs = c.kv_hs, p.kv_ss = c.kv_ss;
+  p.log2_units = log2_of(a->d * (c.format == kCacheBf16 ? 2 : 1) / 16);
+  p.k_scale = per_token ? c.k_scale : nullptr;
+  p.v_scale = per_token ? c.v_scale : nullptr;
+  p.g_cache = c.g_cache;
+  p.w_cache = w_cache;
+  p.status = device_status_ptr();
+  if (!p.status) return GCS_ERR_CUDA;
+  return cuda_status(launch_cache_move(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int gcs_set_device_checks(int enable) {

@@ -1,0 +1,344 @@
+// The attention weight that cached tokens gather from a call's query rows:
+//     w_j <- decay * w_j + sum over rows t and the query heads h of the kv head of exp(s_thj - lse_th),
+// with the scores s, masks and sums of exponentials of the paged attention calls.  w_cache is paged
+// like the scales.  The tokens that the rows themselves stand for (the last q_len positions) are
+// written without the old value.
+//
+// Two kernels of one walk over the keys: the first leaves (max, sum) of every row and context
+// segment, the second joins them to the row's sum, walks the keys again and adds up the weights; with
+// the sums given there is only the second.  A warp takes 32 keys a step as the rows of two m16n8k16
+// products, the query rows are the columns: a key's weight is then a sum over a thread's own
+// accumulators and four lanes.  Key dims go from memory straight to the product's registers (a lane's
+// 16 bytes of each 64 dims, the query's dims in the same order).
+#include <algorithm>
+
+#include "kernels.h"
+#include "sm103_ptx.cuh"
+
+namespace gcs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStep = 32;  // keys of a warp's step
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ void record_bad(int* status) { atomicCAS(status, kDevOk, kDevInvalidArg); }
+
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Joins (m2, l2) to (m, l): sums of exponentials relative to their maxima (log2 units).
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+  const float M = fmaxf(m, m2);
+  l = (m == neg_inf() ? 0.f : l * ex2(m - M)) + (m2 == neg_inf() ? 0.f : l2 * ex2(m2 - M));
+  m = M;
+}
+
+// NT: blocks of 8 query rows a walk takes; WRITE: the second kernel.
+template <bool BF16, int D, int NT, bool WRITE>
+__global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsParams p) {
+  constexpr int kRows = NT * 8;
+  constexpr int kChunks = D / 64;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint2* qf = reinterpret_cast<uint2*>(smem);  // [chunk][k-step][row block][lane]
+  float* row_g = reinterpret_cast<float*>(smem + (size_t)kChunks * 4 * NT * 32 * sizeof(uint2));
+  float* row_sum = row_g + kRows;   // WRITE: the row's sum (log2 units), +inf: no such row
+  int* row_last = reinterpret_cast<int*>(row_sum + kRows);  // last key the row sees; -1: none
+  int* row_head = row_last + kRows;
+  float2* warp_ml = reinterpret_cast<float2*>(row_head + kRows);   // first kernel: [warp][row]
+  float* gathered = reinterpret_cast<float*>(row_head + kRows);    // second: [key of the segment]
+
+  const int seg = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  const int q0 = __ldg(p.cu_q + r), q1 = __ldg(p.cu_q + r + 1), L = __ldg(p.seq_lens + r);
+  const int ql = q1 - q0;
+  if (q0 < 0 || q1 < q0 || q1 > p.total_q || ql > p.max_q_len || L < ql || L > p.max_seq_len) {
+    if (tid == 0) record_bad(p.status);
+    return;
+  }
+  const int k_begin = seg * p.seg_len, k_end = min(k_begin + p.seg_len, L);
+  if (k_begin >= k_end || (ql == 0 && p.decay == 1.f)) return;
+  const int G = p.group, nrows = ql * G;
+  const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
+  const bool gates = p.g_cache != nullptr;
+  const float sl2 = p.scale * kLog2e;
+  const float kst = p.format == kCachePerTensor ? __ldg(p.k_scale) : 1.f;
+  auto block_of = [&](int pos) {
+    const int blk = __ldg(table + (pos >> p.log2_block));
+    if (blk >= 0 && blk < p.num_blocks) return blk;
+    record_bad(p.status);
+    return -1;
+  };
+  if (WRITE)
+    for (int i = tid; i < p.seg_len; i += kThreads) gathered[i] = 0.f;
+
+  for (int row0 = 0; row0 < nrows; row0 += kRows) {
+    __syncthreads();
+    // the rows' constants and, in the second kernel, their sums
+    for (int i = tid; i < kRows; i += kThreads) {
+      const int row = row0 + i, t = row / G, head = row - t * G;
+      const bool valid = row < nrows;
+      row_head[i] = head;
+      row_last[i] = valid ? L - ql + t : -1;
+      float gq = 0.f;
+      if (gates && valid) {
+        const int pos = L - ql + t, blk = block_of(pos);
+        if (blk >= 0)
+          gq = __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + head) << p.log2_block) + (pos & (p.block_size - 1)));
+      }
+      row_g[i] = gq;
+      if (WRITE) {
+        float z = __int_as_float(0x7f800000);
+        if (valid) {
+          const size_t at = (size_t)(q0 + t) * p.hq + kvh * G + head;
+          if (p.lse) {
+            z = __ldg(p.lse + (size_t)(kvh * G + head) * p.total_q + q0 + t) * kLog2e;
+          } else {
+            float m = neg_inf(), l = 0.f;
+            const int first = p.window > 0 ? max(0, L - ql + t - p.window + 1) / p.seg_len : 0;
+            const int last = (L - ql + t) / p.seg_len;
+            for (int s = first; s <= last; ++s) {
+              const float2 v = p.part[(size_t)s * p.total_q * p.hq + at];
+              join(m, l, v.x, v.y);
+            }
+            if (p.sink) join(m, l, __ldg(p.sink + kvh * G + head) * kLog2e, 1.f);
+            if (l != 0.f) z = m + log2f(l);  // 0: a row whose every key lies outside the cache
+          }
+        }
+        row_sum[i] = z;
+      }
+    }
+    // the query rows, as the product's second operand: k-step s of a chunk holds this lane's dims
+    // dim0(s) .. + 3 of it
+    for (int i = tid; i < kChunks * 4 * NT * 32; i += kThreads) {
+      const int ln = i & 31, nt = (i >> 5) % NT, s = (i >> 5) / NT % 4, c = (i >> 5) / NT / 4;
+      const int row = row0 + nt * 8 + (ln >> 2), t = row / G, head = row - t * G;
+      const int dim = c * 64 + (BF16 ? (s >> 1) * 32 + (ln & 3) * 8 + (s & 1) * 4 : (ln & 3) * 16 + s * 4);
+      uint2 v = make_uint2(0, 0);
+      if (row < nrows)
+        v = __ldg(reinterpret_cast<const uint2*>(p.q + (size_t)(q0 + t) * p.q_ts + (size_t)(kvh * G + head) * p.q_hs + dim));
+      if (!BF16) v = make_uint2(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y));
+      qf[i] = v;
+    }
+    __syncthreads();
+    const int rows_here = min(kRows, nrows - row0);
+    const int last_max = L - ql + (row0 + rows_here - 1) / G;  // last key any of these rows sees
+    const int last_min = L - ql + row0 / G;
+    const int key_first = p.window > 0 ? max(0, last_min - p.window + 1) : 0;
+
+    float m[NT][2], l[NT][2];
+    if (!WRITE) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = neg_inf(), l[nt][0] = l[nt][1] = 0.f;
+    }
+    for (int key0 = k_begin + warp * kStep; key0 < k_end; key0 += kWarps * kStep) {
+      if (key0 > last_max || key0 + kStep <= key_first) continue;
+      // two pages of 16 keys; this lane's keys are 16 u + g and 16 u + g + 8
+      int blk[2];
+      float ks[2][2];
+      const uint8_t* at[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pos = key0 + 16 * u, slot = pos & (p.block_size - 1);
+        blk[u] = pos < L ? block_of(pos) : -1;
+        at[u] = p.k_cache + (size_t)max(blk[u], 0) * p.kv_bs + (size_t)kvh * p.kv_hs + (size_t)(slot + g) * p.kv_ss + tq * 16;
+        ks[u][0] = ks[u][1] = kst * sl2;
+        if (p.format == kCachePerToken && blk[u] >= 0) {
+          const float* sc = p.k_scale + (((size_t)blk[u] * p.hkv + kvh) << p.log2_block) + slot + g;
+          ks[u][0] = __ldg(sc) * sl2;
+          ks[u][1] = __ldg(sc + 8) * sl2;
+        }
+      }
+      float acc[2][NT][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[u][nt][0] = acc[u][nt][1] = acc[u][nt][2] = acc[u][nt][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        uint32_t a[2][2][BF16 ? 8 : 4];  // [page][key g, g + 8][this lane's 16 dims]
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int x = 0; x < (BF16 ? 2 : 1); ++x) {
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (blk[u] >= 0)
+                v = __ldg(reinterpret_cast<const uint4*>(at[u] + k * 8 * p.kv_ss + c * (BF16 ? 128 : 64) + x * 64));
+              a[u][k][4 * x] = v.x, a[u][k][4 * x + 1] = v.y, a[u][k][4 * x + 2] = v.z, a[u][k][4 * x + 3] = v.w;
+            }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t f[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (BF16) {
+              f[u][0] = a[u][0][2 * s], f[u][2] = a[u][0][2 * s + 1];
+              f[u][1] = a[u][1][2 * s], f[u][3] = a[u][1][2 * s + 1];
+            } else {
+              e4m3x4_to_f16x2x2(a[u][0][s], f[u][0], f[u][2]);
+              e4m3x4_to_f16x2x2(a[u][1][s], f[u][1], f[u][3]);
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 b = qf[((c * 4 + s) * NT + nt) * 32 + lane];
+            mma<BF16>(acc[0][nt], f[0][0], f[0][1], f[0][2], f[0][3], b);
+            mma<BF16>(acc[1][nt], f[1][0], f[1][1], f[1][2], f[1][3], b);
+          }
+        }
+      }
+      const bool inner = key0 + kStep - 1 <= last_min && rows_here == kRows && blk[0] >= 0 && blk[1] >= 0 &&
+                         (p.window == 0 || key0 > last_max - p.window);
+      float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int col = nt * 8 + 2 * tq;
+        float x[2][2][2];  // [page][key][column]
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = acc[u][nt][2 * k + e] * ks[u][k];
+              if (gates && blk[u] >= 0) {
+                const float gk = __ldg(p.g_cache + (((size_t)blk[u] * p.hq + kvh * G + row_head[col + e]) << p.log2_block) +
+                                       ((key0 + 16 * u) & (p.block_size - 1)) + g + 8 * k);
+                v = fmaf(row_g[col + e] - gk, kLog2e, v);
+              }
+              if (!inner) {
+                const int key = key0 + 16 * u + g + 8 * k, lk = row_last[col + e];
+                if (key > lk || blk[u] < 0 || (p.window > 0 && key <= lk - p.window)) v = neg_inf();
+              }
+              x[u][k][e] = v;
+            }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (WRITE) {
+            const float z = row_sum[col + e];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) w[u][k] += ex2(x[u][k][e] - z);
+          } else {
+            const float top = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
+            const float mn = fmaxf(m[nt][e], top), ref = mn == neg_inf() ? 0.f : mn;
+            l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + ((ex2(x[0][0][e] - ref) + ex2(x[0][1][e] - ref)) +
+                                                         (ex2(x[1][0][e] - ref) + ex2(x[1][1][e] - ref)));
+            m[nt][e] = mn;
+          }
+        }
+      }
+      if (WRITE) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            w[u][k] += __shfl_xor_sync(0xffffffffu, w[u][k], 1);
+            w[u][k] += __shfl_xor_sync(0xffffffffu, w[u][k], 2);
+            // the key's only owner, in every round of rows
+            if (tq == 0) gathered[key0 - k_begin + 16 * u + g + 8 * k] += w[u][k];
+          }
+      }
+    }
+    if (!WRITE) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            join(m[nt][e], l[nt][e], __shfl_xor_sync(0xffffffffu, m[nt][e], o),
+                 __shfl_xor_sync(0xffffffffu, l[nt][e], o));
+          if (g == 0) warp_ml[warp * kRows + nt * 8 + 2 * tq + e] = make_float2(m[nt][e], l[nt][e]);
+        }
+      __syncthreads();
+      for (int i = tid; i < rows_here; i += kThreads) {
+        float2 v = warp_ml[i];
+        for (int k = 1; k < kWarps; ++k) join(v.x, v.y, warp_ml[k * kRows + i].x, warp_ml[k * kRows + i].y);
+        const int row = row0 + i, t = row / G, head = row - t * G;
+        p.part[(size_t)seg * p.total_q * p.hq + (size_t)(q0 + t) * p.hq + kvh * G + head] = v;
+      }
+    }
+  }
+  if (WRITE) {
+    __syncthreads();
+    for (int i = tid; i < k_end - k_begin; i += kThreads) {
+      const int pos = k_begin + i, blk = block_of(pos);
+      if (blk < 0) continue;
+      float* w = p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
+      const bool old = p.decay != 0.f && pos < L - ql;
+      *w = old ? fmaf(p.decay, *w, gathered[i]) : gathered[i];
+    }
+  }
+}
+
+template <bool BF16, int D, int NT>
+cudaError_t launch_t(const WeightsParams& p, cudaStream_t s) {
+  constexpr size_t kFixed = (size_t)(D / 64) * 4 * NT * 32 * 8 + 4 * NT * 8 * 4;
+  const dim3 grid(p.segs, p.hkv, p.num_reqs);
+  cudaError_t e = cudaSuccess;
+  if (!p.lse) {
+    constexpr size_t smem = kFixed + kWarps * NT * 8 * 8;
+    auto kern = cache_weights_kernel<BF16, D, NT, false>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kThreads, smem, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const size_t smem = kFixed + (size_t)p.seg_len * 4;
+  auto kern = cache_weights_kernel<BF16, D, NT, true>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+template <bool BF16, int D>
+cudaError_t launch_d(const WeightsParams& p, cudaStream_t s) {
+  return (long long)p.max_q_len * p.group <= 16 ? launch_t<BF16, D, 2>(p, s) : launch_t<BF16, D, 8>(p, s);
+}
+template <bool BF16>
+cudaError_t launch_f(const WeightsParams& p, cudaStream_t s) {
+  return p.d == 64 ? launch_d<BF16, 64>(p, s) : p.d == 128 ? launch_d<BF16, 128>(p, s)
+         : p.d == 256 ? launch_d<BF16, 256>(p, s) : launch_d<BF16, 512>(p, s);
+}
+
+}  // namespace
+
+// Context segments: enough blocks for about eight an SM, of 256 to 2048 keys.
+int cache_weights_segment(int max_seq_len, long long units, int sms) {
+  const long long want = (8LL * sms + units - 1) / units;
+  long long len = (max_seq_len + want - 1) / want;
+  len = std::min(std::max((len + 255) / 256 * 256, 256LL), 2048LL);
+  return (int)len;
+}
+
+cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t s) {
+  return p.format == kCacheBf16 ? launch_f<true>(p, s) : launch_f<false>(p, s);
+}
+
+}  // namespace gcs

@@ -105,7 +105,63 @@ __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
   finish_check(bad, &bad_s, cu_q, num_reqs + 1, cu_out, status);
 }
 
+// The groups of a call with shared prefixes: cu_groups starts at 0, ends at num_reqs and is sorted;
+// a group has at most max_group_q query rows and a prefix of 0 .. max_prefix tokens, whose blocks the
+// table of its first request holds; every request of it has prefix <= seq_len <= prefix + max_suffix.
+// cu_q is the checked copy (ending at 0: an earlier check failed).
+__global__ void __launch_bounds__(kCheckThreads) check_groups_kernel(
+    const int32_t* __restrict__ cu_groups, const int32_t* __restrict__ prefix_lens, int num_groups,
+    const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ table, int num_reqs, int max_blocks,
+    int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix, int max_suffix, int32_t* cu_q,
+    int32_t* __restrict__ groups_out, int* status) {
+  __shared__ int bad_s;
+  if (threadIdx.x == 0) bad_s = cu_q[num_reqs] != total_q;  // already recorded
+  __syncthreads();
+  bool bad = false;
+  if (threadIdx.x == 0) bad = __ldg(cu_groups) != 0 || __ldg(cu_groups + num_groups) != num_reqs;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+  for (int g = warp; g < num_groups; g += nwarps) {
+    const int a = __ldg(cu_groups + g), b = __ldg(cu_groups + g + 1), P = __ldg(prefix_lens + g);
+    if (a < 0 || b < a || b > num_reqs || P < 0 || P > max_prefix) {
+      bad = true;
+      continue;
+    }
+    if (a == b) continue;
+    bad = bad || (long long)cu_q[b] - cu_q[a] > max_group_q;
+    bool fits = true;
+    for (int r = a + lane; r < b; r += 32) {
+      const int L = __ldg(seq_lens + r);
+      fits = fits && P <= L && (long long)L - P <= max_suffix;
+    }
+    if (!__all_sync(0xffffffffu, fits)) {
+      bad = true;
+      continue;
+    }
+    for (int pg = lane; pg < (P + block_size - 1) / block_size; pg += 32) {  // P <= seq_len <= the table
+      const int blk = __ldg(table + (size_t)a * max_blocks + pg);
+      bad = bad || blk < 0 || blk >= num_blocks;
+    }
+  }
+  if (bad) atomicOr(&bad_s, 1);
+  __syncthreads();
+  const bool any = bad_s != 0;
+  if (any && threadIdx.x == 0) atomicCAS(status, kDevOk, kDevInvalidArg);
+  for (int i = threadIdx.x; i <= num_groups; i += blockDim.x) groups_out[i] = any ? 0 : __ldg(cu_groups + i);
+  if (any)
+    for (int i = threadIdx.x; i <= num_reqs; i += blockDim.x) cu_q[i] = 0;
+}
+
 }  // namespace
+
+cudaError_t launch_check_groups(const int32_t* cu_groups, const int32_t* prefix_lens, int num_groups,
+                                const int32_t* seq_lens, const int32_t* table, int num_reqs, int max_blocks,
+                                int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix,
+                                int max_suffix, int32_t* cu_q, int32_t* groups_out, int* status, cudaStream_t s) {
+  check_groups_kernel<<<1, kCheckThreads, 0, s>>>(cu_groups, prefix_lens, num_groups, seq_lens, table, num_reqs,
+                                                  max_blocks, num_blocks, block_size, total_q, max_group_q, max_prefix,
+                                                  max_suffix, cu_q, groups_out, status);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_check_prefill(const int32_t* cu, int num_seqs, int total, int max_seqlen, int32_t* cu_out,
                                  int* status, cudaStream_t s) {

@@ -156,6 +156,16 @@ struct DecodeParams {
   float* part_acc;       // [units, 4*16, 128]
   float* part_ml;        // [units, 4*16, 2]
   int* status;
+  // shared prefixes only
+  int num_groups;
+  const int32_t* cu_groups;    // [num_groups + 1] first request of each group
+  const int32_t* prefix_lens;  // [num_groups]
+  int max_prefix;
+  int total_q;
+  int max_group_q;             // query rows of a group
+  int pre_segs, pre_seg_keys;  // segments of a prefix, keys of one (a multiple of 128)
+  float* pre_acc;              // [pre_segs][total_q][hq][128]
+  float2* pre_ml;              // [pre_segs][total_q][hq]
 };
 
 // fp8 K and V caches as 4-D maps {128 B, slot, kv head, block} (slot and kv head swapped when
@@ -175,6 +185,17 @@ cudaError_t launch_decode_combine(const DecodeParams& p, cudaStream_t s);
 // per request, the kernel writes p.out; otherwise split-K partials and the combine.
 cudaError_t launch_prefill_paged(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s,
                                  const cudaEvent_t* ev_before, const cudaEvent_t* ev_after);
+
+// Decoding behind shared prefixes: p.part_* hold the partials of the tokens behind the prefix,
+// p.pre_* those of the prefix.  bf16 caches: maps of bf16 elements, box 64 dims x 16 slots.
+cudaError_t launch_decode_shared(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s);
+// The groups' arrays of such a call, after launch_check_paged wrote its copy of cu_q: records
+// kDevInvalidArg where they break a precondition (see the public header) and writes groups_out, the copy of
+// cu_groups; on a failure, or when the copy of cu_q is already an empty batch, both copies are zeros.
+cudaError_t launch_check_groups(const int32_t* cu_groups, const int32_t* prefix_lens, int num_groups,
+                                const int32_t* seq_lens, const int32_t* table, int num_reqs, int max_blocks,
+                                int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix,
+                                int max_suffix, int32_t* cu_q, int32_t* groups_out, int* status, cudaStream_t s);
 
 // One CTA that waits on a barrier phase nothing completes; its bounded wait records a
 // timeout in *status and the kernel exits.
@@ -254,6 +275,58 @@ bool cache_gates_need_sums(int max_rows);
 // rope: queries and keys go through the norm and rotation first (rope->k, rope->q; p.k unused).
 cudaError_t launch_cache_append(const CacheParams& p, const RopeParams* rope, cudaStream_t s);
 cudaError_t launch_cache_gather(const CacheParams& p, cudaStream_t s);
+
+// Weight that cached tokens gather from query rows (cache_weights.cu).
+struct WeightsParams {
+  const int32_t *cu_q, *seq_lens, *block_table;
+  int max_blocks, num_blocks, block_size, log2_block;
+  int num_reqs, total_q, max_q_len, max_seq_len;
+  int hq, hkv, group, d;
+  int format;                     // kCache...
+  const uint8_t* k_cache;
+  long long kv_bs, kv_hs, kv_ss;  // byte strides (block, kv head, slot)
+  const float* k_scale;
+  const float* g_cache;           // [num_blocks, hq, block_size] or null
+  const float* sink;              // [hq] or null
+  int window;
+  float scale, decay;
+  const uint16_t* q;              // bf16, element strides (token, head)
+  long long q_ts, q_hs;
+  const float* lse;               // [hq, total_q] natural log, or null: summed here
+  float* w_cache;                 // [num_blocks, hkv, block_size]
+  float2* part;                   // [segs][total_q][hq] (max, sum) of every segment, without lse
+  int seg_len, segs;              // context segments
+  int* status;
+};
+// Tokens of a context segment for `units` (requests x kv heads) on a device of `sms` SMs.
+int cache_weights_segment(int max_seq_len, long long units, int sms);
+cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t s);
+
+// Choice of the cached tokens that stay, and their move to the front (cache_evict.cu).
+struct SelectParams {
+  int num_reqs, hkv;
+  const int32_t *seq_lens, *block_table;
+  int max_blocks, num_blocks, block_size, log2_block, max_seq_len;
+  const float* w_cache;
+  const int32_t *budgets, *first_lens;  // first_lens: or null
+  int recent, max_keep;
+  int32_t *kept, *kept_lens;
+  int* status;
+};
+cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s);
+struct MoveParams {
+  int num_reqs, hkv, group;
+  const int32_t *seq_lens, *block_table, *kept, *kept_lens;
+  int max_blocks, num_blocks, block_size, log2_block, max_keep;
+  long long capacity;             // max_blocks * block_size
+  uint8_t *k_cache, *v_cache;
+  long long kv_bs, kv_hs, kv_ss;  // byte strides (block, kv head, slot)
+  int log2_units;                 // log2 of the 16-byte pieces of a row
+  float *k_scale, *v_scale;       // per token, or null
+  float *g_cache, *w_cache;       // or null
+  int* status;
+};
+cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s);
 
 // Size of the static scratch behind attn_decode_paged_noalloc (64 MiB).
 constexpr size_t kNoAllocScratchBytes = size_t(64) << 20;

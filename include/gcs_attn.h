@@ -6,10 +6,13 @@
  *   attn_bwd           prefill backward (dQ, dK, dV, d log_gate, d sink)
  *   attn_decode_paged  paged single-query / short-query decode over an fp8 e4m3 KV cache
  *   attn_prefill_paged paged chunked prefill (query chunks of any length) over the same cache
+ *   attn_decode_paged_shared  paged decode of requests that share a prefix, which is read once
  * and these make what the four read (library calls with no counterpart in the pages):
  *   attn_qk_norm_rope_fwd, attn_qk_norm_rope_bwd   per-head norm and rotation of q and k
  *   attn_cache_append, attn_cache_append_rope      write of k, v and log gates into the paged cache
  *   attn_cache_gather                              read of the paged cache into packed tensors
+ *   attn_cache_weights, attn_cache_select, attn_cache_compact   eviction: the weight that cached
+ *                                                  tokens gather, the choice of those that stay, their move
  *
  * Sources for what each call computes (page title, section):
  *   [FLA] fla-org/flash-linear-attention issue #1322 "[Perf] Gluon attention backend with
@@ -279,6 +282,39 @@ size_t attn_prefill_paged_workspace(const gcs_decode_args* a);
 int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, size_t workspace_bytes,
                        gcs_stream_t stream);
 
+/* ------------------------------------------------------------------ paged decode behind shared prefixes
+ * attn_decode_paged for requests that share the front of their contexts (a system prompt, one long
+ * document): the same result, with the shared tokens read once for all of them.  Group g is
+ * the requests cu_groups[g] .. cu_groups[g+1]-1; the tokens at positions below prefix_lens[g] are the
+ * same for all of them and are read through the block table of the group's first request.  A
+ * request's own table is read from there on (from the start of the cache block that holds position
+ * prefix_lens[g]; the last, partly shared block may be each request's own copy).  A group may be one
+ * request or none, a prefix 0.
+ * Everything of attn_decode_paged is supported (formats, groups of 16 or 8 heads, block sizes,
+ * strides, q_len 1..4, gates, window, sink), except: segment_len is that of the tokens behind the
+ * prefixes, 0 lets the library choose; and no kernel events are recorded (they stay armed).
+ * Preconditions on the device's arrays, beside those of attn_decode_paged: cu_groups[0] == 0,
+ * cu_groups[num_groups] == num_reqs, sorted; prefix_lens[g] <= max_prefix_len and the seq_len of
+ * every request of the group; seq_len - prefix_lens[g] <= max_suffix_len; at most
+ * max_group_q query rows a group; the first request's table holds the prefix's blocks, whatever the window.
+ * Checked mode checks them; where one fails the call's kernels see an empty batch. */
+typedef struct {
+  int num_groups;              /* >= 1                                                    */
+  const int32_t* cu_groups;    /* device int32 [num_groups + 1]                          */
+  const int32_t* prefix_lens;  /* device int32 [num_groups]                              */
+  int max_group_q;             /* host upper bound on the query rows of a group, 1 .. total_q */
+  int max_prefix_len;          /* host upper bound on prefix_lens, 0 .. max_seq_len      */
+  int max_suffix_len;          /* host upper bound on seq_len - prefix_len, 0 .. max_seq_len */
+} gcs_prefix_args;
+
+/* Workspace bytes (split-K partials of the prefixes and of what lies behind them; the choice of
+ * segments depends on the current device's SM count). */
+size_t attn_decode_paged_shared_workspace(const gcs_decode_args* a, const gcs_prefix_args* x);
+
+/* out: bf16 [total_q, hq, d]. */
+int attn_decode_paged_shared(const gcs_decode_args* a, const gcs_prefix_args* x, void* out, void* workspace,
+                             size_t workspace_bytes, gcs_stream_t stream);
+
 /* ------------------------------------------------------------------ norm and rotation of q and k
  * Between the projections and the attention calls: each query and key head goes through an
  * RMS norm over its d elements and a rotation by its token's position, in one pass:
@@ -410,6 +446,76 @@ int attn_cache_append_rope(const gcs_cache_args* a, const gcs_qk_rope_args* r, c
  * neither the rows nor the gate before the first are not looked at.  The caches, scales and g_cache
  * are only read.  No workspace. */
 int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate, gcs_stream_t stream);
+
+/* ------------------------------------------------------------------ eviction from the paged cache
+ * A cache that outgrows its memory keeps the tokens that the queries look at.  attn_cache_weights adds
+ * up the attention weight of every cached token, attn_cache_select chooses the tokens that stay, and
+ * attn_cache_compact moves them to the front of the request's pages; the blocks behind them are
+ * free.  Each kv head keeps tokens of its own, as many as the others, in their order.  After it:
+ *   - seq_lens of the next calls are kept_lens, and a token's position in the cache is no longer its
+ *     place in the text: attn_cache_append_rope then takes the positions from the caller, and a
+ *     window counts cached tokens.  Cumulative gates stay as they are: their differences
+ *     are still the sums of the log gates between two tokens.
+ *   - blocks whose tokens all stay where they are (a shared prefix within first_lens) are not written.
+ * w_cache is fp32 [num_blocks, hkv, block_size], contiguous and 16-byte aligned, like the scales.
+ * Like the cache calls, these check every index that they take from a device array, in every
+ * mode: a request whose lengths do not fit (cu_q not sorted within 0 .. total_q, q_len above
+ * max_q_len or seq_len, seq_len above max_seq_len or the table) is left out, a key whose block-table entry is
+ * not in [0, num_blocks) is left out, and GCS_ERR_INVALID_ARG is recorded in the device status word.
+ *
+ * Weights.  With the scores s of attn_decode_paged (scale, causal mask at the end of the context,
+ * and gates, window and sink where given), for every cached token j of a request and every kv head:
+ *     w_j = decay * w_j + sum_t sum_h exp(s_thj - lse_th)
+ * over the request's query rows t and the kv head's query heads h, lse_th the row's sum of exponentials
+ * with the sink.  The rows' own tokens (the last q_len positions) start from 0: no earlier call has
+ * written them.  So do all with decay = 0 (w_cache is not read then).  Slots past seq_len are not
+ * touched.  A request without query rows has its weights multiplied by decay.
+ * a: the arguments of attn_decode_paged or attn_prefill_paged; v_cache, v_scale, segment_len
+ * and out_stride are not looked at.  Any q_len in 0 .. seq_len, d 64, 128, 256 or 512, any hq and
+ * hkv with hq % hkv == 0, fp8 or bf16 caches.  With an fp8 cache q is rounded to f16, as in the
+ * attention calls (|q| <= 65504).
+ * lse: fp32 [hq, total_q] natural log, as attn_fwd gives it, or NULL: summed here first, which reads
+ * the keys once more.  decay: finite.
+ * Every sum has a fixed order: repeated calls give the same bits.  The workspace (256-byte aligned)
+ * holds the sums' parts (none with lse); calls that may run at the same time need one each. */
+size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse);
+int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, float* w_cache, void* workspace,
+                       size_t workspace_bytes, gcs_stream_t stream);
+
+/* Choice.  Of the L = seq_lens[r] tokens of request r, n = min(budgets[r], L, max_keep) stay (0 if
+ * that is negative): the last `recent` (the latest of them when n is smaller), then the first
+ * first_lens[r] (the lowest positions), then those of the largest weight; of equal weights (0 and -0 are
+ * equal) the lowest positions, and a NaN or a token whose block lies outside the cache weighs less
+ * than anything.  kept int32 [num_reqs, hkv, max_keep]: their positions in
+ * ascending order, -1 behind them; kept_lens int32 [num_reqs]: n (0 for a request that is left out).
+ * No workspace. */
+typedef struct {
+  int num_reqs;                /* >= 1                                                    */
+  const int32_t* seq_lens;     /* device int32 [num_reqs], each <= max_seq_len           */
+  int max_seq_len;             /* host upper bound on seq_lens, within the table          */
+  const int32_t* block_table;  /* device int32 [num_reqs, max_blocks_per_req]            */
+  int max_blocks_per_req;
+  int num_blocks, block_size;  /* block_size 16 x 2^k, 16..4096                           */
+  int hkv;
+  const float* w_cache;        /* fp32 [num_blocks, hkv, block_size]                     */
+  const int32_t* budgets;      /* device int32 [num_reqs]: tokens that may stay          */
+  const int32_t* first_lens;   /* device int32 [num_reqs], or NULL: 0                    */
+  int recent;                  /* >= 0                                                    */
+  int max_keep;                /* >= 1: row length of kept                                */
+} gcs_select_args;
+int attn_cache_select(const gcs_select_args* a, int32_t* kept, int32_t* kept_lens, gcs_stream_t stream);
+
+/* Move.  For every request r, kv head and i < kept_lens[r], cached position i takes what position
+ * kept[r][kv head][i] holds: K, V, per-token scales, with a->g_cache the gates of the kv head's
+ * query heads, with w_cache the weights (NULL: left).  In place; every source is read before it is
+ * overwritten.  Needs kept[i] >= i (ascending positions are): an entry below i or at or past
+ * seq_lens[r] is left out and recorded, and so is a request with kept_lens outside 0 ..
+ * min(seq_len, max_keep).  Slots from kept_lens[r] on are left as they were.
+ * a: the cache, its index arrays and hq (with gates); a->seq_lens are the lengths before the
+ * move; cu_rows, total_rows, max_rows, k_stride and v_stride are not looked at.  No block
+ * that is written may belong to another request.  No workspace. */
+int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32_t* kept_lens, int max_keep,
+                       float* w_cache, gcs_stream_t stream);
 
 /* ------------------------------------------------------------------ status
  * Per-device status word written by kernels that gave up on a bounded wait.
