@@ -9,7 +9,7 @@ library routines (fp64 ``scaled_dot_product_attention``, ``torch.autograd``,
 ``torch.float8_e4m3fn`` / ``torch.bfloat16`` conversions), closed forms, finite
 differences, invariants and hand-derived fixtures (``tests/golden/``), and on random small
 cases in ``tests/test_oracle_properties.py`` (the functions of ``rows.py`` in
-``tests/test_oracle_rows.py``).  No function is "parity unpinned".
+``tests/test_oracle_rows.py``, those of ``evict.py`` in ``tests/test_oracle_evict.py``).  No function is "parity unpinned".
 """
 from .formats import bf16_round, e4m3_decode  # noqa: F401
 from .attention import (  # noqa: F401
@@ -23,6 +23,7 @@ from .attention import (  # noqa: F401
     gather_kv,
     rel_rms,
 )
+from .evict import compact, select_tokens, token_weights  # noqa: F401
 from .rows import (  # noqa: F401
     cache_gates,
     cache_gather,
