@@ -115,13 +115,13 @@ bool make_page_map_u8(CUtensorMap* m, const void* base, int num_blocks, int hkv,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The same of a bf16 cache with head dim 128: one box is 64 dims of a page (16 rows of 128 bytes).
-bool make_page_map_bf16(CUtensorMap* m, const void* base, int num_blocks, int hkv, int block_size,
+// The same of a bf16 cache with head dim d: one box is 64 dims of a page (16 rows of 128 bytes).
+bool make_page_map_bf16(CUtensorMap* m, const void* base, int num_blocks, int hkv, int block_size, int d,
                         const CacheLayout& l) {
   auto enc = encode_fn();
   if (!enc) return false;
   const bool hi = l.head_inner();
-  cuuint64_t dims[4] = {128, (cuuint64_t)(hi ? hkv : block_size), (cuuint64_t)(hi ? block_size : hkv),
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)(hi ? hkv : block_size), (cuuint64_t)(hi ? block_size : hkv),
                         (cuuint64_t)num_blocks};
   cuuint64_t strides[3] = {(cuuint64_t)(hi ? l.hs : l.ss), (cuuint64_t)(hi ? l.ss : l.hs), (cuuint64_t)l.bs};
   cuuint32_t box[4] = {64, hi ? 1u : 16u, hi ? 16u : 1u, 1};
@@ -129,6 +129,21 @@ bool make_page_map_bf16(CUtensorMap* m, const void* base, int num_blocks, int hk
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D 16-bit map {dim, heads, tokens} whose box is 64 dims of `group` heads of `box_tokens` tokens: rows in
+// the order (token, head), 128-byte swizzle.
+bool make_query_map(CUtensorMap* m, const void* base, bool f16, int dim, int heads, int tokens, const Layout& l,
+                    int group, int box_tokens) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  cuuint64_t strides[2] = {(cuuint64_t)l.hs * 2, (cuuint64_t)l.ts * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)box_tokens};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -1021,7 +1036,7 @@ int attn_decode_paged_shared(const gcs_decode_args* a, const gcs_prefix_args* x,
   DecodeMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   auto map = [&](CUtensorMap* m, const void* base) {
-    return a->kv_format == GCS_KV_BF16 ? make_page_map_bf16(m, base, a->num_blocks, a->hkv, a->block_size, cl)
+    return a->kv_format == GCS_KV_BF16 ? make_page_map_bf16(m, base, a->num_blocks, a->hkv, a->block_size, a->d, cl)
                                        : make_page_map_u8(m, base, a->num_blocks, a->hkv, a->block_size, cl);
   };
   if (!map(&maps.k, a->k_cache) || !map(&maps.v, a->v_cache)) return GCS_ERR_CUDA;
@@ -1447,15 +1462,24 @@ static int check_weights(const gcs_decode_args* a) {
 }
 
 struct WeightsPlan {
+  bool wide = false;  // the long form
   int seg_len = 0, segs = 0;
-  size_t ws = 0;
+  size_t part = 0, rows = 0;  // bytes of the sums' parts; long form: of the rows' constants
+  size_t ws = 0;              // + long form, fp8: the queries in f16
 };
 static bool plan_weights(const gcs_decode_args* a, bool with_lse, WeightsPlan* pl) {
   const int sms = current_sms();
   if (!sms) return false;
-  pl->seg_len = cache_weights_segment(a->max_seq_len, (long long)a->num_reqs * a->hkv, sms);
+  const int group = a->hq / a->hkv;
+  const long long units = (long long)a->num_reqs * a->hkv;
+  const size_t rows = (size_t)a->total_q * a->hq;
+  pl->wide = cache_weights_long(a->max_q_len, group, a->g_cache != nullptr);
+  pl->seg_len = pl->wide ? cache_weights_long_segment(a->max_seq_len, a->max_q_len, group, a->d, units, sms)
+                         : cache_weights_segment(a->max_seq_len, units, sms);
   pl->segs = (a->max_seq_len + pl->seg_len - 1) / pl->seg_len;
-  pl->ws = with_lse ? 0 : round_up((size_t)pl->segs * a->total_q * a->hq * sizeof(float2));
+  pl->part = with_lse ? 0 : round_up(pl->segs * rows * sizeof(float2));
+  pl->rows = pl->wide ? round_up(rows * sizeof(float2)) : 0;
+  pl->ws = pl->part + pl->rows + (pl->wide && a->kv_format != GCS_KV_BF16 ? round_up(rows * a->d * 2) : 0);
   return true;
 }
 
@@ -1525,8 +1549,24 @@ int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, 
   p.part = static_cast<float2*>(workspace);
   p.seg_len = pl.seg_len;
   p.segs = pl.segs;
+  p.kv_head_inner = cl.head_inner() ? 1 : 0;
   p.status = device_status_ptr();
   if (!p.status) return GCS_ERR_CUDA;
+  if (pl.wide) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.rows = reinterpret_cast<float2*>(ws + pl.part);
+    p.q16 = reinterpret_cast<uint16_t*>(ws + pl.part + pl.rows);
+    const bool bf16 = a->kv_format == GCS_KV_BF16;
+    WeightsMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    const Layout packed{(long long)a->hq * a->d, a->d};
+    if (bf16 && !make_page_map_bf16(&maps.k, a->k_cache, a->num_blocks, a->hkv, a->block_size, a->d, cl))
+      return GCS_ERR_CUDA;
+    if (!make_query_map(&maps.q, bf16 ? static_cast<const void*>(a->q) : p.q16, !bf16, a->d, a->hq, a->total_q,
+                        bf16 ? lq : packed, p.group, 128 / p.group))
+      return GCS_ERR_CUDA;
+    return cuda_status(launch_cache_weights_long(p, maps, reinterpret_cast<cudaStream_t>(stream)));
+  }
   return cuda_status(launch_cache_weights(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,685 @@
+// Gathered attention weights (see cache_weights.cu for what is computed) with many query rows to a key:
+// the chunks of a prefill, the last rows of a prompt.  Bound by the exponentials, of which each pair
+// of a row and a key takes one in each of two kernels, beside d multiply-adds on the tensor cores.
+//
+//   sums kernel      S = Q K^T: rows on the accumulator's lanes, so a row's maximum and sum stay in
+//                    its thread; K tiles stream by.  One partial (max, sum) a row and segment.
+//   rows kernel      joins a row's partials and the sink: b = -lse (log2 units), beside its gate.
+//   weights kernel   S^T = K Q^T: keys on the lanes, so a key's weight, the sum over rows of
+//                    2^(scale s + b), stays in its thread too; the query tiles stream by.
+// Neither kernel moves data between threads, and nothing but (max, sum) leaves the SM.
+//
+// Both kernels are one engine: NA resident operand tiles of 128 rows x d (two, one at d 512), streamed
+// tiles of 128 rows x d in a ring of 64-dim stages, and accumulators of 128 x 128 in a double buffer for
+// each resident tile.  A query tile is floor(128 / G) tokens x the G query heads of a kv head; the rows
+// left over are zero.  With an fp8 cache the operands are f16 (codes are exact in it; the queries are
+// rounded to it by a kernel of their own for the streamed side), with a bf16 one bf16.
+//
+// Warp roles (512 threads):
+//   warp 0        streamed tiles by tensor copies (bf16 keys, queries)
+//   warp 1        tcgen05 issuer
+//   warps 2-3     per-column vectors of the streamed tile (scales or b, gates, last visible keys)
+//   warps 4-11    two groups of 128 lanes: sums or weights
+//   warps 12-15   sums kernel over an fp8 cache: e4m3 -> f16 stages, straight from memory
+#include <algorithm>
+
+#include "kernels.h"
+#include "rows.cuh"
+#include "sm103_ptx.cuh"
+
+namespace gcs {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;
+constexpr int kStage = 16384;  // 128 rows x 64 dims of 16 bits
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxGates = 16;          // heads of a kv head, with gates
+constexpr int kGateRow = kTile + 4;    // floats of a head's gates: rows 16 bytes apart in the banks
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ void record_bad(int* status) { atomicCAS(status, kDevOk, kDevInvalidArg); }
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return fma2(a, both(1.f), b); }
+
+__device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+      " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  return pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// 16 e4m3 codes to the two 16-byte units 2 u and 2 u + 1 of row r of a swizzled stage
+__device__ __forceinline__ void put_codes(uint8_t* stage, int r, int u, uint4 v) {
+  uint32_t w[8];
+  e4m3x4_to_f16x2x2(v.x, w[0], w[1]);
+  e4m3x4_to_f16x2x2(v.y, w[2], w[3]);
+  e4m3x4_to_f16x2x2(v.z, w[4], w[5]);
+  e4m3x4_to_f16x2x2(v.w, w[6], w[7]);
+  *reinterpret_cast<uint4*>(stage + sw128_offset(r, 2 * u)) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(stage + sw128_offset(r, 2 * u + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int NCH>
+struct Cfg {
+  static constexpr int NA = NCH == 8 ? 1 : 2;               // resident tiles
+  static constexpr int NST = NCH <= 2 ? 6 : 4;              // stages of the ring
+  static constexpr int OFF_RING = NA * NCH * kStage;
+  static constexpr int OFF_AUX = OFF_RING + NST * kStage;   // [2] x vectors of the streamed tile
+  static constexpr int VECS = 3 * kTile * 4;                // 3 x [128]
+  static constexpr int AUX = VECS + kMaxGates * kGateRow * 4;
+  static constexpr int OFF_BAR = OFF_AUX + 2 * AUX;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * NST + 16) * 8;
+  static constexpr int SMEM = OFF_MISC + 32 + 1024;
+  static_assert(SMEM <= 226 * 1024, "shared memory budget");
+};
+
+struct Request {
+  int q0, ql, L;
+  bool ok;
+};
+__device__ __forceinline__ Request request(const WeightsParams& p, int r) {
+  Request x;
+  x.q0 = __ldg(p.cu_q + r);
+  const int q1 = __ldg(p.cu_q + r + 1);
+  x.ql = q1 - x.q0;
+  x.L = __ldg(p.seq_lens + r);
+  x.ok = !(x.q0 < 0 || q1 < x.q0 || q1 > p.total_q || x.ql > p.max_q_len || x.L < x.ql || x.L > p.max_seq_len);
+  return x;
+}
+// Block of a cached position, -1 (recorded) outside the cache.
+__device__ __forceinline__ int block_of(const WeightsParams& p, const int32_t* table, int pos) {
+  const int blk = __ldg(table + (pos >> p.log2_block));
+  if (blk >= 0 && blk < p.num_blocks) return blk;
+  record_bad(p.status);
+  return -1;
+}
+
+// WRITE false: the sums kernel, true: the weights kernel.  NCH: d / 64.
+template <bool BF16, int NCH, bool WRITE>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_long_kernel(const __grid_constant__ CUtensorMap tm, const WeightsParams p) {
+  using C = Cfg<NCH>;
+  constexpr int NA = C::NA, NST = C::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align_1k(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.y, r = blockIdx.z;
+  const Request rq = request(p, r);
+  if (!rq.ok) {
+    if (threadIdx.x == 0) record_bad(p.status);
+    return;
+  }
+  const int ql = rq.ql, L = rq.L, G = p.group, W = p.window;
+  const int ntok = kTile / G, nrow = ntok * G;  // tokens and rows of a query tile
+  const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
+  const bool gates = p.g_cache != nullptr;
+  const float sl2 = p.scale * kLog2e;
+  const float kst = p.format == kCachePerTensor ? __ldg(p.k_scale) : 1.f;
+
+  // resident rows: tokens a0 .. (sums) or keys a0 .. (weights); streamed tiles b_lo .. b_hi, tile i
+  // from token i ntok or key key0 + 128 i on
+  int a0, b_lo, b_hi, key0 = 0, seg = 0;
+  if (!WRITE) {
+    seg = blockIdx.x % p.segs;
+    a0 = blockIdx.x / p.segs * NA * ntok;
+    key0 = seg * p.seg_len;
+    if (a0 >= ql || key0 >= L) return;
+    const int see = L - ql + min(a0 + NA * ntok, ql) - 1;  // last key that any of the rows sees
+    const int from = W > 0 ? max(0, L - ql + a0 - W + 1) : 0;
+    const int key1 = min(min(key0 + p.seg_len, L), see + 1);
+    b_lo = max(0, from - key0) / kTile;
+    b_hi = key1 > key0 ? (key1 - key0 - 1) / kTile : -1;
+  } else {
+    a0 = blockIdx.x * NA * kTile;
+    if (a0 >= L) return;
+    const int last = min(a0 + NA * kTile, L) - 1;  // last of the keys
+    // token t sees key j iff j <= L - ql + t, and L - ql + t < j + W
+    b_lo = max(0, a0 - (L - ql)) / ntok;
+    b_hi = ql > 0 ? (W > 0 ? (int)min((long long)ql - 1, (long long)last + W - 1 - (L - ql)) : ql - 1) : -1;
+    b_hi = b_hi < 0 ? -1 : b_hi / ntok;
+  }
+  const int nt = max(0, b_hi - b_lo + 1);
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* full = bars;               // [NST]
+  uint64_t* empty = bars + NST;        // [NST]
+  uint64_t* s_full = bars + 2 * NST;   // [4] accumulators: slot 2 x + buffer
+  uint64_t* s_empty = s_full + 4;      // [4]
+  uint64_t* aux_full = s_full + 8;     // [2]
+  uint64_t* aux_empty = s_full + 10;   // [2]
+  uint64_t* drain = s_full + 12;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 8);  // [2] pages of a key tile that are not there
+  const Abort ab{abort_flag, p.status};
+  constexpr bool kCopied = BF16 || WRITE;  // the streamed tiles come by tensor copies
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&full[i], kCopied ? 1 : 4);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&aux_full[i], 2);
+      mbar_init(&aux_empty[i], NA == 2 ? 8 : 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // the resident rows, 16-bit, 128-byte-swizzled, K-major: tile x, chunk c at (x NCH + c) stages
+  if (!WRITE) {
+    constexpr int kUnits = NCH * 8;  // 16-byte units of a row
+    for (int i = threadIdx.x; i < NA * kTile * kUnits; i += kThreads) {
+      const int u = i % kUnits, row = i / kUnits, x = row / kTile, rr = row % kTile;
+      const int t = a0 + x * ntok + rr / G, head = rr % G;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (rr < nrow && t < ql)
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(rq.q0 + t) * p.q_ts + (size_t)(kvh * G + head) * p.q_hs) + u);
+      if (!BF16)
+        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+      *reinterpret_cast<uint4*>(smem + (x * NCH + u / 8) * kStage + sw128_offset(rr, u % 8)) = v;
+    }
+  } else {
+    constexpr int kUnits = NCH * (BF16 ? 8 : 4);
+    for (int i = threadIdx.x; i < NA * kTile * kUnits; i += kThreads) {
+      const int u = i % kUnits, row = i / kUnits, x = row / kTile, rr = row % kTile, pos = a0 + row;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      const int blk = pos < L ? block_of(p, table, pos) : -1;
+      if (blk >= 0)
+        v = __ldg(reinterpret_cast<const uint4*>(p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
+                                                 (size_t)(pos & (p.block_size - 1)) * p.kv_ss) + u);
+      if (BF16) *reinterpret_cast<uint4*>(smem + (x * NCH + u / 8) * kStage + sw128_offset(rr, u % 8)) = v;
+      else put_codes(smem + (x * NCH + u / 4) * kStage, rr, u % 4, v);
+    }
+    // rows of the streamed tiles that no copy writes
+    for (int i = threadIdx.x; i < NST * (kTile - nrow) * 8; i += kThreads) {
+      const int st = i / ((kTile - nrow) * 8), k = i % ((kTile - nrow) * 8);
+      *reinterpret_cast<uint4*>(smem + C::OFF_RING + st * kStage + nrow * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto ring_next = [&](uint32_t& stage, uint32_t& phase) {
+    if (++stage == NST) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+
+  if (warp == 0) {
+    if (kCopied) {
+      if (lane == 0) prefetch_tmap(&tm);
+      uint32_t stage = 0, phase = 0;
+      for (int n = 0; n < nt; ++n) {
+        const int b = b_lo + n;
+        int blk = -1, cy = 0, cz = 0, tok = 0;
+        uint32_t bytes = 64 * 2 * nrow;
+        if (WRITE) {
+          tok = rq.q0 + b * ntok;
+        } else {  // lane = page
+          const int pos = key0 + b * kTile + lane * 16;
+          if (lane < 8 && pos < L) blk = block_of(p, table, pos);
+          const int sub = pos & (p.block_size - 1);
+          cy = p.kv_head_inner ? kvh : sub;
+          cz = p.kv_head_inner ? sub : kvh;
+          bytes = __popc(__ballot_sync(0xffffffffu, blk >= 0)) * 2048;
+        }
+        bool okl = true;
+        for (int c = 0; c < NCH && okl; ++c) {
+          okl = wait_bar(&empty[stage], phase ^ 1, ab);
+          okl = __all_sync(0xffffffffu, okl);
+          if (!okl) break;
+          if (lane == 0) mbar_expect_tx(&full[stage], bytes);
+          __syncwarp();
+          uint8_t* st = smem + C::OFF_RING + stage * kStage;
+          if (WRITE) {
+            if (lane == 0) tma_load_3d(st, &tm, &full[stage], 64 * c, kvh * G, tok);
+          } else if (blk >= 0) {
+            tma_load_4d(st + lane * 2048, &tm, &full[stage], 64 * c, cy, cz, blk);
+          }
+          ring_next(stage, phase);
+        }
+        if (!okl) break;
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = BF16 ? idesc_bf16(kTile, kTile, false, false) : idesc_f16(kTile, kTile, false, false);
+      const uint64_t dA = sdesc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t dB = sdesc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
+      constexpr uint32_t kSt16 = kStage >> 4;
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int n = 0; n < nt && ok; ++n) {
+        const int s0 = NA == 2 ? (n & 1) : (n & 1) * 2 + ((n >> 1) & 1);  // slot of resident tile 0
+        const uint32_t use = NA == 2 ? n >> 1 : n >> 2;
+        ok = wait_bar(&s_empty[s0], (use & 1) ^ 1, ab) && (NA == 1 || wait_bar(&s_empty[s0 + 2], (use & 1) ^ 1, ab));
+        for (int c = 0; c < NCH && ok; ++c) {
+          ok = wait_bar(&full[stage], phase, ab);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < NA; ++x) {
+            const uint64_t a = dA + (x * NCH + c) * kSt16, b = dB + stage * kSt16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_ss(tmem + (s0 + 2 * x) * kTile, a + 2 * k, b + 2 * k, id, (c | k) != 0);
+          }
+          mma_commit(&empty[stage]);
+          ring_next(stage, phase);
+        }
+        if (ok) {
+          mma_commit(&s_full[s0]);
+          if (NA == 2) mma_commit(&s_full[s0 + 2]);
+        }
+      }
+      if (!ok) {
+        mma_commit(drain);
+        mbar_wait(drain, 0, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- per-column vectors
+    const int c = threadIdx.x - 64;  // 0 .. 63
+    for (int n = 0; n < nt; ++n) {
+      const int a = n & 1;
+      if (!wait_bar(&aux_empty[a], ((n >> 1) & 1) ^ 1, ab)) break;
+      float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
+      uint32_t bad = 0;
+      for (int i = c; i < kTile; i += 64) {
+        if (WRITE) {
+          const int t = (b_lo + n) * ntok + i / G, head = i % G;
+          const bool valid = i < nrow && t < ql;
+          float2 v = make_float2(neg_inf(), 0.f);
+          if (valid) v = __ldg(p.rows + (size_t)(rq.q0 + t) * p.hq + kvh * G + head);
+          ax[i] = v.x;
+          ax[kTile + i] = v.y;
+          reinterpret_cast<int*>(ax)[2 * kTile + i] = valid ? L - ql + t : -1;
+        } else {
+          const int pos = key0 + (b_lo + n) * kTile + i;
+          const int blk = pos < L ? block_of(p, table, pos) : -1;
+          const int slot = pos & (p.block_size - 1);
+          float ks = kst;
+          if (blk >= 0 && p.format == kCachePerToken)
+            ks = __ldg(p.k_scale + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot);
+          ax[i] = ks * sl2;
+          if (blk < 0 && pos < L) bad |= 1u << (i >> 4);
+          if (gates)
+            for (int h = 0; h < G; ++h)
+              ax[3 * kTile + h * kGateRow + i] =
+                  blk >= 0 ? __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h) << p.log2_block) + slot) : 0.f;
+        }
+      }
+      if (!WRITE) {
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        // each warp has four of the tile's eight pages
+        if (lane == 0) reinterpret_cast<uint8_t*>(bad_pages + a)[warp - 2] = (uint8_t)bad;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&aux_full[a]);
+    }
+    __syncwarp();
+  } else if (warp < 12) {
+    // ---------------------------------------------------------- sums or weights, group y
+    const int y = (warp - 4) >> 2, quarter = warp & 3;
+    const int rr = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const int x = NA == 2 ? y : 0;  // its resident tile; with one, the groups take the streamed tiles in turn
+    // sums: the row's token and last visible key; weights: the key and its constants
+    const int t = a0 + x * ntok + rr / G, head = rr % G;
+    const bool row_ok = rr < nrow && t < ql;
+    const int pos = WRITE ? a0 + x * kTile + rr : L - ql + min(t, ql - 1);
+    float gi = 0.f, ks = 0.f;
+    float gk[kMaxGates];
+    int blk = -1;
+    const bool repeat = gates && (kMaxGates % G) == 0;  // column i has head i % 16 % G
+    if (WRITE) {
+      blk = pos < L ? block_of(p, table, pos) : -1;
+      if (blk >= 0) {
+        const int slot = pos & (p.block_size - 1);
+        ks = kst * sl2;
+        if (p.format == kCachePerToken) ks = __ldg(p.k_scale + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot) * sl2;
+        if (gates) {
+#pragma unroll
+          for (int h = 0; h < kMaxGates; ++h)
+            gk[h] = __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h % G) << p.log2_block) + slot);
+        }
+      }
+      if (blk < 0 || !gates) {
+#pragma unroll
+        for (int h = 0; h < kMaxGates; ++h) gk[h] = 0.f;
+      }
+    } else if (gates && row_ok) {
+      const int b = block_of(p, table, pos);
+      if (b >= 0)
+        gi = __ldg(p.g_cache + (((size_t)b * p.hq + kvh * G + head) << p.log2_block) + (pos & (p.block_size - 1)));
+    }
+    float m = neg_inf();
+    float2 acc[4];  // sums, or the weight
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+    bool ok = true;
+    for (int n = 0; n < nt; ++n) {
+      if (NA == 1 && (n & 1) != y) continue;
+      const int a = n & 1;
+      const int slot = NA == 2 ? x * 2 + (n & 1) : (n & 1) * 2 + ((n >> 1) & 1);
+      const uint32_t use = NA == 2 ? n >> 1 : n >> 2;
+      ok = wait_bar(&aux_full[a], (n >> 1) & 1, ab) && wait_bar(&s_full[slot], use & 1, ab);
+      if (!ok) break;
+      tc_fence_after();
+      const float* ax = reinterpret_cast<const float*>(smem + C::OFF_AUX + a * C::AUX);
+      const uint32_t tS = tmem + lane_off + slot * kTile;
+      if constexpr (!WRITE) {
+        const int j0 = key0 + (b_lo + n) * kTile;
+        const uint32_t bw = bad_pages[a], bad = (bw | bw >> 8) & 0xffu;
+        const int first_t = a0 + x * ntok, last_t = min(first_t + ntok, ql) - 1;
+        const bool need_mask = j0 + kTile - 1 > L - ql + first_t || bad != 0 || (W > 0 && j0 <= L - ql + last_t - W);
+        const float4* g4 = reinterpret_cast<const float4*>(ax + 3 * kTile + head * kGateRow);
+        const float4* ks4 = reinterpret_cast<const float4*>(ax);
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t sv[32];
+          tmem_ld32(tS + cc * 32, sv);
+          tmem_ld_wait();
+          float2 v[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 k4 = ks4[cc * 8 + q];
+            v[2 * q] = make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1]));
+            v[2 * q + 1] = make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3]));
+            if (gates) {
+              const float4 g = g4[cc * 8 + q];
+              const float2 ga = make_float2((gi - g.x) * kLog2e, (gi - g.y) * kLog2e);
+              const float2 gb = make_float2((gi - g.z) * kLog2e, (gi - g.w) * kLog2e);
+              v[2 * q] = fma2(v[2 * q], make_float2(k4.x, k4.y), ga);
+              v[2 * q + 1] = fma2(v[2 * q + 1], make_float2(k4.z, k4.w), gb);
+            } else {
+              v[2 * q] = mul2(v[2 * q], make_float2(k4.x, k4.y));
+              v[2 * q + 1] = mul2(v[2 * q + 1], make_float2(k4.z, k4.w));
+            }
+          }
+          if (need_mask) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int j = j0 + cc * 32 + 2 * q;
+              const bool off = bad >> (cc * 2 + q / 8) & 1;
+              if (off || j > pos || (W > 0 && j <= pos - W)) v[q].x = neg_inf();
+              if (off || j + 1 > pos || (W > 0 && j + 1 <= pos - W)) v[q].y = neg_inf();
+            }
+          }
+          float mx = neg_inf();
+#pragma unroll
+          for (int q = 0; q < 16; ++q) mx = fmaxf(mx, fmaxf(v[q].x, v[q].y));
+          // the reference moves only when the maximum grows by more than 2^8: sums of 2^8 per term stay
+          // far from fp32's limits
+          if (mx > m + 8.f) {
+            const float f = ex2(m - mx);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = mul2(acc[e], both(f));
+            m = mx;
+          }
+          const float ref = m == neg_inf() ? 0.f : -m;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 z = add2(v[q], both(ref));
+            acc[q & 3] = add2(acc[q & 3], make_float2(ex2(z.x), ex2(z.y)));
+          }
+        }
+      } else {
+        const int t0 = (b_lo + n) * ntok;
+        const int j_lo = a0 + x * kTile, j_hi = j_lo + kTile - 1;
+        const bool need_mask = t0 + ntok > ql || j_hi > L - ql + t0 || (W > 0 && j_lo <= L - ql + t0 + ntok - 1 - W);
+        const float4* b4 = reinterpret_cast<const float4*>(ax);
+        const float4* gi4 = reinterpret_cast<const float4*>(ax + kTile);
+        const int* see = reinterpret_cast<const int*>(ax) + 2 * kTile;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t sv[32];
+          tmem_ld32(tS + cc * 32, sv);
+          tmem_ld_wait();
+          float2 v[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float4 b = b4[cc * 8 + q];
+            if (gates) {
+              const float4 g = gi4[cc * 8 + q];
+              float k4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                k4[e] = gk[(4 * q + e) % kMaxGates];
+                if (!repeat) {  // groups that 16 is no multiple of
+                  const int h = (cc * 32 + 4 * q + e) % G;
+#pragma unroll
+                  for (int w = 0; w < kMaxGates; ++w)
+                    if (h == w) k4[e] = gk[w];
+                }
+              }
+              b.x = fmaf(g.x - k4[0], kLog2e, b.x);
+              b.y = fmaf(g.y - k4[1], kLog2e, b.y);
+              b.z = fmaf(g.z - k4[2], kLog2e, b.z);
+              b.w = fmaf(g.w - k4[3], kLog2e, b.w);
+            }
+            v[2 * q] = fma2(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])), both(ks),
+                            make_float2(b.x, b.y));
+            v[2 * q + 1] = fma2(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])), both(ks),
+                                make_float2(b.z, b.w));
+          }
+          if (need_mask) {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int2 lk = *reinterpret_cast<const int2*>(see + cc * 32 + 2 * q);
+              if (pos > lk.x || (W > 0 && pos <= lk.x - W)) v[q].x = neg_inf();
+              if (pos > lk.y || (W > 0 && pos <= lk.y - W)) v[q].y = neg_inf();
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[q & 3] = add2(acc[q & 3], make_float2(ex2(v[q].x), ex2(v[q].y)));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s_empty[slot]);
+        mbar_arrive(&aux_empty[a]);
+      }
+    }
+    const float2 s2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+    float sum = s2.x + s2.y;
+    if (NA == 1) {  // the second group's part by shared memory (the aux vectors are done with)
+      float2* other = reinterpret_cast<float2*>(smem + C::OFF_RING);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (y == 1) other[rr] = make_float2(m, sum);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (y == 0) {
+        const float2 o = other[rr];
+        if (WRITE) {
+          sum += o.y;
+        } else {
+          const float M = fmaxf(m, o.x);
+          sum = (m == neg_inf() ? 0.f : sum * ex2(m - M)) + (o.x == neg_inf() ? 0.f : o.y * ex2(o.x - M));
+          m = M;
+        }
+      }
+    }
+    if (!*abort_flag && (NA == 2 || y == 0)) {
+      if (!WRITE) {
+        if (row_ok)
+          p.part[((size_t)seg * p.total_q + rq.q0 + t) * p.hq + kvh * G + head] = make_float2(m, sum);
+      } else if (blk >= 0) {
+        float* w = p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
+        *w = p.decay != 0.f && pos < L - ql ? fmaf(p.decay, *w, sum) : sum;
+      }
+    }
+  } else if (!kCopied) {
+    // ---------------------------------------------------------- e4m3 -> f16 stages (warps 12-15)
+    // thread c takes the 16-byte piece c & 3 of keys 32 i + c / 4; two chunks are on their way
+    // while one is converted
+    const int c = threadIdx.x - 384, piece = c & 3, row = c >> 2;
+    const int total = nt * NCH;
+    uint4 ring[2][4];
+    auto fetch = [&](int q, uint4 (&d)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        d[i] = make_uint4(0, 0, 0, 0);
+        const int pos = key0 + (b_lo + q / NCH) * kTile + 32 * i + row;
+        if (q < total && pos < L) {
+          const int blk = __ldg(table + (pos >> p.log2_block));  // the vectors' warps record it
+          if (blk >= 0 && blk < p.num_blocks)
+            d[i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
+                                                        (size_t)(pos & (p.block_size - 1)) * p.kv_ss) +
+                         (q % NCH) * 4 + piece);
+        }
+      }
+    };
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    auto store = [&](const uint4 (&d)[4]) {
+      ok = wait_bar(&empty[stage], phase ^ 1, ab);
+      if (!ok) return;
+      uint8_t* st = smem + C::OFF_RING + stage * kStage;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) put_codes(st, 32 * i + row, piece, d[i]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
+      ring_next(stage, phase);
+    };
+    fetch(0, ring[0]);
+    fetch(1, ring[1]);
+    for (int q = 0; q < total && ok; q += 2) {
+      store(ring[0]);
+      fetch(q + 2, ring[0]);
+      if (!ok || q + 1 >= total) break;
+      store(ring[1]);
+      fetch(q + 3, ring[1]);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {  // copies in flight land before the shared memory is given back
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// (b, own gate) of every query row: b = -log2 of its sum of exponentials, joined over the segments it
+// sees.
+__global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p) {
+  const int r = blockIdx.y;
+  const Request rq = request(p, r);
+  if (!rq.ok) return;
+  const long long n = (long long)rq.ql * p.hq;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const int t = (int)(i / p.hq), h = (int)(i % p.hq), pos = rq.L - rq.ql + t;
+    const size_t at = (size_t)(rq.q0 + t) * p.hq + h;
+    float b = neg_inf();
+    if (p.lse) {
+      b = -__ldg(p.lse + (size_t)h * p.total_q + rq.q0 + t) * kLog2e;
+    } else {
+      float m = neg_inf(), l = 0.f;
+      auto join = [&](float m2, float l2) {
+        const float M = fmaxf(m, m2);
+        l = (m == neg_inf() ? 0.f : l * ex2(m - M)) + (m2 == neg_inf() ? 0.f : l2 * ex2(m2 - M));
+        m = M;
+      };
+      const int first = p.window > 0 ? max(0, pos - p.window + 1) / p.seg_len : 0;
+      for (int s = first; s <= pos / p.seg_len; ++s) {
+        const float2 v = p.part[(size_t)s * p.total_q * p.hq + at];
+        join(v.x, v.y);
+      }
+      if (p.sink) join(__ldg(p.sink + h) * kLog2e, 1.f);
+      if (l != 0.f) b = -(m + log2f(l));  // 0: a row whose every key lies outside the cache
+    }
+    float g = 0.f;
+    if (p.g_cache) {
+      const int blk = block_of(p, p.block_table + (size_t)r * p.max_blocks, pos);
+      if (blk >= 0) g = __ldg(p.g_cache + (((size_t)blk * p.hq + h) << p.log2_block) + (pos & (p.block_size - 1)));
+    }
+    p.rows[at] = make_float2(b, g);
+  }
+}
+
+// The queries in f16, [total_q, hq, d].
+__global__ void __launch_bounds__(256) queries_f16_kernel(const WeightsParams p) {
+  const int units = p.d / 8;
+  const long long n = (long long)p.total_q * p.hq * units;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const long long row = i / units, t = row / p.hq, h = row % p.hq;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_ts + h * p.q_hs) + i % units);
+    reinterpret_cast<uint4*>(p.q16)[i] =
+        make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+  }
+}
+
+template <bool BF16, int NCH, bool WRITE>
+cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, cudaStream_t s) {
+  using C = Cfg<NCH>;
+  auto kern = weights_long_kernel<BF16, NCH, WRITE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const int per = WRITE ? C::NA * kTile : C::NA * (kTile / p.group);
+  const int n = WRITE ? (p.max_seq_len + per - 1) / per : (p.max_q_len + per - 1) / per * p.segs;
+  kern<<<dim3(n, p.hkv, p.num_reqs), kThreads, C::SMEM, s>>>(map, p);
+  return cudaGetLastError();
+}
+template <bool BF16, int NCH>
+cudaError_t launch_d(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
+  cudaError_t e;
+  if (!p.lse && (e = launch_t<BF16, NCH, false>(p, maps.k, s)) != cudaSuccess) return e;
+  const long long rows = (long long)p.max_q_len * p.hq;
+  weights_rows_kernel<<<dim3((unsigned)std::min(1024LL, (rows + 255) / 256), p.num_reqs), 256, 0, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_t<BF16, NCH, true>(p, maps.q, s);
+}
+template <bool BF16>
+cudaError_t launch_f(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
+  return p.d == 64 ? launch_d<BF16, 1>(p, maps, s) : p.d == 128 ? launch_d<BF16, 2>(p, maps, s)
+         : p.d == 256 ? launch_d<BF16, 4>(p, maps, s) : launch_d<BF16, 8>(p, maps, s);
+}
+
+}  // namespace
+
+// From more than 64 rows a (request, kv head) on, where the tensor cores' tiles are half full.
+bool cache_weights_long(int max_q_len, int group, bool gates) {
+  return (long long)max_q_len * group > 64 && group <= kTile && (!gates || group <= kMaxGates);
+}
+
+// Context segments of the sums kernel: enough blocks for one an SM, of 128 tokens or more.
+int cache_weights_long_segment(int max_seq_len, int max_q_len, int group, int d, long long units, int sms) {
+  const long long per = (long long)(d == 512 ? 1 : 2) * (kTile / group);
+  const long long blocks = (max_q_len + per - 1) / per * units;
+  const long long want = std::max(1LL, 2LL * sms / blocks);
+  const long long tiles = (max_seq_len + kTile - 1) / kTile;
+  return (int)((tiles + want - 1) / want * kTile);
+}
+
+cudaError_t launch_cache_weights_long(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
+  if (p.format == kCacheBf16) return launch_f<true>(p, maps, s);
+  const long long units = (long long)p.total_q * p.hq * (p.d / 8);
+  queries_f16_kernel<<<(unsigned)std::min(4096LL, (units + 255) / 256), 256, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_f<false>(p, maps, s);
+}
+
+}  // namespace gcs

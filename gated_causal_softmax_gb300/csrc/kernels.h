@@ -296,8 +296,20 @@ struct WeightsParams {
   float* w_cache;                 // [num_blocks, hkv, block_size]
   float2* part;                   // [segs][total_q][hq] (max, sum) of every segment, without lse
   int seg_len, segs;              // context segments
+  int kv_head_inner;              // as in DecodeParams
+  float2* rows;                   // long form: [total_q][hq] (-lse in log2 units, own gate)
+  uint16_t* q16;                  // long form, fp8: the queries in f16, [total_q, hq, d]
   int* status;
 };
+// The long form's maps.  k (bf16 caches): {dim, slot, kv head, block}, box 64 dims of a page; q: {dim, head,
+// token} of the queries (bf16 caches) or of q16, box 64 dims x the heads of a kv head x 128 / heads tokens.
+struct WeightsMaps {
+  CUtensorMap k, q;
+};
+// Whether a call takes the long form, and the tokens of its context segments.
+bool cache_weights_long(int max_q_len, int group, bool gates);
+int cache_weights_long_segment(int max_seq_len, int max_q_len, int group, int d, long long units, int sms);
+cudaError_t launch_cache_weights_long(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s);
 // Tokens of a context segment for `units` (requests x kv heads) on a device of `sms` SMs.
 int cache_weights_segment(int max_seq_len, long long units, int sms);
 cudaError_t launch_cache_weights(const WeightsParams& p, cudaStream_t s);
