@@ -23,8 +23,9 @@ __device__ __forceinline__ void record_bad(int* status) { atomicCAS(status, kDev
 // ------------------------------------------------------------------------------------ choice
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kCopies = 8;           // of the histogram, one for every eighth lane
+constexpr int kBins = 2048;          // digits of 11, 11 and 10 bits
 constexpr int kMaxSlice = 40 * 1024; // keys of a block in shared memory
+constexpr int kRanked = 512;         // keys up to which each counts those above it
 
 // Weights as integers of the same order: NaN below everything, -0 equal to 0.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -36,20 +37,26 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 
 // One cluster for a (request, kv head): its blocks take equal slices of the positions between the
 // first and the last ones, as quads of four neighbouring positions (one vector load: a quad lies in
-// one cache block).  The key of rank c from the top is found by four histograms of 8 bits, each
+// one cache block).  The key of rank c from the top is found by three histograms of 11, 11 and 10 bits, each
 // added up over the cluster; a last walk in the order of the positions writes those above it and as
-// many equal ones as are still missing.  HELD: the slice's keys stay in shared memory; otherwise
-// (slices past kMaxSlice) each walk reads the weights again.
-template <bool HELD>
+// many equal ones as are still missing.  11 bits of a positive float are its exponent and two bits
+// more, so few of a warp's keys meet in a bin, and the second histogram is of few keys.
+// HELD: the slice's keys stay in shared memory; otherwise (slices past kMaxSlice) each walk reads the
+// weights again.  CLUSTER: more than one block.
+template <bool HELD, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint4 keys[];
-  __shared__ uint32_t hist[256 * kCopies];
-  __shared__ uint32_t bins[256];
-  __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
   __shared__ uint32_t tot_gt, tot_eq;
   __shared__ uint32_t digit_s, above_s;
   cg::cluster_group cluster = cg::this_cluster();
-  const int cs = cluster.num_blocks(), rank = cluster.block_rank();
+  const int cs = CLUSTER ? cluster.num_blocks() : 1, rank = CLUSTER ? cluster.block_rank() : 0;
+  auto all_sync = [&]() {
+    if (CLUSTER) cluster.sync();
+    else __syncthreads();
+  };
+  auto of_rank = [&](uint32_t* x, int k) { return CLUSTER ? *cluster.map_shared_rank(x, k) : *x; };
   const int row = blockIdx.x / cs;
   const int r = row / p.hkv, h = row % p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -78,78 +85,120 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
     for (int i = rank * kSelThreads + tid; i < need; i += cs * kSelThreads) out[lead + i] = lead + i;
     return;
   }
+  const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
+  auto weights = [&](int pos) -> const float* {  // null: never looked at, as if nothing weighed less
+    const int blk = __ldg(table + (pos >> p.log2_block));
+    if (blk < 0 || blk >= p.num_blocks) {
+      record_bad(p.status);
+      return nullptr;
+    }
+    return p.w_cache + (((size_t)blk * p.hkv + h) << p.log2_block) + (pos & (p.block_size - 1));
+  };
+
+  if (end - lead <= kRanked) {
+    // few keys: each counts those that go before it
+    if (rank != 0) return;
+    const int m = end - lead;
+    uint32_t mine = 0;
+    if (tid < m) {
+      const float* w = weights(lead + tid);
+      mine = w ? order_key(__ldg(w)) : 0u;
+    }
+    hist[tid] = mine;
+    __syncthreads();
+    int before = 0;
+    for (int j = 0; j < m; ++j) {
+      const uint32_t k = hist[j];
+      before += k > mine || (k == mine && j < tid);
+    }
+    const bool stays = tid < m && before < need;
+    const uint32_t votes = __ballot_sync(0xffffffffu, stays);
+    if (lane == 0) warp_a[warp] = __popc(votes);
+    __syncthreads();
+    int at = lead + __popc(votes & ((1u << lane) - 1));
+    for (int w = 0; w < warp; ++w) at += warp_a[w];
+    if (stays) out[at] = lead + tid;
+    return;
+  }
 
   const int q0 = lead >> 2, nq = ((end + 3) >> 2) - q0;  // quads, the first and last partly outside
   const int per = (nq + cs - 1) / cs;
   const int a = q0 + min(nq, rank * per), b = q0 + min(nq, rank * per + per);
-  const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
   auto load = [&](int q) -> uint4 {
-    const int pos = q * 4;
-    const int blk = __ldg(table + (pos >> p.log2_block));
-    if (blk < 0 || blk >= p.num_blocks) {  // never looked at: as if nothing weighed less
-      record_bad(p.status);
-      return make_uint4(0, 0, 0, 0);
-    }
-    const float4 w = __ldg(reinterpret_cast<const float4*>(
-        p.w_cache + (((size_t)blk * p.hkv + h) << p.log2_block) + (pos & (p.block_size - 1))));
+    const float* at = weights(q * 4);
+    if (!at) return make_uint4(0, 0, 0, 0);
+    const float4 w = __ldg(reinterpret_cast<const float4*>(at));
     return make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
   };
   auto quad = [&](int q) -> uint4 { return HELD ? keys[q - a] : load(q); };
-  if (HELD) {
-    for (int q = a + tid; q < b; q += kSelThreads) keys[q - a] = load(q);
-  }
+  for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+  __syncthreads();
 
   uint32_t prefix = 0, left = need;  // bits found so far; how many are wanted among the keys with them
 #pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256 * kCopies; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int q = a + tid; q < b; q += kSelThreads) {
-      const uint4 k = quad(q);
+  for (int round = 0; round < 3; ++round) {
+    const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
+    const uint32_t digits = round == 2 ? 1023 : 2047;
+    const uint32_t mask = round == 0 ? 0u : round == 1 ? 0xffe00000u : 0xfffffc00u;
+    auto count = [&](int q, const uint4& k) {
       const uint32_t e[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if ((e[j] & mask) == prefix && q * 4 + j >= lead && q * 4 + j < end)
-          atomicAdd(&hist[((e[j] >> shift) & 255) * kCopies + (lane & (kCopies - 1))], 1u);
+          atomicAdd(&hist[(e[j] >> shift) & digits], 1u);
+    };
+    if (HELD && round == 0) {  // the only read of the weights
+      for (int q = a + tid; q < b; q += 4 * kSelThreads) {
+        uint4 k[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (q + u * kSelThreads < b) k[u] = load(q + u * kSelThreads);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (q + u * kSelThreads < b) {
+            keys[q + u * kSelThreads - a] = k[u];
+            count(q + u * kSelThreads, k[u]);
+          }
+      }
+    } else {
+      for (int q = a + tid; q < b; q += kSelThreads) count(q, quad(q));
     }
+    all_sync();
+    // thread's 4 bins from the top: 2047 - 4 tid .. 2044 - 4 tid
+    uint4 c = make_uint4(0, 0, 0, 0);
+    const int top = kBins / 4 - 1 - tid;
+    for (int k = 0; k < cs; ++k) {
+      const uint4* hk = reinterpret_cast<const uint4*>(CLUSTER ? cluster.map_shared_rank(hist, k) : hist);
+      const uint4 v = hk[top];
+      c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
+    }
+    const uint32_t sum = c.x + c.y + c.z + c.w;
+    uint32_t before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += t;
+    }
+    if (lane == 31) warp_a[warp] = before;
+    before -= sum;
     __syncthreads();
-    if (tid < 256) {
-      uint32_t s = 0;
+    for (int w = 0; w < warp; ++w) before += warp_a[w];
+    if (before < left && before + sum >= left) {  // one thread's
+      const uint32_t v[4] = {c.w, c.z, c.y, c.x};
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) s += hist[tid * kCopies + ((j + tid) & (kCopies - 1))];
-      bins[tid] = s;
-    }
-    cluster.sync();
-    if (warp == 0) {
-      // lane's 8 bins from the top: bins 255 - 8 lane .. 248 - 8 lane
-      uint32_t c[8], s = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c[j] = 0;
-        for (int k = 0; k < cs; ++k) c[j] += *cluster.map_shared_rank(&bins[255 - 8 * lane - j], k);
-        s += c[j];
-      }
-      uint32_t before = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += t;
-      }
-      before -= s;  // keys above this lane's bins
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (before < left && before + c[j] >= left) {
-          digit_s = 255 - 8 * lane - j;
+      for (int j = 0; j < 4; ++j) {
+        if (before < left && before + v[j] >= left) {
+          digit_s = kBins - 1 - 4 * tid - j;
           above_s = before;
         }
-        before += c[j];
+        before += v[j];
       }
     }
-    __syncthreads();
+    all_sync();  // the bins are read
     prefix |= digit_s << shift;
     left -= above_s;
-    cluster.sync();  // the bins are read
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
   }
 
   // prefix is the key of rank `need`; `left` of those equal to it stay
@@ -169,28 +218,30 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
-    warp_gt[warp] = gt;
-    warp_eq[warp] = eq;
+    warp_a[warp] = gt;
+    warp_b[warp] = eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t g = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      g += warp_gt[w];
-      e += warp_eq[w];
+  if (CLUSTER) {
+    if (tid == 0) {
+      uint32_t g = 0, e = 0;
+      for (int w = 0; w < kSelWarps; ++w) {
+        g += warp_a[w];
+        e += warp_b[w];
+      }
+      tot_gt = g;
+      tot_eq = e;
     }
-    tot_gt = g;
-    tot_eq = e;
+    all_sync();
   }
-  cluster.sync();
   uint32_t gt0 = 0, eq0 = 0;
   for (int k = 0; k < rank; ++k) {
-    gt0 += *cluster.map_shared_rank(&tot_gt, k);
-    eq0 += *cluster.map_shared_rank(&tot_eq, k);
+    gt0 += of_rank(&tot_gt, k);
+    eq0 += of_rank(&tot_eq, k);
   }
   for (int w = 0; w < warp; ++w) {
-    gt0 += warp_gt[w];
-    eq0 += warp_eq[w];
+    gt0 += warp_a[w];
+    eq0 += warp_b[w];
   }
   for (int q = wa; q < wb; q += 32) {  // the warp's quads in order
     const bool here = q + lane < wb;
@@ -224,89 +275,130 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
     gt0 += all & 0xffffu;
     eq0 += all >> 16;
   }
-  cluster.sync();  // no block leaves while its totals are read
+  if (CLUSTER) all_sync();  // no block leaves while its totals are read
 }
 
 // -------------------------------------------------------------------------------------- move
 constexpr int kMoveThreads = 256;
-constexpr int kPieces = 4;   // 16-byte pieces of K or V a thread holds
-constexpr int kVectors = 8;  // 4-byte vectors of a block
+constexpr int kPieces = 4;   // 16-byte pieces of K or V a thread moves in a chunk
+constexpr int kVectors = 8;  // 4-byte vectors of a block, one element each of a thread's chunk
+constexpr int kDepth = 4;    // chunks on their way
+constexpr int kMoveSmem = kDepth * kMoveThreads * kPieces * 16;
 
 // A stream is one array's part of one (request, kv head): the K rows, the V rows, or up to eight of
 // the 4-byte vectors (scales, weights, gates of its query heads).  A cluster takes one stream's
-// target positions in ascending order, a chunk at a time; a chunk is written only when every
-// block of the cluster has it in its registers, and the next one is already being read.  In place this
+// target positions in ascending order, a chunk at a time, kDepth chunks ahead into shared memory; a chunk
+// is written only when every block of the cluster has read it.  In place this
 // is right for any kept[i] >= i: the sources of chunk c lie at or behind its first target, so no
 // earlier chunk's targets hold them, and a target that is a source of its own or an earlier
-// chunk has been read before it is written.
-struct Places {
-  int to, from;            // blocks
-  int to_slot, from_slot;  // -1 in `to`: nothing to move
+// chunk has been read before it is written.  Every thread writes what it read itself: shared memory is
+// only its queue, and the barrier of chunk c + 1 is under way while chunk c is written.
+struct Target {
+  int to, slot;  // block (-1: nothing to move) and slot
 };
-__device__ __forceinline__ Places places(const MoveParams& p, int row, int i, int n, int L, const int32_t* table) {
-  Places x{-1, 0, 0, 0};
-  if (i >= n) return x;
-  const int src = __ldg(p.kept + (size_t)row * p.max_keep + i);
-  if (src == i) return x;
-  if (src < i || src >= L) {
-    record_bad(p.status);
-    return x;
-  }
-  const int from = __ldg(table + (src >> p.log2_block)), to = __ldg(table + (i >> p.log2_block));
-  if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
-    record_bad(p.status);
-    return x;
-  }
-  return Places{to, from, i & (p.block_size - 1), src & (p.block_size - 1)};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveParams p, int cs) {
-  const int rank = blockIdx.x % cs, row = blockIdx.x / cs, kind = blockIdx.y;
+template <bool CLUSTER>
+__device__ __forceinline__ void all_arrive() {
+  if (CLUSTER) cg::cluster_group::barrier_arrive();
+}
+template <bool CLUSTER>
+__device__ __forceinline__ void all_wait() {
+  if (CLUSTER) cg::cluster_group::barrier_wait();
+  else __syncthreads();
+}
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kMoveThreads, 3) cache_move_kernel(const MoveParams p, int cs) {
+  extern __shared__ __align__(16) uint8_t queue[];
+  const int rank = CLUSTER ? blockIdx.x % cs : 0, row = CLUSTER ? blockIdx.x / cs : blockIdx.x, kind = blockIdx.y;
   const int r = row / p.hkv, h = row % p.hkv;
   const int tid = threadIdx.x;
-  int L = __ldg(p.seq_lens + r), n = __ldg(p.kept_lens + r);
+  const int L = __ldg(p.seq_lens + r), n = __ldg(p.kept_lens + r);
   if (L < 0 || L > p.capacity || n < 0 || n > p.max_keep || n > L) {  // the same for the whole cluster
     if (tid == 0) record_bad(p.status);
     return;
   }
   const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
+  const int32_t* kept = p.kept + (size_t)row * p.max_keep;
+  // Source of target i (from kept, read ahead): block and slot, -1 where there is nothing to move.
+  auto source = [&](int i, int src) -> Target {
+    if (i >= n || src == i) return Target{-1, 0};
+    if (src < i || src >= L) {
+      record_bad(p.status);
+      return Target{-1, 0};
+    }
+    const int from = __ldg(table + (src >> p.log2_block)), to = __ldg(table + (i >> p.log2_block));
+    if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
+      record_bad(p.status);
+      return Target{-1, 0};
+    }
+    return Target{from, src & (p.block_size - 1)};
+  };
+  auto index = [&](int i) { return i < n ? __ldg(kept + i) : 0; };
 
   if (kind < 2) {
-    uint8_t* cache = kind ? p.v_cache : p.k_cache;
+    uint8_t* cache = (kind ? p.v_cache : p.k_cache) + (size_t)h * p.kv_hs;
     const int log2_units = p.log2_units;  // 16-byte pieces of a row: 4 .. 64
     const int rows = (kMoveThreads * kPieces) >> log2_units;  // of a block's chunk
-    const int unit = tid & ((1 << log2_units) - 1), lane_row = tid >> log2_units;
-    const int step = kMoveThreads >> log2_units;
-    auto at = [&](int blk, int slot) {
-      return reinterpret_cast<uint4*>(cache + (size_t)blk * p.kv_bs + (size_t)h * p.kv_hs + (size_t)slot * p.kv_ss) + unit;
-    };
-    uint4 x[kPieces], y[kPieces];
-    uint4 *to[kPieces], *to_next[kPieces];
-    auto read = [&](int i0, uint4 (&d)[kPieces], uint4* (&t)[kPieces]) {
+    const int unit = (tid & ((1 << log2_units) - 1)) * 16, lane_row = tid >> log2_units;
+    const int step = kMoveThreads >> log2_units, stride = cs * rows;
+    uint4* q = reinterpret_cast<uint4*>(queue) + tid;
+    uint32_t moves = 0;  // kPieces bits a chunk, the latest lowest
+    int src[kPieces];    // kept of the chunk that is read next
+    int ahead = rank * rows + lane_row;  // its first target
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) src[u] = index(ahead + u * step);
+    int at = 0;  // its place in the queue
+    auto read = [&]() {
+      moves <<= kPieces;
 #pragma unroll
       for (int u = 0; u < kPieces; ++u) {
-        const Places w = places(p, row, i0 + u * step + lane_row, n, L, table);
-        t[u] = nullptr;
-        if (w.to >= 0) {
-          t[u] = at(w.to, w.to_slot);
-          d[u] = *at(w.from, w.from_slot);
+        const Target s = source(ahead + u * step, src[u]);
+        if (s.to >= 0) {
+          copy16(q + (at * kPieces + u) * kMoveThreads, cache + (size_t)s.to * p.kv_bs + (size_t)s.slot * p.kv_ss + unit);
+          moves |= 1u << u;
+        }
+        src[u] = index(ahead + stride + u * step);
+      }
+      copies_end();
+      ahead += stride;
+      at = at + 1 == kDepth ? 0 : at + 1;
+    };
+    for (int d = 0; d < kDepth - 1; ++d) read();
+    copies_wait<kDepth - 2>();
+    all_arrive<CLUSTER>();
+    all_wait<CLUSTER>();  // chunk 0 is read
+    int i0 = rank * rows + lane_row, out = 0;
+    for (int c0 = 0; c0 < n; c0 += stride) {  // c0: the cluster's chunk
+      read();
+      copies_wait<kDepth - 2>();  // the next chunk is here
+      all_arrive<CLUSTER>();
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        if (moves >> (kPieces * (kDepth - 1) + u) & 1) {
+          const int i = i0 + u * step;
+          *reinterpret_cast<uint4*>(cache + (size_t)__ldg(table + (i >> p.log2_block)) * p.kv_bs +
+                                    (size_t)(i & (p.block_size - 1)) * p.kv_ss + unit) =
+              q[(out * kPieces + u) * kMoveThreads];
         }
       }
-    };
-    int i0 = rank * rows;
-    read(i0, x, to);
-    for (int c0 = 0; c0 < n; c0 += cs * rows) {  // c0: the cluster's chunk
-      cg::cluster_group::barrier_arrive();
-      i0 += cs * rows;
-      read(i0, y, to_next);
-      cg::cluster_group::barrier_wait();
-#pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        if (to[u]) *to[u] = x[u];
-        x[u] = y[u];
-        to[u] = to_next[u];
-      }
+      i0 += stride;
+      out = out + 1 == kDepth ? 0 : out + 1;
+      all_wait<CLUSTER>();
     }
+    copies_wait<0>();
     return;
   }
 
@@ -320,7 +412,7 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MovePara
     base[v] = nullptr;
     heads[v] = p.hkv;
     if (p.k_scale) {
-      if (i < 2) base[v] = (i ? p.v_scale : p.k_scale) + (((size_t)h) << p.log2_block);
+      if (i >= 0 && i < 2) base[v] = (i ? p.v_scale : p.k_scale) + (((size_t)h) << p.log2_block);
       i -= 2;
     }
     if (p.w_cache) {
@@ -333,29 +425,44 @@ __global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MovePara
     }
   }
   auto cell = [&](int v, int blk, int slot) { return base[v] + (((size_t)blk * heads[v]) << p.log2_block) + slot; };
-  float x[kVectors], y[kVectors];
-  Places w{-1, 0, 0, 0}, w_next;
-  auto read = [&](int i, float (&d)[kVectors], Places& t) {
-    t = places(p, row, i, n, L, table);
-    if (t.to < 0) return;
+  float* q = reinterpret_cast<float*>(queue) + tid;
+  const int stride = cs * kMoveThreads;
+  int ahead = rank * kMoveThreads + tid, at = 0, out = 0, i = ahead;
+  int src = index(ahead);
+  uint32_t moves = 0;
+  auto read = [&]() {
+    const Target s = source(ahead, src);
+    src = index(ahead + stride);
+    moves <<= 1;
+    if (s.to >= 0) {
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v)
-      if (base[v]) d[v] = *cell(v, t.from, t.from_slot);
-  };
-  int i = rank * kMoveThreads + tid;
-  read(i, x, w);
-  for (int c0 = 0; c0 < n; c0 += cs * kMoveThreads) {
-    cg::cluster_group::barrier_arrive();
-    i += cs * kMoveThreads;
-    read(i, y, w_next);
-    cg::cluster_group::barrier_wait();
-#pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      if (w.to >= 0 && base[v]) *cell(v, w.to, w.to_slot) = x[v];
-      x[v] = y[v];
+      for (int v = 0; v < kVectors; ++v)
+        if (base[v]) copy4(q + (at * kVectors + v) * kMoveThreads, cell(v, s.to, s.slot));
+      moves |= 1;
     }
-    w = w_next;
+    copies_end();
+    ahead += stride;
+    at = at + 1 == kDepth ? 0 : at + 1;
+  };
+  for (int d = 0; d < kDepth - 1; ++d) read();
+  copies_wait<kDepth - 2>();
+  all_arrive<CLUSTER>();
+  all_wait<CLUSTER>();
+  for (int c0 = 0; c0 < n; c0 += stride) {
+    read();
+    copies_wait<kDepth - 2>();
+    all_arrive<CLUSTER>();
+    if (moves >> (kDepth - 1) & 1) {
+      const int to = __ldg(table + (i >> p.log2_block)), slot = i & (p.block_size - 1);
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v)
+        if (base[v]) *cell(v, to, slot) = q[(out * kVectors + v) * kMoveThreads];
+    }
+    i += stride;
+    out = out + 1 == kDepth ? 0 : out + 1;
+    all_wait<CLUSTER>();
   }
+  copies_wait<0>();
 }
 
 int sm_count() {
@@ -392,11 +499,16 @@ cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s) {
   while (cs < 16 && rows * cs < 2 * sms && p.max_seq_len / cs > 2048) cs *= 2;
   const long long slice = ((long long)(p.max_seq_len + 3) / 4 + cs) / cs * 4 + 8;  // keys of a block, at most
   const bool held = slice <= kMaxSlice;
-  auto kern = held ? cache_select_kernel<true> : cache_select_kernel<false>;
+  auto kern = cs == 1 ? (held ? cache_select_kernel<true, false> : cache_select_kernel<false, false>)
+                      : (held ? cache_select_kernel<true, true> : cache_select_kernel<false, true>);
   const size_t smem = held ? (size_t)slice * 4 : 0;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cs > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
+  if (cs == 1) {
+    kern<<<(unsigned)rows, kSelThreads, smem, s>>>(p);
+    return cudaGetLastError();
+  }
   return launch_clusters(kern, dim3((unsigned)(rows * cs)), kSelThreads, cs, smem, s, p);
 }
 
@@ -410,7 +522,13 @@ cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s) {
   const int chunk = (kMoveThreads * kPieces) >> p.log2_units;
   int cs = 1;
   while (cs < 8 && rows * kinds * cs < 4 * sms && p.max_keep > cs * chunk) cs *= 2;
-  return launch_clusters(cache_move_kernel, dim3((unsigned)(rows * cs), kinds), kMoveThreads, cs, 0, s, p, cs);
+  const dim3 grid((unsigned)(rows * cs), kinds);
+  auto kern = cs > 1 ? cache_move_kernel<true> : cache_move_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+  if (e != cudaSuccess) return e;
+  if (cs > 1) return launch_clusters(kern, grid, kMoveThreads, cs, kMoveSmem, s, p, cs);
+  kern<<<grid, kMoveThreads, kMoveSmem, s>>>(p, cs);
+  return cudaGetLastError();
 }
 
 }  // namespace gcs
