@@ -26,37 +26,40 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;          // digits of 11, 11 and 10 bits
 constexpr int kMaxSlice = 40 * 1024; // keys of a block in shared memory
 constexpr int kRanked = 512;         // keys up to which each counts those above it
+constexpr int kFew = 128;            // the same, of what a histogram leaves
 
-// Weights as integers of the same order: NaN below everything, -0 equal to 0.
+// Weights as integers of the same order: NaN below everything, -0 equal to 0.  0 is left for what is
+// no key at all.
+constexpr uint32_t kNanKey = 1;
 __device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if (f != f) return 0u;
-  if (f == 0.f) return 0x80000000u;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(f + 0.f);  // -0 + 0 = 0
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return f != f ? kNanKey : k;
 }
 
 // One cluster for a (request, kv head): its blocks take equal slices of the positions between the
 // first and the last ones, as quads of four neighbouring positions (one vector load: a quad lies in
-// one cache block).  The key of rank c from the top is found by three histograms of 11, 11 and 10 bits, each
-// added up over the cluster; a last walk in the order of the positions writes those above it and as
-// many equal ones as are still missing.  11 bits of a positive float are its exponent and two bits
-// more, so few of a warp's keys meet in a bin, and the second histogram is of few keys.
+// one cache block).  The key of rank c from the top is found by histograms of 11, 11 and 10 bits, each
+// added up in the cluster's first block, until few keys are left to be ranked; a last walk in the order
+// of the positions writes those that stay.  11 bits of a positive float are its exponent and two bits
+// more, so few of a warp's keys meet in a bin, and mostly one histogram is enough.
 // HELD: the slice's keys stay in shared memory; otherwise (slices past kMaxSlice) each walk reads the
 // weights again.  CLUSTER: more than one block.
 template <bool HELD, bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 3) cache_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint4 keys[];
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
-  __shared__ uint32_t tot_gt, tot_eq;
-  __shared__ uint32_t digit_s, above_s;
+  __shared__ uint2 few[kFew];  // (key, position)
+  __shared__ uint32_t few_n;
+  __shared__ uint3 found;         // digit, keys above it, keys with it; then the limit and its position
+  __shared__ uint32_t of_block[16];  // tokens that stay (or equal the limit) in each block of the cluster
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = CLUSTER ? cluster.num_blocks() : 1, rank = CLUSTER ? cluster.block_rank() : 0;
   auto all_sync = [&]() {
     if (CLUSTER) cluster.sync();
     else __syncthreads();
   };
-  auto of_rank = [&](uint32_t* x, int k) { return CLUSTER ? *cluster.map_shared_rank(x, k) : *x; };
   const int row = blockIdx.x / cs;
   const int r = row / p.hkv, h = row % p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
     uint32_t mine = 0;
     if (tid < m) {
       const float* w = weights(lead + tid);
-      mine = w ? order_key(__ldg(w)) : 0u;
+      mine = w ? order_key(__ldg(w)) : kNanKey;
     }
     hist[tid] = mine;
     __syncthreads();
@@ -125,27 +128,39 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
   const int per = (nq + cs - 1) / cs;
   const int a = q0 + min(nq, rank * per), b = q0 + min(nq, rank * per + per);
   auto load = [&](int q) -> uint4 {
-    const float* at = weights(q * 4);
-    if (!at) return make_uint4(0, 0, 0, 0);
-    const float4 w = __ldg(reinterpret_cast<const float4*>(at));
-    return make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
+    const int pos = q * 4;
+    const float* at = weights(pos);
+    uint4 k = make_uint4(kNanKey, kNanKey, kNanKey, kNanKey);
+    if (at) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(at));
+      k = make_uint4(order_key(w.x), order_key(w.y), order_key(w.z), order_key(w.w));
+    }
+    if (pos < lead || pos + 3 >= end) {  // tokens outside are below every key
+      if (pos < lead) k.x = 0;
+      if (pos + 1 < lead || pos + 1 >= end) k.y = 0;
+      if (pos + 2 < lead || pos + 2 >= end) k.z = 0;
+      if (pos + 3 < lead || pos + 3 >= end) k.w = 0;
+    }
+    return k;
   };
   auto quad = [&](int q) -> uint4 { return HELD ? keys[q - a] : load(q); };
   for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+  if (tid == 0) few_n = 0;
   __syncthreads();
 
-  uint32_t prefix = 0, left = need;  // bits found so far; how many are wanted among the keys with them
+  // The bits of the key of rank `need` found so far, and how many are wanted among the keys with
+  // them.  Once those are few, they are ranked by (key, position) one against the other; the last
+  // one that stays, limit, then tells for every token by itself whether it stays.
+  uint32_t prefix = 0, mask = 0, left = need, same = 0;
 #pragma unroll 1
   for (int round = 0; round < 3; ++round) {
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0;
     const uint32_t digits = round == 2 ? 1023 : 2047;
-    const uint32_t mask = round == 0 ? 0u : round == 1 ? 0xffe00000u : 0xfffffc00u;
-    auto count = [&](int q, const uint4& k) {
+    auto count = [&](const uint4& k) {
       const uint32_t e[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if ((e[j] & mask) == prefix && q * 4 + j >= lead && q * 4 + j < end)
-          atomicAdd(&hist[(e[j] >> shift) & digits], 1u);
+        if ((e[j] & mask) == prefix) atomicAdd(&hist[(e[j] >> shift) & digits], 1u);
     };
     if (HELD && round == 0) {  // the only read of the weights
       for (int q = a + tid; q < b; q += 4 * kSelThreads) {
@@ -157,125 +172,176 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const SelectP
         for (int u = 0; u < 4; ++u)
           if (q + u * kSelThreads < b) {
             keys[q + u * kSelThreads - a] = k[u];
-            count(q + u * kSelThreads, k[u]);
+            count(k[u]);
           }
       }
     } else {
-      for (int q = a + tid; q < b; q += kSelThreads) count(q, quad(q));
+      for (int q = a + tid; q < b; q += kSelThreads) count(quad(q));
     }
-    all_sync();
-    // thread's 4 bins from the top: 2047 - 4 tid .. 2044 - 4 tid
-    uint4 c = make_uint4(0, 0, 0, 0);
-    const int top = kBins / 4 - 1 - tid;
-    for (int k = 0; k < cs; ++k) {
-      const uint4* hk = reinterpret_cast<const uint4*>(CLUSTER ? cluster.map_shared_rank(hist, k) : hist);
-      const uint4 v = hk[top];
-      c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
-    }
-    const uint32_t sum = c.x + c.y + c.z + c.w;
-    uint32_t before = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += t;
-    }
-    if (lane == 31) warp_a[warp] = before;
-    before -= sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before += warp_a[w];
-    if (before < left && before + sum >= left) {  // one thread's
-      const uint32_t v[4] = {c.w, c.z, c.y, c.x};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (before < left && before + v[j] >= left) {
-          digit_s = kBins - 1 - 4 * tid - j;
-          above_s = before;
-        }
-        before += v[j];
+    if (CLUSTER) {
+      cluster.sync();
+      if (rank != 0) {  // the first block adds up
+        uint32_t* to = cluster.map_shared_rank(hist, 0);
+        for (int i = tid; i < kBins; i += kSelThreads)
+          if (hist[i]) atomicAdd(to + i, hist[i]);
       }
     }
-    all_sync();  // the bins are read
-    prefix |= digit_s << shift;
-    left -= above_s;
+    all_sync();
+    if (rank == 0) {
+      // thread's 4 bins from the top: 2047 - 4 tid .. 2044 - 4 tid
+      const uint4 c = reinterpret_cast<const uint4*>(hist)[kBins / 4 - 1 - tid];
+      const uint32_t sum = c.x + c.y + c.z + c.w;
+      uint32_t before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += t;
+      }
+      if (lane == 31) warp_a[warp] = before;
+      before -= sum;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) before += warp_a[w];
+      if (before < left && before + sum >= left) {  // one thread's
+        const uint32_t v[4] = {c.w, c.z, c.y, c.x};
+        uint3 f = make_uint3(0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (before < left && before + v[j] >= left) f = make_uint3(kBins - 1 - 4 * tid - j, before, v[j]);
+          before += v[j];
+        }
+        for (int k = 0; k < cs; ++k) *(CLUSTER ? cluster.map_shared_rank(&found, k) : &found) = f;
+      }
+    }
+    all_sync();
+    prefix |= found.x << shift;
+    mask |= digits << shift;
+    left -= found.y;
+    same = found.z;
+    if (same <= kFew) break;
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
   }
 
-  // prefix is the key of rank `need`; `left` of those equal to it stay
-  const int nql = b - a, chunk = (nql + kSelWarps - 1) / kSelWarps;
-  const int wa = a + min(nql, warp * chunk), wb = a + min(nql, warp * chunk + chunk);
-  uint32_t gt = 0, eq = 0;
-  for (int q = wa + lane; q < wb; q += 32) {
-    const uint4 k = quad(q);
-    const uint32_t e[4] = {k.x, k.y, k.z, k.w};
+  // limit: keys above it stay, and those equal to it up to position limit_at
+  uint32_t limit = prefix;
+  int limit_at = 0x7fffffff;
+  const bool ranked = same <= kFew;  // otherwise: the many equal to it are counted below
+  if (ranked) {
+    // the list is in the first block; slots from any block, in any order
+    uint2* list = CLUSTER ? cluster.map_shared_rank(few, 0) : few;
+    uint32_t* used = CLUSTER ? cluster.map_shared_rank(&few_n, 0) : &few_n;
+    for (int q = a + tid; q < b; q += kSelThreads) {
+      const uint4 k = quad(q);
+      const uint32_t e[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = q * 4 + j >= lead && q * 4 + j < end;
-      gt += in && e[j] > prefix;
-      eq += in && e[j] == prefix;
-    }
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) {
-    warp_a[warp] = gt;
-    warp_b[warp] = eq;
-  }
-  __syncthreads();
-  if (CLUSTER) {
-    if (tid == 0) {
-      uint32_t g = 0, e = 0;
-      for (int w = 0; w < kSelWarps; ++w) {
-        g += warp_a[w];
-        e += warp_b[w];
-      }
-      tot_gt = g;
-      tot_eq = e;
+      for (int j = 0; j < 4; ++j)
+        if ((e[j] & mask) == prefix) list[atomicAdd(used, 1u)] = make_uint2(e[j], q * 4 + j);
     }
     all_sync();
-  }
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int k = 0; k < rank; ++k) {
-    gt0 += of_rank(&tot_gt, k);
-    eq0 += of_rank(&tot_eq, k);
-  }
-  for (int w = 0; w < warp; ++w) {
-    gt0 += warp_a[w];
-    eq0 += warp_b[w];
-  }
-  for (int q = wa; q < wb; q += 32) {  // the warp's quads in order
-    const bool here = q + lane < wb;
-    uint4 k = make_uint4(0, 0, 0, 0);
-    if (here) k = quad(q + lane);
-    const uint32_t e[4] = {k.x, k.y, k.z, k.w};
-    const int pos = (q + lane) * 4;
-    uint32_t g = 0, t = 0;  // bits
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in = here && pos + j >= lead && pos + j < end;
-      g |= (in && e[j] > prefix ? 1u : 0u) << j;
-      t |= (in && e[j] == prefix ? 1u : 0u) << j;
+    if (rank == 0 && tid < same) {
+      const uint2 mine = few[tid];
+      uint32_t before = 0;
+      for (int j = 0; j < (int)same; ++j) {
+        const uint2 x = few[j];
+        before += x.x > mine.x || (x.x == mine.x && x.y < mine.y);
+      }
+      if (before == left - 1)
+        for (int k = 0; k < cs; ++k)
+          *(CLUSTER ? cluster.map_shared_rank(&found, k) : &found) = make_uint3(mine.x, mine.y, 0);
     }
-    const uint32_t mine = __popc(g) | __popc(t) << 16;
-    uint32_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t s = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += s;
-    }
-    const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
-    uint32_t gb = gt0 + ((sum - mine) & 0xffffu), eb = eq0 + ((sum - mine) >> 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool is_g = g >> j & 1, is_t = t >> j & 1;
-      if (is_g || (is_t && eb < left)) out[lead + gb + min(eb, left)] = pos + j;
-      gb += is_g;
-      eb += is_t;
-    }
-    gt0 += all & 0xffffu;
-    eq0 += all >> 16;
+    all_sync();
+    limit = found.x;
+    limit_at = found.y;
   }
-  if (CLUSTER) all_sync();  // no block leaves while its totals are read
+
+  // in the order of the positions, a warp's quads at a time: how many stay, then which.  Ranked: a token
+  // stays iff its key is at least the limit, past limit_at one more.
+  const int nql = b - a, chunk = (nql + kSelWarps - 1) / kSelWarps;
+  const int wa = a + min(nql, warp * chunk), wb = a + min(nql, warp * chunk + chunk);
+  auto above = [&](int q, const uint4& k) -> uint32_t {  // bits of the quad's tokens that stay
+    const int pos = q * 4;
+    uint32_t m = limit + (pos > limit_at);
+    uint32_t v = (k.x >= m) | (k.y >= m) << 1 | (k.z >= m) << 2 | (k.w >= m) << 3;
+    if (pos <= limit_at && pos + 3 > limit_at) {  // the quad that holds it
+      const uint32_t strict = (k.x > m) | (k.y > m) << 1 | (k.z > m) << 2 | (k.w > m) << 3;
+      const uint32_t low = (2u << (limit_at - pos)) - 1;
+      v = (v & low) | (strict & ~low);
+    }
+    return v;
+  };
+  auto equal = [&](const uint4& k) -> uint32_t {
+    return (k.x == limit) | (k.y == limit) << 1 | (k.z == limit) << 2 | (k.w == limit) << 3;
+  };
+  if (!ranked) {
+    // more tokens than were ranked have the limit itself: the first `left` of them stay, and the last of
+    // those is limit_at
+    uint32_t eq = 0;
+    for (int q = wa + lane; q < wb; q += 32) eq += __popc(equal(quad(q)));
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) warp_b[warp] = eq;
+    __syncthreads();
+    uint32_t eq0 = 0;
+    if (CLUSTER) {
+      if (tid < 32) {
+        const uint32_t e = __reduce_add_sync(0xffffffffu, tid < kSelWarps ? warp_b[tid] : 0u);
+        if (tid < cs) *cluster.map_shared_rank(&of_block[rank], tid) = e;
+      }
+      all_sync();
+      for (int k = 0; k < rank; ++k) eq0 += of_block[k];
+    }
+    for (int w = 0; w < warp; ++w) eq0 += warp_b[w];
+    if (eq0 < left && eq0 + eq >= left) {  // one warp's
+      for (int q = wa; q < wb; q += 32) {
+        const uint32_t t = q + lane < wb ? equal(quad(q + lane)) : 0u;
+        uint32_t before = __popc(t), sum = before;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t s = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += s;
+        }
+        before = eq0 + sum - before;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (t >> j & 1) {
+            if (before == left - 1)
+              for (int k = 0; k < cs; ++k)
+                *(CLUSTER ? cluster.map_shared_rank(&found, k) : &found) = make_uint3(limit, (q + lane) * 4 + j, 0);
+            ++before;
+          }
+        }
+        eq0 += __shfl_sync(0xffffffffu, sum, 31);
+      }
+    }
+    all_sync();
+    limit_at = found.y;
+    if (CLUSTER) all_sync();  // of_block is written again
+  }
+  uint32_t stay = 0;
+  for (int q = wa + lane; q < wb; q += 32) stay += __popc(above(q, quad(q)));
+  stay = __reduce_add_sync(0xffffffffu, stay);
+  if (lane == 0) warp_a[warp] = stay;
+  __syncthreads();
+  uint32_t at = lead;
+  if (CLUSTER) {
+    if (tid < 32) {
+      const uint32_t s = __reduce_add_sync(0xffffffffu, tid < kSelWarps ? warp_a[tid] : 0u);
+      if (tid < cs) *cluster.map_shared_rank(&of_block[rank], tid) = s;
+    }
+    all_sync();
+    for (int k = 0; k < rank; ++k) at += of_block[k];
+  }
+  for (int w = 0; w < warp; ++w) at += warp_a[w];
+  const uint32_t lower = (1u << lane) - 1;
+  for (int q = wa; q < wb; q += 32) {
+    const uint32_t v = q + lane < wb ? above(q + lane, quad(q + lane)) : 0u;
+    const uint32_t v0 = __ballot_sync(0xffffffffu, v & 1), v1 = __ballot_sync(0xffffffffu, v & 2);
+    const uint32_t v2 = __ballot_sync(0xffffffffu, v & 4), v3 = __ballot_sync(0xffffffffu, v & 8);
+    int32_t* to = out + at + __popc(v0 & lower) + __popc(v1 & lower) + __popc(v2 & lower) + __popc(v3 & lower);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (v >> j & 1) *to++ = (q + lane) * 4 + j;
+    at += __popc(v0) + __popc(v1) + __popc(v2) + __popc(v3);
+  }
 }
 
 // -------------------------------------------------------------------------------------- move
