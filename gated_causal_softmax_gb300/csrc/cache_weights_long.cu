@@ -9,19 +9,22 @@
 //                    2^(scale s + b), stays in its thread too; the query tiles stream by.
 // Neither kernel moves data between threads, and nothing but (max, sum) leaves the SM.
 //
-// Both kernels are one engine: NA resident operand tiles of 128 rows x d (two, one at d 512), streamed
-// tiles of 128 rows x d in a ring of 64-dim stages, and accumulators of 128 x 128 in a double buffer for
-// each resident tile.  A query tile is floor(128 / G) tokens x the G query heads of a kv head; the rows
+// Both kernels are one engine: NA resident operand tiles of 128 rows x d (two, one at d 512) in tensor
+// memory, streamed tiles of 128 rows x d in a shared-memory ring of 64-dim stages, and accumulators of
+// 128 x 128 in turn.  With the resident side out of tensor memory an MMA reads 64 bytes a cycle of shared
+// memory; out of shared memory it would be the 128 there are, and the vectors' reads would wait for it.
+// A query tile is floor(128 / G) tokens x the G query heads of a kv head; the rows
 // left over are zero.  With an fp8 cache the operands are f16 (codes are exact in it; the queries are
 // rounded to it by a kernel of their own for the streamed side), with a bf16 one bf16.
 //
-// Warp roles (512 threads):
+// Warp roles (640 threads, 768 where codes are converted):
 //   warp 0        streamed tiles by tensor copies (bf16 keys, queries)
 //   warp 1        tcgen05 issuer
 //   warps 2-3     per-column vectors of the streamed tile (scales or b, gates, last visible keys)
-//   warps 4-11    two groups of 128 lanes: sums or weights
-//   warps 12-15   sums kernel over an fp8 cache: e4m3 -> f16 stages, straight from memory
+//   warps 4-19    sums or weights: four groups of 128 lanes, one accumulator at a time each
+//   warps 20-23   sums kernel over an fp8 cache: e4m3 -> f16 stages, straight from memory
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "rows.cuh"
@@ -30,7 +33,10 @@
 namespace gcs {
 namespace {
 
-constexpr int kThreads = 512;
+// 4 warps, 16 of the accumulators and, where codes are converted, 4 more
+constexpr int kEpiWarps = 16;
+template <bool CONVERT>
+constexpr int kThreadsOf = (4 + kEpiWarps + (CONVERT ? 4 : 0)) * 32;
 constexpr int kTile = 128;
 constexpr int kStage = 16384;  // 128 rows x 64 dims of 16 bits
 constexpr float kLog2e = 1.4426950408889634f;
@@ -64,13 +70,17 @@ __device__ __forceinline__ void put_codes(uint8_t* stage, int r, int u, uint4 v)
 template <int NCH>
 struct Cfg {
   static constexpr int NA = NCH == 8 ? 1 : 2;               // resident tiles
-  static constexpr int NST = NCH <= 2 ? 6 : 4;              // stages of the ring
-  static constexpr int OFF_RING = NA * NCH * kStage;
-  static constexpr int OFF_AUX = OFF_RING + NST * kStage;   // [2] x vectors of the streamed tile
+  static constexpr int A_COLS = NCH * 32;                   // tensor memory columns of one
+  static constexpr int SLOTS = NCH <= 2 ? 3 : 2;            // accumulators
+  static_assert(NA * A_COLS + SLOTS * kTile <= 512, "tensor memory");
+  static constexpr int NST = NCH == 1 ? 6 : 8;              // stages of the ring
+  static constexpr int OFF_RING = 0;
+  static constexpr int NAUX = 4;                            // vectors of as many streamed tiles
+  static constexpr int OFF_AUX = OFF_RING + NST * kStage;
   static constexpr int VECS = 3 * kTile * 4;                // 3 x [128]
   static constexpr int AUX = VECS + kMaxGates * kGateRow * 4;
-  static constexpr int OFF_BAR = OFF_AUX + 2 * AUX;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * NST + 16) * 8;
+  static constexpr int OFF_BAR = OFF_AUX + NAUX * AUX;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * NST + 8 + 2 * NAUX + 2) * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory budget");
 };
@@ -98,10 +108,10 @@ __device__ __forceinline__ int block_of(const WeightsParams& p, const int32_t* t
 
 // WRITE false: the sums kernel, true: the weights kernel.  NCH: d / 64.
 template <bool BF16, int NCH, bool WRITE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     weights_long_kernel(const __grid_constant__ CUtensorMap tm, const WeightsParams p) {
   using C = Cfg<NCH>;
-  constexpr int NA = C::NA, NST = C::NST;
+  constexpr int NA = C::NA, NST = C::NST, kThreads = kThreadsOf<!BF16 && !WRITE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align_1k(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,14 +155,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;               // [NST]
   uint64_t* empty = bars + NST;        // [NST]
-  uint64_t* s_full = bars + 2 * NST;   // [4] accumulators: slot 2 x + buffer
-  uint64_t* s_empty = s_full + 4;      // [4]
-  uint64_t* aux_full = s_full + 8;     // [2]
-  uint64_t* aux_empty = s_full + 10;   // [2]
-  uint64_t* drain = s_full + 12;
+  uint64_t* s_full = bars + 2 * NST;   // [4 groups] the group's next product (a group sees every phase of its
+                                       // barrier, which a barrier of a slot would not give it)
+  uint64_t* s_empty = s_full + 4;      // [SLOTS] accumulators
+  uint64_t* aux_full = s_full + 8;     // [NAUX]
+  uint64_t* aux_empty = aux_full + C::NAUX;
+  uint64_t* drain = aux_empty + C::NAUX;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 8);  // [2] pages of a key tile that are not there
+  uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 8);  // [NAUX] pages of a key tile that are not there
   const Abort ab{abort_flag, p.status};
   constexpr bool kCopied = BF16 || WRITE;  // the streamed tiles come by tensor copies
   if (threadIdx.x == 0) {
@@ -160,12 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], kCopied ? 1 : 4);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&aux_full[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s_empty[i], 4);
+    for (int i = 0; i < C::NAUX; ++i) {
+      mbar_init(&aux_full[i], 1);
       mbar_init(&aux_empty[i], NA == 2 ? 8 : 4);
     }
     mbar_init(drain, 1);
@@ -177,42 +186,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
 
-  // the resident rows, 16-bit, 128-byte-swizzled, K-major: tile x, chunk c at (x NCH + c) stages
-  if (!WRITE) {
-    constexpr int kUnits = NCH * 8;  // 16-byte units of a row
-    for (int i = threadIdx.x; i < NA * kTile * kUnits; i += kThreads) {
-      const int u = i % kUnits, row = i / kUnits, x = row / kTile, rr = row % kTile;
-      const int t = a0 + x * ntok + rr / G, head = rr % G;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (rr < nrow && t < ql)
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + (size_t)(rq.q0 + t) * p.q_ts + (size_t)(kvh * G + head) * p.q_hs) + u);
-      if (!BF16)
-        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
-      *reinterpret_cast<uint4*>(smem + (x * NCH + u / 8) * kStage + sw128_offset(rr, u % 8)) = v;
-    }
-  } else {
-    constexpr int kUnits = NCH * (BF16 ? 8 : 4);
-    for (int i = threadIdx.x; i < NA * kTile * kUnits; i += kThreads) {
-      const int u = i % kUnits, row = i / kUnits, x = row / kTile, rr = row % kTile, pos = a0 + row;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      const int blk = pos < L ? block_of(p, table, pos) : -1;
-      if (blk >= 0)
-        v = __ldg(reinterpret_cast<const uint4*>(p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
-                                                 (size_t)(pos & (p.block_size - 1)) * p.kv_ss) + u);
-      if (BF16) *reinterpret_cast<uint4*>(smem + (x * NCH + u / 8) * kStage + sw128_offset(rr, u % 8)) = v;
-      else put_codes(smem + (x * NCH + u / 4) * kStage, rr, u % 4, v);
-    }
+  if (WRITE) {
     // rows of the streamed tiles that no copy writes
     for (int i = threadIdx.x; i < NST * (kTile - nrow) * 8; i += kThreads) {
       const int st = i / ((kTile - nrow) * 8), k = i % ((kTile - nrow) * 8);
       *reinterpret_cast<uint4*>(smem + C::OFF_RING + st * kStage + nrow * 128 + k * 16) = make_uint4(0, 0, 0, 0);
     }
+    fence_proxy_async_smem();
   }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  constexpr uint32_t kAccCol = NA * C::A_COLS;  // first column of the accumulators
+  if (warp >= 4 && warp < 4 + kEpiWarps) {
+    // the resident rows, 16-bit, one row a lane, two dims a column; a row is shared out over the
+    // warps of its lanes
+    constexpr int kParts = NA == 2 ? 2 : 4;
+    const int grp = (warp - 4) >> 2, x = NA == 2 ? grp & 1 : 0, part = NA == 2 ? grp >> 1 : grp;
+    const int rr = (warp & 3) * 32 + lane;
+    const uint4* src = nullptr;
+    if (!WRITE) {
+      const int t = a0 + x * ntok + rr / G;
+      if (rr < nrow && t < ql)
+        src = reinterpret_cast<const uint4*>(p.q + (size_t)(rq.q0 + t) * p.q_ts + (size_t)(kvh * G + rr % G) * p.q_hs);
+    } else {
+      const int pos = a0 + x * kTile + rr, blk = pos < L ? block_of(p, table, pos) : -1;
+      if (blk >= 0)
+        src = reinterpret_cast<const uint4*>(p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
+                                             (size_t)(pos & (p.block_size - 1)) * p.kv_ss);
+    }
+    const uint32_t col0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * C::A_COLS;
+#pragma unroll
+    for (int c = 0; c < C::A_COLS / kParts; c += 16) {  // 32 dims
+      const int col = part * (C::A_COLS / kParts) + c;
+      uint32_t w[16];
+      if (BF16 || !WRITE) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint4 v = src ? __ldg(src + col / 4 + u) : make_uint4(0, 0, 0, 0);
+          w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
+        }
+        if (!BF16) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) w[u] = bf16x2_to_f16x2(w[u]);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint4 v = src ? __ldg(src + col / 8 + u) : make_uint4(0, 0, 0, 0);
+          e4m3x4_to_f16x2x2(v.x, w[8 * u], w[8 * u + 1]);
+          e4m3x4_to_f16x2x2(v.y, w[8 * u + 2], w[8 * u + 3]);
+          e4m3x4_to_f16x2x2(v.z, w[8 * u + 4], w[8 * u + 5]);
+          e4m3x4_to_f16x2x2(v.w, w[8 * u + 6], w[8 * u + 7]);
+        }
+      }
+      tmem_st16(col0 + col, w);
+    }
+    tmem_st_wait();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   auto ring_next = [&](uint32_t& stage, uint32_t& phase) {
     if (++stage == NST) {
       stage = 0;
@@ -259,31 +294,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t id = BF16 ? idesc_bf16(kTile, kTile, false, false) : idesc_f16(kTile, kTile, false, false);
-      const uint64_t dA = sdesc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t dB = sdesc_sw128(smem_u32(smem + C::OFF_RING), 16, 1024);
       constexpr uint32_t kSt16 = kStage >> 4;
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0;
       bool ok = true;
       for (int n = 0; n < nt && ok; ++n) {
-        const int s0 = NA == 2 ? (n & 1) : (n & 1) * 2 + ((n >> 1) & 1);  // slot of resident tile 0
-        const uint32_t use = NA == 2 ? n >> 1 : n >> 2;
-        ok = wait_bar(&s_empty[s0], (use & 1) ^ 1, ab) && (NA == 1 || wait_bar(&s_empty[s0 + 2], (use & 1) ^ 1, ab));
-        for (int c = 0; c < NCH && ok; ++c) {
-          ok = wait_bar(&full[stage], phase, ab);
-          if (!ok) break;
-          tc_fence_after();
+        const uint32_t first = stage;
 #pragma unroll
-          for (int x = 0; x < NA; ++x) {
-            const uint64_t a = dA + (x * NCH + c) * kSt16, b = dB + stage * kSt16;
+        for (int x = 0; x < NA; ++x) {  // a tile's stages are held until its last product
+          if (ok) ok = wait_bar(&s_empty[slot], slot_phase ^ 1, ab);
+          uint32_t st = first;
+          for (int c = 0; c < NCH && ok; ++c) {
+            if (x == 0) {
+              ok = wait_bar(&full[stage], phase, ab);
+              if (!ok) break;
+              ring_next(stage, phase);
+            }
+            tc_fence_after();
+            const uint64_t b = dB + st * kSt16;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss(tmem + (s0 + 2 * x) * kTile, a + 2 * k, b + 2 * k, id, (c | k) != 0);
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + kAccCol + slot * kTile, tmem + x * C::A_COLS + c * 32 + k * 8, b + 2 * k, id, (c | k) != 0);
+            if (x == NA - 1) mma_commit(&empty[st]);
+            st = st + 1 == NST ? 0 : st + 1;
           }
-          mma_commit(&empty[stage]);
-          ring_next(stage, phase);
-        }
-        if (ok) {
-          mma_commit(&s_full[s0]);
-          if (NA == 2) mma_commit(&s_full[s0 + 2]);
+          if (ok) mma_commit(&s_full[(n * NA + x) & 3]);
+          if (++slot == C::SLOTS) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
         }
       }
       if (!ok) {
@@ -294,74 +333,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------- per-column vectors
-    const int c = threadIdx.x - 64;  // 0 .. 63
-    for (int n = 0; n < nt; ++n) {
-      const int a = n & 1;
-      if (!wait_bar(&aux_empty[a], ((n >> 1) & 1) ^ 1, ab)) break;
-      float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
-      uint32_t bad = 0;
-      for (int i = c; i < kTile; i += 64) {
+    // The two warps take the tiles in turn, a lane columns lane + 32 k; what a tile needs from memory is
+    // on its way while the one before it is written.
+    float2 next[4];  // weights: (b, own gate); sums: (scale, -)
+    int next_blk[4];
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lane + 32 * k;
+        next_blk[k] = -1;
         if (WRITE) {
-          const int t = (b_lo + n) * ntok + i / G, head = i % G;
-          const bool valid = i < nrow && t < ql;
-          float2 v = make_float2(neg_inf(), 0.f);
-          if (valid) v = __ldg(p.rows + (size_t)(rq.q0 + t) * p.hq + kvh * G + head);
-          ax[i] = v.x;
-          ax[kTile + i] = v.y;
-          reinterpret_cast<int*>(ax)[2 * kTile + i] = valid ? L - ql + t : -1;
+          const int t = (b_lo + n) * ntok + i / G;
+          next[k] = make_float2(neg_inf(), 0.f);
+          if (n < nt && i < nrow && t < ql) {
+            next[k] = __ldg(p.rows + (size_t)(rq.q0 + t) * p.hq + kvh * G + i % G);
+            next_blk[k] = L - ql + t;  // the last key it sees
+          }
         } else {
           const int pos = key0 + (b_lo + n) * kTile + i;
-          const int blk = pos < L ? block_of(p, table, pos) : -1;
-          const int slot = pos & (p.block_size - 1);
-          float ks = kst;
-          if (blk >= 0 && p.format == kCachePerToken)
-            ks = __ldg(p.k_scale + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot);
-          ax[i] = ks * sl2;
-          if (blk < 0 && pos < L) bad |= 1u << (i >> 4);
-          if (gates)
+          next[k].x = kst;
+          if (n < nt && pos < L) next_blk[k] = block_of(p, table, pos);
+          if (next_blk[k] >= 0 && p.format == kCachePerToken)
+            next[k].x = __ldg(p.k_scale + (((size_t)next_blk[k] * p.hkv + kvh) << p.log2_block) +
+                              (pos & (p.block_size - 1)));
+        }
+      }
+    };
+    fetch(warp - 2);
+    for (int n = warp - 2; n < nt; n += 2) {
+      const int a = n % C::NAUX;
+      float2 v[4];
+      int blk[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = next[k], blk[k] = next_blk[k];
+      fetch(n + 2);
+      if (!wait_bar(&aux_empty[a], ((n / C::NAUX) & 1) ^ 1, ab)) break;
+      float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
+      uint32_t bad = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = lane + 32 * k;
+        if (WRITE) {
+          ax[i] = v[k].x;
+          ax[kTile + i] = v[k].y;
+          reinterpret_cast<int*>(ax)[2 * kTile + i] = blk[k];
+        } else {
+          const int pos = key0 + (b_lo + n) * kTile + i;
+          ax[i] = v[k].x * sl2;
+          if (blk[k] < 0 && pos < L) bad |= 1u << (i >> 4);
+          if (gates) {
+            const float* src = p.g_cache + (((size_t)max(blk[k], 0) * p.hq + kvh * G) << p.log2_block) +
+                               (pos & (p.block_size - 1));
+#pragma unroll 8
             for (int h = 0; h < G; ++h)
-              ax[3 * kTile + h * kGateRow + i] =
-                  blk >= 0 ? __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h) << p.log2_block) + slot) : 0.f;
+              ax[3 * kTile + h * kGateRow + i] = blk[k] >= 0 ? __ldg(src + ((size_t)h << p.log2_block)) : 0.f;
+          }
         }
       }
       if (!WRITE) {
         bad = __reduce_or_sync(0xffffffffu, bad);
-        // each warp has four of the tile's eight pages
-        if (lane == 0) reinterpret_cast<uint8_t*>(bad_pages + a)[warp - 2] = (uint8_t)bad;
+        if (lane == 0) bad_pages[a] = bad;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&aux_full[a]);
     }
     __syncwarp();
-  } else if (warp < 12) {
-    // ---------------------------------------------------------- sums or weights, group y
-    const int y = (warp - 4) >> 2, quarter = warp & 3;
+  } else if (warp < 4 + kEpiWarps) {
+    // ---------------------------------------------------------- sums or weights
+    // Four groups of 128 lanes take the products in turn: while one waits for its product or its registers,
+    // others keep the exponentials going (two groups of half the columns each: 1.30 ms, four: see below)
+    const int grp = (warp - 4) >> 2, quarter = warp & 3;
     const int rr = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int x = NA == 2 ? y : 0;  // its resident tile; with one, the groups take the streamed tiles in turn
+    const int x = NA == 2 ? grp & 1 : 0;  // its resident tile
     // sums: the row's token and last visible key; weights: the key and its constants
     const int t = a0 + x * ntok + rr / G, head = rr % G;
     const bool row_ok = rr < nrow && t < ql;
     const int pos = WRITE ? a0 + x * kTile + rr : L - ql + min(t, ql - 1);
     float gi = 0.f, ks = 0.f;
-    float gk[kMaxGates];
-    int blk = -1;
-    const bool repeat = gates && (kMaxGates % G) == 0;  // column i has head i % 16 % G
+    int blk = -1, slot_k = 0;
     if (WRITE) {
       blk = pos < L ? block_of(p, table, pos) : -1;
       if (blk >= 0) {
-        const int slot = pos & (p.block_size - 1);
+        slot_k = pos & (p.block_size - 1);
         ks = kst * sl2;
-        if (p.format == kCachePerToken) ks = __ldg(p.k_scale + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot) * sl2;
-        if (gates) {
-#pragma unroll
-          for (int h = 0; h < kMaxGates; ++h)
-            gk[h] = __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h % G) << p.log2_block) + slot);
-        }
-      }
-      if (blk < 0 || !gates) {
-#pragma unroll
-        for (int h = 0; h < kMaxGates; ++h) gk[h] = 0.f;
+        if (p.format == kCachePerToken)
+          ks = __ldg(p.k_scale + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot_k) * sl2;
       }
     } else if (gates && row_ok) {
       const int b = block_of(p, table, pos);
@@ -369,143 +426,177 @@ __global__ void __launch_bounds__(kThreads, 1)
         gi = __ldg(p.g_cache + (((size_t)b * p.hq + kvh * G + head) << p.log2_block) + (pos & (p.block_size - 1)));
     }
     float m = neg_inf();
-    float2 acc[4];  // sums, or the weight
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = make_float2(0.f, 0.f);
+    float2 acc[2];  // sums, or the weight
+    acc[0] = acc[1] = make_float2(0.f, 0.f);
     bool ok = true;
-    for (int n = 0; n < nt; ++n) {
-      if (NA == 1 && (n & 1) != y) continue;
-      const int a = n & 1;
-      const int slot = NA == 2 ? x * 2 + (n & 1) : (n & 1) * 2 + ((n >> 1) & 1);
-      const uint32_t use = NA == 2 ? n >> 1 : n >> 2;
-      ok = wait_bar(&aux_full[a], (n >> 1) & 1, ab) && wait_bar(&s_full[slot], use & 1, ab);
-      if (!ok) break;
-      tc_fence_after();
-      const float* ax = reinterpret_cast<const float*>(smem + C::OFF_AUX + a * C::AUX);
-      const uint32_t tS = tmem + lane_off + slot * kTile;
-      if constexpr (!WRITE) {
-        const int j0 = key0 + (b_lo + n) * kTile;
-        const uint32_t bw = bad_pages[a], bad = (bw | bw >> 8) & 0xffu;
-        const int first_t = a0 + x * ntok, last_t = min(first_t + ntok, ql) - 1;
-        const bool need_mask = j0 + kTile - 1 > L - ql + first_t || bad != 0 || (W > 0 && j0 <= L - ql + last_t - W);
-        const float4* g4 = reinterpret_cast<const float4*>(ax + 3 * kTile + head * kGateRow);
-        const float4* ks4 = reinterpret_cast<const float4*>(ax);
+
+    auto columns = [&](auto with_gates) {
+      constexpr bool kGates = decltype(with_gates)::value;
+      float gk[kGates && WRITE ? kMaxGates : 1];
+      [[maybe_unused]] const bool repeat = (kMaxGates % G) == 0;  // column i has head i % 16 % G
+      if (kGates && WRITE) {
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t sv[32];
-          tmem_ld32(tS + cc * 32, sv);
-          tmem_ld_wait();
-          float2 v[16];
+        for (int h = 0; h < kMaxGates; ++h)
+          gk[h] = blk >= 0 ? __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h % G) << p.log2_block) + slot_k) : 0.f;
+      }
+      for (int u = grp; u < nt * NA; u += 4) {  // streamed tile n with resident tile x
+        const int n = NA == 2 ? u >> 1 : u, a = n % C::NAUX;
+        const int slot = u % C::SLOTS;
+        ok = wait_bar(&aux_full[a], (n / C::NAUX) & 1, ab) && wait_bar(&s_full[grp], (u >> 2) & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        const float* ax = reinterpret_cast<const float*>(smem + C::OFF_AUX + a * C::AUX);
+        const uint32_t tS = tmem + lane_off + kAccCol + slot * kTile;
+        if constexpr (!WRITE) {
+          const int j0 = key0 + (b_lo + n) * kTile;
+          const uint32_t bad = bad_pages[a];
+          const int first_t = a0 + x * ntok, last_t = min(first_t + ntok, ql) - 1;
+          const bool need_mask = j0 + kTile - 1 > L - ql + first_t || bad != 0 || (W > 0 && j0 <= L - ql + last_t - W);
+          const float4* g4 = reinterpret_cast<const float4*>(ax + 3 * kTile + head * kGateRow);
+          const float4* ks4 = reinterpret_cast<const float4*>(ax);
+          // one straight run of code for each case: a branch within it would part the exponentials
+          auto tile = [&](auto masked) {
+            constexpr bool kMask = decltype(masked)::value;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 k4 = ks4[cc * 8 + q];
-            v[2 * q] = make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1]));
-            v[2 * q + 1] = make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3]));
-            if (gates) {
-              const float4 g = g4[cc * 8 + q];
-              const float2 ga = make_float2((gi - g.x) * kLog2e, (gi - g.y) * kLog2e);
-              const float2 gb = make_float2((gi - g.z) * kLog2e, (gi - g.w) * kLog2e);
-              v[2 * q] = fma2(v[2 * q], make_float2(k4.x, k4.y), ga);
-              v[2 * q + 1] = fma2(v[2 * q + 1], make_float2(k4.z, k4.w), gb);
-            } else {
-              v[2 * q] = mul2(v[2 * q], make_float2(k4.x, k4.y));
-              v[2 * q + 1] = mul2(v[2 * q + 1], make_float2(k4.z, k4.w));
-            }
-          }
-          if (need_mask) {
+            for (int cc = 0; cc < 4; ++cc) {
+              // four scores (log2 units) and `base` at a time into f
+              auto scores = [&](float base, auto f) {
+                uint32_t sv[32];
+                tmem_ld32(tS + cc * 32, sv);
+                tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const int j = j0 + cc * 32 + 2 * q;
-              const bool off = bad >> (cc * 2 + q / 8) & 1;
-              if (off || j > pos || (W > 0 && j <= pos - W)) v[q].x = neg_inf();
-              if (off || j + 1 > pos || (W > 0 && j + 1 <= pos - W)) v[q].y = neg_inf();
-            }
-          }
-          float mx = neg_inf();
-#pragma unroll
-          for (int q = 0; q < 16; ++q) mx = fmaxf(mx, fmaxf(v[q].x, v[q].y));
-          // the reference moves only when the maximum grows by more than 2^8: sums of 2^8 per term stay
-          // far from fp32's limits
-          if (mx > m + 8.f) {
-            const float f = ex2(m - mx);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = mul2(acc[e], both(f));
-            m = mx;
-          }
-          const float ref = m == neg_inf() ? 0.f : -m;
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float2 z = add2(v[q], both(ref));
-            acc[q & 3] = add2(acc[q & 3], make_float2(ex2(z.x), ex2(z.y)));
-          }
-        }
-      } else {
-        const int t0 = (b_lo + n) * ntok;
-        const int j_lo = a0 + x * kTile, j_hi = j_lo + kTile - 1;
-        const bool need_mask = t0 + ntok > ql || j_hi > L - ql + t0 || (W > 0 && j_lo <= L - ql + t0 + ntok - 1 - W);
-        const float4* b4 = reinterpret_cast<const float4*>(ax);
-        const float4* gi4 = reinterpret_cast<const float4*>(ax + kTile);
-        const int* see = reinterpret_cast<const int*>(ax) + 2 * kTile;
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t sv[32];
-          tmem_ld32(tS + cc * 32, sv);
-          tmem_ld_wait();
-          float2 v[16];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float4 b = b4[cc * 8 + q];
-            if (gates) {
-              const float4 g = gi4[cc * 8 + q];
-              float k4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                k4[e] = gk[(4 * q + e) % kMaxGates];
-                if (!repeat) {  // groups that 16 is no multiple of
-                  const int h = (cc * 32 + 4 * q + e) % G;
-#pragma unroll
-                  for (int w = 0; w < kMaxGates; ++w)
-                    if (h == w) k4[e] = gk[w];
+                for (int q = 0; q < 8; ++q) {
+                  const float4 k4 = ks4[cc * 8 + q];
+                  float2 va = both(base), vb = both(base);
+                  if (kGates) {
+                    const float4 g = g4[cc * 8 + q];
+                    va = fma2(make_float2(gi - g.x, gi - g.y), both(kLog2e), va);
+                    vb = fma2(make_float2(gi - g.z, gi - g.w), both(kLog2e), vb);
+                  }
+                  va = fma2(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])),
+                            make_float2(k4.x, k4.y), va);
+                  vb = fma2(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])),
+                            make_float2(k4.z, k4.w), vb);
+                  if (kMask) {
+                    const int j = j0 + cc * 32 + 4 * q;
+                    const bool off = bad >> (cc * 2 + q / 4) & 1;
+                    va.x = off || j > pos || (W > 0 && j <= pos - W) ? neg_inf() : va.x;
+                    va.y = off || j + 1 > pos || (W > 0 && j + 1 <= pos - W) ? neg_inf() : va.y;
+                    vb.x = off || j + 2 > pos || (W > 0 && j + 2 <= pos - W) ? neg_inf() : vb.x;
+                    vb.y = off || j + 3 > pos || (W > 0 && j + 3 <= pos - W) ? neg_inf() : vb.y;
+                  }
+                  f(va, vb);
                 }
+              };
+              auto sum = [&]() {
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                scores(m == neg_inf() ? 0.f : -m, [&](const float2& va, const float2& vb) {
+                  s0.x += ex2(va.x);
+                  s0.y += ex2(va.y);
+                  s1.x += ex2(vb.x);
+                  s1.y += ex2(vb.y);
+                });
+                return add2(s0, s1);
+              };
+              // the reference m keeps exponentials below 2^60 or so: as long as a chunk's sum says that, no
+              // maximum is looked for
+              float2 s = sum();
+              if (__any_sync(0xffffffffu, m == neg_inf() || !(s.x + s.y < 0x1p60f))) {
+                // the first keys, or far larger ones (or a NaN): the reference becomes the maximum
+                float mx = m;
+                scores(0.f, [&](const float2& va, const float2& vb) {
+                  mx = fmaxf(fmaxf(mx, fmaxf(va.x, va.y)), fmaxf(vb.x, vb.y));
+                });
+                const float f = m == neg_inf() ? 0.f : ex2(m - mx);
+                acc[0] = mul2(acc[0], both(f));
+                acc[1] = mul2(acc[1], both(f));
+                m = mx;
+                s = sum();
               }
-              b.x = fmaf(g.x - k4[0], kLog2e, b.x);
-              b.y = fmaf(g.y - k4[1], kLog2e, b.y);
-              b.z = fmaf(g.z - k4[2], kLog2e, b.z);
-              b.w = fmaf(g.w - k4[3], kLog2e, b.w);
+              acc[cc & 1] = add2(acc[cc & 1], s);
             }
-            v[2 * q] = fma2(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])), both(ks),
-                            make_float2(b.x, b.y));
-            v[2 * q + 1] = fma2(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])), both(ks),
-                                make_float2(b.z, b.w));
-          }
-          if (need_mask) {
+          };
+          if (need_mask) tile(std::true_type());
+          else tile(std::false_type());
+        } else {
+          const int t0 = (b_lo + n) * ntok;
+          const int j_lo = a0 + x * kTile, j_hi = j_lo + kTile - 1;
+          const bool need_mask = t0 + ntok > ql || j_hi > L - ql + t0 || (W > 0 && j_lo <= L - ql + t0 + ntok - 1 - W);
+          const float4* b4 = reinterpret_cast<const float4*>(ax);
+          const float4* gi4 = reinterpret_cast<const float4*>(ax + kTile);
+          const int* see = reinterpret_cast<const int*>(ax) + 2 * kTile;
+          auto tile = [&](auto masked) {
+            constexpr bool kMask = decltype(masked)::value;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const int2 lk = *reinterpret_cast<const int2*>(see + cc * 32 + 2 * q);
-              if (pos > lk.x || (W > 0 && pos <= lk.x - W)) v[q].x = neg_inf();
-              if (pos > lk.y || (W > 0 && pos <= lk.y - W)) v[q].y = neg_inf();
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t sv[32];
+              tmem_ld32(tS + cc * 32, sv);
+              tmem_ld_wait();
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                float4 b = b4[cc * 8 + q];
+                if (kGates) {
+                  const float4 g = gi4[cc * 8 + q];
+                  float k4[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    k4[e] = gk[(4 * q + e) % kMaxGates];
+                    if (!repeat) {  // groups that 16 is no multiple of
+                      const int h = (cc * 32 + 4 * q + e) % G;
+#pragma unroll
+                      for (int w = 0; w < kMaxGates; ++w) k4[e] = h == w ? gk[w] : k4[e];
+                    }
+                  }
+                  b.x = fmaf(g.x - k4[0], kLog2e, b.x);
+                  b.y = fmaf(g.y - k4[1], kLog2e, b.y);
+                  b.z = fmaf(g.z - k4[2], kLog2e, b.z);
+                  b.w = fmaf(g.w - k4[3], kLog2e, b.w);
+                }
+                const uint32_t* s4 = sv + 4 * q;
+                float2 va = fma2(make_float2(__uint_as_float(s4[0]), __uint_as_float(s4[1])), both(ks),
+                                 make_float2(b.x, b.y));
+                float2 vb = fma2(make_float2(__uint_as_float(s4[2]), __uint_as_float(s4[3])), both(ks),
+                                 make_float2(b.z, b.w));
+                if (kMask) {
+                  const int4 lk = *reinterpret_cast<const int4*>(see + cc * 32 + 4 * q);
+                  va.x = pos > lk.x || (W > 0 && pos <= lk.x - W) ? neg_inf() : va.x;
+                  va.y = pos > lk.y || (W > 0 && pos <= lk.y - W) ? neg_inf() : va.y;
+                  vb.x = pos > lk.z || (W > 0 && pos <= lk.z - W) ? neg_inf() : vb.x;
+                  vb.y = pos > lk.w || (W > 0 && pos <= lk.w - W) ? neg_inf() : vb.y;
+                }
+                acc[0].x += ex2(va.x);
+                acc[0].y += ex2(va.y);
+                acc[1].x += ex2(vb.x);
+                acc[1].y += ex2(vb.y);
+              }
             }
-          }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) acc[q & 3] = add2(acc[q & 3], make_float2(ex2(v[q].x), ex2(v[q].y)));
+          };
+          if (need_mask) tile(std::true_type());
+          else tile(std::false_type());
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_empty[slot]);
+          mbar_arrive(&aux_empty[a]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s_empty[slot]);
-        mbar_arrive(&aux_empty[a]);
-      }
-    }
-    const float2 s2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+    };
+    if (gates) columns(std::true_type());
+    else columns(std::false_type());
+    const float2 s2 = add2(acc[0], acc[1]);
     float sum = s2.x + s2.y;
-    if (NA == 1) {  // the second group's part by shared memory (the aux vectors are done with)
-      float2* other = reinterpret_cast<float2*>(smem + C::OFF_RING);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (y == 1) other[rr] = make_float2(m, sum);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (y == 0) {
-        const float2 o = other[rr];
+    // the other groups' parts of the same rows, in a fixed order, by shared memory (the ring is done with)
+    constexpr int kParts = NA == 2 ? 2 : 4;
+    const int part = NA == 2 ? grp >> 1 : grp;
+    float2* others = reinterpret_cast<float2*>(smem + C::OFF_RING) + x * kParts * kTile;
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    if (part > 0) others[part * kTile + rr] = make_float2(m, sum);
+    asm volatile("bar.sync 1, 512;" ::: "memory");
+    if (part == 0 && !*abort_flag) {
+#pragma unroll
+      for (int k = 1; k < kParts; ++k) {
+        const float2 o = others[k * kTile + rr];
         if (WRITE) {
           sum += o.y;
         } else {
@@ -514,13 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = M;
         }
       }
-    }
-    if (!*abort_flag && (NA == 2 || y == 0)) {
       if (!WRITE) {
         if (row_ok)
           p.part[((size_t)seg * p.total_q + rq.q0 + t) * p.hq + kvh * G + head] = make_float2(m, sum);
       } else if (blk >= 0) {
-        float* w = p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
+        float* w = p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + slot_k;
         *w = p.decay != 0.f && pos < L - ql ? fmaf(p.decay, *w, sum) : sum;
       }
     }
@@ -528,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- e4m3 -> f16 stages (warps 12-15)
     // thread c takes the 16-byte piece c & 3 of keys 32 i + c / 4; two chunks are on their way
     // while one is converted
-    const int c = threadIdx.x - 384, piece = c & 3, row = c >> 2;
+    const int c = threadIdx.x - (4 + kEpiWarps) * 32, piece = c & 3, row = c >> 2;
     const int total = nt * NCH;
     uint4 ring[2][4];
     auto fetch = [&](int q, uint4 (&d)[4]) {
@@ -640,7 +729,7 @@ cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, cudaStream_
   if (e != cudaSuccess) return e;
   const int per = WRITE ? C::NA * kTile : C::NA * (kTile / p.group);
   const int n = WRITE ? (p.max_seq_len + per - 1) / per : (p.max_q_len + per - 1) / per * p.segs;
-  kern<<<dim3(n, p.hkv, p.num_reqs), kThreads, C::SMEM, s>>>(map, p);
+  kern<<<dim3(n, p.hkv, p.num_reqs), kThreadsOf<!BF16 && !WRITE>, C::SMEM, s>>>(map, p);
   return cudaGetLastError();
 }
 template <bool BF16, int NCH>
