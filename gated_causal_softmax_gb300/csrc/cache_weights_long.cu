@@ -217,15 +217,20 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
                                              (size_t)(pos & (p.block_size - 1)) * p.kv_ss);
     }
     const uint32_t col0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + x * C::A_COLS;
+    constexpr int kWords = C::A_COLS / kParts;      // columns of a thread's share: 16 .. 64
+    constexpr bool kCodes = !BF16 && WRITE;
+    constexpr int kLoads = kWords / (kCodes ? 8 : 4);
+    uint4 v[kLoads];  // all on their way at once
 #pragma unroll
-    for (int c = 0; c < C::A_COLS / kParts; c += 16) {  // 32 dims
-      const int col = part * (C::A_COLS / kParts) + c;
+    for (int i = 0; i < kLoads; ++i) v[i] = src ? __ldg(src + part * kLoads + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < kWords; c += 16) {  // 32 dims
       uint32_t w[16];
-      if (BF16 || !WRITE) {
+      if (!kCodes) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint4 v = src ? __ldg(src + col / 4 + u) : make_uint4(0, 0, 0, 0);
-          w[4 * u] = v.x, w[4 * u + 1] = v.y, w[4 * u + 2] = v.z, w[4 * u + 3] = v.w;
+          const uint4 x4 = v[c / 4 + u];
+          w[4 * u] = x4.x, w[4 * u + 1] = x4.y, w[4 * u + 2] = x4.z, w[4 * u + 3] = x4.w;
         }
         if (!BF16) {
 #pragma unroll
@@ -234,14 +239,14 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint4 v = src ? __ldg(src + col / 8 + u) : make_uint4(0, 0, 0, 0);
-          e4m3x4_to_f16x2x2(v.x, w[8 * u], w[8 * u + 1]);
-          e4m3x4_to_f16x2x2(v.y, w[8 * u + 2], w[8 * u + 3]);
-          e4m3x4_to_f16x2x2(v.z, w[8 * u + 4], w[8 * u + 5]);
-          e4m3x4_to_f16x2x2(v.w, w[8 * u + 6], w[8 * u + 7]);
+          const uint4 x4 = v[c / 8 + u];
+          e4m3x4_to_f16x2x2(x4.x, w[8 * u], w[8 * u + 1]);
+          e4m3x4_to_f16x2x2(x4.y, w[8 * u + 2], w[8 * u + 3]);
+          e4m3x4_to_f16x2x2(x4.z, w[8 * u + 4], w[8 * u + 5]);
+          e4m3x4_to_f16x2x2(x4.w, w[8 * u + 6], w[8 * u + 7]);
         }
       }
-      tmem_st16(col0 + col, w);
+      tmem_st16(col0 + part * kWords + c, w);
     }
     tmem_st_wait();
   }
@@ -454,70 +459,71 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
           const bool need_mask = j0 + kTile - 1 > L - ql + first_t || bad != 0 || (W > 0 && j0 <= L - ql + last_t - W);
           const float4* g4 = reinterpret_cast<const float4*>(ax + 3 * kTile + head * kGateRow);
           const float4* ks4 = reinterpret_cast<const float4*>(ax);
-          // one straight run of code for each case: a branch within it would part the exponentials
-          auto tile = [&](auto masked) {
+          // four scores (log2 units) and `base` at a time of 32 columns into f
+          auto scores = [&](auto masked, int cc, float base, auto f) {
             constexpr bool kMask = decltype(masked)::value;
+            uint32_t sv[32];
+            tmem_ld32(tS + cc * 32, sv);
+            tmem_ld_wait();
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
-              // four scores (log2 units) and `base` at a time into f
-              auto scores = [&](float base, auto f) {
-                uint32_t sv[32];
-                tmem_ld32(tS + cc * 32, sv);
-                tmem_ld_wait();
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  const float4 k4 = ks4[cc * 8 + q];
-                  float2 va = both(base), vb = both(base);
-                  if (kGates) {
-                    const float4 g = g4[cc * 8 + q];
-                    va = fma2(make_float2(gi - g.x, gi - g.y), both(kLog2e), va);
-                    vb = fma2(make_float2(gi - g.z, gi - g.w), both(kLog2e), vb);
-                  }
-                  va = fma2(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])),
-                            make_float2(k4.x, k4.y), va);
-                  vb = fma2(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])),
-                            make_float2(k4.z, k4.w), vb);
-                  if (kMask) {
-                    const int j = j0 + cc * 32 + 4 * q;
-                    const bool off = bad >> (cc * 2 + q / 4) & 1;
-                    va.x = off || j > pos || (W > 0 && j <= pos - W) ? neg_inf() : va.x;
-                    va.y = off || j + 1 > pos || (W > 0 && j + 1 <= pos - W) ? neg_inf() : va.y;
-                    vb.x = off || j + 2 > pos || (W > 0 && j + 2 <= pos - W) ? neg_inf() : vb.x;
-                    vb.y = off || j + 3 > pos || (W > 0 && j + 3 <= pos - W) ? neg_inf() : vb.y;
-                  }
-                  f(va, vb);
-                }
-              };
-              auto sum = [&]() {
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-                scores(m == neg_inf() ? 0.f : -m, [&](const float2& va, const float2& vb) {
-                  s0.x += ex2(va.x);
-                  s0.y += ex2(va.y);
-                  s1.x += ex2(vb.x);
-                  s1.y += ex2(vb.y);
-                });
-                return add2(s0, s1);
-              };
-              // the reference m keeps exponentials below 2^60 or so: as long as a chunk's sum says that, no
-              // maximum is looked for
-              float2 s = sum();
-              if (__any_sync(0xffffffffu, m == neg_inf() || !(s.x + s.y < 0x1p60f))) {
-                // the first keys, or far larger ones (or a NaN): the reference becomes the maximum
-                float mx = m;
-                scores(0.f, [&](const float2& va, const float2& vb) {
-                  mx = fmaxf(fmaxf(mx, fmaxf(va.x, va.y)), fmaxf(vb.x, vb.y));
-                });
-                const float f = m == neg_inf() ? 0.f : ex2(m - mx);
-                acc[0] = mul2(acc[0], both(f));
-                acc[1] = mul2(acc[1], both(f));
-                m = mx;
-                s = sum();
+            for (int q = 0; q < 8; ++q) {
+              const float4 k4 = ks4[cc * 8 + q];
+              float2 va = both(base), vb = both(base);
+              if (kGates) {
+                const float4 g = g4[cc * 8 + q];
+                va = fma2(make_float2(gi - g.x, gi - g.y), both(kLog2e), va);
+                vb = fma2(make_float2(gi - g.z, gi - g.w), both(kLog2e), vb);
               }
-              acc[cc & 1] = add2(acc[cc & 1], s);
+              va = fma2(make_float2(__uint_as_float(sv[4 * q]), __uint_as_float(sv[4 * q + 1])),
+                        make_float2(k4.x, k4.y), va);
+              vb = fma2(make_float2(__uint_as_float(sv[4 * q + 2]), __uint_as_float(sv[4 * q + 3])),
+                        make_float2(k4.z, k4.w), vb);
+              if (kMask) {
+                const int j = j0 + cc * 32 + 4 * q;
+                const bool off = bad >> (cc * 2 + q / 4) & 1;
+                va.x = off || j > pos || (W > 0 && j <= pos - W) ? neg_inf() : va.x;
+                va.y = off || j + 1 > pos || (W > 0 && j + 1 <= pos - W) ? neg_inf() : va.y;
+                vb.x = off || j + 2 > pos || (W > 0 && j + 2 <= pos - W) ? neg_inf() : vb.x;
+                vb.y = off || j + 3 > pos || (W > 0 && j + 3 <= pos - W) ? neg_inf() : vb.y;
+              }
+              f(va, vb);
             }
           };
-          if (need_mask) tile(std::true_type());
-          else tile(std::false_type());
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          auto add = [&](const float2& va, const float2& vb) {
+            s0.x += ex2(va.x);
+            s0.y += ex2(va.y);
+            s1.x += ex2(vb.x);
+            s1.y += ex2(vb.y);
+          };
+          // One straight run of code for each case: a branch within it would part the exponentials.  The
+          // reference m keeps them below 2^60 or so: as long as a tile's sum says that, no maximum is looked for.
+          if (need_mask) {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) scores(std::true_type(), cc, m == neg_inf() ? 0.f : -m, add);
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < 4; ++cc) scores(std::false_type(), cc, m == neg_inf() ? 0.f : -m, add);
+          }
+          float2 s = add2(s0, s1);
+          if (__any_sync(0xffffffffu, m == neg_inf() || !(s.x + s.y < 0x1p60f))) {
+            // the first keys, or far larger ones (or a NaN): the reference becomes the maximum
+            float mx = m;
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc)
+              scores(std::true_type(), cc, 0.f, [&](const float2& va, const float2& vb) {
+                mx = fmaxf(fmaxf(mx, fmaxf(va.x, va.y)), fmaxf(vb.x, vb.y));
+              });
+            const float f = m == neg_inf() ? 0.f : ex2(m - mx);
+            acc[0] = mul2(acc[0], both(f));
+            acc[1] = mul2(acc[1], both(f));
+            m = mx;
+            s0 = s1 = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) scores(std::true_type(), cc, m == neg_inf() ? 0.f : -m, add);
+            s = add2(s0, s1);
+          }
+          acc[0] = add2(acc[0], s);
         } else {
           const int t0 = (b_lo + n) * ntok;
           const int j_lo = a0 + x * kTile, j_hi = j_lo + kTile - 1;
@@ -620,19 +626,31 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     const int c = threadIdx.x - (4 + kEpiWarps) * 32, piece = c & 3, row = c >> 2;
     const int total = nt * NCH;
     uint4 ring[2][4];
-    auto fetch = [&](int q, uint4 (&d)[4]) {
+    // this thread's keys of the tile that is fetched, and of the one after it (looked up a tile ahead)
+    const uint8_t *src[4], *src_next[4];
+    auto look_up = [&](int n) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        d[i] = make_uint4(0, 0, 0, 0);
-        const int pos = key0 + (b_lo + q / NCH) * kTile + 32 * i + row;
-        if (q < total && pos < L) {
+        const int pos = key0 + (b_lo + n) * kTile + 32 * i + row;
+        src_next[i] = nullptr;
+        if (n < nt && pos < L) {
           const int blk = __ldg(table + (pos >> p.log2_block));  // the vectors' warps record it
           if (blk >= 0 && blk < p.num_blocks)
-            d[i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
-                                                        (size_t)(pos & (p.block_size - 1)) * p.kv_ss) +
-                         (q % NCH) * 4 + piece);
+            src_next[i] = p.k_cache + (size_t)blk * p.kv_bs + (size_t)kvh * p.kv_hs +
+                          (size_t)(pos & (p.block_size - 1)) * p.kv_ss + piece * 16;
         }
       }
+    };
+    look_up(0);
+    auto fetch = [&](int q, uint4 (&d)[4]) {
+      if (q % NCH == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] = src_next[i];
+        look_up(q / NCH + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        d[i] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i] + (q % NCH) * 64)) : make_uint4(0, 0, 0, 0);
     };
     uint32_t stage = 0, phase = 0;
     bool ok = true;
