@@ -11,6 +11,7 @@
 // accumulators and four lanes.  Key dims go from memory straight to the product's registers (a lane's
 // 16 bytes of each 64 dims, the query's dims in the same order).
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "sm103_ptx.cuh"
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
   float2* warp_ml = reinterpret_cast<float2*>(row_head + kRows);   // first kernel: [warp][row]
   float* gathered = reinterpret_cast<float*>(row_head + kRows);    // second: [key of the segment]
 
-  const int seg = blockIdx.x, kvh = blockIdx.y, r = blockIdx.z;
+  // the second kernel takes the requests in the other order: the last ones' keys are still in L2
+  const int seg = blockIdx.x, kvh = blockIdx.y, r = WRITE ? gridDim.z - 1 - blockIdx.z : blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   const int q0 = __ldg(p.cu_q + r), q1 = __ldg(p.cu_q + r + 1), L = __ldg(p.seq_lens + r);
   const int ql = q1 - q0;
@@ -95,6 +97,67 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
     for (int i = tid; i < p.seg_len; i += kThreads) gathered[i] = 0.f;
 
   for (int row0 = 0; row0 < nrows; row0 += kRows) {
+    const int rows_here = min(kRows, nrows - row0);
+    const int last_max = L - ql + (row0 + rows_here - 1) / G;  // last key any of these rows sees
+    const int last_min = L - ql + row0 / G;
+    const int key_first = p.window > 0 ? max(0, last_min - p.window + 1) : 0;
+
+    // A step's key dims come in units of 128 codes or 64 bf16 dims, one ahead of the products (across the
+    // steps too), its blocks another step ahead.  This lane's keys are 16 u + g and 16 u + g + 8.
+    constexpr int kUnitChunks = BF16 || kChunks == 1 ? 1 : 2, kUnits = kChunks / kUnitChunks;
+    constexpr int kVecs = kUnitChunks * (BF16 ? 2 : 1);
+    struct Unit {
+      uint4 v[2][2][kVecs];  // [page][key][chunk, or half of its dims]
+    };
+    struct Keys {
+      int blk[2];
+      float ks[2][2];
+    };
+    const uint8_t* k_lane = p.k_cache + (size_t)kvh * p.kv_hs + (size_t)g * p.kv_ss + tq * 16;
+    const int key_lo = max(k_begin, key_first & ~(kStep - 1)), key_hi = min(k_end, last_max + 1);
+    auto blocks = [&](int key0, int (&blk)[2]) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int pos = key0 + 16 * u;
+        blk[u] = key0 < key_hi && pos < L ? block_of(pos) : -1;
+      }
+    };
+    auto load_unit = [&](int key0, const int (&blk)[2], int unit, Unit& x) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int slot = (key0 + 16 * u) & (p.block_size - 1);
+        const uint8_t* at = k_lane + (size_t)max(blk[u], 0) * p.kv_bs + (size_t)slot * p.kv_ss +
+                            unit * (BF16 ? 128 : 64 * kUnitChunks);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < kVecs; ++i)
+            x.v[u][k][i] = blk[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(at + k * 8 * p.kv_ss + i * 64))
+                                       : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_scales = [&](int key0, Keys& x) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        x.ks[u][0] = x.ks[u][1] = kst;
+        if (p.format == kCachePerToken && x.blk[u] >= 0) {
+          const float* sc = p.k_scale + (((size_t)x.blk[u] * p.hkv + kvh) << p.log2_block) +
+                            ((key0 + 16 * u) & (p.block_size - 1)) + g;
+          x.ks[u][0] = __ldg(sc);
+          x.ks[u][1] = __ldg(sc + 8);
+        }
+      }
+    };
+    Keys next;
+    Unit cur;
+    int ahead[2];
+    {
+      const int key0 = key_lo + warp * kStep;
+      blocks(key0, next.blk);
+      blocks(key0 + kWarps * kStep, ahead);
+      load_scales(key0, next);
+      load_unit(key0, next.blk, 0, cur);
+    }
     __syncthreads();
     // the rows' constants and, in the second kernel, their sums
     for (int i = tid; i < kRows; i += kThreads) {
@@ -143,115 +206,112 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
       qf[i] = v;
     }
     __syncthreads();
-    const int rows_here = min(kRows, nrows - row0);
-    const int last_max = L - ql + (row0 + rows_here - 1) / G;  // last key any of these rows sees
-    const int last_min = L - ql + row0 / G;
-    const int key_first = p.window > 0 ? max(0, last_min - p.window + 1) : 0;
-
     float m[NT][2], l[NT][2];
     if (!WRITE) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = neg_inf(), l[nt][0] = l[nt][1] = 0.f;
     }
-    for (int key0 = k_begin + warp * kStep; key0 < k_end; key0 += kWarps * kStep) {
-      if (key0 > last_max || key0 + kStep <= key_first) continue;
-      // two pages of 16 keys; this lane's keys are 16 u + g and 16 u + g + 8
-      int blk[2];
+    for (int key0 = key_lo + warp * kStep; key0 < key_hi; key0 += kWarps * kStep) {
+      const int key1 = key0 + kWarps * kStep;  // the warp's next step
+      const Keys here = next;
+      next.blk[0] = ahead[0], next.blk[1] = ahead[1];
+      blocks(key1 + kWarps * kStep, ahead);
+      load_scales(key1, next);
+      const int(&blk)[2] = here.blk;
       float ks[2][2];
-      const uint8_t* at[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int pos = key0 + 16 * u, slot = pos & (p.block_size - 1);
-        blk[u] = pos < L ? block_of(pos) : -1;
-        at[u] = p.k_cache + (size_t)max(blk[u], 0) * p.kv_bs + (size_t)kvh * p.kv_hs + (size_t)(slot + g) * p.kv_ss + tq * 16;
-        ks[u][0] = ks[u][1] = kst * sl2;
-        if (p.format == kCachePerToken && blk[u] >= 0) {
-          const float* sc = p.k_scale + (((size_t)blk[u] * p.hkv + kvh) << p.log2_block) + slot + g;
-          ks[u][0] = __ldg(sc) * sl2;
-          ks[u][1] = __ldg(sc + 8) * sl2;
-        }
-      }
+      for (int u = 0; u < 2; ++u) ks[u][0] = here.ks[u][0] * sl2, ks[u][1] = here.ks[u][1] * sl2;
       float acc[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[u][nt][0] = acc[u][nt][1] = acc[u][nt][2] = acc[u][nt][3] = 0.f;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        uint32_t a[2][2][BF16 ? 8 : 4];  // [page][key g, g + 8][this lane's 16 dims]
+      for (int unit = 0; unit < kUnits; ++unit) {
+        Unit soon;
+        if (unit + 1 < kUnits) load_unit(key0, here.blk, unit + 1, soon);
+        else load_unit(key1, next.blk, 0, soon);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int cu = 0; cu < kUnitChunks; ++cu) {
+          const int c = unit * kUnitChunks + cu;
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int s = 0; s < 4; ++s) {
+            uint32_t f[2][4];
 #pragma unroll
-            for (int x = 0; x < (BF16 ? 2 : 1); ++x) {
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (blk[u] >= 0)
-                v = __ldg(reinterpret_cast<const uint4*>(at[u] + k * 8 * p.kv_ss + c * (BF16 ? 128 : 64) + x * 64));
-              a[u][k][4 * x] = v.x, a[u][k][4 * x + 1] = v.y, a[u][k][4 * x + 2] = v.z, a[u][k][4 * x + 3] = v.w;
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4 v = cur.v[u][k][BF16 ? s >> 1 : cu];
+                if constexpr (BF16) {
+                  f[u][k] = s & 1 ? v.z : v.x;
+                  f[u][2 + k] = s & 1 ? v.w : v.y;
+                } else {
+                  e4m3x4_to_f16x2x2(s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, f[u][k], f[u][2 + k]);
+                }
+              }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 b = qf[((c * 4 + s) * NT + nt) * 32 + lane];
+              mma<BF16>(acc[0][nt], f[0][0], f[0][1], f[0][2], f[0][3], b);
+              mma<BF16>(acc[1][nt], f[1][0], f[1][1], f[1][2], f[1][3], b);
             }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t f[2][4];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if constexpr (BF16) {
-              f[u][0] = a[u][0][2 * s], f[u][2] = a[u][0][2 * s + 1];
-              f[u][1] = a[u][1][2 * s], f[u][3] = a[u][1][2 * s + 1];
-            } else {
-              e4m3x4_to_f16x2x2(a[u][0][s], f[u][0], f[u][2]);
-              e4m3x4_to_f16x2x2(a[u][1][s], f[u][1], f[u][3]);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 b = qf[((c * 4 + s) * NT + nt) * 32 + lane];
-            mma<BF16>(acc[0][nt], f[0][0], f[0][1], f[0][2], f[0][3], b);
-            mma<BF16>(acc[1][nt], f[1][0], f[1][1], f[1][2], f[1][3], b);
           }
         }
+        cur = soon;
       }
       const bool inner = key0 + kStep - 1 <= last_min && rows_here == kRows && blk[0] >= 0 && blk[1] >= 0 &&
                          (p.window == 0 || key0 > last_max - p.window);
       float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+      // one straight run of code for each case: a branch within it would part the exponentials
+      auto columns = [&](auto with_gates, auto masked) {
+        constexpr bool kGates = decltype(with_gates)::value, kMask = decltype(masked)::value;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int col = nt * 8 + 2 * tq;
-        float x[2][2][2];  // [page][key][column]
+        for (int nt = 0; nt < NT; ++nt) {
+          const int col = nt * 8 + 2 * tq;
+          float x[2][2][2];  // [page][key][column]
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float v = acc[u][nt][2 * k + e] * ks[u][k];
-              if (gates && blk[u] >= 0) {
-                const float gk = __ldg(p.g_cache + (((size_t)blk[u] * p.hq + kvh * G + row_head[col + e]) << p.log2_block) +
-                                       ((key0 + 16 * u) & (p.block_size - 1)) + g + 8 * k);
-                v = fmaf(row_g[col + e] - gk, kLog2e, v);
+              for (int e = 0; e < 2; ++e) {
+                float v = acc[u][nt][2 * k + e] * ks[u][k];
+                if (kGates) {
+                  const float gk =
+                      __ldg(p.g_cache + (((size_t)max(blk[u], 0) * p.hq + kvh * G + row_head[col + e]) << p.log2_block) +
+                            ((key0 + 16 * u) & (p.block_size - 1)) + g + 8 * k);
+                  v = fmaf(row_g[col + e] - gk, kLog2e, v);
+                }
+                if (kMask) {
+                  const int key = key0 + 16 * u + g + 8 * k, lk = row_last[col + e];
+                  v = key > lk || blk[u] < 0 || (p.window > 0 && key <= lk - p.window) ? neg_inf() : v;
+                }
+                x[u][k][e] = v;
               }
-              if (!inner) {
-                const int key = key0 + 16 * u + g + 8 * k, lk = row_last[col + e];
-                if (key > lk || blk[u] < 0 || (p.window > 0 && key <= lk - p.window)) v = neg_inf();
-              }
-              x[u][k][e] = v;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (WRITE) {
+              const float z = row_sum[col + e];
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) w[u][k] += ex2(x[u][k][e] - z);
+            } else {
+              const float top = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
+              const float mn = fmaxf(m[nt][e], top), ref = mn == neg_inf() ? 0.f : mn;
+              l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + ((ex2(x[0][0][e] - ref) + ex2(x[0][1][e] - ref)) +
+                                                           (ex2(x[1][0][e] - ref) + ex2(x[1][1][e] - ref)));
+              m[nt][e] = mn;
             }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (WRITE) {
-            const float z = row_sum[col + e];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) w[u][k] += ex2(x[u][k][e] - z);
-          } else {
-            const float top = fmaxf(fmaxf(x[0][0][e], x[0][1][e]), fmaxf(x[1][0][e], x[1][1][e]));
-            const float mn = fmaxf(m[nt][e], top), ref = mn == neg_inf() ? 0.f : mn;
-            l[nt][e] = l[nt][e] * ex2(m[nt][e] - ref) + ((ex2(x[0][0][e] - ref) + ex2(x[0][1][e] - ref)) +
-                                                         (ex2(x[1][0][e] - ref) + ex2(x[1][1][e] - ref)));
-            m[nt][e] = mn;
           }
         }
+      };
+      if (gates) {
+        if (inner) columns(std::true_type(), std::false_type());
+        else columns(std::true_type(), std::true_type());
+      } else {
+        if (inner) columns(std::false_type(), std::false_type());
+        else columns(std::false_type(), std::true_type());
       }
       if (WRITE) {
 #pragma unroll
@@ -329,11 +389,11 @@ cudaError_t launch_f(const WeightsParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Context segments: enough blocks for about eight an SM, of 256 to 2048 keys.
+// Context segments: enough blocks for about eight an SM, of 256 to 4096 keys (a block spends a few microseconds before its first products: 64 requests up to 32K with 1024, 2048, 4096: 349, 298, 283 us).
 int cache_weights_segment(int max_seq_len, long long units, int sms) {
   const long long want = (8LL * sms + units - 1) / units;
   long long len = (max_seq_len + want - 1) / want;
-  len = std::min(std::max((len + 255) / 256 * 256, 256LL), 2048LL);
+  len = std::min(std::max((len + 255) / 256 * 256, 256LL), 4096LL);
   return (int)len;
 }
 
