@@ -13,21 +13,25 @@
 // not the cache's bytes.  Operands as in the chunked prefill: f16 from an fp8 cache (converted in
 // the CTA), bf16 from a bf16 one (copied straight into the operand tiles).
 //
-// Warp roles (384 threads):
-//   warp 0      producer: per 128-key tile the 8 pages' K and V (fp8: raw pages with their
-//               scales; bf16: the operand tiles, 64 dims x 16 slots a copy) and the gates
-//   warp 1      tcgen05 issuer: S_x = Q_x K^T and O_x += P_x V (P in TMEM)
-//   warps 2-3   fp8: e4m3 -> f16 operand tiles; bf16: zeros over the values past the prefix; both:
-//               the per-key vectors for the softmax
-//   warps 4-7   softmax of tile A, warps 8-11 of tile B, one thread per row
+// Warp roles (512 threads):
+//   warp 0        tensor copies: fp8: tiles of codes; bf16: the operand tiles, 64 dims x 16 slots each
+//   warp 1        tcgen05 issuer: S_x = Q_x K^T and O_x += P_x V (P in TMEM)
+//   warps 2-3     per-key vectors of the tiles in turn (scales, gates), up to four tiles ahead
+//   warps 4-11    softmax of tiles A and B, one thread per row
+//   warps 12-15   fp8: e4m3 -> f16 operand tiles; bf16: zeros over the values of the last tile past the
+//                 prefix
+#include <type_traits>
+
 #include "decode_split.cuh"
+#include "rows.cuh"
 
 namespace gcs {
 namespace {
 
 constexpr int kTileKeys = 128;    // 8 pages
-constexpr int kPreThreads = 384;
+constexpr int kPreThreads = 512;
 constexpr int kStage = 16384;     // one operand stage: 128 rows x 64 dims or 64 keys x 128 dims
+constexpr int kVecs = 4;          // tiles whose vectors are held
 constexpr float kPrePScale = 16.f;  // P * vscale carried x 2^4
 constexpr float kPreLazy = 4.f;     // lazy rescale threshold (log2 units): P <= 2^4
 
@@ -36,40 +40,61 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return fma2(a, both(1.f), b); }
 
-template <bool BF16, bool FEAT>
+template <bool BF16, bool GATES>
 struct PreCfg {
-  static constexpr int NST = BF16 ? 8 : FEAT ? 6 : 7;      // operand stages
+  static constexpr int STAGES = BF16 ? 8 : 6;              // a tile's K dims 0..63, 64..127, V keys 0..63, 64..127
+  static constexpr int RAW = BF16 ? 0 : GATES ? 2 : 3;     // K or V tiles of codes, on their way to be converted
   static constexpr int OFF_Q = 0;                          // [2 tiles][2 dim chunks] x 16 KB
   static constexpr int OFF_RING = 4 * kStage;
-  static constexpr int OFF_KRAW = OFF_RING + NST * kStage; // (fp8: K pages | K scales | V scales |) gates
-  static constexpr int KR_KS = BF16 ? 0 : 8 * 2048, KR_VS = KR_KS + (BF16 ? 0 : 512), KR_G = KR_VS + (BF16 ? 0 : 512);
-  static constexpr int KRAW = KR_G + (FEAT ? 8 * 1024 : 0);
-  static constexpr int OFF_VRAW = OFF_KRAW + KRAW;         // V pages
-  static constexpr int OFF_AUX = OFF_VRAW + (BF16 ? 0 : 8 * 2048);  // [2] x {ks'[128], vs'[128], G'[16][128]}
-  static constexpr int AUX = 1024 + (FEAT ? 8192 : 0);
-  static constexpr int OFF_BAR = OFF_AUX + 2 * AUX;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * NST + 24) * 8;
+  static constexpr int OFF_RAW = OFF_RING + STAGES * kStage;   // [RAW] x 16 KB
+  static constexpr int OFF_VEC = OFF_RAW + RAW * kStage;   // [HELD] x {ks'[128], vs'[128], G[16][132]}
+  static constexpr int GATE_ROW = kTileKeys + 4;           // floats: the heads' rows 16 bytes apart in the banks
+  static constexpr int VEC = 1024 + (GATES ? 16 * GATE_ROW * 4 : 0);
+  static constexpr int HELD = GATES ? 2 : kVecs;           // tiles whose vectors are held
+  static constexpr int OFF_BAR = OFF_VEC + HELD * VEC;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kVecs + 18) * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory budget");
 };
 
-// 128 x 88 + 256 x 208 = 64512 = 384 threads x 168 at launch
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory"); }
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory"); }
+// 128 x (64 + 96 + 176 + 176) = 65536 = 512 threads x 128 at launch
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void sts128(uint8_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+// 16 e4m3 codes to the units 2 u and 2 u + 1 of row r of a swizzled tile
+__device__ __forceinline__ void put_codes(uint8_t* tile, int r, int u, uint4 v) {
+  uint32_t w[8];
+  e4m3x4_to_f16x2x2(v.x, w[0], w[1]);
+  e4m3x4_to_f16x2x2(v.y, w[2], w[3]);
+  e4m3x4_to_f16x2x2(v.z, w[4], w[5]);
+  e4m3x4_to_f16x2x2(v.w, w[6], w[7]);
+  sts128(tile + sw128_offset(r, 2 * u), make_uint4(w[0], w[1], w[2], w[3]));
+  sts128(tile + sw128_offset(r, 2 * u + 1), make_uint4(w[4], w[5], w[6], w[7]));
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrives once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 // Tokens that group g shares, as far as the first request's cache and the host's bound go.
 __device__ __forceinline__ int group_len(const DecodeParams& p, int g, int first) {
   return max(0, min(min(__ldg(p.prefix_lens + g), p.max_prefix), __ldg(p.seq_lens + first)));
 }
 
-template <bool BF16, bool FEAT>
+template <bool BF16, bool GATES>
 __global__ void __launch_bounds__(kPreThreads, 1)
     decode_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const DecodeParams p) {
-  using C = PreCfg<BF16, FEAT>;
+  using C = PreCfg<BF16, GATES>;
+  constexpr int kStages = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align_1k(smem_raw);
 
@@ -82,47 +107,43 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int P = group_len(p, grp, r0);
   const int G = p.group, lgG = G == 16 ? 4 : 3;
   const int pos_tile = 128 / G;  // query rows of a 128-row tile
-  const int lbp = p.log2_block_pages;
   const int row0 = qp * 2 * pos_tile;
   const int key0 = seg * p.pre_seg_keys;
   if (row0 >= ql || key0 >= P) return;
   const int key1 = min(P, key0 + p.pre_seg_keys);
-  const int W = FEAT ? p.window : 0;
+  const int W = p.window;
+  const int32_t* trow = p.block_table + (size_t)r0 * p.max_blocks;
+  const int lb = p.log2_block_pages + 4;  // log2 of a cache block's tokens
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* full = bars;               // [NST] operand stages written
-  uint64_t* empty = bars + C::NST;     // [NST] consumed
-  uint64_t* kr_full = bars + 2 * C::NST;
-  uint64_t* kr_empty = kr_full + 1;
-  uint64_t* vr_full = kr_full + 2;
-  uint64_t* vr_empty = kr_full + 3;
-  uint64_t* aux_full = kr_full + 4;    // [2]
-  uint64_t* aux_empty = kr_full + 6;   // [2]
-  uint64_t* q_full = kr_full + 8;      // [2 tiles]
-  uint64_t* s_full = kr_full + 10;     // [2 tiles]
-  uint64_t* p_full = kr_full + 12;     // [2 tiles]
-  uint64_t* pv_done = kr_full + 14;    // [2 tiles]
-  uint64_t* drain = kr_full + 16;
+  uint64_t* full = bars;                 // [kStages] operand stages written
+  uint64_t* empty = bars + kStages;      // [kStages] consumed
+  uint64_t* vec_full = bars + 2 * kStages;   // [HELD]
+  uint64_t* vec_empty = vec_full + kVecs;    // [HELD]
+  uint64_t* q_full = vec_empty + kVecs;  // [2 tiles]
+  uint64_t* s_full = q_full + 2;         // [2 tiles]
+  uint64_t* p_full = q_full + 4;         // [2 tiles]
+  uint64_t* pv_done = q_full + 6;        // [2 tiles]
+  uint64_t* tail_full = q_full + 8;      // bf16: the values of the last tile
+  uint64_t* drain = q_full + 9;
+  uint64_t* raw_full = q_full + 10;      // [RAW] fp8
+  uint64_t* raw_empty = q_full + 13;     // [RAW]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* see = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // [2 tiles] x {least, greatest last key of a row}
   const Abort ab{abort_flag, p.status};
-  uint8_t* kraw = smem + C::OFF_KRAW;
-  uint8_t* vraw = smem + C::OFF_VRAW;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&full[i], BF16 ? 1 : 2);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], BF16 ? 1 : 4);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(kr_full, 1);
-    mbar_init(kr_empty, 2);
-    mbar_init(vr_full, 1);
-    mbar_init(vr_empty, 2);
+    for (int i = 0; i < C::HELD; ++i) {
+      mbar_init(&vec_full[i], GATES ? 64 : 32);
+      mbar_init(&vec_empty[i], 8);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&aux_full[i], 2);
-      mbar_init(&aux_empty[i], 8);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
@@ -130,6 +151,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       see[2 * i] = 0x7fffffff;
       see[2 * i + 1] = -1;
     }
+    for (int i = 0; i < C::RAW; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
+    mbar_init(tail_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -140,14 +166,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
   __syncthreads();
   // the softmax threads' rows: packed row, its request's last visible key
-  const int x_of = warp < 4 ? 0 : (warp - 4) >> 2;
+  const bool softmax = warp >= 4 && warp < 12;
+  const int x_of = softmax ? (warp - 4) >> 2 : 0;
   const int rr = (warp & 3) * 32 + lane;  // row of the tile
   const int head = rr & (G - 1);
   const int pos = row0 + x_of * pos_tile + (rr >> lgG);
-  const bool row_valid = warp >= 4 && pos < ql;
+  const bool row_valid = softmax && pos < ql;
   const int tt = q_begin + min(pos, ql - 1);  // packed row
   int lastk = -1, req = r0;
-  if (warp >= 4) {
+  if (softmax) {
     int lo = r0, hi = r1;  // cu_q[lo] <= tt < cu_q[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -192,105 +219,97 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     n_last[x] = any ? hi[x] - lo_t : -1;
   }
   auto part = [&](int x, int n) -> bool { return n >= n_first[x] && n <= n_last[x]; };
+  auto ring_next = [&](uint32_t& stage, uint32_t& phase) {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
 
   if (warp < 4) {
-    reg_dec();
-    if (nt == 0) {
-    } else if (warp == 0) {
-      // ---------------------------------------------------------- page producer
-      const int32_t* trow = p.block_table + (size_t)r0 * p.max_blocks;
-      const bool per_token = !BF16 && p.scale_mode == 0;
-      const bool has_gate = FEAT && p.g_cache != nullptr;
-      const int pl = lane & 7, kind = lane >> 3;
-      if (lane == 0) {
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-      }
-      const int last_page = (P + kPage - 1) / kPage;
-      uint32_t stage = 0, phase = 0;
-      for (int n = 0; n < nt; ++n) {
-        const int pg0 = key0 / kPage + (lo_t + n) * 8;
-        const int nv = min(8, last_page - pg0);  // pages of the tile that exist
-        const uint32_t par = (n & 1) ^ 1;
-        const int pg = pg0 + pl;
-        const int blk = pl < nv ? __ldg(trow + (pg >> lbp)) : 0;
-        const int sub = (pg & ((1 << lbp) - 1)) * kPage;  // first slot of the page in its block
-        const int cy = p.kv_head_inner ? kvh : sub, cz = p.kv_head_inner ? sub : kvh;
-        auto gates = [&](uint64_t* bar) {
-          // the group's G heads x 16 slots: adjacent when a block is one page
-          const float* src = p.g_cache + ((size_t)blk * p.hq + kvh * G) * p.block_size + sub;
-          if (lbp == 0) {
-            bulk_load(kraw + C::KR_G + pl * 1024, src, G * kPage * 4, bar);
-          } else {
-            for (int hh = 0; hh < G; ++hh)
-              bulk_load(kraw + C::KR_G + pl * 1024 + hh * kPage * 4, src + (size_t)hh * p.block_size, kPage * 4, bar);
-          }
-        };
-        if constexpr (!BF16) {
-          bool okl = wait_bar(kr_empty, par, ab);
-          if (!__all_sync(0xffffffffu, okl)) break;
-          if (lane == 0)
-            mbar_expect_tx(kr_full, nv * (2048 + (per_token ? 128 : 0) + (has_gate ? G * kPage * 4 : 0)));
-          __syncwarp();
-          if (pl < nv) {
-            const size_t slot0 = ((size_t)blk * p.hkv + kvh) * p.block_size + sub;
-            if (kind == 0) tma_load_4d(kraw + pl * 2048, &tmK, kr_full, 0, cy, cz, blk);
-            else if (kind == 1 && per_token) bulk_load(kraw + C::KR_KS + pl * 64, p.k_scale + slot0, 64, kr_full);
-            else if (kind == 2 && per_token) bulk_load(kraw + C::KR_VS + pl * 64, p.v_scale + slot0, 64, kr_full);
-            else if (kind == 3 && has_gate) gates(kr_full);
-          }
-          okl = wait_bar(vr_empty, par, ab);
-          if (!__all_sync(0xffffffffu, okl)) break;
-          if (lane == 0) mbar_expect_tx(vr_full, nv * 2048);
-          __syncwarp();
-          if (kind == 0 && pl < nv) tma_load_4d(vraw + pl * 2048, &tmV, vr_full, 0, cy, cz, blk);
-        } else {
-          // operand stages of the tile: K dims 0..63, K dims 64..127, V keys 0..63, V keys 64..127.  The
-          // values of the prefix's last, partly filled tile go by vr_full to warp 2, which zeroes what
-          // lies past the prefix (whatever its bytes hold) before the stages count as written.
-          const bool tail = key0 + (lo_t + n + 1) * kTileKeys > P;
-          uint8_t* st[4];
-          uint64_t* fb[4];
+    reg_dec<64>();
+    if (warp == 0) {
+      if (!BF16) {
+        // ---------------------------------------------------------- codes: K and V tiles in turn, lane = page
+        if (lane == 0) {
+          prefetch_tmap(&tmK);
+          prefetch_tmap(&tmV);
+        }
+        const int last_page = (P + kPage - 1) / kPage;
+        int i = 0;  // K or V tile
+        uint32_t buf = 0, phase = 0;
+        for (int n = 0; n < nt; ++n) {
+          const int pg0 = key0 / kPage + (lo_t + n) * 8, pg = pg0 + lane;
+          const int nv = min(8, last_page - pg0);  // pages of the tile that exist
+          const int blk = lane < nv ? __ldg(trow + (pg >> p.log2_block_pages)) : 0;
+          const int sub = (pg & ((1 << p.log2_block_pages) - 1)) * kPage;
+          const int cy = p.kv_head_inner ? kvh : sub, cz = p.kv_head_inner ? sub : kvh;
           bool okl = true;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            st[i] = smem + C::OFF_RING + stage * kStage;
-            fb[i] = &full[stage];
-            if (okl) okl = wait_bar(&empty[stage], phase ^ 1, ab);
-            if (++stage == C::NST) {
-              stage = 0;
+          for (int v = 0; v < 2 && okl; ++v, ++i) {
+            okl = __all_sync(0xffffffffu, wait_bar(&raw_empty[buf], phase ^ 1, ab));
+            if (!okl) break;
+            if (lane == 0) mbar_expect_tx(&raw_full[buf], nv * 2048);
+            __syncwarp();
+            if (lane < nv)
+              tma_load_4d(smem + C::OFF_RAW + buf * kStage + lane * 2048, v ? &tmV : &tmK, &raw_full[buf], 0, cy, cz, blk);
+            if (++buf == (uint32_t)C::RAW) {
+              buf = 0;
               phase ^= 1;
             }
           }
-          if (has_gate && okl) okl = wait_bar(kr_empty, par, ab);
-          if (!__all_sync(0xffffffffu, okl)) break;
-          if (lane == 0) {
-            mbar_expect_tx(fb[0], nv * 2048);
-            mbar_expect_tx(fb[1], nv * 2048);
-            if (tail) {
-              mbar_expect_tx(vr_full, nv * 4096);
-            } else {
-              mbar_expect_tx(fb[2], 4 * 4096);
-              mbar_expect_tx(fb[3], 4 * 4096);
+          if (!okl) break;
+        }
+      } else {
+        // ---------------------------------------------------------- operand tiles by tensor copies
+        // The values of the prefix's last, partly filled tile go by tail_full to warp 12, which zeroes what
+        // lies past the prefix (whatever its bytes hold) before the stages count as written.
+        const int pl = lane & 7, c = lane >> 3 & 1;  // page, 64 dims
+        if (lane == 0) {
+          prefetch_tmap(&tmK);
+          prefetch_tmap(&tmV);
+        }
+        const int last_page = (P + kPage - 1) / kPage;
+        uint32_t stage = 0, phase = 0;
+        for (int n = 0; n < nt; ++n) {
+          const int pg0 = key0 / kPage + (lo_t + n) * 8, pg = pg0 + pl;
+          const int nv = min(8, last_page - pg0);  // pages of the tile that exist
+          const int blk = pl < nv ? __ldg(trow + (pg >> p.log2_block_pages)) : 0;
+          const int sub = (pg & ((1 << p.log2_block_pages) - 1)) * kPage;  // first slot of the page in its block
+          const int cy = p.kv_head_inner ? kvh : sub, cz = p.kv_head_inner ? sub : kvh;
+          const bool tail = key0 + (lo_t + n + 1) * kTileKeys > P;
+          bool okl = true;
+          for (int v = 0; v < 2 && okl; ++v) {  // K, V
+            const uint32_t s0 = stage;
+            okl = wait_bar(&empty[stage], phase ^ 1, ab);
+            ring_next(stage, phase);
+            const uint32_t s1 = stage;
+            if (okl) okl = wait_bar(&empty[stage], phase ^ 1, ab);
+            ring_next(stage, phase);
+            okl = __all_sync(0xffffffffu, okl);
+            if (!okl) break;
+            if (lane == 0) {
+              if (v == 0) {
+                mbar_expect_tx(&full[s0], nv * 2048);
+                mbar_expect_tx(&full[s1], nv * 2048);
+              } else if (tail) {
+                mbar_expect_tx(tail_full, nv * 4096);
+              } else {
+                mbar_expect_tx(&full[s0], 4 * 4096);
+                mbar_expect_tx(&full[s1], 4 * 4096);
+              }
             }
-            if (has_gate) mbar_expect_tx(kr_full, nv * G * kPage * 4);
-          }
-          __syncwarp();
-          if (pl < nv) {
-            const int c = kind & 1;  // 64 dims
-            if (kind < 2) {
-              tma_load_4d(st[c] + pl * 2048, &tmK, fb[c], 64 * c, cy, cz, blk);
-            } else {
-              const int hv = pl >> 2;
-              tma_load_4d(st[2 + hv] + c * (kStage / 2) + (pl & 3) * 2048, &tmV, tail ? vr_full : fb[2 + hv], 64 * c, cy,
-                          cz, blk);
+            __syncwarp();
+            if (lane < 16 && pl < nv) {
+              const uint32_t st = (v == 0 ? c : pl >> 2) ? s1 : s0;
+              uint8_t* dst = smem + C::OFF_RING + st * kStage + (v == 0 ? pl * 2048 : c * (kStage / 2) + (pl & 3) * 2048);
+              tma_load_4d(dst, v == 0 ? &tmK : &tmV, v == 1 && tail ? tail_full : &full[st], 64 * c, cy, cz, blk);
             }
-            if (kind == 0 && has_gate) gates(kr_full);
           }
+          if (!okl) break;
         }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (lane == 0 && nt > 0) {
         // -------------------------------------------------------- MMA issuer
         const uint32_t idS = BF16 ? idesc_bf16(128, kTileKeys, false, false) : idesc_f16(128, kTileKeys, false, false);
         const uint32_t idPV = BF16 ? idesc_bf16(128, kD, false, true) : idesc_f16(128, kD, false, true);
@@ -302,10 +321,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         auto next = [&](uint32_t& st, uint32_t& ph) {
           st = stage;
           ph = phase;
-          if (++stage == C::NST) {
-            stage = 0;
-            phase ^= 1;
-          }
+          ring_next(stage, phase);
         };
         auto mma_s = [&](int x, uint32_t k0, uint32_t k1) {  // S_x = Q_x K^T
 #pragma unroll
@@ -398,133 +414,133 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       __syncwarp();
     } else {
-      // ---------------------------------------------------------- converters (warps 2-3)
-      const int c = threadIdx.x - 64;  // 0 .. 63
+      // ---------------------------------------------------------- per-key vectors
+      // The two warps take the tiles in turn, lane l the keys 4 l .. 4 l + 3 (of one page).  A tile's scales
+      // are on their way while the one before is written; the gates go straight into shared memory.
       const bool per_token = !BF16 && p.scale_mode == 0;
-      const bool has_gate = FEAT && p.g_cache != nullptr;
       const float kst = BF16 ? 1.f : per_token ? 0.f : __ldg(p.k_scale);
       const float vst = BF16 ? 1.f : per_token ? 0.f : __ldg(p.v_scale);
       const float sl2 = p.scale * kLog2e;
-      uint8_t* ring = smem + C::OFF_RING;
-      uint32_t stage = 0, phase = 0;
-      auto next = [&](uint32_t& st, uint32_t& ph) {
-        st = stage;
-        ph = phase;
-        if (++stage == C::NST) {
-          stage = 0;
-          phase ^= 1;
+      float4 ks, vs;
+      int blk, slot;
+      auto fetch = [&](int n) {
+        const int k = key0 + (lo_t + n) * kTileKeys + 4 * lane;
+        ks = make_float4(kst, kst, kst, kst);
+        vs = make_float4(vst, vst, vst, vst);
+        blk = -1;
+        if (n < nt && k < P) {
+          blk = __ldg(trow + (k >> lb));
+          slot = k & (p.block_size - 1);
+          if (per_token) {
+            const size_t at = ((size_t)blk * p.hkv + kvh) * p.block_size + slot;
+            ks = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
+            vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
+          }
         }
       };
-      // 8 pages of fp8 rows (128 B, 128-byte swizzled) -> f16 operand rows.  Thread c takes the
-      // keys 8 i + (c & 7), i = 0..15, and the 16-dim group q = c / 8 of each: a quarter warp
-      // reads one group of eight consecutive keys and writes the two 16-B halves of each result
-      // to units (2 (q & 3), 2 (q & 3) + 1) of their swizzled rows, all in different bank groups.
-      //   K (is_v false): stage sa holds dims 0..63, sb dims 64..127; row = key (K-major).
-      //   V (is_v true):  stage sa holds keys 0..63, sb keys 64..127; inside a stage, dims
-      //                   0..63 then 64..127 (8 KB apart), row = key (MN-major).
-      const int cq = c >> 3, ck = c & 7;
-      const uint32_t su0 = ((2 * (cq & 3)) ^ ck) << 4, su1 = ((2 * (cq & 3) + 1) ^ ck) << 4;
-      auto convert = [&](const uint8_t* raw, int kbase, bool is_v, uint32_t sa, uint32_t sb) {
-        const uint8_t* src = raw + ck * 128 + ((cq ^ ck) << 4);
-        uint8_t* dst_a;
-        uint8_t* dst_b;
-        if (!is_v) {
-          dst_a = dst_b = ring + ((cq >> 2) ? sb : sa) * kStage + ck * 128;
-        } else {
-          dst_a = ring + sa * kStage + (cq >> 2) * (kStage / 2) + ck * 128;
-          dst_b = ring + sb * kStage + (cq >> 2) * (kStage / 2) + ck * 128;
-        }
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-          uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-          if (kbase + 8 * i + ck < P) xv = lds128(src + i * 1024);
-          uint32_t w[8];
-          e4m3x4_to_f16x2x2(xv.x, w[0], w[1]);
-          e4m3x4_to_f16x2x2(xv.y, w[2], w[3]);
-          e4m3x4_to_f16x2x2(xv.z, w[4], w[5]);
-          e4m3x4_to_f16x2x2(xv.w, w[6], w[7]);
-          uint8_t* row = !is_v ? dst_a + i * 1024 : (i < 8 ? dst_a + i * 1024 : dst_b + (i - 8) * 1024);
-          sts128(row + su0, make_uint4(w[0], w[1], w[2], w[3]));
-          sts128(row + su1, make_uint4(w[4], w[5], w[6], w[7]));
-        }
-      };
-      for (int n = 0; n < nt; ++n) {
-        const int kbase = key0 + (lo_t + n) * kTileKeys;
-        const int a = n & 1;
-        bool ok = wait_bar(&aux_empty[a], ((n >> 1) & 1) ^ 1, ab);
-        if (ok && (!BF16 || has_gate)) ok = wait_bar(kr_full, n & 1, ab);
-        if (!ok) break;
-        // per-key vectors of this tile (zero past the prefix)
-        float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
-        for (int k = c; k < kTileKeys; k += 64) {
-          const bool valid = kbase + k < P;
-          const float ks = per_token ? reinterpret_cast<const float*>(kraw + C::KR_KS)[k] : kst;
-          const float vs = per_token ? reinterpret_cast<const float*>(kraw + C::KR_VS)[k] : vst;
-          ax[k] = valid ? ks * sl2 : 0.f;
-          ax[kTileKeys + k] = valid ? vs * kPrePScale : 0.f;
-        }
-        if (FEAT) {
-          // G_j for the group's G heads: raw pages hold [head][slot], 1 KB apart
-          const float* gr = reinterpret_cast<const float*>(kraw + C::KR_G);
-          for (int i = c; i < p.group * kTileKeys; i += 64) {
-            const int h = i >> 7, k = i & 127;
-            ax[2 * kTileKeys + i] = (has_gate && kbase + k < P) ? gr[(k >> 4) * 256 + h * kPage + (k & 15)] : 0.f;
+      fetch(warp - 2);
+      for (int n = warp - 2; n < nt; n += 2) {
+        const int a = n % C::HELD, left = P - (key0 + (lo_t + n) * kTileKeys + 4 * lane);  // of this lane's keys
+        float4 k4 = ks, v4 = vs;
+        const int b = blk, sl = slot;
+        fetch(n + 2);
+        if (!wait_bar(&vec_empty[a], ((n / C::HELD) & 1) ^ 1, ab)) break;
+        float* vec = reinterpret_cast<float*>(smem + C::OFF_VEC + a * C::VEC);
+        if (GATES) {
+          if (b >= 0) {
+            const float* g = p.g_cache + ((size_t)b * p.hq + kvh * G) * p.block_size + sl;
+            for (int h = 0; h < G; ++h) copy16(vec + 2 * kTileKeys + h * C::GATE_ROW + 4 * lane, g + (size_t)h * p.block_size);
           }
+          copies_arrive(&vec_full[a]);
         }
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&aux_full[a]);
-          if (BF16 && has_gate) mbar_arrive(kr_empty);
-        }
-        uint32_t s0, p0, s1, p1, s2, p2, s3, p3;
-        next(s0, p0);
-        next(s1, p1);
-        next(s2, p2);
-        next(s3, p3);
-        if constexpr (BF16) {
-          if (kbase + kTileKeys > P && warp == 2) {  // the last tile
-            ok = wait_bar(vr_full, 0, ab);
-            if (!ok) break;
-            for (int i = lane; i < kTileKeys * 16; i += 32) {
-              const int k = i >> 4, u = i & 15;  // key, 16 bytes of it
-              if (kbase + k >= P)
-                sts128(ring + (k >> 6 ? s3 : s2) * kStage + (u >> 3) * (kStage / 2) + (k & 63) * 128 + (u & 7) * 16,
-                       make_uint4(0u, 0u, 0u, 0u));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&full[s2]);
-              mbar_arrive(&full[s3]);
-            }
+        // zeros past the prefix, whatever is there
+        k4.x = left > 0 ? k4.x * sl2 : 0.f, v4.x = left > 0 ? v4.x * kPrePScale : 0.f;
+        k4.y = left > 1 ? k4.y * sl2 : 0.f, v4.y = left > 1 ? v4.y * kPrePScale : 0.f;
+        k4.z = left > 2 ? k4.z * sl2 : 0.f, v4.z = left > 2 ? v4.z * kPrePScale : 0.f;
+        k4.w = left > 3 ? k4.w * sl2 : 0.f, v4.w = left > 3 ? v4.w * kPrePScale : 0.f;
+        reinterpret_cast<float4*>(vec)[lane] = k4;
+        reinterpret_cast<float4*>(vec + kTileKeys)[lane] = v4;
+        mbar_arrive(&vec_full[a]);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    reg_dec<96>();
+    uint32_t stage = 0, phase = 0;
+    if (BF16) {
+      // ---------------------------------------------------------- zeros past the prefix
+      // (the segment's last tile is processed by some query tile only if a row sees it)
+      if (warp == 12 && nt > 0 && key0 + (lo_t + nt) * kTileKeys > P) {
+        if (wait_bar(tail_full, 0, ab)) {
+          const uint32_t s2 = (4 * (nt - 1) + 2) % kStages, s3 = s2 + 1;
+          const int kbase = key0 + (lo_t + nt - 1) * kTileKeys;
+          for (int i = lane; i < kTileKeys * 16; i += 32) {
+            const int k = i >> 4, u = i & 15;  // key, 16 bytes of it
+            if (kbase + k >= P)
+              sts128(smem + C::OFF_RING + (k >> 6 ? s3 : s2) * kStage + (u >> 3) * (kStage / 2) + (k & 63) * 128 +
+                         (u & 7) * 16,
+                     make_uint4(0u, 0u, 0u, 0u));
           }
-        } else {
-          ok = wait_bar(&empty[s0], p0 ^ 1, ab) && wait_bar(&empty[s1], p1 ^ 1, ab);
-          if (!ok) break;
-          convert(kraw, kbase, false, s0, s1);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[s0]);
-            mbar_arrive(&full[s1]);
-            mbar_arrive(kr_empty);
-          }
-          ok = wait_bar(vr_full, n & 1, ab) && wait_bar(&empty[s2], p2 ^ 1, ab) && wait_bar(&empty[s3], p3 ^ 1, ab);
-          if (!ok) break;
-          convert(vraw, kbase, true, s2, s3);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&full[s2]);
             mbar_arrive(&full[s3]);
-            mbar_arrive(vr_empty);
           }
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- e4m3 -> f16 operand tiles
+      // A tile of codes is 128 keys x 128 B, 128-byte swizzled.  Thread t takes the keys 8 i + (t & 7) of one
+      // half of them and the 16-dim group (t / 8) & 7 of each: a quarter warp reads one group of eight
+      // neighbouring keys and writes the two 16-B halves of each result to units of their swizzled
+      // rows that are all in different bank groups.
+      //   K: the first stage holds dims 0..63, the second dims 64..127; row = key (K-major)
+      //   V: the first stage holds keys 0..63, the second keys 64..127; inside a stage, dims 0..63 then
+      //      64..127 (8 KB apart), row = key (MN-major)
+      const int t = threadIdx.x - 384, ck = t & 7, cq = t >> 3 & 7, hf = t >> 6;
+      uint32_t buf = 0, raw_phase = 0;
+      bool ok = true;
+      for (int i = 0; i < 2 * nt && ok; ++i) {
+        const bool v = i & 1;
+        const int kbase = key0 + (lo_t + (i >> 1)) * kTileKeys + 64 * hf + ck;
+        const uint32_t sa = stage, pa = phase;
+        ring_next(stage, phase);
+        const uint32_t sb = stage, pb = phase;
+        ring_next(stage, phase);
+        ok = wait_bar(&raw_full[buf], raw_phase, ab) && wait_bar(&empty[sa], pa ^ 1, ab) && wait_bar(&empty[sb], pb ^ 1, ab);
+        if (!ok) break;
+        const uint8_t* src = smem + C::OFF_RAW + buf * kStage + (64 * hf + ck) * 128 + ((cq ^ ck) << 4);
+        uint8_t* dst = smem + C::OFF_RING;
+        int row = ck;  // of the operand tile
+        if (v) {
+          dst += (hf ? sb : sa) * kStage + (cq >> 2) * (kStage / 2);
+        } else {
+          dst += (cq >> 2 ? sb : sa) * kStage;
+          row += 64 * hf;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);  // past the prefix, whatever is there
+          if (kbase + 8 * j < P) x = lds128(src + j * 1024);
+          put_codes(dst, row + 8 * j, cq & 3, x);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[sa]);
+          mbar_arrive(&full[sb]);
+          mbar_arrive(&raw_empty[buf]);
+        }
+        if (++buf == (uint32_t)C::RAW) {
+          buf = 0;
+          raw_phase ^= 1;
         }
       }
     }
     __syncwarp();
   } else {
-    reg_inc();
+    reg_inc<176>();
     // ------------------------------------------------------------ softmax, tile x
     const int x = x_of, quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -534,7 +550,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // this row of Q into the 128-B-swizzled K-major tile (two 64-dim chunks)
       const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)tt * p.q_ts + (size_t)(kvh * G + head) * p.q_hs);
       uint8_t* qs = smem + C::OFF_Q + x * 2 * kStage;
-#pragma unroll 4
+#pragma unroll
       for (int u = 0; u < 16; ++u) {
         uint4 f = row_valid ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
         if (!BF16)
@@ -546,9 +562,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[x]);
     }
-    const bool has_gate = FEAT && p.g_cache != nullptr;
     float gi = 0.f;  // the row's own G
-    if (has_gate && row_valid) {
+    if (GATES && row_valid) {
       const int blk = __ldg(p.block_table + (size_t)req * p.max_blocks + lastk / p.block_size);
       gi = __ldg(p.g_cache + ((size_t)blk * p.hq + kvh * G + head) * p.block_size + lastk % p.block_size);
     }
@@ -557,8 +572,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     bool ok = true;
     int kx = 0;  // key tiles processed by this query tile
     for (int n = 0; n < nt; ++n) {
-      const int a = n & 1;
-      ok = wait_bar(&aux_full[a], (n >> 1) & 1, ab);
+      const int a = n % C::HELD;
+      ok = wait_bar(&vec_full[a], (n / C::HELD) & 1, ab);
       if (!ok) break;
       if (n >= my_first && n <= my_last) {
         const int j0 = key0 + (lo_t + n) * kTileKeys;
@@ -571,41 +586,45 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         tmem_ld32(tS + 64, sv + 64);
         tmem_ld32(tS + 96, sv + 96);
         tmem_ld_wait();
-        const float* ax = reinterpret_cast<const float*>(smem + C::OFF_AUX + a * C::AUX);
-        const float4* ks4 = reinterpret_cast<const float4*>(ax);
-        const float4* vs4 = reinterpret_cast<const float4*>(ax + kTileKeys);
-        const float4* g4 = reinterpret_cast<const float4*>(ax + 2 * kTileKeys + head * kTileKeys);
+        const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC + a * C::VEC);
+        const float4* ks4 = reinterpret_cast<const float4*>(vec);
+        const float4* vs4 = reinterpret_cast<const float4*>(vec + kTileKeys);
+        const float4* g4 = reinterpret_cast<const float4*>(vec + 2 * kTileKeys + head * C::GATE_ROW);
         const bool need_mask = j0 + kTileKeys > P || j0 + kTileKeys - 1 > lk_min || (W > 0 && j0 < lk_max - W + 1);
         const int jmax = min(lastk, P - 1) - j0;
         const int jmin = W > 0 ? lastk - W + 1 - j0 : -(1 << 30);
-        float mxp[8];
+        float mxp[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+        // one straight run of code for each case: a branch within it would part it
+        auto scores = [&](auto masked) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mxp[e] = neg_inf();
-#pragma unroll
-        for (int j4 = 0; j4 < 32; ++j4) {
-          const float4 k4 = ks4[j4];
-          const float ks[4] = {k4.x, k4.y, k4.z, k4.w};
-          float gs[4] = {0.f, 0.f, 0.f, 0.f};
-          if (FEAT) {  // G_i - G_j before the change of units: the difference is what is small
-            const float4 g = g4[j4];
-            gs[0] = (gi - g.x) * kLog2e;
-            gs[1] = (gi - g.y) * kLog2e;
-            gs[2] = (gi - g.z) * kLog2e;
-            gs[3] = (gi - g.w) * kLog2e;
+          for (int j4 = 0; j4 < 32; ++j4) {
+            const float4 k4 = ks4[j4];
+            float2 ta = make_float2(__uint_as_float(sv[4 * j4]), __uint_as_float(sv[4 * j4 + 1]));
+            float2 tb = make_float2(__uint_as_float(sv[4 * j4 + 2]), __uint_as_float(sv[4 * j4 + 3]));
+            if (GATES) {  // G_i - G_j before the change of units: the difference is what is small
+              const float4 g = g4[j4];
+              ta = fma2(ta, make_float2(k4.x, k4.y), make_float2((gi - g.x) * kLog2e, (gi - g.y) * kLog2e));
+              tb = fma2(tb, make_float2(k4.z, k4.w), make_float2((gi - g.z) * kLog2e, (gi - g.w) * kLog2e));
+            } else {
+              ta = mul2(ta, make_float2(k4.x, k4.y));
+              tb = mul2(tb, make_float2(k4.z, k4.w));
+            }
+            if (decltype(masked)::value) {
+              const int j = 4 * j4;
+              ta.x = j >= jmin && j <= jmax ? ta.x : neg_inf();
+              ta.y = j + 1 >= jmin && j + 1 <= jmax ? ta.y : neg_inf();
+              tb.x = j + 2 >= jmin && j + 2 <= jmax ? tb.x : neg_inf();
+              tb.y = j + 3 >= jmin && j + 3 <= jmax ? tb.y : neg_inf();
+            }
+            sv[4 * j4] = __float_as_uint(ta.x), sv[4 * j4 + 1] = __float_as_uint(ta.y);
+            sv[4 * j4 + 2] = __float_as_uint(tb.x), sv[4 * j4 + 3] = __float_as_uint(tb.y);
+            mxp[(2 * j4) & 3] = fmax3(mxp[(2 * j4) & 3], ta.x, ta.y);
+            mxp[(2 * j4 + 1) & 3] = fmax3(mxp[(2 * j4 + 1) & 3], tb.x, tb.y);
           }
-          float t[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 4 * j4 + e;
-            t[e] = FEAT ? fmaf(__uint_as_float(sv[j]), ks[e], gs[e]) : __uint_as_float(sv[j]) * ks[e];
-            if (need_mask) t[e] = (j >= jmin && j <= jmax) ? t[e] : neg_inf();
-            sv[j] = __float_as_uint(t[e]);
-          }
-          mxp[(2 * j4) & 7] = fmax3(mxp[(2 * j4) & 7], t[0], t[1]);
-          mxp[(2 * j4 + 1) & 7] = fmax3(mxp[(2 * j4 + 1) & 7], t[2], t[3]);
-        }
-        const float mx = fmax3(fmax3(mxp[0], mxp[1], mxp[2]), fmax3(mxp[3], mxp[4], mxp[5]), fmaxf(mxp[6], mxp[7]));
-        const float m_new = fmaxf(m, mx);
+        };
+        if (need_mask) scores(std::true_type());
+        else scores(std::false_type());
+        const float m_new = fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), fmaxf(mxp[3], m));
         const bool need = m_new > m + kPreLazy;
         if (__any_sync(0xffffffffu, need)) {
           const float alpha = need ? ex2(m - m_new) : 1.f;
@@ -615,41 +634,41 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < kD / 32; ++cc) {
-              uint32_t ov[32];
-              tmem_ld32(tO + cc * 32, ov);
+            for (int cc = 0; cc < kD / 16; ++cc) {
+              uint32_t ov[16];
+              tmem_ld16(tO + cc * 16, ov);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-              tmem_st32(tO + cc * 32, ov);
+              for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
+              tmem_st16(tO + cc * 16, ov);
             }
             tmem_st_wait();
           }
           l *= alpha;
           if (need) m = m_new;
         }
-        const float mu = (m == neg_inf()) ? 0.f : m;
-        float lsp[8];
+        const float2 mu = both(m == neg_inf() ? 0.f : -m);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) lsp[e] = 0.f;
+        for (int half = 0; half < 4; ++half) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int jj = 0; jj < 16; ++jj) {
-            const int j = half * 64 + 4 * jj;
+          for (int jj = 0; jj < 8; ++jj) {
+            const int j = half * 32 + 4 * jj;
             const float4 v4 = vs4[j >> 2];
-            const float p0 = ex2(__uint_as_float(sv[j]) - mu), p1 = ex2(__uint_as_float(sv[j + 1]) - mu);
-            const float p2 = ex2(__uint_as_float(sv[j + 2]) - mu), p3 = ex2(__uint_as_float(sv[j + 3]) - mu);
-            lsp[(2 * jj) & 7] += p0 + p1;
-            lsp[(2 * jj + 1) & 7] += p2 + p3;
+            const float2 za = add2(make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), mu);
+            const float2 zb = add2(make_float2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), mu);
+            const float2 pa = make_float2(ex2(za.x), ex2(za.y)), pb = make_float2(ex2(zb.x), ex2(zb.y));
+            ls[0] = add2(ls[0], pa);
+            ls[1] = add2(ls[1], pb);
             // V scales multiply the probabilities after the row sum
-            pk[2 * jj] = BF16 ? pack_bf16x2(p0 * v4.x, p1 * v4.y) : pack_f16x2(p0 * v4.x, p1 * v4.y);
-            pk[2 * jj + 1] = BF16 ? pack_bf16x2(p2 * v4.z, p3 * v4.w) : pack_f16x2(p2 * v4.z, p3 * v4.w);
+            const float2 wa = mul2(pa, make_float2(v4.x, v4.y)), wb = mul2(pb, make_float2(v4.z, v4.w));
+            pk[2 * jj] = BF16 ? pack_bf16x2(wa.x, wa.y) : pack_f16x2(wa.x, wa.y);
+            pk[2 * jj + 1] = BF16 ? pack_bf16x2(wb.x, wb.y) : pack_f16x2(wb.x, wb.y);
           }
-          tmem_st32(tS + half * 32, pk);
+          tmem_st16(tS + half * 16, pk);
         }
-        l += ((lsp[0] + lsp[1]) + (lsp[2] + lsp[3])) + ((lsp[4] + lsp[5]) + (lsp[6] + lsp[7]));
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -657,7 +676,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ++kx;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&aux_empty[a]);
+      if (lane == 0) mbar_arrive(&vec_empty[a]);
     }
     if (ok && kx > 0) ok = wait_bar(&pv_done[x], (kx - 1) & 1, ab);
     if (ok) {
@@ -772,10 +791,10 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) 
   *reinterpret_cast<uint4*>(p.out + (size_t)(q_begin + t) * p.out_ts + (size_t)(kvh * G + hh) * p.out_hs + d0) = o;
 }
 
-template <bool BF16, bool FEAT>
+template <bool BF16, bool GATES>
 cudaError_t launch_prefix(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s) {
-  using C = PreCfg<BF16, FEAT>;
-  auto kern = decode_prefix_kernel<BF16, FEAT>;
+  using C = PreCfg<BF16, GATES>;
+  auto kern = decode_prefix_kernel<BF16, GATES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const int rows = 2 * (128 / p.group);  // query rows of one CTA
@@ -810,7 +829,7 @@ cudaError_t launch_behind(const DecodeParams& p, const DecodeMaps& maps, cudaStr
 cudaError_t launch_decode_shared(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p.pre_segs > 0) {
-    const bool feat = p.g_cache != nullptr || p.window > 0;
+    const bool feat = p.g_cache != nullptr;
     if (p.kv_format == 1) e = feat ? launch_prefix<true, true>(p, maps, s) : launch_prefix<true, false>(p, maps, s);
     else e = feat ? launch_prefix<false, true>(p, maps, s) : launch_prefix<false, false>(p, maps, s);
     if (e != cudaSuccess) return e;
