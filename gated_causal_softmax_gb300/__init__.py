@@ -156,6 +156,7 @@ class PrefixArgs(ctypes.Structure):
         ("max_prefix_len", _c_int),
         ("max_suffix_len", _c_int),
     ]
+    _pack = struct.Struct("@iPPiii4x").pack
 
 
 class QkRopeArgs(ctypes.Structure):
@@ -676,36 +677,30 @@ def attn_decode_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table,
     max_suffix_len on the tokens behind them.  segment_len: of those, 0 = the library's choice."""
     L = load()
     dev = _current_device()
-    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (block_table, "block_table"),
-                    (seq_lens, "seq_lens"), (cu_q, "cu_q"), (k_scale, "k_scale"), (v_scale, "v_scale"),
-                    (g_cache, "g_cache"), (sink, "sink"), (out, "out")):
-        if t is not None and t.get_device() != dev:
-            _refuse(t, t.dtype, name, t.shape, dev, True)
-    if k_cache is None or k_cache.dim() != 4 or v_cache is None or q is None or q.dim() != 3:
-        raise ValueError("expected q [tokens, heads, dim] and caches [num_blocks, num_kv_heads, block_size, d]")
-    if v_cache.dtype is not k_cache.dtype:
-        raise ValueError("k_cache and v_cache types differ")
-    if block_table is None or block_table.dim() != 2 or seq_lens is None or cu_q is None or cu_groups is None:
-        raise ValueError("block_table, seq_lens, cu_q and cu_groups are [R, max_blocks], [R], [R + 1] and [groups + 1]")
-    num_reqs = block_table.shape[0]
-    if seq_lens.shape != (num_reqs,) or cu_q.shape != (num_reqs + 1,) or q.shape[2] != k_cache.shape[3]:
-        raise ValueError("seq_lens must be [R], cu_q [R + 1], and q and the caches of one head dim")
-    if sink is not None and sink.shape != (q.shape[1],):
-        raise ValueError("sink must be [num_q_heads]")
-    a = decode_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len,
-                    scale, segment_len, g_cache, sink, window)
-    groups = cu_groups.numel() - 1
-    x = PrefixArgs(groups, _vector(cu_groups, _I32, "cu_groups", (groups + 1,), dev) or None,
-                   _vector(prefix_lens, _I32, "prefix_lens", (groups,), dev) or None, int(max_group_q),
-                   int(max_prefix_len), int(max_suffix_len))
+    cs, fmt, ks, mode = _one_cache(k_cache, k_scale, "k", dev)
+    if v_cache is None or v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache shapes or types differ")
+    v_strides, _, vs, v_mode = _one_cache(v_cache, v_scale, "v", dev)
+    if v_strides != cs:
+        raise ValueError("k_cache and v_cache must share one layout")
+    if v_mode != mode:
+        raise NotImplementedError("k_scale and v_scale must both be per token or both per tensor")
+    if cu_groups is None or cu_groups.dim() != 1:
+        raise ValueError("cu_groups is [groups + 1]")
+    groups = cu_groups.shape[0] - 1
+    if q is None or q.dim() != 3:
+        raise ValueError("expected a [tokens, heads, dim] tensor q")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    _, token, head = _rows(out, "out", q.shape, dev)
-    a.out_stride = Strides(token, head)
-    need = 0 if workspace is not None else L.attn_decode_paged_shared_workspace(ctypes.byref(a), ctypes.byref(x))
+        out = torch.empty(q.shape, dtype=_BF16, device=k_cache.device)
+    op, *out_stride = _rows(out, "out", q.shape, dev)
+    a = _paged_args(q, k_cache, cs, fmt, mode, ks, v_cache.data_ptr(), vs, block_table, seq_lens, cu_q,
+                    max_q_len, max_seq_len, scale, segment_len, g_cache, sink, window, dev, out_stride)
+    x = PrefixArgs.from_buffer_copy(PrefixArgs._pack(
+        groups, _vector(cu_groups, _I32, "cu_groups", (groups + 1,), dev),
+        _vector(prefix_lens, _I32, "prefix_lens", (groups,), dev), max_group_q, max_prefix_len, max_suffix_len))
+    need = 0 if workspace is not None else L.attn_decode_paged_shared_workspace(a, x)
     ws, ws_bytes = _workspace(workspace, need, dev)
-    _check(L.attn_decode_paged_shared(ctypes.byref(a), ctypes.byref(x), out.data_ptr(), _ptr(ws), ws_bytes,
-                                      _raw_stream(dev)), "attn_decode_paged_shared")
+    _check(L.attn_decode_paged_shared(a, x, op, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_decode_paged_shared")
     return out
 
 
@@ -972,38 +967,58 @@ def attn_cache_gather(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
     return k, v, log_gate
 
 
-# ------------------------------------------------------------------ eviction from the paged cache
-def _cache_scales(k_cache, k_scale, dev: int):
-    """(kv_format, scale_mode, address of the scales) of one cache and its scales, by decode_args'
-    rules."""
-    if k_cache.dtype is _BF16:
-        if k_scale is not None:
-            raise ValueError("a bf16 KV cache takes no scales")
-        return KV_BF16, SCALE_PER_TOKEN, 0
-    if k_scale is None:
-        raise ValueError("k_scale is required")
-    page = k_cache.shape[:3]
-    if k_scale.shape != page and k_scale.numel() != 1:
+# ------------------------------------------------------------------ one paged cache and the rows over it
+def _scale_mode(cache, scale) -> int:
+    if scale.shape == cache.shape[:3]:
+        return SCALE_PER_TOKEN
+    if scale.numel() != 1:
         raise NotImplementedError("fp8 scales must have the page shape [num_blocks, num_kv_heads, block_size] "
                                   "(per token) or hold one value (per tensor)")
-    mode = SCALE_PER_TOKEN if k_scale.shape == page else SCALE_PER_TENSOR
-    return KV_FP8_E4M3, mode, _vector(k_scale, _F32, "k_scale", k_scale.shape, dev)
+    return SCALE_PER_TENSOR
 
 
-def _one_cache(t, name: str, dev: int):
-    """Checks one paged cache [num_blocks, hkv, block_size, d] of any layout the library may take."""
-    if t is None or t.dim() != 4:
-        raise ValueError(f"{name} must be [num_blocks, num_kv_heads, block_size, d]")
-    if t.dtype not in (_BF16, _U8, _E4M3):
-        raise ValueError(f"{name} must be bf16, uint8 or float8_e4m3fn, got {t.dtype}")
-    cs = t.stride()
-    if cs[3] != 1 or t.get_device() != dev:
-        _refuse(t, t.dtype, name, t.shape, dev, True)
+def _one_cache(cache, scale, name: str, dev: int):
+    """(strides, kv_format, address of the scales, scale_mode) of a paged cache [num_blocks, hkv,
+    block_size, d] of any layout the library may take, and its scales by decode_args' rules."""
+    if cache is None or cache.dim() != 4:
+        raise ValueError(f"{name}_cache must be [num_blocks, num_kv_heads, block_size, d]")
+    fmt, cs = cache.dtype, cache.stride()
+    if fmt not in (_BF16, _U8, _E4M3):
+        raise ValueError(f"{name}_cache must be bf16, uint8 or float8_e4m3fn, got {fmt}")
+    if cs[3] != 1 or cache.get_device() != dev:
+        _refuse(cache, fmt, f"{name}_cache", cache.shape, dev, True)
     if not (cs[0] or cs[1] or cs[2]):  # would say "contiguous" to the library
-        _refuse_broadcast(name)
-    return cs
+        _refuse_broadcast(f"{name}_cache")
+    if fmt is _BF16:
+        if scale is not None:
+            raise ValueError("a bf16 KV cache takes no scales")
+        return cs, KV_BF16, 0, SCALE_PER_TOKEN
+    if scale is None:
+        raise ValueError(f"{name}_scale is required")
+    return cs, KV_FP8_E4M3, _vector(scale, _F32, f"{name}_scale", scale.shape, dev), _scale_mode(cache, scale)
 
 
+def _paged_args(q, k_cache, cs, fmt, mode, ks, v_ptr, vs, block_table, seq_lens, cu_q, max_q_len, max_seq_len, scale,
+                segment_len, g_cache, sink, window, dev: int, out_stride=(0, 0)) -> DecodeArgs:
+    """decode_args for the calls that look at every tensor once."""
+    nb, hkv, bs, d = k_cache.shape
+    if q is None or q.dim() != 3:
+        raise ValueError("expected a [tokens, heads, dim] tensor q")
+    n, hq = q.shape[0], q.shape[1]
+    qp, q_token, q_head = _rows(q, "q", (n, hq, d), dev)
+    if block_table is None or seq_lens is None or cu_q is None or block_table.dim() != 2:
+        raise ValueError("block_table, seq_lens and cu_q are [R, max_blocks], [R] and [R + 1]")
+    num_reqs, max_blocks = block_table.shape
+    return DecodeArgs.from_buffer_copy(DecodeArgs._pack(
+        num_reqs, _vector(cu_q, _I32, "cu_q", (num_reqs + 1,), dev), n, max_q_len,
+        _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev), max_seq_len,
+        _vector(block_table, _I32, "block_table", (num_reqs, max_blocks), dev), max_blocks, k_cache.data_ptr(), v_ptr,
+        ks, vs, nb, bs, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, segment_len, qp, fmt, mode,
+        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), _vector(sink, _F32, "sink", (hq,), dev), window, q_token,
+        q_head, *out_stride, cs[0], cs[1], cs[2]))
+
+
+# ------------------------------------------------------------------ eviction from the paged cache
 def attn_cache_weights(q, k_cache, k_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len, w_cache, decay=1.0,
                        lse=None, scale=None, g_cache=None, sink=None, window=0, workspace=None):
     """Adds the attention weight that every cached token gets from the query rows (summed over the
@@ -1014,27 +1029,13 @@ def attn_cache_weights(q, k_cache, k_scale, block_table, seq_lens, cu_q, max_q_l
     reads of the keys.  Returns w_cache."""
     L = load()
     dev = _current_device()
-    cs = _one_cache(k_cache, "k_cache", dev)
-    nb, hkv, bs, d = k_cache.shape
-    if q is None or q.dim() != 3:
-        raise ValueError("expected a [tokens, heads, dim] tensor q")
-    n, hq = q.shape[0], q.shape[1]
-    qp, q_token, q_head = _rows(q, "q", (n, hq, d), dev)
-    fmt, mode, ks = _cache_scales(k_cache, k_scale, dev)
-    if block_table is None or seq_lens is None or cu_q is None or block_table.dim() != 2:
-        raise ValueError("block_table, seq_lens and cu_q are [R, max_blocks], [R] and [R + 1]")
-    num_reqs, max_blocks = block_table.shape
+    cs, fmt, ks, mode = _one_cache(k_cache, k_scale, "k", dev)
+    a = _paged_args(q, k_cache, cs, fmt, mode, ks, 0, 0, block_table, seq_lens, cu_q, max_q_len, max_seq_len, scale, 0,
+                    g_cache, sink, window, dev)
     if w_cache is None:
         raise ValueError("w_cache is required")
-    a = DecodeArgs.from_buffer_copy(DecodeArgs._pack(
-        num_reqs, _vector(cu_q, _I32, "cu_q", (num_reqs + 1,), dev), n, max_q_len,
-        _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev), max_seq_len,
-        _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(), 0, ks, 0,
-        nb, bs, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, 0, qp, fmt, mode,
-        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), _vector(sink, _F32, "sink", (hq,), dev), window, q_token,
-        q_head, 0, 0, cs[0], cs[1], cs[2]))
-    wp = _vector(w_cache, _F32, "w_cache", (nb, hkv, bs), dev)
-    lp = _vector(lse, _F32, "lse", (hq, n), dev)
+    wp = _vector(w_cache, _F32, "w_cache", k_cache.shape[:3], dev)
+    lp = _vector(lse, _F32, "lse", (a.hq, a.total_q), dev)
     need = 0 if workspace is not None else L.attn_cache_weights_workspace(a, 1 if lp else 0)
     ws, ws_bytes = _workspace(workspace, need, dev)
     _check(L.attn_cache_weights(a, lp, decay, wp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_weights")

@@ -11,6 +11,7 @@
 
 #include "../../include/gcs_attn.h"
 #include "kernels.h"
+#include "launch.h"
 
 namespace gcs {
 
@@ -924,12 +925,6 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
 }
 
 // ------------------------------------------------------------------ decoding behind shared prefixes
-
-static int current_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
-}
 
 static int check_shared(const gcs_decode_args* a, const gcs_prefix_args* x) {
   if (!a || !x || a->segment_len < 0) return GCS_ERR_INVALID_ARG;

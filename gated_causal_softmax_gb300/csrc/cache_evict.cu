@@ -11,6 +11,7 @@
 #include <cooperative_groups.h>
 
 #include "kernels.h"
+#include "launch.h"
 #include "sm103_ptx.cuh"
 
 namespace gcs {
@@ -531,12 +532,6 @@ __global__ void __launch_bounds__(kMoveThreads, 3) cache_move_kernel(const MoveP
   copies_wait<0>();
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
-}
-
 template <typename... Args, typename... Given>
 cudaError_t launch_clusters(void (*kern)(Args...), dim3 grid, int threads, int cs, size_t smem, cudaStream_t s,
                             Given... given) {
@@ -554,10 +549,25 @@ cudaError_t launch_clusters(void (*kern)(Args...), dim3 grid, int threads, int c
   return cudaLaunchKernelEx(&cfg, kern, given...);
 }
 
+template <bool HELD, bool CLUSTER>
+cudaError_t launch_select(const SelectParams& p, long long rows, int cs, long long slice, cudaStream_t s) {
+  auto kern = cache_select_kernel<HELD, CLUSTER>;
+  const size_t smem = HELD ? (size_t)slice * 4 : 0;
+  cudaError_t e = allow_smem<cache_select_kernel<HELD, CLUSTER>>(HELD ? kMaxSlice * 4 : 0);
+  if (e != cudaSuccess) return e;
+  if (!CLUSTER) {
+    kern<<<(unsigned)rows, kSelThreads, smem, s>>>(p);
+    return cudaGetLastError();
+  }
+  if (cs > 8 && (e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return e;
+  return launch_clusters(kern, dim3((unsigned)(rows * cs)), kSelThreads, cs, smem, s, p);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s) {
-  const int sms = sm_count();
+  const int sms = current_sms();
   if (!sms) return cudaErrorInvalidDevice;
   // blocks: about two an SM, no fewer than 2048 keys each
   const long long rows = (long long)p.num_reqs * p.hkv;
@@ -565,21 +575,13 @@ cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s) {
   while (cs < 16 && rows * cs < 2 * sms && p.max_seq_len / cs > 2048) cs *= 2;
   const long long slice = ((long long)(p.max_seq_len + 3) / 4 + cs) / cs * 4 + 8;  // keys of a block, at most
   const bool held = slice <= kMaxSlice;
-  auto kern = cs == 1 ? (held ? cache_select_kernel<true, false> : cache_select_kernel<false, false>)
-                      : (held ? cache_select_kernel<true, true> : cache_select_kernel<false, true>);
-  const size_t smem = held ? (size_t)slice * 4 : 0;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && cs > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  if (cs == 1) {
-    kern<<<(unsigned)rows, kSelThreads, smem, s>>>(p);
-    return cudaGetLastError();
-  }
-  return launch_clusters(kern, dim3((unsigned)(rows * cs)), kSelThreads, cs, smem, s, p);
+  if (cs == 1)
+    return held ? launch_select<true, false>(p, rows, cs, slice, s) : launch_select<false, false>(p, rows, cs, slice, s);
+  return held ? launch_select<true, true>(p, rows, cs, slice, s) : launch_select<false, true>(p, rows, cs, slice, s);
 }
 
 cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s) {
-  const int sms = sm_count();
+  const int sms = current_sms();
   if (!sms) return cudaErrorInvalidDevice;
   const long long rows = (long long)p.num_reqs * p.hkv;
   const int vectors = (p.k_scale ? 2 : 0) + (p.w_cache ? 1 : 0) + (p.g_cache ? p.group : 0);
@@ -589,11 +591,10 @@ cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s) {
   int cs = 1;
   while (cs < 8 && rows * kinds * cs < 4 * sms && p.max_keep > cs * chunk) cs *= 2;
   const dim3 grid((unsigned)(rows * cs), kinds);
-  auto kern = cs > 1 ? cache_move_kernel<true> : cache_move_kernel<false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+  cudaError_t e = cs > 1 ? allow_smem<cache_move_kernel<true>>(kMoveSmem) : allow_smem<cache_move_kernel<false>>(kMoveSmem);
   if (e != cudaSuccess) return e;
-  if (cs > 1) return launch_clusters(kern, grid, kMoveThreads, cs, kMoveSmem, s, p, cs);
-  kern<<<grid, kMoveThreads, kMoveSmem, s>>>(p, cs);
+  if (cs > 1) return launch_clusters(cache_move_kernel<true>, grid, kMoveThreads, cs, kMoveSmem, s, p, cs);
+  cache_move_kernel<false><<<grid, kMoveThreads, kMoveSmem, s>>>(p, cs);
   return cudaGetLastError();
 }
 

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.h"
 #include "sm103_ptx.cuh"
 
 namespace gcs {
@@ -365,14 +366,14 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t s) {
   if (!p.lse) {
     constexpr size_t smem = kFixed + kWarps * NT * 8 * 8;
     auto kern = cache_weights_kernel<BF16, D, NT, false>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem<cache_weights_kernel<BF16, D, NT, false>>((int)smem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads, smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const size_t smem = kFixed + (size_t)p.seg_len * 4;
   auto kern = cache_weights_kernel<BF16, D, NT, true>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = allow_smem<cache_weights_kernel<BF16, D, NT, true>>((int)(kFixed + 4096 * 4));
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();

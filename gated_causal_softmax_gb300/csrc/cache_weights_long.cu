@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "launch.h"
 #include "rows.cuh"
 #include "sm103_ptx.cuh"
 
@@ -743,7 +744,7 @@ template <bool BF16, int NCH, bool WRITE>
 cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, cudaStream_t s) {
   using C = Cfg<NCH>;
   auto kern = weights_long_kernel<BF16, NCH, WRITE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = allow_smem<weights_long_kernel<BF16, NCH, WRITE>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int per = WRITE ? C::NA * kTile : C::NA * (kTile / p.group);
   const int n = WRITE ? (p.max_seq_len + per - 1) / per : (p.max_q_len + per - 1) / per * p.segs;

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "decode_split.cuh"
+#include "launch.h"
 #include "rows.cuh"
 
 namespace gcs {
@@ -57,6 +58,7 @@ struct PreCfg {
   static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kVecs + 18) * 8;
   static constexpr int SMEM = OFF_MISC + 32 + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory budget");
+  static_assert(256 * 528 <= OFF_VEC, "the rows that leave");
 };
 
 // 128 x (64 + 96 + 176 + 176) = 65536 = 512 threads x 128 at launch
@@ -82,6 +84,13 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // Arrives once this thread's copies so far have landed.
 __device__ __forceinline__ void copies_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Plain bulk copy shared -> global: both addresses and the size in 16-byte steps; tracked by this thread's bulk
+// group.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
 }
 
 // Tokens that group g shares, as far as the first request's cache and the host's bound go.
@@ -174,15 +183,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const bool row_valid = softmax && pos < ql;
   const int tt = q_begin + min(pos, ql - 1);  // packed row
   int lastk = -1, req = r0;
+  uint4 qv[16];  // this row of Q, on its way
   if (softmax) {
-    int lo = r0, hi = r1;  // cu_q[lo] <= tt < cu_q[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.cu_q + mid) <= tt) lo = mid;
-      else hi = mid;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)tt * p.q_ts + (size_t)(kvh * G + head) * p.q_hs);
+#pragma unroll
+    for (int u = 0; u < 16; ++u) qv[u] = row_valid ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+    // the request whose rows hold tt: where rows of one length would have it, or searched for
+    req = r0 + (int)((long long)(tt - q_begin) * (r1 - r0) / ql);
+    int from = __ldg(p.cu_q + req), to = __ldg(p.cu_q + req + 1), len = __ldg(p.seq_lens + req);
+    if (from > tt || to <= tt) {
+      int lo = r0, hi = r1;  // cu_q[lo] <= tt < cu_q[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.cu_q + mid) <= tt) lo = mid;
+        else hi = mid;
+      }
+      req = lo;
+      to = __ldg(p.cu_q + req + 1);
+      len = __ldg(p.seq_lens + req);
     }
-    req = lo;
-    lastk = __ldg(p.seq_lens + req) - (__ldg(p.cu_q + req + 1) - tt);
+    lastk = len - (to - tt);
     if (row_valid) {
       atomicMin(&see[2 * x_of], lastk);
       atomicMax(&see[2 * x_of + 1], lastk);
@@ -548,11 +568,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int my_first = x ? n_first[1] : n_first[0], my_last = x ? n_last[1] : n_last[0];
     if (my_first <= my_last) {
       // this row of Q into the 128-B-swizzled K-major tile (two 64-dim chunks)
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)tt * p.q_ts + (size_t)(kvh * G + head) * p.q_hs);
       uint8_t* qs = smem + C::OFF_Q + x * 2 * kStage;
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        uint4 f = row_valid ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 f = qv[u];
         if (!BF16)
           f = make_uint4(bf16pair_to_f16x2(f.x), bf16pair_to_f16x2(f.y), bf16pair_to_f16x2(f.z),
                          bf16pair_to_f16x2(f.w));
@@ -679,27 +698,33 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (lane == 0) mbar_arrive(&vec_empty[a]);
     }
     if (ok && kx > 0) ok = wait_bar(&pv_done[x], (kx - 1) & 1, ab);
-    if (ok) {
+    // Both tiles are through with the operands: their shared memory takes the rows, 16 bytes apart in the
+    // banks, and each thread's row leaves in one copy of 512 bytes (stores by row would be 32 lanes in 32
+    // rows).
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (ok && !*abort_flag) {
       const size_t at = ((size_t)seg * p.total_q + tt) * p.hq + kvh * G + head;
       if (kx > 0) {
         tc_fence_after();
-        float4* arow = reinterpret_cast<float4*>(p.pre_acc + at * kD);
+        uint8_t* mine = smem + (x * 128 + rr) * 528;
         constexpr float kInv = 1.f / kPrePScale;
-#pragma unroll 1
+#pragma unroll
         for (int cc = 0; cc < kD / 32; ++cc) {
           uint32_t ov[32];
           tmem_ld32(tO + cc * 32, ov);
           tmem_ld_wait();
-          if (row_valid) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              arow[cc * 8 + j] = make_float4(__uint_as_float(ov[4 * j]) * kInv, __uint_as_float(ov[4 * j + 1]) * kInv,
-                                             __uint_as_float(ov[4 * j + 2]) * kInv,
-                                             __uint_as_float(ov[4 * j + 3]) * kInv);
-          }
+          for (int j = 0; j < 8; ++j)
+            reinterpret_cast<float4*>(mine)[cc * 8 + j] =
+                make_float4(__uint_as_float(ov[4 * j]) * kInv, __uint_as_float(ov[4 * j + 1]) * kInv,
+                            __uint_as_float(ov[4 * j + 2]) * kInv, __uint_as_float(ov[4 * j + 3]) * kInv);
         }
+        fence_proxy_async_smem();
+        if (row_valid) bulk_store(p.pre_acc + at * kD, mine, kD * 4);
+        bulk_commit_group();
+        bulk_wait_group0();
       }
-      // the combine does not read the accumulators of an empty partial
+      // the combine does not use the accumulators of an empty partial
       if (row_valid) p.pre_ml[at] = kx > 0 ? make_float2(m, l) : make_float2(neg_inf(), 0.f);
     }
   }
@@ -743,21 +768,14 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) 
   float m = neg_inf(), l = 0.f;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (hh < G) {
-#pragma unroll 2
+#pragma unroll 4
     for (int i = sl; i < n; i += SL) {
-      float2 v;
-      const float4* a;
-      if (i < npre) {
-        const size_t at = ((size_t)i * p.total_q + q_begin + t) * p.hq + kvh * G + hh;
-        v = p.pre_ml[at];
-        a = reinterpret_cast<const float4*>(p.pre_acc + at * kD + d0);
-      } else {
-        const size_t at = (((size_t)r * p.max_segs + s_begin + i - npre) * p.hkv + kvh) * rows + t * G + hh;
-        v = reinterpret_cast<const float2*>(p.part_ml)[at];
-        a = reinterpret_cast<const float4*>(p.part_acc + at * kD + d0);
-      }
-      if (v.x == neg_inf()) continue;
-      const float4 x0 = a[0], x1 = a[1];
+      const size_t pre = ((size_t)i * p.total_q + q_begin + t) * p.hq + kvh * G + hh;
+      const size_t own = (((size_t)r * p.max_segs + s_begin + i - npre) * p.hkv + kvh) * rows + t * G + hh;
+      const float2 v = i < npre ? p.pre_ml[pre] : reinterpret_cast<const float2*>(p.part_ml)[own];
+      const float4* a = reinterpret_cast<const float4*>((i < npre ? p.pre_acc + pre * kD : p.part_acc + own * kD) + d0);
+      float4 x0 = a[0], x1 = a[1];
+      if (v.x == neg_inf()) x0 = x1 = make_float4(0.f, 0.f, 0.f, 0.f);  // empty: not written
       const float a2[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
       merge_partial(m, l, acc, v.x, v.y, a2);
     }
@@ -795,7 +813,7 @@ template <bool BF16, bool GATES>
 cudaError_t launch_prefix(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s) {
   using C = PreCfg<BF16, GATES>;
   auto kern = decode_prefix_kernel<BF16, GATES>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  cudaError_t e = allow_smem<decode_prefix_kernel<BF16, GATES>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int rows = 2 * (128 / p.group);  // query rows of one CTA
   const dim3 grid((p.max_group_q + rows - 1) / rows * p.pre_segs, p.hkv, p.num_groups);
@@ -803,19 +821,22 @@ cudaError_t launch_prefix(const DecodeParams& p, const DecodeMaps& maps, cudaStr
   return cudaGetLastError();
 }
 
+template <int KVF, bool PT, bool FEAT, int G, bool SQ>
+cudaError_t launch_split(const DecodeParams& p, const DecodeMaps& maps, dim3 grid, cudaStream_t s) {
+  constexpr int smem = DecCfg<KVF, PT, FEAT, SQ>::SMEM;  // + 4 KB of query fragments a position
+  auto kern = decode_split_kernel<KVF, PT, FEAT, G, SQ, false, true>;
+  const cudaError_t e = allow_smem<decode_split_kernel<KVF, PT, FEAT, G, SQ, false, true>>(smem + 4096 * 4);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem + 4096 * p.max_q_len, s>>>(maps.k, maps.v, p);
+  return cudaGetLastError();
+}
+
 // The tokens behind the prefixes.
 cudaError_t launch_behind(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s) {
   const dim3 grid(p.max_segs, p.hkv, p.num_reqs);
-  auto run = [&](auto kern, int smem) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem + 4096 * 4);
-    if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, smem + 4096 * p.max_q_len, s>>>(maps.k, maps.v, p);  // + the query fragments
-    return cudaGetLastError();
-  };
   const bool feat = p.g_cache != nullptr || p.window > 0;
-#define GCS_RUN2(KVF, PT, F, SQ)                                                                                    \
-  (p.group == 8 ? run(decode_split_kernel<KVF, PT, F, 8, SQ, false, true>, DecCfg<KVF, PT, F, SQ>::SMEM)            \
-                : run(decode_split_kernel<KVF, PT, F, 16, SQ, false, true>, DecCfg<KVF, PT, F, SQ>::SMEM))
+#define GCS_RUN2(KVF, PT, F, SQ) \
+  (p.group == 8 ? launch_split<KVF, PT, F, 8, SQ>(p, maps, grid, s) : launch_split<KVF, PT, F, 16, SQ>(p, maps, grid, s))
 #define GCS_RUN(KVF, PT, F) (p.max_q_len > 2 ? GCS_RUN2(KVF, PT, F, true) : GCS_RUN2(KVF, PT, F, false))
   if (p.kv_format == 1) return feat ? GCS_RUN(1, false, true) : GCS_RUN(1, false, false);
   if (p.scale_mode == 1) return feat ? GCS_RUN(0, true, true) : GCS_RUN(0, true, false);
