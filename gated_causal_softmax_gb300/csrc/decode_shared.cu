@@ -13,12 +13,14 @@
 // not the cache's bytes.  Operands as in the chunked prefill: f16 from an fp8 cache (converted in
 // the CTA), bf16 from a bf16 one (copied straight into the operand tiles).
 //
-// Warp roles (512 threads):
+// Warp roles (768 threads):
 //   warp 0        tensor copies: fp8: tiles of codes; bf16: the operand tiles, 64 dims x 16 slots each
 //   warp 1        tcgen05 issuer: S_x = Q_x K^T and O_x += P_x V (P in TMEM)
 //   warps 2-3     per-key vectors of the tiles in turn (scales, gates), up to four tiles ahead
-//   warps 4-11    softmax of tiles A and B, one thread per row
-//   warps 12-15   fp8: e4m3 -> f16 operand tiles; bf16: zeros over the values of the last tile past the
+//   warps 4-19    softmax of tiles A and B, two threads a row with half of a tile's keys each (a tile's next
+//                 products wait for its softmax, so its length counts; the halves agree on a row's maximum
+//                 by shared memory)
+//   warps 20-23   fp8: e4m3 -> f16 operand tiles; bf16: zeros over the values of the last tile past the
 //                 prefix
 #include <type_traits>
 
@@ -30,7 +32,7 @@ namespace gcs {
 namespace {
 
 constexpr int kTileKeys = 128;    // 8 pages
-constexpr int kPreThreads = 512;
+constexpr int kPreThreads = 768;
 constexpr int kStage = 16384;     // one operand stage: 128 rows x 64 dims or 64 keys x 128 dims
 constexpr int kVecs = 4;          // tiles whose vectors are held
 constexpr float kPrePScale = 16.f;  // P * vscale carried x 2^4
@@ -55,13 +57,14 @@ struct PreCfg {
   static constexpr int VEC = 1024 + (GATES ? 16 * GATE_ROW * 4 : 0);
   static constexpr int HELD = GATES ? 2 : kVecs;           // tiles whose vectors are held
   static constexpr int OFF_BAR = OFF_VEC + HELD * VEC;
-  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kVecs + 18) * 8;
-  static constexpr int SMEM = OFF_MISC + 32 + 1024;
+  static constexpr int OFF_MISC = OFF_BAR + (2 * STAGES + 2 * kVecs + 26) * 8;
+  static constexpr int OFF_MAX = OFF_MISC + 32;            // [2] x [2 tiles][2 halves][128 rows]
+  static constexpr int SMEM = OFF_MAX + 2 * 512 * 4 + 1024;
   static_assert(SMEM <= 226 * 1024, "shared memory budget");
   static_assert(256 * 528 <= OFF_VEC, "the rows that leave");
 };
 
-// 128 x (64 + 96 + 176 + 176) = 65536 = 512 threads x 128 at launch
+// 128 x (48 + 4 x 96 + 48) = 61440 = 768 threads x 80 at launch
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N) : "memory"); }
 template <int N>
@@ -137,6 +140,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   uint64_t* drain = q_full + 9;
   uint64_t* raw_full = q_full + 10;      // [RAW] fp8
   uint64_t* raw_empty = q_full + 13;     // [RAW]
+  uint64_t* agreed = q_full + 16;        // [2 tiles][4 quarters] both halves' maxima written
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* see = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // [2 tiles] x {least, greatest last key of a row}
@@ -150,12 +154,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     for (int i = 0; i < C::HELD; ++i) {
       mbar_init(&vec_full[i], GATES ? 64 : 32);
-      mbar_init(&vec_empty[i], 8);
+      mbar_init(&vec_empty[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], 8);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
       see[2 * i] = 0x7fffffff;
       see[2 * i + 1] = -1;
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&agreed[i], 2);
     mbar_init(tail_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -175,19 +180,19 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
   __syncthreads();
   // the softmax threads' rows: packed row, its request's last visible key
-  const bool softmax = warp >= 4 && warp < 12;
-  const int x_of = softmax ? (warp - 4) >> 2 : 0;
+  const bool softmax = warp >= 4 && warp < 20;
+  const int x_of = softmax ? (warp - 4) >> 3 : 0, half = (warp - 4) >> 2 & 1;
   const int rr = (warp & 3) * 32 + lane;  // row of the tile
   const int head = rr & (G - 1);
   const int pos = row0 + x_of * pos_tile + (rr >> lgG);
   const bool row_valid = softmax && pos < ql;
   const int tt = q_begin + min(pos, ql - 1);  // packed row
   int lastk = -1, req = r0;
-  uint4 qv[16];  // this row of Q, on its way
+  uint4 qv[8];  // half of this row of Q, on its way
   if (softmax) {
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)tt * p.q_ts + (size_t)(kvh * G + head) * p.q_hs);
 #pragma unroll
-    for (int u = 0; u < 16; ++u) qv[u] = row_valid ? __ldg(src + u) : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < 8; ++u) qv[u] = row_valid ? __ldg(src + 8 * half + u) : make_uint4(0u, 0u, 0u, 0u);
     // the request whose rows hold tt: where rows of one length would have it, or searched for
     req = r0 + (int)((long long)(tt - q_begin) * (r1 - r0) / ql);
     int from = __ldg(p.cu_q + req), to = __ldg(p.cu_q + req + 1), len = __ldg(p.seq_lens + req);
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       len = __ldg(p.seq_lens + req);
     }
     lastk = len - (to - tt);
-    if (row_valid) {
+    if (row_valid && half == 0) {
       atomicMin(&see[2 * x_of], lastk);
       atomicMax(&see[2 * x_of + 1], lastk);
     }
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   };
 
   if (warp < 4) {
-    reg_dec<64>();
+    reg_dec<48>();
     if (warp == 0) {
       if (!BF16) {
         // ---------------------------------------------------------- codes: K and V tiles in turn, lane = page
@@ -281,7 +286,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       } else {
         // ---------------------------------------------------------- operand tiles by tensor copies
-        // The values of the prefix's last, partly filled tile go by tail_full to warp 12, which zeroes what
+        // The values of the prefix's last, partly filled tile go by tail_full to warp 20, which zeroes what
         // lies past the prefix (whatever its bytes hold) before the stages count as written.
         const int pl = lane & 7, c = lane >> 3 & 1;  // page, 64 dims
         if (lane == 0) {
@@ -484,13 +489,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 12) {
-    reg_dec<96>();
+  } else if (warp >= 20) {
+    reg_dec<48>();
     uint32_t stage = 0, phase = 0;
     if (BF16) {
       // ---------------------------------------------------------- zeros past the prefix
       // (the segment's last tile is processed by some query tile only if a row sees it)
-      if (warp == 12 && nt > 0 && key0 + (lo_t + nt) * kTileKeys > P) {
+      if (warp == 20 && nt > 0 && key0 + (lo_t + nt) * kTileKeys > P) {
         if (wait_bar(tail_full, 0, ab)) {
           const uint32_t s2 = (4 * (nt - 1) + 2) % kStages, s3 = s2 + 1;
           const int kbase = key0 + (lo_t + nt - 1) * kTileKeys;
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       //   K: the first stage holds dims 0..63, the second dims 64..127; row = key (K-major)
       //   V: the first stage holds keys 0..63, the second keys 64..127; inside a stage, dims 0..63 then
       //      64..127 (8 KB apart), row = key (MN-major)
-      const int t = threadIdx.x - 384, ck = t & 7, cq = t >> 3 & 7, hf = t >> 6;
+      const int t = threadIdx.x - 640, ck = t & 7, cq = t >> 3 & 7, hf = t >> 6;
       uint32_t buf = 0, raw_phase = 0;
       bool ok = true;
       for (int i = 0; i < 2 * nt && ok; ++i) {
@@ -539,7 +544,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           dst += (cq >> 2 ? sb : sa) * kStage;
           row += 64 * hf;
         }
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < 8; ++j) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);  // past the prefix, whatever is there
           if (kbase + 8 * j < P) x = lds128(src + j * 1024);
@@ -560,22 +565,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     __syncwarp();
   } else {
-    reg_inc<176>();
+    reg_inc<96>();
     // ------------------------------------------------------------ softmax, tile x
     const int x = x_of, quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + 128 * x, tO = tmem + lane_off + 256 + 128 * x;
     const int my_first = x ? n_first[1] : n_first[0], my_last = x ? n_last[1] : n_last[0];
     if (my_first <= my_last) {
-      // this row of Q into the 128-B-swizzled K-major tile (two 64-dim chunks)
-      uint8_t* qs = smem + C::OFF_Q + x * 2 * kStage;
+      // 64 dims of this row of Q into their 128-B-swizzled K-major tile
+      uint8_t* qs = smem + C::OFF_Q + (x * 2 + half) * kStage;
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
+      for (int u = 0; u < 8; ++u) {
         uint4 f = qv[u];
         if (!BF16)
           f = make_uint4(bf16pair_to_f16x2(f.x), bf16pair_to_f16x2(f.y), bf16pair_to_f16x2(f.z),
                          bf16pair_to_f16x2(f.w));
-        sts128(qs + (u >> 3) * kStage + rr * 128 + (((u & 7) ^ (rr & 7)) << 4), f);
+        sts128(qs + sw128_offset(rr, u), f);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int blk = __ldg(p.block_table + (size_t)req * p.max_blocks + lastk / p.block_size);
       gi = __ldg(p.g_cache + ((size_t)blk * p.hq + kvh * G + head) * p.block_size + lastk % p.block_size);
     }
+    const float sl2 = p.scale * kLog2e;
     float m = neg_inf(), l = 0.f;
     const int lk_min = see[2 * x], lk_max = see[2 * x + 1];
     bool ok = true;
@@ -599,34 +605,36 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ok = wait_bar(&s_full[x], kx & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[128];
-        tmem_ld32(tS + 0, sv);
-        tmem_ld32(tS + 32, sv + 32);
-        tmem_ld32(tS + 64, sv + 64);
-        tmem_ld32(tS + 96, sv + 96);
+        uint32_t sv[64];  // this thread's keys: 64 half .. of the tile
+        tmem_ld32(tS + 64 * half, sv);
+        tmem_ld32(tS + 64 * half + 32, sv + 32);
         tmem_ld_wait();
-        const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC + a * C::VEC);
+        const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC + a * C::VEC) + 64 * half;
         const float4* ks4 = reinterpret_cast<const float4*>(vec);
         const float4* vs4 = reinterpret_cast<const float4*>(vec + kTileKeys);
         const float4* g4 = reinterpret_cast<const float4*>(vec + 2 * kTileKeys + head * C::GATE_ROW);
         const bool need_mask = j0 + kTileKeys > P || j0 + kTileKeys - 1 > lk_min || (W > 0 && j0 < lk_max - W + 1);
-        const int jmax = min(lastk, P - 1) - j0;
-        const int jmin = W > 0 ? lastk - W + 1 - j0 : -(1 << 30);
+        const int jmax = min(lastk, P - 1) - j0 - 64 * half;
+        const int jmin = W > 0 ? lastk - W + 1 - j0 - 64 * half : -(1 << 30);
         float mxp[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
         // one straight run of code for each case: a branch within it would part it
         auto scores = [&](auto masked) {
 #pragma unroll
-          for (int j4 = 0; j4 < 32; ++j4) {
-            const float4 k4 = ks4[j4];
+          for (int j4 = 0; j4 < 16; ++j4) {
+            float2 ka = both(sl2), kb = both(sl2);
+            if (!BF16) {
+              const float4 k4 = ks4[j4];
+              ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
+            }
             float2 ta = make_float2(__uint_as_float(sv[4 * j4]), __uint_as_float(sv[4 * j4 + 1]));
             float2 tb = make_float2(__uint_as_float(sv[4 * j4 + 2]), __uint_as_float(sv[4 * j4 + 3]));
             if (GATES) {  // G_i - G_j before the change of units: the difference is what is small
               const float4 g = g4[j4];
-              ta = fma2(ta, make_float2(k4.x, k4.y), make_float2((gi - g.x) * kLog2e, (gi - g.y) * kLog2e));
-              tb = fma2(tb, make_float2(k4.z, k4.w), make_float2((gi - g.z) * kLog2e, (gi - g.w) * kLog2e));
+              ta = fma2(ta, ka, make_float2((gi - g.x) * kLog2e, (gi - g.y) * kLog2e));
+              tb = fma2(tb, kb, make_float2((gi - g.z) * kLog2e, (gi - g.w) * kLog2e));
             } else {
-              ta = mul2(ta, make_float2(k4.x, k4.y));
-              tb = mul2(tb, make_float2(k4.z, k4.w));
+              ta = mul2(ta, ka);
+              tb = mul2(tb, kb);
             }
             if (decltype(masked)::value) {
               const int j = 4 * j4;
@@ -643,23 +651,33 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         };
         if (need_mask) scores(std::true_type());
         else scores(std::false_type());
-        const float m_new = fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), fmaxf(mxp[3], m));
+        // the halves agree (and both have read their scores: P takes the place of some of them)
+        const float mine = fmaxf(fmax3(mxp[0], mxp[1], mxp[2]), mxp[3]);
+        float* mx = reinterpret_cast<float*>(smem + C::OFF_MAX) + (kx & 1) * 512 + x * 256 + rr;
+        mx[half * 128] = mine;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&agreed[x * 4 + quarter]);
+        ok = wait_bar(&agreed[x * 4 + quarter], kx & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        const float m_new = fmax3(m, mine, mx[(half ^ 1) * 128]);
         const bool need = m_new > m + kPreLazy;
         if (__any_sync(0xffffffffu, need)) {
           const float alpha = need ? ex2(m - m_new) : 1.f;
           if (kx > 0) {
-            // O holds the previous key tiles: wait for their PV before scaling it
+            // O holds the previous key tiles: wait for their PV before scaling it, half of its columns
             ok = wait_bar(&pv_done[x], (kx - 1) & 1, ab);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < kD / 16; ++cc) {
+            for (int cc = 0; cc < 4; ++cc) {
               uint32_t ov[16];
-              tmem_ld16(tO + cc * 16, ov);
+              tmem_ld16(tO + half * 64 + cc * 16, ov);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * alpha);
-              tmem_st16(tO + cc * 16, ov);
+              tmem_st16(tO + half * 64 + cc * 16, ov);
             }
             tmem_st_wait();
           }
@@ -669,23 +687,27 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const float2 mu = both(m == neg_inf() ? 0.f : -m);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int half = 0; half < 4; ++half) {
+        for (int qt = 0; qt < 2; ++qt) {
           uint32_t pk[16];
 #pragma unroll
           for (int jj = 0; jj < 8; ++jj) {
-            const int j = half * 32 + 4 * jj;
-            const float4 v4 = vs4[j >> 2];
+            const int j = qt * 32 + 4 * jj;
             const float2 za = add2(make_float2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), mu);
             const float2 zb = add2(make_float2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), mu);
             const float2 pa = make_float2(ex2(za.x), ex2(za.y)), pb = make_float2(ex2(zb.x), ex2(zb.y));
             ls[0] = add2(ls[0], pa);
             ls[1] = add2(ls[1], pb);
-            // V scales multiply the probabilities after the row sum
-            const float2 wa = mul2(pa, make_float2(v4.x, v4.y)), wb = mul2(pb, make_float2(v4.z, v4.w));
-            pk[2 * jj] = BF16 ? pack_bf16x2(wa.x, wa.y) : pack_f16x2(wa.x, wa.y);
-            pk[2 * jj + 1] = BF16 ? pack_bf16x2(wb.x, wb.y) : pack_f16x2(wb.x, wb.y);
+            if (BF16) {
+              pk[2 * jj] = pack_bf16x2(pa.x, pa.y);
+              pk[2 * jj + 1] = pack_bf16x2(pb.x, pb.y);
+            } else {  // V scales multiply the probabilities after the row sum
+              const float4 v4 = vs4[j >> 2];
+              const float2 wa = mul2(pa, make_float2(v4.x, v4.y)), wb = mul2(pb, make_float2(v4.z, v4.w));
+              pk[2 * jj] = pack_f16x2(wa.x, wa.y);
+              pk[2 * jj + 1] = pack_f16x2(wb.x, wb.y);
+            }
           }
-          tmem_st16(tS + half * 16, pk);
+          tmem_st16(tS + half * 32 + qt * 16, pk);
         }
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_st_wait();
@@ -699,19 +721,21 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     if (ok && kx > 0) ok = wait_bar(&pv_done[x], (kx - 1) & 1, ab);
     // Both tiles are through with the operands: their shared memory takes the rows, 16 bytes apart in the
-    // banks, and each thread's row leaves in one copy of 512 bytes (stores by row would be 32 lanes in 32
+    // banks, and each thread's half row leaves in one copy of 256 bytes (stores by row would be 32 lanes in 32
     // rows).
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    float* sums = reinterpret_cast<float*>(smem + C::OFF_MAX) + (kx & 1) * 512 + x * 256 + rr;
+    if (half) *sums = l;
+    asm volatile("bar.sync 1, 512;" ::: "memory");
     if (ok && !*abort_flag) {
       const size_t at = ((size_t)seg * p.total_q + tt) * p.hq + kvh * G + head;
       if (kx > 0) {
         tc_fence_after();
-        uint8_t* mine = smem + (x * 128 + rr) * 528;
-        constexpr float kInv = 1.f / kPrePScale;
+        uint8_t* mine = smem + (x * 128 + rr) * 528 + half * 256;
+        constexpr float kInv = BF16 ? 1.f : 1.f / kPrePScale;
 #pragma unroll
-        for (int cc = 0; cc < kD / 32; ++cc) {
+        for (int cc = 0; cc < 2; ++cc) {
           uint32_t ov[32];
-          tmem_ld32(tO + cc * 32, ov);
+          tmem_ld32(tO + half * 64 + cc * 32, ov);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -720,12 +744,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                             __uint_as_float(ov[4 * j + 2]) * kInv, __uint_as_float(ov[4 * j + 3]) * kInv);
         }
         fence_proxy_async_smem();
-        if (row_valid) bulk_store(p.pre_acc + at * kD, mine, kD * 4);
+        if (row_valid) bulk_store(p.pre_acc + at * kD + half * 64, mine, kD * 2);
         bulk_commit_group();
         bulk_wait_group0();
       }
       // the combine does not use the accumulators of an empty partial
-      if (row_valid) p.pre_ml[at] = kx > 0 ? make_float2(m, l) : make_float2(neg_inf(), 0.f);
+      if (row_valid && !half) p.pre_ml[at] = kx > 0 ? make_float2(m, l + *sums) : make_float2(neg_inf(), 0.f);
     }
   }
 
