@@ -1012,6 +1012,7 @@ int attn_decode_paged_shared(const gcs_decode_args* a, const gcs_prefix_args* x,
   if (!status) return GCS_ERR_CUDA;
   DecodeParams p{};
   fill_paged_params(a, out, status, p);
+  if (p.window >= a->max_seq_len) p.window = 0;  // sees everything; position - window stays within 32 bits
   p.max_segs = pl.max_segs;
   p.seg_pages = pl.seg_pages > 0 ? pl.seg_pages : 1;
   p.num_groups = x->num_groups;
@@ -1534,7 +1535,7 @@ int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, 
   p.k_scale = a->k_scale;
   p.g_cache = a->g_cache;
   p.sink = a->sink;
-  p.window = a->window;
+  p.window = a->window < a->max_seq_len ? a->window : 0;  // sees everything; position - window stays within 32 bits
   p.scale = a->scale;
   p.decay = decay;
   p.q = static_cast<const uint16_t*>(a->q);

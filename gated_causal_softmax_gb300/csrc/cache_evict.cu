@@ -346,11 +346,12 @@ __global__ void __launch_bounds__(kSelThreads, 3) cache_select_kernel(const Sele
 }
 
 // -------------------------------------------------------------------------------------- move
-constexpr int kMoveThreads = 256;
-constexpr int kPieces = 4;   // 16-byte pieces of K or V a thread moves in a chunk
+constexpr int kMoveThreads = 512;
+constexpr int kPieces = 2;   // 16-byte pieces of K or V a thread moves in a chunk
 constexpr int kVectors = 8;  // 4-byte vectors of a block, one element each of a thread's chunk
-constexpr int kDepth = 4;    // chunks on their way
+constexpr int kDepth = 3;    // chunks on their way
 constexpr int kMoveSmem = kDepth * kMoveThreads * kPieces * 16;
+static_assert(kPieces * 16 == kVectors * 4 && kPieces * kDepth <= 32, "the queue's places and the marks of what moves");
 
 // A stream is one array's part of one (request, kv head): the K rows, the V rows, or up to eight of
 // the 4-byte vectors (scales, weights, gates of its query heads).  A cluster takes one stream's
@@ -586,7 +587,7 @@ cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s) {
   const long long rows = (long long)p.num_reqs * p.hkv;
   const int vectors = (p.k_scale ? 2 : 0) + (p.w_cache ? 1 : 0) + (p.g_cache ? p.group : 0);
   const int kinds = 2 + (vectors + kVectors - 1) / kVectors;
-  // blocks: about four an SM, no more than the chunks of max_keep rows
+  // blocks: about four an SM (three run at once), no more than the chunks of max_keep rows
   const int chunk = (kMoveThreads * kPieces) >> p.log2_units;
   int cs = 1;
   while (cs < 8 && rows * kinds * cs < 4 * sms && p.max_keep > cs * chunk) cs *= 2;

@@ -15,6 +15,7 @@
 
 #include "kernels.h"
 #include "launch.h"
+#include "rows.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gcs {
@@ -75,6 +76,14 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
   // the second kernel takes the requests in the other order: the last ones' keys are still in L2
   const int seg = blockIdx.x, kvh = blockIdx.y, r = WRITE ? gridDim.z - 1 - blockIdx.z : blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
+  if (!WRITE) grid_release();
+  // The second kernel may run beside the first, and what comes after it waits for it alone: none of its
+  // blocks ends before the first kernel has.
+  struct AtEnd {
+    __device__ ~AtEnd() {
+      if (WRITE) grid_wait();
+    }
+  } at_end;
   const int q0 = __ldg(p.cu_q + r), q1 = __ldg(p.cu_q + r + 1), L = __ldg(p.seq_lens + r);
   const int ql = q1 - q0;
   if (q0 < 0 || q1 < q0 || q1 > p.total_q || ql > p.max_q_len || L < ql || L > p.max_seq_len) {
@@ -159,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
       load_scales(key0, next);
       load_unit(key0, next.blk, 0, cur);
     }
+    if (WRITE) grid_wait();  // the first kernel's parts
     __syncthreads();
     // the rows' constants and, in the second kernel, their sums
     for (int i = tid; i < kRows; i += kThreads) {
@@ -375,6 +385,7 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t s) {
   auto kern = cache_weights_kernel<BF16, D, NT, true>;
   e = allow_smem<cache_weights_kernel<BF16, D, NT, true>>((int)(kFixed + 4096 * 4));
   if (e != cudaSuccess) return e;
+  if (!p.lse) return launch_beside(kern, grid, kThreads, smem, s, p);  // its first keys are on their way by then
   kern<<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }

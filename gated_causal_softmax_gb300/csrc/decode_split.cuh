@@ -22,6 +22,7 @@
 #pragma once
 
 #include "kernels.h"
+#include "rows.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gcs {
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int q_begin = __ldg(p.cu_q + r);
   const int ql = __ldg(p.cu_q + r + 1) - q_begin;
   const int npages = (L + kPage - 1) / kPage;
+  if (SH) grid_release();  // the prefix's kernel needs nothing of this one
   const int start = SH ? shared_len(p, r) : 0;  // first key
   int pb = (SH ? start / kPage : 0) + seg * p.seg_pages;
   if (pb >= npages || (SH && start >= L) || ql < 1 || ql > 4) return;

@@ -39,4 +39,21 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Launches a kernel that may start while the stream's kernel before it still runs (once that one has
+// let it, or has ended): it waits by itself for what it needs of it, or needs nothing.
+template <typename... Args, typename... Given>
+cudaError_t launch_beside(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Given... given) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, given...);
+}
+
 }  // namespace gcs

@@ -335,6 +335,47 @@ def test_eviction_between_decoding_steps(gcs_lib, kv_format):
     assert torch.isfinite(w[blk, :, keep % 16]).all() and (w[blk, :, keep % 16] > 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv_format", ["fp8", "bf16"])
+def test_blocks_past_32_bits(gcs_lib, kv_format):
+    """The last blocks of caches of more than 2^32 bytes: the same bits as the first blocks' give."""
+    gcs, hq, hkv, d, block, n, keep = gcs_lib, 32, 4, 128, 1024, 1500, 333
+    bf16 = kv_format == "bf16"
+    nb = (1 << 32) // (block * hkv * d * (2 if bf16 else 1)) + 3
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    dt = torch.bfloat16 if bf16 else torch.uint8
+    kv = [torch.empty((nb, hkv, block, d), dtype=dt, device="cuda") for _ in range(2)]
+    small = [torch.empty((nb, h, block), device="cuda") for h in (hkv, hkv, hkv, hq)]
+    assert kv[0].numel() * kv[0].element_size() > 1 << 32
+    for t in kv:
+        x = rnd(2, hkv, block, d)
+        t[:2] = t[-2:] = x.to(dt) if bf16 else (50 * x).to(torch.float8_e4m3fn).view(torch.uint8)
+    for t, x in zip(small, (0.02, 0.02, 1.0, 0.0)):
+        t[:2] = t[-2:] = x * torch.rand(2, t.shape[1], block, generator=gen, device="cuda") + 0.01
+    ks, vs, w, g = small
+    if bf16:
+        ks = vs = None
+    q = [rnd(1, hq, d).to(torch.bfloat16), rnd(80, hq, d).to(torch.bfloat16)]
+    lens, out = i32([n]), []
+    for bt in (i32([[0, 1]]), i32([[nb - 2, nb - 1]])):
+        got = []
+        for x in q[:1]:
+            got.append(gcs.attn_decode_paged_shared(x, *kv, ks, vs, bt, lens, i32([0, 1]), 1, n, i32([0, 1]), i32([1100]), 1,
+                                                    1100, n, g_cache=g))
+        for x in q:
+            gcs.attn_cache_weights(x, kv[0], ks, bt, lens, i32([0, len(x)]), len(x), n, w, g_cache=g)
+        kept, m = gcs.attn_cache_select(w, bt, lens, n, i32([keep]), keep, recent=5)
+        gcs.attn_cache_compact(*kv, ks, vs, bt, lens, kept, m, g_cache=g, w_cache=w)
+        rows = bt[0].long()
+        got += [kept, w[rows], g[rows], kv[0][rows], kv[1][rows]]
+        out.append([t.view(torch.int16) if t.dtype == torch.bfloat16 else t for t in got])
+    torch.cuda.synchronize()
+    assert gcs.get_device_status() == 0
+    for a, b in zip(*out):
+        assert torch.equal(a, b)
+
+
 def select_args(**over):
     import gated_causal_softmax_gb300 as gcs
     from test_cabi import FAKE

@@ -105,6 +105,15 @@ CASES = {
     "gates_bf16_d256": ([300, 140], [33, 140], 8, 2, 256, dict(features=True, kv_format="bf16")),
     "window_1": ([100, 40], [1, 7], 8, 1, 64, dict(features=True, window=1)),
     "window_chunk": ([700, 300], [200, 300], 8, 2, 128, dict(features=True, window=130)),
+    "group7_chunk": ([300, 90], [60, 90], 14, 2, 128, dict(nhd=True)),
+    "gates_group7_chunk": ([300, 90], [60, 90], 14, 2, 128, dict(features=True, window=70, block=64)),
+    "gates_group3_chunk_bf16": ([130], [70], 3, 1, 64, dict(features=True, kv_format="bf16")),
+    "mqa_128_heads": ([260, 33], [2, 1], 128, 1, 128, {}),
+    "mqa_200_heads": ([150], [2], 200, 1, 64, {}),
+    "d512_chunk": ([400, 140], [130, 20], 8, 1, 512, dict(block=128)),
+    "bf16_d512_chunk": ([400, 140], [130, 20], 4, 1, 512, dict(features=True, kv_format="bf16", nhd=True)),
+    "d64_chunk": ([700, 140], [300, 20], 8, 2, 64, dict(scale_mode="per_tensor")),
+    "window_past_everything": ([300], [3], 8, 1, 128, dict(features=True, window=(1 << 31) - 1)),
     "long": ([9001], [1], 8, 1, 128, dict(block=256)),
     "long_chunk": ([3100], [140], 8, 1, 128, dict(block=256)),
 }

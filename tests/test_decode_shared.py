@@ -92,6 +92,7 @@ CASES = {
     "gates_sink": ([(301, [(1, 20), (2, 300), (4, 9)]), (70, [(1, 3)])], 16, 2, dict(features=True)),
     "gates_bf16": ([(301, [(1, 20), (2, 300), (4, 9)])], 32, 2, dict(features=True, kv_format="bf16", block=64)),
     "window_inside": ([(301, [(1, 20), (1, 300), (3, 9), (1, 90)])], 16, 2, dict(features=True, window=100)),
+    "window_past_everything": ([(301, [(1, 20), (1, 300)])], 16, 2, dict(features=True, window=(1 << 31) - 1)),
     "window_1": ([(200, [(1, 1), (2, 30)])], 16, 1, dict(features=True, window=1)),
     "window_wide": ([(1000, [(1, 1), (1, 900), (2, 40)])], 16, 2, dict(features=True, window=700, kv_format="bf16")),
 }
