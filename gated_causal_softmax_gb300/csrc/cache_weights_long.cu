@@ -152,6 +152,8 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     b_hi = b_hi < 0 ? -1 : b_hi / ntok;
   }
   const int nt = max(0, b_hi - b_lo + 1);
+  // resident tiles with anything in them
+  const int nx = NA == 2 && (WRITE ? a0 + kTile < L : a0 + ntok < ql) ? 2 : 1;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* full = bars;               // [NST]
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s_empty[i], 4);
     for (int i = 0; i < C::NAUX; ++i) {
       mbar_init(&aux_full[i], 1);
-      mbar_init(&aux_empty[i], NA == 2 ? 8 : 4);
+      mbar_init(&aux_empty[i], 4 * nx);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -304,33 +306,38 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
       constexpr uint32_t kSt16 = kStage >> 4;
       uint32_t stage = 0, phase = 0, slot = 0, slot_phase = 0;
       bool ok = true;
-      for (int n = 0; n < nt && ok; ++n) {
-        const uint32_t first = stage;
+      auto products = [&](auto tiles) {
+        constexpr int kX = decltype(tiles)::value;
+        for (int n = 0; n < nt && ok; ++n) {
+          const uint32_t first = stage;
 #pragma unroll
-        for (int x = 0; x < NA; ++x) {  // a tile's stages are held until its last product
-          if (ok) ok = wait_bar(&s_empty[slot], slot_phase ^ 1, ab);
-          uint32_t st = first;
-          for (int c = 0; c < NCH && ok; ++c) {
-            if (x == 0) {
-              ok = wait_bar(&full[stage], phase, ab);
-              if (!ok) break;
-              ring_next(stage, phase);
+          for (int x = 0; x < kX; ++x) {  // a tile's stages are held until its last product
+            if (ok) ok = wait_bar(&s_empty[slot], slot_phase ^ 1, ab);
+            uint32_t st = first;
+            for (int c = 0; c < NCH && ok; ++c) {
+              if (x == 0) {
+                ok = wait_bar(&full[stage], phase, ab);
+                if (!ok) break;
+                ring_next(stage, phase);
+              }
+              tc_fence_after();
+              const uint64_t b = dB + st * kSt16;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(tmem + kAccCol + slot * kTile, tmem + x * C::A_COLS + c * 32 + k * 8, b + 2 * k, id, (c | k) != 0);
+              if (x == kX - 1) mma_commit(&empty[st]);
+              st = st + 1 == NST ? 0 : st + 1;
             }
-            tc_fence_after();
-            const uint64_t b = dB + st * kSt16;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(tmem + kAccCol + slot * kTile, tmem + x * C::A_COLS + c * 32 + k * 8, b + 2 * k, id, (c | k) != 0);
-            if (x == NA - 1) mma_commit(&empty[st]);
-            st = st + 1 == NST ? 0 : st + 1;
-          }
-          if (ok) mma_commit(&s_full[(n * NA + x) & 3]);
-          if (++slot == C::SLOTS) {
-            slot = 0;
-            slot_phase ^= 1;
+            if (ok) mma_commit(&s_full[(n * kX + x) & 3]);
+            if (++slot == C::SLOTS) {
+              slot = 0;
+              slot_phase ^= 1;
+            }
           }
         }
-      }
+      };
+      if (nx == NA) products(std::integral_constant<int, NA>());
+      else products(std::integral_constant<int, 1>());
       if (!ok) {
         mma_commit(drain);
         mbar_wait(drain, 0, nullptr);
@@ -407,11 +414,13 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
   } else if (warp < 4 + kEpiWarps) {
     // ---------------------------------------------------------- sums or weights
     // Four groups of 128 lanes take the products in turn: while one waits for its product or its registers,
-    // others keep the exponentials going (two groups of half the columns each: 1.30 ms, four: see below)
+    // others keep the exponentials going.  The code between two waits has no branch: with one for the mask every
+    // four columns the weights kernel took 1.48 ms (4 x 1024 rows over up to 32K keys, 64 / 4 heads of 128,
+    // bf16), without 1.03; its exponentials alone are 0.55, its products 0.55.
     const int grp = (warp - 4) >> 2, quarter = warp & 3;
     const int rr = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int x = NA == 2 ? grp & 1 : 0;  // its resident tile
+    const int x = nx == 2 ? grp & 1 : 0;  // its resident tile
     // sums: the row's token and last visible key; weights: the key and its constants
     const int t = a0 + x * ntok + rr / G, head = rr % G;
     const bool row_ok = rr < nrow && t < ql;
@@ -445,8 +454,8 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
         for (int h = 0; h < kMaxGates; ++h)
           gk[h] = blk >= 0 ? __ldg(p.g_cache + (((size_t)blk * p.hq + kvh * G + h % G) << p.log2_block) + slot_k) : 0.f;
       }
-      for (int u = grp; u < nt * NA; u += 4) {  // streamed tile n with resident tile x
-        const int n = NA == 2 ? u >> 1 : u, a = n % C::NAUX;
+      for (int u = grp; u < nt * nx; u += 4) {  // streamed tile n with resident tile x
+        const int n = nx == 2 ? u >> 1 : u, a = n % C::NAUX;
         const int slot = u % C::SLOTS;
         ok = wait_bar(&aux_full[a], (n / C::NAUX) & 1, ab) && wait_bar(&s_full[grp], (u >> 2) & 1, ab);
         if (!ok) break;
@@ -594,15 +603,13 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     const float2 s2 = add2(acc[0], acc[1]);
     float sum = s2.x + s2.y;
     // the other groups' parts of the same rows, in a fixed order, by shared memory (the ring is done with)
-    constexpr int kParts = NA == 2 ? 2 : 4;
-    const int part = NA == 2 ? grp >> 1 : grp;
-    float2* others = reinterpret_cast<float2*>(smem + C::OFF_RING) + x * kParts * kTile;
+    const int parts = 4 / nx, part = nx == 2 ? grp >> 1 : grp;
+    float2* others = reinterpret_cast<float2*>(smem + C::OFF_RING) + x * 2 * kTile;
     asm volatile("bar.sync 1, 512;" ::: "memory");
     if (part > 0) others[part * kTile + rr] = make_float2(m, sum);
     asm volatile("bar.sync 1, 512;" ::: "memory");
     if (part == 0 && !*abort_flag) {
-#pragma unroll
-      for (int k = 1; k < kParts; ++k) {
+      for (int k = 1; k < parts; ++k) {
         const float2 o = others[k * kTile + rr];
         if (WRITE) {
           sum += o.y;
@@ -773,11 +780,12 @@ bool cache_weights_long(int max_q_len, int group, bool gates) {
   return (long long)max_q_len * group > 64 && group <= kTile && (!gates || group <= kMaxGates);
 }
 
-// Context segments of the sums kernel: enough blocks for one an SM, of 128 tokens or more.
+// Context segments of the sums kernel: blocks for about three an SM (contexts shorter than max_seq_len leave some
+// of them empty; 8 x 33 rows of 256 dims: two 313 us, three 281, four 297), of 128 tokens or more.
 int cache_weights_long_segment(int max_seq_len, int max_q_len, int group, int d, long long units, int sms) {
   const long long per = (long long)(d == 512 ? 1 : 2) * (kTile / group);
   const long long blocks = (max_q_len + per - 1) / per * units;
-  const long long want = std::max(1LL, 2LL * sms / blocks);
+  const long long want = std::max(1LL, 3LL * sms / blocks);
   const long long tiles = (max_seq_len + kTile - 1) / kTile;
   return (int)((tiles + want - 1) / want * kTile);
 }
