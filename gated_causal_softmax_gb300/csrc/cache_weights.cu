@@ -193,9 +193,13 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
             float m = neg_inf(), l = 0.f;
             const int first = p.window > 0 ? max(0, L - ql + t - p.window + 1) / p.seg_len : 0;
             const int last = (L - ql + t) / p.seg_len;
-            for (int s = first; s <= last; ++s) {
-              const float2 v = p.part[(size_t)s * p.total_q * p.hq + at];
-              join(m, l, v.x, v.y);
+            for (int s = first; s <= last; s += 8) {  // eight on their way at once
+              float2 v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                v[j] = s + j <= last ? p.part[(size_t)(s + j) * p.total_q * p.hq + at] : make_float2(neg_inf(), 0.f);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) join(m, l, v[j].x, v[j].y);
             }
             if (p.sink) join(m, l, __ldg(p.sink + kvh * G + head) * kLog2e, 1.f);
             if (l != 0.f) z = m + log2f(l);  // 0: a row whose every key lies outside the cache
@@ -358,12 +362,37 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
   }
   if (WRITE) {
     __syncthreads();
-    for (int i = tid; i < k_end - k_begin; i += kThreads) {
-      const int pos = k_begin + i, blk = block_of(pos);
-      if (blk < 0) continue;
-      float* w = p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
-      const bool old = p.decay != 0.f && pos < L - ql;
-      *w = old ? fmaf(p.decay, *w, gathered[i]) : gathered[i];
+    // four neighbouring keys a thread, four of those on their way at once
+    const int n = k_end - k_begin, fresh = L - ql - k_begin;  // keys from `fresh` on start from 0
+    for (int i0 = tid * 4; i0 < n; i0 += 4 * 4 * kThreads) {
+      float* at[4];
+      float old[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * 4 * kThreads, pos = k_begin + i;
+        const int blk = i < n ? block_of(pos) : -1;
+        at[j] = blk < 0 ? nullptr : p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at[j] && p.decay != 0.f && i < fresh) v = *reinterpret_cast<const float4*>(at[j]);
+        old[j][0] = v.x, old[j][1] = v.y, old[j][2] = v.z, old[j][3] = v.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * 4 * kThreads;
+        if (!at[j]) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          v[e] = i + e < n ? (p.decay != 0.f && i + e < fresh ? fmaf(p.decay, old[j][e], gathered[i + e]) : gathered[i + e])
+                           : 0.f;
+        if (i + 3 < n) {
+          *reinterpret_cast<float4*>(at[j]) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (i + e < n) at[j][e] = v[e];
+        }
+      }
     }
   }
 }

@@ -719,9 +719,14 @@ __global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p
         m = M;
       };
       const int first = p.window > 0 ? max(0, pos - p.window + 1) / p.seg_len : 0;
-      for (int s = first; s <= pos / p.seg_len; ++s) {
-        const float2 v = p.part[(size_t)s * p.total_q * p.hq + at];
-        join(v.x, v.y);
+      const int last = pos / p.seg_len;
+      for (int s = first; s <= last; s += 8) {  // eight on their way at once
+        float2 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] = s + j <= last ? p.part[(size_t)(s + j) * p.total_q * p.hq + at] : make_float2(neg_inf(), 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) join(v[j].x, v[j].y);
       }
       if (p.sink) join(__ldg(p.sink + h) * kLog2e, 1.f);
       if (l != 0.f) b = -(m + log2f(l));  // 0: a row whose every key lies outside the cache
