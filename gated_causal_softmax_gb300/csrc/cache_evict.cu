@@ -570,10 +570,16 @@ cudaError_t launch_select(const SelectParams& p, long long rows, int cs, long lo
 cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s) {
   const int sms = current_sms();
   if (!sms) return cudaErrorInvalidDevice;
-  // blocks: about two an SM, no fewer than 2048 keys each
+  // Blocks: up to two and a half an SM, of a thousand keys or more each; a wider cluster waits longer at each
+  // of its steps than its shorter slices save (64 rows of 32K keys: 4 blocks a row 20.2 us, 8 29.0, 1 26.3;
+  // 192 of 16K: 1 21.0, 2 24.2; 16 of 4K: 4 15.3, 1 21.6). Slices past 28K keys leave an SM one block at a
+  // time, past kMaxSlice they are read again at each step: halved however many the rows (256 rows of 32K: 2
+  // blocks 40.0, 1 44.0; of 100K: 4 92.9, 2 129.5).
   const long long rows = (long long)p.num_reqs * p.hkv;
   int cs = 1;
-  while (cs < 16 && rows * cs < 2 * sms && p.max_seq_len / cs > 2048) cs *= 2;
+  while (cs < 16 &&
+         ((rows * cs * 4 <= 5 * sms && p.max_seq_len / cs > 1024) || p.max_seq_len / cs > 28 * 1024))
+    cs *= 2;
   const long long slice = ((long long)(p.max_seq_len + 3) / 4 + cs) / cs * 4 + 8;  // keys of a block, at most
   const bool held = slice <= kMaxSlice;
   if (cs == 1)

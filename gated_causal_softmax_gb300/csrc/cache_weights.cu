@@ -77,13 +77,8 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
   const int seg = blockIdx.x, kvh = blockIdx.y, r = WRITE ? gridDim.z - 1 - blockIdx.z : blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
   if (!WRITE) grid_release();
-  // The second kernel may run beside the first, and what comes after it waits for it alone: none of its
-  // blocks ends before the first kernel has.
-  struct AtEnd {
-    __device__ ~AtEnd() {
-      if (WRITE) grid_wait();
-    }
-  } at_end;
+  std::conditional_t<WRITE, WaitAtEnd, int> at_end{};  // the second kernel may run beside the first
+  (void)at_end;
   const int q0 = __ldg(p.cu_q + r), q1 = __ldg(p.cu_q + r + 1), L = __ldg(p.seq_lens + r);
   const int ql = q1 - q0;
   if (q0 < 0 || q1 < q0 || q1 > p.total_q || ql > p.max_q_len || L < ql || L > p.max_seq_len) {

@@ -113,6 +113,10 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     weights_long_kernel(const __grid_constant__ CUtensorMap tm, const WeightsParams p) {
   using C = Cfg<NCH>;
   constexpr int NA = C::NA, NST = C::NST, kThreads = kThreadsOf<!BF16 && !WRITE>;
+  // Each kernel of a call may run beside the one before it: the sums need nothing of the queries in f16, the
+  // weights wait for the rows' constants (behind the sums) once their keys are in place.
+  WaitAtEnd at_end;
+  grid_release();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align_1k(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -253,6 +257,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     }
     tmem_st_wait();
   }
+  if (WRITE) grid_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -701,9 +706,12 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
 // (b, own gate) of every query row: b = -log2 of its sum of exponentials, joined over the segments it
 // sees.
 __global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p) {
+  WaitAtEnd at_end;
+  grid_release();
   const int r = blockIdx.y;
   const Request rq = request(p, r);
   if (!rq.ok) return;
+  grid_wait();  // the sums
   const long long n = (long long)rq.ql * p.hq;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
     const int t = (int)(i / p.hq), h = (int)(i % p.hq), pos = rq.L - rq.ql + t;
@@ -742,6 +750,7 @@ __global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p
 
 // The queries in f16, [total_q, hq, d].
 __global__ void __launch_bounds__(256) queries_f16_kernel(const WeightsParams p) {
+  grid_release();
   const int units = p.d / 8;
   const long long n = (long long)p.total_q * p.hq * units;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
@@ -753,24 +762,33 @@ __global__ void __launch_bounds__(256) queries_f16_kernel(const WeightsParams p)
 }
 
 template <bool BF16, int NCH, bool WRITE>
-cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, cudaStream_t s) {
+cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, bool beside, cudaStream_t s) {
   using C = Cfg<NCH>;
   auto kern = weights_long_kernel<BF16, NCH, WRITE>;
   cudaError_t e = allow_smem<weights_long_kernel<BF16, NCH, WRITE>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int per = WRITE ? C::NA * kTile : C::NA * (kTile / p.group);
   const int n = WRITE ? (p.max_seq_len + per - 1) / per : (p.max_q_len + per - 1) / per * p.segs;
-  kern<<<dim3(n, p.hkv, p.num_reqs), kThreadsOf<!BF16 && !WRITE>, C::SMEM, s>>>(map, p);
+  const dim3 grid(n, p.hkv, p.num_reqs);
+  if (beside) return launch_beside(kern, grid, kThreadsOf<!BF16 && !WRITE>, C::SMEM, s, map, p);
+  kern<<<grid, kThreadsOf<!BF16 && !WRITE>, C::SMEM, s>>>(map, p);
   return cudaGetLastError();
 }
 template <bool BF16, int NCH>
 cudaError_t launch_d(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
   cudaError_t e;
-  if (!p.lse && (e = launch_t<BF16, NCH, false>(p, maps.k, s)) != cudaSuccess) return e;
+  bool beside = !BF16;  // behind the queries in f16
+  if (!p.lse && (e = launch_t<BF16, NCH, false>(p, maps.k, beside, s)) != cudaSuccess) return e;
+  beside = beside || !p.lse;
   const long long rows = (long long)p.max_q_len * p.hq;
-  weights_rows_kernel<<<dim3((unsigned)std::min(1024LL, (rows + 255) / 256), p.num_reqs), 256, 0, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_t<BF16, NCH, true>(p, maps.q, s);
+  const dim3 grid((unsigned)std::min(1024LL, (rows + 255) / 256), p.num_reqs);
+  if (beside) {
+    e = launch_beside(weights_rows_kernel, grid, 256, 0, s, p);
+  } else {
+    weights_rows_kernel<<<grid, 256, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  return e != cudaSuccess ? e : launch_t<BF16, NCH, true>(p, maps.q, true, s);
 }
 template <bool BF16>
 cudaError_t launch_f(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {

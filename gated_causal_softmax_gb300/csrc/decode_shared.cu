@@ -112,9 +112,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
   // This kernel may run beside the one before it, and what comes after it waits for it alone: no block ends
   // before that one has.
-  struct AtEnd {
-    __device__ ~AtEnd() { grid_wait(); }
-  } at_end;
+  WaitAtEnd at_end;
+  grid_release();
   const int seg = blockIdx.x % p.pre_segs, qp = blockIdx.x / p.pre_segs;
   const int kvh = blockIdx.y, grp = blockIdx.z;
   const int r0 = __ldg(p.cu_groups + grp), r1 = __ldg(p.cu_groups + grp + 1);
@@ -779,6 +778,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 template <int SL>
 __global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) {
   constexpr int kHeads = 16 / SL;  // query heads per CTA
+  WaitAtEnd at_end;
   const int r = blockIdx.x / p.max_q_len, t = blockIdx.x % p.max_q_len;
   const int kvh = blockIdx.y;
   const int q_begin = __ldg(p.cu_q + r);
@@ -798,6 +798,7 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) 
   const int n = npre + max(0, nseg - s_begin);
   float m = neg_inf(), l = 0.f;
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  grid_wait();  // the partials
   if (hh < G) {
 #pragma unroll 4
     for (int i = sl; i < n; i += SL) {
@@ -893,12 +894,15 @@ cudaError_t launch_decode_shared(const DecodeParams& p, const DecodeMaps& maps, 
       e = gates ? launch_prefix<false, true>(p, maps, both, s) : launch_prefix<false, false>(p, maps, both, s);
     if (e != cudaSuccess) return e;
   }
-  if (p.pre_segs + p.max_segs >= 32) {
-    decode_join_kernel<8><<<dim3(p.num_reqs * p.max_q_len, p.hkv, p.group / 2), 256, 0, s>>>(p);
-  } else {
-    decode_join_kernel<4><<<dim3(p.num_reqs * p.max_q_len, p.hkv, (p.group + 3) / 4), 256, 0, s>>>(p);
+  const int segs = p.pre_segs + p.max_segs;
+  const dim3 grid(p.num_reqs * p.max_q_len, p.hkv, segs >= 32 ? p.group / 2 : (p.group + 3) / 4);
+  if (segs == 0) {  // no partials, and no kernel of this call to run beside
+    decode_join_kernel<4><<<grid, 256, 0, s>>>(p);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  // the join finds its places while the kernel before it ends
+  if (segs >= 32) return launch_beside(decode_join_kernel<8>, grid, 256, 0, s, p);
+  return launch_beside(decode_join_kernel<4>, grid, 256, 0, s, p);
 }
 
 }  // namespace gcs

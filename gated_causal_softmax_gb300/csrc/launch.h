@@ -39,6 +39,14 @@ cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+#ifdef __CUDACC__
+// In a kernel that may run beside the one before it: what comes after it waits for it alone, so none of
+// its blocks ends before that one has.
+struct WaitAtEnd {
+  __device__ __forceinline__ ~WaitAtEnd() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+};
+#endif
+
 // Launches a kernel that may start while the stream's kernel before it still runs (once that one has
 // let it, or has ended): it waits by itself for what it needs of it, or needs nothing.
 template <typename... Args, typename... Given>
