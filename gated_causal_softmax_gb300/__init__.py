@@ -293,7 +293,7 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.attn_cache_gather.restype = _c_int
     lib.attn_cache_weights_workspace.argtypes = [P(DecodeArgs), _c_int]
     lib.attn_cache_weights_workspace.restype = ctypes.c_size_t
-    lib.attn_cache_weights.argtypes = [P(DecodeArgs), _vp, _c_float, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.attn_cache_weights.argtypes = [P(DecodeArgs), _vp, _vp, _c_float, _vp, _vp, ctypes.c_size_t, _vp]
     lib.attn_cache_weights.restype = _c_int
     lib.attn_cache_select.argtypes = [P(SelectArgs), _vp, _vp, _vp]
     lib.attn_cache_select.restype = _c_int
@@ -1020,13 +1020,14 @@ def _paged_args(q, k_cache, cs, fmt, mode, ks, v_ptr, vs, block_table, seq_lens,
 
 # ------------------------------------------------------------------ eviction from the paged cache
 def attn_cache_weights(q, k_cache, k_scale, block_table, seq_lens, cu_q, max_q_len, max_seq_len, w_cache, decay=1.0,
-                       lse=None, scale=None, g_cache=None, sink=None, window=0, workspace=None):
+                       lse=None, scale=None, g_cache=None, sink=None, window=0, first_lens=None, workspace=None):
     """Adds the attention weight that every cached token gets from the query rows (summed over the
     rows and the kv head's query heads) to w_cache fp32 [num_blocks, hkv, block_size], whose old
     values are multiplied by `decay`; the rows' own tokens, and all with decay 0, start from 0.  The
     other arguments are those of attn_decode_paged; q bf16 [total_q, hq, d] with d 64, 128, 256 or
     512 and any group, any q_len.  lse fp32 [hq, total_q] (as attn_fwd gives it) saves one of two
-    reads of the keys.  Returns w_cache."""
+    reads of the keys.  first_lens int32 [R]: the first tokens, whose weights are left as they are
+    (a prefix whose blocks other requests share must be among them).  Returns w_cache."""
     L = load()
     dev = _current_device()
     cs, fmt, ks, mode = _one_cache(k_cache, k_scale, "k", dev)
@@ -1038,7 +1039,8 @@ def attn_cache_weights(q, k_cache, k_scale, block_table, seq_lens, cu_q, max_q_l
     lp = _vector(lse, _F32, "lse", (a.hq, a.total_q), dev)
     need = 0 if workspace is not None else L.attn_cache_weights_workspace(a, 1 if lp else 0)
     ws, ws_bytes = _workspace(workspace, need, dev)
-    _check(L.attn_cache_weights(a, lp, decay, wp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_weights")
+    fp = _vector(first_lens, _I32, "first_lens", (a.num_reqs,), dev)
+    _check(L.attn_cache_weights(a, lp, fp, decay, wp, _ptr(ws), ws_bytes, _raw_stream(dev)), "attn_cache_weights")
     return w_cache
 
 

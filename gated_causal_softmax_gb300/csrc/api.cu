@@ -1484,11 +1484,12 @@ size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse) {
   return check_weights(a) == GCS_OK && plan_weights(a, with_lse != 0, &pl) ? pl.ws : 0;
 }
 
-int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, float* w_cache, void* workspace,
-                       size_t workspace_bytes, gcs_stream_t stream) {
+int attn_cache_weights(const gcs_decode_args* a, const float* lse, const int32_t* first_lens, float decay,
+                       float* w_cache, void* workspace, size_t workspace_bytes, gcs_stream_t stream) {
   const int st = check_weights(a);
   if (st != GCS_OK) return st;
-  if (!w_cache || !aligned16(w_cache) || !aligned4(lse) || !std::isfinite(decay)) return GCS_ERR_INVALID_ARG;
+  if (!w_cache || !aligned16(w_cache) || !aligned4(lse) || !aligned4(first_lens) || !std::isfinite(decay))
+    return GCS_ERR_INVALID_ARG;
   CacheLayout cl;
   Layout lq;
   cache_layout(a, &cl);
@@ -1506,7 +1507,8 @@ int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, 
                        tspan(span(a->cu_q, ((size_t)a->num_reqs + 1) * 4)),
                        tspan(span(a->g_cache, (size_t)a->num_blocks * a->hq * a->block_size * 4)),
                        tspan(span(a->sink, (size_t)a->hq * 4)),
-                       tspan(span(lse, (size_t)a->hq * a->total_q * 4))};
+                       tspan(span(lse, (size_t)a->hq * a->total_q * 4)),
+                       tspan(span(first_lens, (size_t)a->num_reqs * 4))};
   if (outputs_overlap(outs, ins)) return GCS_ERR_INVALID_ARG;
   WeightsPlan pl;
   if (!plan_weights(a, lse != nullptr, &pl)) return GCS_ERR_CUDA;
@@ -1541,6 +1543,7 @@ int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, 
   p.q = static_cast<const uint16_t*>(a->q);
   p.q_ts = lq.ts, p.q_hs = lq.hs;
   p.lse = lse;
+  p.first_lens = first_lens;
   p.w_cache = w_cache;
   p.part = static_cast<float2*>(workspace);
   p.seg_len = pl.seg_len;

@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
   }
   const int k_begin = seg * p.seg_len, k_end = min(k_begin + p.seg_len, L);
   if (k_begin >= k_end || (ql == 0 && p.decay == 1.f)) return;
+  const int left = WRITE && p.first_lens ? max(0, __ldg(p.first_lens + r)) : 0;  // keys that are not written
+  if (WRITE && k_end <= left) return;
   const int G = p.group, nrows = ql * G;
   const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
   const bool gates = p.g_cache != nullptr;
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
     const int rows_here = min(kRows, nrows - row0);
     const int last_max = L - ql + (row0 + rows_here - 1) / G;  // last key any of these rows sees
     const int last_min = L - ql + row0 / G;
-    const int key_first = p.window > 0 ? max(0, last_min - p.window + 1) : 0;
+    const int key_first = max(left, p.window > 0 ? last_min - p.window + 1 : 0);
 
     // A step's key dims come in units of 128 codes or 64 bf16 dims, one ahead of the products (across the
     // steps too), its blocks another step ahead.  This lane's keys are 16 u + g and 16 u + g + 8.
@@ -183,7 +185,8 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
         if (valid) {
           const size_t at = (size_t)(q0 + t) * p.hq + kvh * G + head;
           if (p.lse) {
-            z = __ldg(p.lse + (size_t)(kvh * G + head) * p.total_q + q0 + t) * kLog2e;
+            const float lse = __ldg(p.lse + (size_t)(kvh * G + head) * p.total_q + q0 + t);
+            if (lse != neg_inf()) z = lse * kLog2e;
           } else {
             float m = neg_inf(), l = 0.f;
             const int first = p.window > 0 ? max(0, L - ql + t - p.window + 1) / p.seg_len : 0;
@@ -359,13 +362,14 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
     __syncthreads();
     // four neighbouring keys a thread, four of those on their way at once
     const int n = k_end - k_begin, fresh = L - ql - k_begin;  // keys from `fresh` on start from 0
+    const int skip = left - k_begin;
     for (int i0 = tid * 4; i0 < n; i0 += 4 * 4 * kThreads) {
       float* at[4];
       float old[4][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * 4 * kThreads, pos = k_begin + i;
-        const int blk = i < n ? block_of(pos) : -1;
+        const int blk = i < n && i + 3 >= skip ? block_of(pos) : -1;
         at[j] = blk < 0 ? nullptr : p.w_cache + (((size_t)blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (at[j] && p.decay != 0.f && i < fresh) v = *reinterpret_cast<const float4*>(at[j]);
@@ -380,12 +384,12 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
         for (int e = 0; e < 4; ++e)
           v[e] = i + e < n ? (p.decay != 0.f && i + e < fresh ? fmaf(p.decay, old[j][e], gathered[i + e]) : gathered[i + e])
                            : 0.f;
-        if (i + 3 < n) {
+        if (i + 3 < n && i >= skip) {
           *reinterpret_cast<float4*>(at[j]) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (i + e < n) at[j][e] = v[e];
+            if (i + e < n && i + e >= skip) at[j][e] = v[e];
         }
       }
     }

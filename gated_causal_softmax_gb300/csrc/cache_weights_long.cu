@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
 
   // resident rows: tokens a0 .. (sums) or keys a0 .. (weights); streamed tiles b_lo .. b_hi, tile i
   // from token i ntok or key key0 + 128 i on
-  int a0, b_lo, b_hi, key0 = 0, seg = 0;
+  int a0, b_lo, b_hi, key0 = 0, seg = 0, left = 0;  // left: first key whose weight is written
   if (!WRITE) {
     seg = blockIdx.x % p.segs;
     a0 = blockIdx.x / p.segs * NA * ntok;
@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     b_hi = key1 > key0 ? (key1 - key0 - 1) / kTile : -1;
   } else {
     a0 = blockIdx.x * NA * kTile;
-    if (a0 >= L) return;
+    left = p.first_lens ? __ldg(p.first_lens + r) : 0;
+    if (a0 >= L || (long long)a0 + NA * kTile <= left) return;
     const int last = min(a0 + NA * kTile, L) - 1;  // last of the keys
     // token t sees key j iff j <= L - ql + t, and L - ql + t < j + W
     b_lo = max(0, a0 - (L - ql)) / ntok;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     float gi = 0.f, ks = 0.f;
     int blk = -1, slot_k = 0;
     if (WRITE) {
-      blk = pos < L ? block_of(p, table, pos) : -1;
+      blk = pos < L && pos >= left ? block_of(p, table, pos) : -1;
       if (blk >= 0) {
         slot_k = pos & (p.block_size - 1);
         ks = kst * sl2;
@@ -718,7 +719,8 @@ __global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p
     const size_t at = (size_t)(rq.q0 + t) * p.hq + h;
     float b = neg_inf();
     if (p.lse) {
-      b = -__ldg(p.lse + (size_t)h * p.total_q + rq.q0 + t) * kLog2e;
+      const float lse = __ldg(p.lse + (size_t)h * p.total_q + rq.q0 + t);
+      if (lse != neg_inf()) b = -lse * kLog2e;
     } else {
       float m = neg_inf(), l = 0.f;
       auto join = [&](float m2, float l2) {

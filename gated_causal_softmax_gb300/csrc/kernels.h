@@ -293,6 +293,7 @@ struct WeightsParams {
   const uint16_t* q;              // bf16, element strides (token, head)
   long long q_ts, q_hs;
   const float* lse;               // [hq, total_q] natural log, or null: summed here
+  const int32_t* first_lens;      // [num_reqs] first tokens, whose weights are left as they are, or null: 0
   float* w_cache;                 // [num_blocks, hkv, block_size]
   float2* part;                   // [segs][total_q][hq] (max, sum) of every segment, without lse
   int seg_len, segs;              // context segments

@@ -470,17 +470,20 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
  * with the sink.  The rows' own tokens (the last q_len positions) start from 0: no earlier call has
  * written them.  So do all with decay = 0 (w_cache is not read then).  Slots past seq_len are not
  * touched.  A request without query rows has its weights multiplied by decay.
+ * first_lens: device int32 [num_reqs], or NULL (0): the weights of each request's first tokens are left as
+ * they are (those below 0: none).  No block that is written may belong to another request: where
+ * requests share the blocks of a prefix, first_lens covers it, here as in the choice.
  * a: the arguments of attn_decode_paged or attn_prefill_paged; v_cache, v_scale, segment_len
  * and out_stride are not looked at.  Any q_len in 0 .. seq_len, d 64, 128, 256 or 512, any hq and
  * hkv with hq % hkv == 0, fp8 or bf16 caches.  With an fp8 cache q is rounded to f16, as in the
  * attention calls (|q| <= 65504).
  * lse: fp32 [hq, total_q] natural log, as attn_fwd gives it, or NULL: summed here first, which reads
- * the keys once more.  decay: finite.
+ * the keys once more; a row whose lse is -inf adds nothing.  decay: finite.
  * Every sum has a fixed order: repeated calls give the same bits.  The workspace (256-byte aligned)
  * holds the sums' parts (none with lse); calls that may run at the same time need one each. */
 size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse);
-int attn_cache_weights(const gcs_decode_args* a, const float* lse, float decay, float* w_cache, void* workspace,
-                       size_t workspace_bytes, gcs_stream_t stream);
+int attn_cache_weights(const gcs_decode_args* a, const float* lse, const int32_t* first_lens, float decay,
+                       float* w_cache, void* workspace, size_t workspace_bytes, gcs_stream_t stream);
 
 /* Choice.  Of the L = seq_lens[r] tokens of request r, n = min(budgets[r], L, max_keep) stay (0 if
  * that is negative): the last `recent` (the latest of them when n is smaller), then the first

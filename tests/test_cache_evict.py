@@ -303,8 +303,9 @@ def test_eviction_between_decoding_steps(gcs_lib, kv_format):
                                        max_suffix_len=150 - P, g_cache=g, sink=sink)
     assert_close("decode", out, reference(q, lens, cu), DECODE_RTOL)
     w = torch.zeros((kc.shape[0], hkv, 16), device="cuda")
-    gcs.attn_cache_weights(q, kc, ks, tab, lens, cu, 2, 150, w, g_cache=g, sink=sink)
-    kept, n = gcs.attn_cache_select(w, tab, lens, 150, i32([keep] * 3), keep, first_lens=i32([P] * 3), recent=4)
+    shared = i32([P] * 3)
+    gcs.attn_cache_weights(q, kc, ks, tab, lens, cu, 2, 150, w, g_cache=g, sink=sink, first_lens=shared)
+    kept, n = gcs.attn_cache_select(w, tab, lens, 150, i32([keep] * 3), keep, first_lens=shared, recent=4)
     prefix = num(kc)[bt[0, :2].numpy()].copy()
     assert (kept[:, :, :P].cpu() == torch.arange(P)).all() and n.tolist() == [keep] * 3
     before, lens0 = num(kc).copy(), dc.seq_lens.numpy()
@@ -325,7 +326,7 @@ def test_eviction_between_decoding_steps(gcs_lib, kv_format):
     out = gcs.attn_decode_paged_shared(qr, kc, vc, ks, vs, tab, lens2, cu2, 1, keep + 1, **groups, max_group_q=3,
                                        max_suffix_len=keep + 1 - P, g_cache=g, sink=sink)
     plain = gcs.attn_decode_paged(qr, kc, vc, ks, vs, tab, lens2, cu2, 1, keep + 1, g_cache=g, sink=sink)
-    gcs.attn_cache_weights(qr, kc, ks, tab, lens2, cu2, 1, keep + 1, w, 0.9, g_cache=g, sink=sink)
+    gcs.attn_cache_weights(qr, kc, ks, tab, lens2, cu2, 1, keep + 1, w, 0.9, g_cache=g, sink=sink, first_lens=shared)
     torch.cuda.synchronize()
     assert gcs.get_device_status() == 0
     want = reference(qr, lens2, cu2)

@@ -55,7 +55,7 @@ class Case:
         return (f64(dc.q), k, opt(dc.k_scale), dc.block_table.numpy(), dc.seq_lens.numpy(), self.cu, dc.scale), dict(
             g_cache=None if dc.g_cache is None else dc.g_cache.numpy(), sink=opt(dc.sink), window=dc.window)
 
-    def check(self, got, decay, lse=None):
+    def check(self, got, decay, lse=None, first=None):
         args, kw = self.numbers()
         want = oracle.token_weights(*args, lse=lse, **kw)
         q, k, ks, bt = args[:4]
@@ -71,7 +71,7 @@ class Case:
                     A = np.log2(np.e) * self.dc.scale * (np.abs(q[a:a + ql, h * G:(h + 1) * G]) @ keys.T).max()
                 lz = 0.0 if lse is None else np.log2(np.e) * np.abs(lse[:, a:a + ql]).max(initial=0.0)
                 eps = 2 * ((q.shape[2] / 16 + 8) * 2.0**-23 * A + 2.0**-22 * (A + 40 + lz) + 2.0**-22) + 2.0**-17
-                for j in range(L):
+                for j in range(first[r] if first else 0, L):
                     blk, _, slot = self.place(r, j)
                     old = decay * float(self.w[blk, h, slot]) if decay and j < L - ql else 0.0
                     ref = want[r][h, j] + old
@@ -79,9 +79,9 @@ class Case:
                     left[blk, h, slot] = SENTINEL
         self_out = self.w.copy()
         for r, L in enumerate(self.lens):
-            for j in range(L):
+            for j in range(first[r] if first else 0, L):
                 self_out[self.place(r, j)] = SENTINEL
-        assert np.array_equal(left, self_out)  # slots past the contexts are not touched
+        assert np.array_equal(left, self_out)  # slots past the contexts (and before `first`) are not touched
 
 
 CASES = {
@@ -141,6 +141,59 @@ def test_given_sums(gcs_lib, name):
     got = c.run(gcs_lib, lse=torch.from_numpy(lse).cuda())
     assert gcs_lib.get_device_status() == 0
     c.check(got, 1.0, lse.astype(np.float64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["drafts", "chunk", "gates_window", "bf16_d256_chunk"])
+def test_given_sums_of_rows_that_see_nothing(gcs_lib, name):
+    """lse -inf: the row adds nothing, as with lse inf."""
+    lens, qls, hq, hkv, d, kw = CASES[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    lse = torch.from_numpy(np.random.default_rng(3).uniform(3, 9, (hq, sum(qls))).astype(np.float32)).cuda()
+    got = []
+    for x in (float("-inf"), float("inf")):
+        lse[:, 1::2] = x
+        got.append(c.run(gcs_lib, lse=lse))
+    assert gcs_lib.get_device_status() == 0
+    assert np.isfinite(got[0]).all() and np.array_equal(*got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sums", [False, True], ids=["summed", "given"])
+@pytest.mark.parametrize("name", ["decode_gqa16", "drafts", "no_rows", "d256_group7", "gates_window", "long", "chunk",
+                                  "gates_group7_chunk", "window_chunk", "bf16_d256_chunk", "long_chunk"])
+def test_first_tokens_are_left(gcs_lib, name, sums):
+    """The others get the same bits as without first_lens."""
+    lens, qls, hq, hkv, d, kw = CASES[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    lse = np.random.default_rng(3).uniform(3, 9, (hq, sum(qls))).astype(np.float32)
+    more = dict(decay=0.5, lse=torch.from_numpy(lse).cuda() if sums else None)
+    whole = c.run(gcs_lib, **more)
+    for first in ([-5, 7, 3, 600], [130, 20, 1 << 30, 33], [299, 1, 0, -(1 << 31)], [(1 << 31) - 1] * 4, [6001, 512, 77, 256]):
+        first = first[:len(lens)]
+        got = c.run(gcs_lib, first_lens=torch.tensor(first, dtype=torch.int32).cuda(), **more)
+        want = whole.copy()
+        for r, (L, f) in enumerate(zip(lens, first)):
+            for j in range(min(max(f, 0), L)):
+                want[c.place(r, j)] = c.w[c.place(r, j)]
+        assert np.array_equal(got, want), first
+    assert gcs_lib.get_device_status() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("qls", [[1, 2, 1], [70, 2, 33]], ids=["few", "many"])
+@pytest.mark.parametrize("kv_format", ["fp8", "bf16"])
+def test_requests_that_share_a_prefix(gcs_lib, kv_format, qls):
+    """The prefix's blocks are in all tables: first_lens keeps them from being written twice."""
+    c = Case([300, 170, 130], qls, 16, 2, 128, kv_format=kv_format, features=True)
+    bt = c.dc.block_table
+    bt[1:, :4] = bt[:1, :4]
+    c.t["block_table"] = bt.cuda()
+    for j in range(64):  # the last request's place of a token is every request's
+        c.w[c.place(0, j)] = 0.25
+    got = c.run(gcs_lib, decay=0.5, first_lens=torch.tensor([64] * 3, dtype=torch.int32).cuda())
+    assert gcs_lib.get_device_status() == 0
+    c.check(got, 0.5, first=[64] * 3)
 
 
 @pytest.mark.gpu
@@ -244,8 +297,8 @@ def test_refusals_on_host():
 
     L, b = gcs.load(), ctypes.byref
 
-    def call(a=None, w=OUT, lse=None, decay=1.0):
-        return L.attn_cache_weights(b(args() if a is None else a), lse, decay, w, None, 0, None)
+    def call(a=None, w=OUT, lse=None, decay=1.0, first=None):
+        return L.attn_cache_weights(b(args() if a is None else a), lse, first, decay, w, None, 0, None)
 
     passes = (3, 4)  # no workspace; without a GPU its size is not known
     assert call() in passes
@@ -266,8 +319,9 @@ def test_refusals_on_host():
     assert call(w=None) == 1 and call(w=OUT + 4) == 1
     assert call(w=FAKE) == 1  # the queries are there
     assert call(lse=OUT + 16) == 1 and call(lse=at(3) + 1) == 1
+    assert call(first=at(3)) in passes and call(first=at(3) + 2) == 1 and call(first=OUT + 4) == 1
     assert call(decay=float("nan")) == 1 and call(decay=float("inf")) == 1
-    assert L.attn_cache_weights(None, None, 1.0, OUT, None, 0, None) == 1
+    assert L.attn_cache_weights(None, None, None, 1.0, OUT, None, 0, None) == 1
 
 
 def test_binding_refuses_wrong_tensors(monkeypatch):
@@ -287,7 +341,8 @@ def test_binding_refuses_wrong_tensors(monkeypatch):
     for bad in (dict(q=None), dict(q=z(2, 4, 64)), dict(q=z(2, 4, 128, t=torch.bfloat16)), dict(k_cache=z(4, 2, 16, 64)),
                 dict(k_cache=torch.zeros(4, 2, 16, 64, dtype=torch.uint8)), dict(k_scale=None), dict(seq_lens=i(3)),
                 dict(cu_q=i(2)), dict(block_table=None), dict(w_cache=None), dict(w_cache=z(4, 4, 16)),
-                dict(w_cache=z(4, 2, 16, t=torch.float64)), dict(lse=z(2, 4)), dict(sink=z(2)), dict(g_cache=z(4, 2, 16)),
+                dict(w_cache=z(4, 2, 16, t=torch.float64)), dict(lse=z(2, 4)), dict(first_lens=i(3)),
+                dict(first_lens=z(2)), dict(sink=z(2)), dict(g_cache=z(4, 2, 16)),
                 dict(w_cache=OnGpu(torch.zeros(4, 2, 16), 1)), dict(k_cache=z(4, 2, 16, 64, t=torch.bfloat16))):
         with pytest.raises(ValueError):
             gcs.attn_cache_weights(**{**good, **bad})
