@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], 1);
     for (int i = 0; i < C::SLOTS; ++i) mbar_init(&s_empty[i], 4);
     for (int i = 0; i < C::NAUX; ++i) {
-      mbar_init(&aux_full[i], 1);
+      mbar_init(&aux_full[i], !WRITE && gates ? 33 : 1);  // with gates each lane's copies, too
       mbar_init(&aux_empty[i], 4 * nx);
     }
     mbar_init(drain, 1);
@@ -194,14 +194,6 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     tmem_relinquish();
   }
 
-  if (WRITE) {
-    // rows of the streamed tiles that no copy writes
-    for (int i = threadIdx.x; i < NST * (kTile - nrow) * 8; i += kThreads) {
-      const int st = i / ((kTile - nrow) * 8), k = i % ((kTile - nrow) * 8);
-      *reinterpret_cast<uint4*>(smem + C::OFF_RING + st * kStage + nrow * 128 + k * 16) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -228,9 +220,33 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     constexpr int kWords = C::A_COLS / kParts;      // columns of a thread's share: 16 .. 64
     constexpr bool kCodes = !BF16 && WRITE;
     constexpr int kLoads = kWords / (kCodes ? 8 : 4);
-    uint4 v[kLoads];  // all on their way at once
+    // All on their way at once.  Neighbouring lanes read neighbouring pieces of a row and change them in the ring's
+    // place (not in use yet; the pieces permuted by the row, so that both ways spread over the banks): with a row a
+    // lane each load touches 32 lines (8 x 33 rows of 256 dims 275 us, so 251; two pieces a row: 286, 293).
+    uint4 v[kLoads];
+    if constexpr (kLoads == 2) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) v[i] = src ? __ldg(src + part * kLoads + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kLoads; ++i) v[i] = src ? __ldg(src + part * kLoads + i) : make_uint4(0, 0, 0, 0);
+    } else {
+      static_assert(kEpiWarps * 32 * kLoads * 16 <= NST * kStage, "the ring holds the rows");
+      uint8_t* mine = smem + C::OFF_RING + (warp - 4) * 32 * kLoads * 16;
+      constexpr int kPerm = kLoads < 8 ? kLoads : 8;
+      auto place = [&](int row, int piece) {
+        return reinterpret_cast<uint4*>(mine + (row * kLoads + (piece ^ (row * kPerm / 8 & (kPerm - 1)))) * 16);
+      };
+      const int piece = lane % kLoads;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint4* from = reinterpret_cast<const uint4*>(__shfl_sync(
+            0xffffffffu, reinterpret_cast<unsigned long long>(src), i * (32 / kLoads) + lane / kLoads));
+        v[i] = from ? __ldg(from + part * kLoads + piece) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) *place(i * (32 / kLoads) + lane / kLoads, piece) = v[i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) v[i] = *place(lane, i);
+    }
 #pragma unroll
     for (int c = 0; c < kWords; c += 16) {  // 32 dims
       uint32_t w[16];
@@ -257,6 +273,15 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
       tmem_st16(col0 + part * kWords + c, w);
     }
     tmem_st_wait();
+    fence_proxy_async_smem();
+  }
+  if (WRITE && nrow < kTile) {  // rows of the streamed tiles that no copy writes
+    __syncthreads();
+    for (int i = threadIdx.x; i < NST * (kTile - nrow) * 8; i += kThreads) {
+      const int st = i / ((kTile - nrow) * 8), k = i % ((kTile - nrow) * 8);
+      *reinterpret_cast<uint4*>(smem + C::OFF_RING + st * kStage + nrow * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
   }
   if (WRITE) grid_wait();
   tc_fence_before();
@@ -352,69 +377,77 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     __syncwarp();
   } else if (warp < 4) {
     // ---------------------------------------------------------- per-column vectors
-    // The two warps take the tiles in turn, a lane columns lane + 32 k; what a tile needs from memory is
-    // on its way while the one before it is written.
-    float2 next[4];  // weights: (b, own gate); sums: (scale, -)
-    int next_blk[4];
-    auto fetch = [&](int n) {
+    // The two warps take the tiles in turn; what a tile needs from memory is on its way while the one before
+    // it is written.
+    if constexpr (WRITE) {  // (b, own gate) and the last visible key of a row, a lane rows lane + 32 k
+      float2 next[4];
+      int next_see[4];
+      auto fetch = [&](int n) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = lane + 32 * k;
-        next_blk[k] = -1;
-        if (WRITE) {
-          const int t = (b_lo + n) * ntok + i / G;
+        for (int k = 0; k < 4; ++k) {
+          const int i = lane + 32 * k, t = (b_lo + n) * ntok + i / G;
+          next_see[k] = -1;
           next[k] = make_float2(neg_inf(), 0.f);
           if (n < nt && i < nrow && t < ql) {
             next[k] = __ldg(p.rows + (size_t)(rq.q0 + t) * p.hq + kvh * G + i % G);
-            next_blk[k] = L - ql + t;  // the last key it sees
+            next_see[k] = L - ql + t;
           }
-        } else {
-          const int pos = key0 + (b_lo + n) * kTile + i;
-          next[k].x = kst;
-          if (n < nt && pos < L) next_blk[k] = block_of(p, table, pos);
-          if (next_blk[k] >= 0 && p.format == kCachePerToken)
-            next[k].x = __ldg(p.k_scale + (((size_t)next_blk[k] * p.hkv + kvh) << p.log2_block) +
-                              (pos & (p.block_size - 1)));
         }
-      }
-    };
-    fetch(warp - 2);
-    for (int n = warp - 2; n < nt; n += 2) {
-      const int a = n % C::NAUX;
-      float2 v[4];
-      int blk[4];
+      };
+      fetch(warp - 2);
+      for (int n = warp - 2; n < nt; n += 2) {
+        const int a = n % C::NAUX;
+        float2 v[4];
+        int see[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = next[k], blk[k] = next_blk[k];
-      fetch(n + 2);
-      if (!wait_bar(&aux_empty[a], ((n / C::NAUX) & 1) ^ 1, ab)) break;
-      float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
-      uint32_t bad = 0;
+        for (int k = 0; k < 4; ++k) v[k] = next[k], see[k] = next_see[k];
+        fetch(n + 2);
+        if (!wait_bar(&aux_empty[a], ((n / C::NAUX) & 1) ^ 1, ab)) break;
+        float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = lane + 32 * k;
-        if (WRITE) {
+        for (int k = 0; k < 4; ++k) {
+          const int i = lane + 32 * k;
           ax[i] = v[k].x;
           ax[kTile + i] = v[k].y;
-          reinterpret_cast<int*>(ax)[2 * kTile + i] = blk[k];
-        } else {
-          const int pos = key0 + (b_lo + n) * kTile + i;
-          ax[i] = v[k].x * sl2;
-          if (blk[k] < 0 && pos < L) bad |= 1u << (i >> 4);
-          if (gates) {
-            const float* src = p.g_cache + (((size_t)max(blk[k], 0) * p.hq + kvh * G) << p.log2_block) +
-                               (pos & (p.block_size - 1));
-#pragma unroll 8
-            for (int h = 0; h < G; ++h)
-              ax[3 * kTile + h * kGateRow + i] = blk[k] >= 0 ? __ldg(src + ((size_t)h << p.log2_block)) : 0.f;
-          }
+          reinterpret_cast<int*>(ax)[2 * kTile + i] = see[k];
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux_full[a]);
       }
-      if (!WRITE) {
-        bad = __reduce_or_sync(0xffffffffu, bad);
+    } else {  // scales and gates of the keys, a lane four in a row (of one block)
+      float4 next;
+      int next_blk;
+      auto fetch = [&](int n) {
+        const int pos = key0 + (b_lo + n) * kTile + 4 * lane;
+        next_blk = n < nt && pos < L ? block_of(p, table, pos) : -1;
+        next = make_float4(kst, kst, kst, kst);
+        if (next_blk >= 0 && p.format == kCachePerToken) {
+          const float* src = p.k_scale + (((size_t)next_blk * p.hkv + kvh) << p.log2_block) + (pos & (p.block_size - 1));
+          next = make_float4(__ldg(src), __ldg(src + 1), __ldg(src + 2), __ldg(src + 3));
+        }
+      };
+      fetch(warp - 2);
+      for (int n = warp - 2; n < nt; n += 2) {
+        const int a = n % C::NAUX, pos = key0 + (b_lo + n) * kTile + 4 * lane, blk = next_blk;
+        const float4 v = next;
+        fetch(n + 2);
+        if (!wait_bar(&aux_empty[a], ((n / C::NAUX) & 1) ^ 1, ab)) break;
+        float* ax = reinterpret_cast<float*>(smem + C::OFF_AUX + a * C::AUX);
+        if (gates) {  // no lane waits for its copies: they arrive at the barrier by themselves
+          const float* src = p.g_cache + (((size_t)max(blk, 0) * p.hq + kvh * G) << p.log2_block) +
+                             (pos & (p.block_size - 1));
+          for (int h = 0; h < G; ++h)
+            copy_async16(ax + 3 * kTile + h * kGateRow + 4 * lane, src + ((size_t)h << p.log2_block), blk >= 0);
+          copies_arrive(&aux_full[a]);
+        }
+        *reinterpret_cast<float4*>(ax + 4 * lane) = make_float4(v.x * sl2, v.y * sl2, v.z * sl2, v.w * sl2);
+        const uint32_t bad = __reduce_or_sync(0xffffffffu, blk < 0 && pos < L ? 1u << (lane >> 2) : 0u);
         if (lane == 0) bad_pages[a] = bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&aux_full[a]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&aux_full[a]);
+      copy_commit();
+      copy_wait<0>();
     }
     __syncwarp();
   } else if (warp < 4 + kEpiWarps) {
@@ -806,7 +839,7 @@ bool cache_weights_long(int max_q_len, int group, bool gates) {
 }
 
 // Context segments of the sums kernel: blocks for about three an SM (contexts shorter than max_seq_len leave some
-// of them empty; 8 x 33 rows of 256 dims: two 313 us, three 281, four 297), of 128 tokens or more.
+// of them empty; 8 x 33 rows of 256 dims: two 219 us, three 213, four 225), of 128 tokens or more.
 int cache_weights_long_segment(int max_seq_len, int max_q_len, int group, int d, long long units, int sms) {
   const long long per = (long long)(d == 512 ? 1 : 2) * (kTile / group);
   const long long blocks = (max_q_len + per - 1) / per * units;

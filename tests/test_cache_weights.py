@@ -197,6 +197,26 @@ def test_requests_that_share_a_prefix(gcs_lib, kv_format, qls):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name", ["drafts", "chunk", "gates_sink", "gates_window", "gates_group7_chunk", "gates_bf16_d256",
+                                  "d64_chunk", "bf16_d512_chunk"])
+def test_what_lies_behind_the_contexts(gcs_lib, name):
+    """NaN keys, scales and gates in the slots past seq_len of a last block change nothing."""
+    lens, qls, hq, hkv, d, kw = CASES[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    want = c.run(gcs_lib)
+    for r, L in enumerate(lens):
+        if L % c.block:
+            blk, _, slot = c.place(r, L)
+            bf16 = c.t["k_cache"].dtype == torch.bfloat16
+            c.t["k_cache"][blk, :, slot:] = float("nan") if bf16 else 0x7F
+            for key in ("k_scale", "g_cache"):
+                if c.t[key] is not None and c.t[key].dim() == 3:
+                    c.t[key][blk, :, slot:] = float("nan")
+    assert np.array_equal(c.run(gcs_lib), want)
+    assert gcs_lib.get_device_status() == 0
+
+
+@pytest.mark.gpu
 def test_sums_of_the_prefill(gcs_lib):
     """attn_fwd's lse over the same keys: every row's weights add up to 1 a head."""
     gen = torch.Generator().manual_seed(0)
