@@ -580,10 +580,10 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
           const float4* b4 = reinterpret_cast<const float4*>(ax);
           const float4* gi4 = reinterpret_cast<const float4*>(ax + kTile);
           const int* see = reinterpret_cast<const int*>(ax) + 2 * kTile;
-          auto tile = [&](auto masked) {
+          auto tile = [&](auto masked, auto columns32) {
             constexpr bool kMask = decltype(masked)::value;
 #pragma unroll
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < decltype(columns32)::value; ++cc) {
               uint32_t sv[32];
               tmem_ld32(tS + cc * 32, sv);
               tmem_ld_wait();
@@ -626,8 +626,10 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
               }
             }
           };
-          if (need_mask) tile(std::true_type());
-          else tile(std::false_type());
+          using All = std::integral_constant<int, 4>;
+          if (!need_mask) tile(std::false_type(), All());
+          else if ((ql - t0) * G > 32) tile(std::true_type(), All());
+          else tile(std::true_type(), std::integral_constant<int, 1>());  // a last tile of few rows: 211 us, so 203
         }
         tc_fence_before();
         __syncwarp();
