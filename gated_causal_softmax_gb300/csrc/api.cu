@@ -770,11 +770,13 @@ static PagedOperandCheck operand_check(const gcs_decode_args* a) {
   return c;
 }
 
-static int paged_checks(const gcs_decode_args* a, void* workspace, size_t off, DecodeParams& p, cudaStream_t s) {
+static int paged_checks(const gcs_decode_args* a, void* workspace, size_t off, DecodeParams& p, cudaStream_t s,
+                        const SharedPrefixes& prefix = SharedPrefixes{}) {
   int32_t* cu_chk = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + off);
   const int st = cuda_status(launch_check_paged(a->cu_q, a->seq_lens, a->block_table, a->num_reqs, a->total_q,
                                                 a->max_q_len, a->max_seq_len, a->max_blocks_per_req, a->num_blocks,
-                                                a->block_size, a->window, operand_check(a), cu_chk, p.status, s));
+                                                a->block_size, a->window, operand_check(a), prefix, cu_chk, p.status,
+                                                s));
   if (st == GCS_OK) p.cu_q = cu_chk;
   return st;
 }
@@ -1039,12 +1041,13 @@ int attn_decode_paged_shared(const gcs_decode_args* a, const gcs_prefix_args* x,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (chk) {
     const size_t off = pl.part + pl.acc + pl.ml;
-    st = paged_checks(a, workspace, off, p, s);
+    const SharedPrefixes prefix{x->cu_groups, x->prefix_lens, x->num_groups};
+    st = paged_checks(a, workspace, off, p, s, prefix);
     if (st != GCS_OK) return st;
     int32_t* groups = reinterpret_cast<int32_t*>(ws + off + cu_q_copy_ws(a, true));
-    st = cuda_status(launch_check_groups(x->cu_groups, x->prefix_lens, x->num_groups, a->seq_lens, a->block_table,
-                                         a->num_reqs, a->max_blocks_per_req, a->num_blocks, a->block_size, a->total_q,
-                                         x->max_group_q, x->max_prefix_len, x->max_suffix_len,
+    st = cuda_status(launch_check_groups(prefix, a->seq_lens, a->block_table, a->num_reqs, a->max_blocks_per_req,
+                                         a->num_blocks, a->block_size, a->total_q, x->max_group_q, x->max_prefix_len,
+                                         x->max_suffix_len, a->window, operand_check(a),
                                          const_cast<int32_t*>(p.cu_q), groups, status, s));
     if (st != GCS_OK) return st;
     p.cu_groups = groups;
@@ -1691,7 +1694,7 @@ int gcs_check_paged_inputs(const gcs_decode_args* a, gcs_stream_t stream) {
   if (!status) return GCS_ERR_CUDA;
   return cuda_status(launch_check_paged(a->cu_q, a->seq_lens, a->block_table, a->num_reqs, a->total_q, a->max_q_len,
                                         a->max_seq_len, a->max_blocks_per_req, a->num_blocks, a->block_size,
-                                        a->window, operand_check(a), nullptr, status,
+                                        a->window, operand_check(a), SharedPrefixes{}, nullptr, status,
                                         reinterpret_cast<cudaStream_t>(stream)));
 }
 

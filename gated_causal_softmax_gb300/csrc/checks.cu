@@ -44,6 +44,16 @@ __global__ void __launch_bounds__(kCheckThreads) check_prefill_kernel(const int3
   finish_check(bad, &bad_s, cu, num_seqs + 1, cu_out, status);
 }
 
+// Whether one of the first `slots` V scales of an fp8 cache's block is not below 255 in magnitude.
+__device__ __forceinline__ bool bad_scales(const PagedOperandCheck& fp8, int blk, int block_size, int slots) {
+  bool bad = false;
+  if (fp8.hkv > 0 && !fp8.per_tensor)
+    for (int h = 0; h < fp8.hkv; ++h)
+      for (int sl = 0; sl < slots; ++sl)
+        bad = bad || !(fabsf(__ldg(fp8.v_scale + ((size_t)blk * fp8.hkv + h) * block_size + sl)) < 255.f);
+  return bad;
+}
+
 // cu_q starts at 0 and ends at total_q; request r has 0 <= q_len <= max_q_len query rows and
 // q_len <= seq_len <= max_seq_len cached tokens; the page-table entries of the pages the
 // paged calls can read for it lie in [0, num_blocks).  Those pages run from the 128-key tile
@@ -54,10 +64,14 @@ __global__ void __launch_bounds__(kCheckThreads) check_prefill_kernel(const int3
 // With an fp8 cache (f16 operands, fp8.hkv > 0) it also checks the operand limits: every |q| at
 // most 65504 (q, strided, is read in 16-byte units) and every V scale of the slots below
 // seq_len in those pages below 255 in magnitude (per tensor: the one scale).
+//
+// With shared prefixes (prefix.num_groups > 0) the pages are those from the block of the first token behind
+// the prefix on; check_groups_kernel looks at the prefix's.  cu_groups is not checked yet, so no index is taken
+// from it.
 __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
     const int32_t* __restrict__ cu_q, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ table,
     int num_reqs, int total_q, int max_q_len, int max_seq_len, int max_blocks, int num_blocks, int block_size,
-    int window, PagedOperandCheck fp8, int32_t* __restrict__ cu_out, int* status) {
+    int window, PagedOperandCheck fp8, SharedPrefixes prefix, int32_t* __restrict__ cu_out, int* status) {
   __shared__ int bad_s;
   if (threadIdx.x == 0) bad_s = 0;
   __syncthreads();
@@ -89,17 +103,24 @@ __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
     }
     if (ql == 0) continue;
     const int first_key = window > 0 ? max(0, L - static_cast<int>(ql) - window + 1) : 0;
-    const int p0 = (first_key / 128) * 128 / block_size;  // block holding the first key of that tile
+    int p0 = (first_key / 128) * 128 / block_size;  // block holding the first key of that tile
+    if (prefix.num_groups > 0) {
+      int lo = 0, hi = prefix.num_groups;  // the last group that starts at or before r
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(prefix.cu_groups + mid) <= r) lo = mid;
+        else hi = mid;
+      }
+      const int P = __ldg(prefix.prefix_lens + lo);
+      if (P >= L) continue;  // nothing behind it (or a prefix that the other kernel refuses)
+      p0 = max(p0, P / block_size);
+    }
     const int np = (L + block_size - 1) / block_size;  // <= max_blocks: L <= max_seq_len
     for (int pg = p0 + lane; pg < np; pg += 32) {
       const int blk = __ldg(table + (size_t)r * max_blocks + pg);
       bad = bad || blk < 0 || blk >= num_blocks;
-      if (fp8.hkv > 0 && !fp8.per_tensor && blk >= 0 && blk < num_blocks) {
-        const int nslot = min(block_size, L - pg * block_size);
-        for (int h = 0; h < fp8.hkv; ++h)
-          for (int sl = 0; sl < nslot; ++sl)
-            bad = bad || !(fabsf(__ldg(fp8.v_scale + ((size_t)blk * fp8.hkv + h) * block_size + sl)) < 255.f);
-      }
+      if (blk >= 0 && blk < num_blocks)
+        bad = bad || bad_scales(fp8, blk, block_size, min(block_size, L - pg * block_size));
     }
   }
   finish_check(bad, &bad_s, cu_q, num_reqs + 1, cu_out, status);
@@ -107,13 +128,15 @@ __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
 
 // The groups of a call with shared prefixes: cu_groups starts at 0, ends at num_reqs and is sorted;
 // a group has at most max_group_q query rows and a prefix of 0 .. max_prefix tokens, whose blocks the
-// table of its first request holds; every request of it has prefix <= seq_len <= prefix + max_suffix.
+// table of its first request holds (with V scales below 255 from the 128-key tile on that holds the earliest
+// key any of the group's rows sees); every request of it has prefix <= seq_len <= prefix + max_suffix.
 // cu_q is the checked copy (ending at 0: an earlier check failed).
 __global__ void __launch_bounds__(kCheckThreads) check_groups_kernel(
-    const int32_t* __restrict__ cu_groups, const int32_t* __restrict__ prefix_lens, int num_groups,
-    const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ table, int num_reqs, int max_blocks,
-    int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix, int max_suffix, int32_t* cu_q,
-    int32_t* __restrict__ groups_out, int* status) {
+    SharedPrefixes groups, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ table, int num_reqs,
+    int max_blocks, int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix, int max_suffix,
+    int window, PagedOperandCheck fp8, int32_t* cu_q, int32_t* __restrict__ groups_out, int* status) {
+  const int32_t *cu_groups = groups.cu_groups, *prefix_lens = groups.prefix_lens;
+  const int num_groups = groups.num_groups;
   __shared__ int bad_s;
   if (threadIdx.x == 0) bad_s = cu_q[num_reqs] != total_q;  // already recorded
   __syncthreads();
@@ -129,17 +152,22 @@ __global__ void __launch_bounds__(kCheckThreads) check_groups_kernel(
     if (a == b) continue;
     bad = bad || (long long)cu_q[b] - cu_q[a] > max_group_q;
     bool fits = true;
+    int seen = P;  // earliest key that a row sees
     for (int r = a + lane; r < b; r += 32) {
-      const int L = __ldg(seq_lens + r);
+      const int L = __ldg(seq_lens + r), ql = cu_q[r + 1] - cu_q[r];
       fits = fits && P <= L && (long long)L - P <= max_suffix;
+      if (ql > 0) seen = min(seen, window > 0 ? max(0, L - ql - window + 1) : 0);
     }
     if (!__all_sync(0xffffffffu, fits)) {
       bad = true;
       continue;
     }
+    const int from = __reduce_min_sync(0xffffffffu, seen) / 128 * 128 / block_size;
     for (int pg = lane; pg < (P + block_size - 1) / block_size; pg += 32) {  // P <= seq_len <= the table
       const int blk = __ldg(table + (size_t)a * max_blocks + pg);
       bad = bad || blk < 0 || blk >= num_blocks;
+      if (blk >= 0 && blk < num_blocks && pg >= from)
+        bad = bad || bad_scales(fp8, blk, block_size, min(block_size, P - pg * block_size));
     }
   }
   if (bad) atomicOr(&bad_s, 1);
@@ -153,13 +181,14 @@ __global__ void __launch_bounds__(kCheckThreads) check_groups_kernel(
 
 }  // namespace
 
-cudaError_t launch_check_groups(const int32_t* cu_groups, const int32_t* prefix_lens, int num_groups,
-                                const int32_t* seq_lens, const int32_t* table, int num_reqs, int max_blocks,
-                                int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix,
-                                int max_suffix, int32_t* cu_q, int32_t* groups_out, int* status, cudaStream_t s) {
-  check_groups_kernel<<<1, kCheckThreads, 0, s>>>(cu_groups, prefix_lens, num_groups, seq_lens, table, num_reqs,
-                                                  max_blocks, num_blocks, block_size, total_q, max_group_q, max_prefix,
-                                                  max_suffix, cu_q, groups_out, status);
+cudaError_t launch_check_groups(const SharedPrefixes& groups, const int32_t* seq_lens, const int32_t* table,
+                                int num_reqs, int max_blocks, int num_blocks, int block_size, int total_q,
+                                int max_group_q, int max_prefix, int max_suffix, int window,
+                                const PagedOperandCheck& fp8, int32_t* cu_q, int32_t* groups_out, int* status,
+                                cudaStream_t s) {
+  check_groups_kernel<<<1, kCheckThreads, 0, s>>>(groups, seq_lens, table, num_reqs, max_blocks, num_blocks, block_size,
+                                                  total_q, max_group_q, max_prefix, max_suffix, window, fp8, cu_q,
+                                                  groups_out, status);
   return cudaGetLastError();
 }
 
@@ -171,10 +200,11 @@ cudaError_t launch_check_prefill(const int32_t* cu, int num_seqs, int total, int
 
 cudaError_t launch_check_paged(const int32_t* cu_q, const int32_t* seq_lens, const int32_t* table, int num_reqs,
                                int total_q, int max_q_len, int max_seq_len, int max_blocks, int num_blocks,
-                               int block_size, int window, const PagedOperandCheck& fp8, int32_t* cu_out,
-                               int* status, cudaStream_t s) {
+                               int block_size, int window, const PagedOperandCheck& fp8, const SharedPrefixes& prefix,
+                               int32_t* cu_out, int* status, cudaStream_t s) {
   check_paged_kernel<<<1, kCheckThreads, 0, s>>>(cu_q, seq_lens, table, num_reqs, total_q, max_q_len, max_seq_len,
-                                                 max_blocks, num_blocks, block_size, window, fp8, cu_out, status);
+                                                 max_blocks, num_blocks, block_size, window, fp8, prefix, cu_out,
+                                                 status);
   return cudaGetLastError();
 }
 

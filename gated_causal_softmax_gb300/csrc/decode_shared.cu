@@ -593,8 +593,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (lane == 0) mbar_arrive(&q_full[x]);
     }
     float gi = 0.f;  // the row's own G
-    if (GATES && row_valid) {
-      const int blk = __ldg(p.block_table + (size_t)req * p.max_blocks + lastk / p.block_size);
+    if (GATES && row_valid) {  // a row that stands inside the prefix: like every key there, by the first request's table
+      const int32_t* own = lastk < P ? trow : p.block_table + (size_t)req * p.max_blocks;
+      const int blk = __ldg(own + lastk / p.block_size);
       gi = __ldg(p.g_cache + ((size_t)blk * p.hq + kvh * G + head) * p.block_size + lastk % p.block_size);
     }
     const float sl2 = p.scale * kLog2e;
@@ -784,7 +785,8 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const DecodeParams p) 
   const int q_begin = __ldg(p.cu_q + r);
   const int ql = __ldg(p.cu_q + r + 1) - q_begin;
   if (t >= ql) return;
-  const int L = __ldg(p.seq_lens + r), start = shared_len(p, r);
+  int group_first;
+  const int L = __ldg(p.seq_lens + r), start = shared_len(p, r, group_first);
   const int G = p.group;
   const int sl = threadIdx.x & (SL - 1), d0 = ((threadIdx.x / SL) & 15) * 8;
   const int hh = blockIdx.z * kHeads + threadIdx.x / (16 * SL);

@@ -74,16 +74,16 @@ constexpr float kInvPScale = 1.f / 32.f;
 
 // Tokens of request r that its group shares: those below the prefix's length, as far as the
 // cache of the group's first request and the host's bound go.  The group is the last one that
-// starts at or before r.
-__device__ __forceinline__ int shared_len(const DecodeParams& p, int r) {
+// starts at or before r; first: its first request, whose table the shared tokens are read through.
+__device__ __forceinline__ int shared_len(const DecodeParams& p, int r, int& first) {
   int lo = 0, hi = p.num_groups;  // cu_groups[lo] <= r < cu_groups[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(p.cu_groups + mid) <= r) lo = mid;
     else hi = mid;
   }
-  const int n = min(min(__ldg(p.prefix_lens + lo), p.max_prefix), __ldg(p.seq_lens + __ldg(p.cu_groups + lo)));
-  return max(n, 0);
+  first = __ldg(p.cu_groups + lo);
+  return max(min(min(__ldg(p.prefix_lens + lo), p.max_prefix), __ldg(p.seq_lens + first)), 0);
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int ql = __ldg(p.cu_q + r + 1) - q_begin;
   const int npages = (L + kPage - 1) / kPage;
   if (SH) grid_release();  // the prefix's kernel needs nothing of this one
-  const int start = SH ? shared_len(p, r) : 0;  // first key
+  int group_first = r;
+  const int start = SH ? shared_len(p, r, group_first) : 0;  // first key
   int pb = (SH ? start / kPage : 0) + seg * p.seg_pages;
   if (pb >= npages || (SH && start >= L) || ql < 1 || ql > 4) return;
   constexpr int ppt = kRows / G;  // query positions per m16 tile: 1 or 2
@@ -315,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     // each row's own cumulative gate (log2 units) at its position
     float gq0 = 0.f, gq1 = 0.f;
     if (has_gate) {
-      const int32_t* trow = p.block_table + (size_t)r * p.max_blocks;
+      // a row that stands inside the prefix sees no key of this kernel; its gate is the first request's
+      auto table_of = [&](int k) { return p.block_table + (size_t)(SH && k < start ? group_first : r) * p.max_blocks; };
       const int kB = validB ? lastkB : lastkA;  // row B past q_len reads row A's entry (unused)
-      const int bA = __ldg(trow + lastkA / p.block_size), bB = __ldg(trow + kB / p.block_size);
+      const int bA = __ldg(table_of(lastkA) + lastkA / p.block_size), bB = __ldg(table_of(kB) + kB / p.block_size);
       gq0 = __ldg(p.g_cache + ((size_t)bA * p.hq + kvh * G + headA) * p.block_size + lastkA % p.block_size) * kLog2e;
       gq1 = __ldg(p.g_cache + ((size_t)bB * p.hq + kvh * G + headB) * p.block_size + kB % p.block_size) * kLog2e;
     }

@@ -189,14 +189,6 @@ cudaError_t launch_prefill_paged(const DecodeParams& p, const DecodeMaps& maps, 
 // Decoding behind shared prefixes: p.part_* hold the partials of the tokens behind the prefix,
 // p.pre_* those of the prefix.  bf16 caches: maps of bf16 elements, box 64 dims x 16 slots.
 cudaError_t launch_decode_shared(const DecodeParams& p, const DecodeMaps& maps, cudaStream_t s);
-// The groups' arrays of such a call, after launch_check_paged wrote its copy of cu_q: records
-// kDevInvalidArg where they break a precondition (see the public header) and writes groups_out, the copy of
-// cu_groups; on a failure, or when the copy of cu_q is already an empty batch, both copies are zeros.
-cudaError_t launch_check_groups(const int32_t* cu_groups, const int32_t* prefix_lens, int num_groups,
-                                const int32_t* seq_lens, const int32_t* table, int num_reqs, int max_blocks,
-                                int num_blocks, int block_size, int total_q, int max_group_q, int max_prefix,
-                                int max_suffix, int32_t* cu_q, int32_t* groups_out, int* status, cudaStream_t s);
-
 // One CTA that waits on a barrier phase nothing completes; its bounded wait records a
 // timeout in *status and the kernel exits.
 cudaError_t launch_bounded_wait_selftest(int* status, cudaStream_t s);
@@ -214,10 +206,24 @@ struct PagedOperandCheck {
   const float* v_scale;   // per token [num_blocks, hkv, block_size] or per tensor [1]
   int per_tensor;
 };
+// Groups of requests that share a prefix (num_groups 0: none).
+struct SharedPrefixes {
+  const int32_t* cu_groups;    // [num_groups + 1]
+  const int32_t* prefix_lens;  // [num_groups]
+  int num_groups;
+};
 cudaError_t launch_check_paged(const int32_t* cu_q, const int32_t* seq_lens, const int32_t* table, int num_reqs,
                                int total_q, int max_q_len, int max_seq_len, int max_blocks, int num_blocks,
-                               int block_size, int window, const PagedOperandCheck& fp8, int32_t* cu_out,
-                               int* status, cudaStream_t s);
+                               int block_size, int window, const PagedOperandCheck& fp8, const SharedPrefixes& prefix,
+                               int32_t* cu_out, int* status, cudaStream_t s);
+// The groups' arrays of such a call, after launch_check_paged wrote its copy of cu_q: records
+// kDevInvalidArg where they break a precondition (see the public header) and writes groups_out, the copy of
+// cu_groups; on a failure, or when the copy of cu_q is already an empty batch, both copies are zeros.
+cudaError_t launch_check_groups(const SharedPrefixes& groups, const int32_t* seq_lens, const int32_t* table,
+                                int num_reqs, int max_blocks, int num_blocks, int block_size, int total_q,
+                                int max_group_q, int max_prefix, int max_suffix, int window,
+                                const PagedOperandCheck& fp8, int32_t* cu_q, int32_t* groups_out, int* status,
+                                cudaStream_t s);
 
 // Norm and rotation of query and key rows ([tokens, heads, d] bf16, element strides (token, head)).
 struct RopeParams {

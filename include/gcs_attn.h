@@ -288,8 +288,9 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
  * the requests cu_groups[g] .. cu_groups[g+1]-1; the tokens at positions below prefix_lens[g] are the
  * same for all of them and are read through the block table of the group's first request.  A
  * request's own table is read from there on (from the start of the cache block that holds position
- * prefix_lens[g]; the last, partly shared block may be each request's own copy).  A group may be one
- * request or none, a prefix 0.
+ * prefix_lens[g]; the last, partly shared block may be each request's own copy): its entries before
+ * that are not looked at.  A query row may stand inside the prefix (prefix_lens[g] up to the seq_len).
+ * A group may be one request or none, a prefix 0.
  * Everything of attn_decode_paged is supported (formats, groups of 16 or 8 heads, block sizes,
  * strides, q_len 1..4, gates, window, sink), except: segment_len is that of the tokens behind the
  * prefixes, 0 lets the library choose; and no kernel events are recorded (they stay armed).
@@ -542,7 +543,9 @@ int gcs_selftest_bounded_wait(gcs_stream_t stream);
  *            0 <= q_len <= max_q_len and q_len <= seq_len <= max_seq_len; and, for a request
  *            with q_len >= 1, every block_table entry in [0, num_blocks) from the 128-key tile
  *            that holds the earliest key one of its query rows sees (key 0 without a window)
- *            up to the page of its last cached token (the pages the paged calls can read);
+ *            up to the page of its last cached token (the pages the paged calls can read; behind
+ *            a shared prefix those from the block of its first own token on, and for the prefix
+ *            those of the group's first request);
  *            with an fp8 cache, the f16 operand limits: every |q| <= 65504 and every V scale
  *            of those pages' slots below seq_len (or the per-tensor V scale) < 255.
  * A failed check records GCS_ERR_INVALID_ARG in the current device's status word (first
@@ -550,11 +553,11 @@ int gcs_selftest_bounded_wait(gcs_stream_t stream);
  *
  * gcs_set_device_checks(1) turns on checked mode for every later call of this process (0
  * turns it off; other values return GCS_ERR_INVALID_ARG).  In checked mode each attention call
- * (attn_fwd, attn_bwd, attn_decode_paged, attn_prefill_paged) first launches one single-CTA
- * kernel on its stream that checks its arrays and writes a copy of cu_seqlens (or cu_q) to the
- * end of the call's workspace; the call's kernels read that copy.  When a check fails the copy is all zeros, an empty batch: no kernel then reads
- * through an index taken from these arrays, so a broken array cannot send a kernel outside a
- * buffer.
+ * (attn_fwd, attn_bwd, attn_decode_paged, attn_prefill_paged, attn_decode_paged_shared) first
+ * launches one single-CTA kernel (the last one two) on its stream that checks its arrays and writes a
+ * copy of cu_seqlens (or cu_q) to the end of the call's workspace; the call's kernels read that
+ * copy.  When a check fails the copy is all zeros, an empty batch: no kernel then reads through an
+ * index taken from these arrays, so a broken array cannot send a kernel outside a buffer.
  * The outputs of such a call are unspecified.  The copy takes ((num_seqs or num_reqs) + 1)
  * x 4 bytes, rounded up to 256, more workspace: the *_workspace queries include it while
  * checked mode is on (query them after switching the mode), so attn_fwd and
