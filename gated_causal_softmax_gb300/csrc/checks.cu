@@ -44,12 +44,12 @@ __global__ void __launch_bounds__(kCheckThreads) check_prefill_kernel(const int3
   finish_check(bad, &bad_s, cu, num_seqs + 1, cu_out, status);
 }
 
-// Whether one of the first `slots` V scales of an fp8 cache's block is not below 255 in magnitude.
-__device__ __forceinline__ bool bad_scales(const PagedOperandCheck& fp8, int blk, int block_size, int slots) {
+// Whether one of the V scales of the slots first .. end - 1 of an fp8 cache's block is not below 255 in magnitude.
+__device__ __forceinline__ bool bad_scales(const PagedOperandCheck& fp8, int blk, int block_size, int first, int end) {
   bool bad = false;
   if (fp8.hkv > 0 && !fp8.per_tensor)
     for (int h = 0; h < fp8.hkv; ++h)
-      for (int sl = 0; sl < slots; ++sl)
+      for (int sl = first; sl < end; ++sl)
         bad = bad || !(fabsf(__ldg(fp8.v_scale + ((size_t)blk * fp8.hkv + h) * block_size + sl)) < 255.f);
   return bad;
 }
@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
     if (ql == 0) continue;
     const int first_key = window > 0 ? max(0, L - static_cast<int>(ql) - window + 1) : 0;
     int p0 = (first_key / 128) * 128 / block_size;  // block holding the first key of that tile
+    int own = 0;  // first key that is read through this table
     if (prefix.num_groups > 0) {
       int lo = 0, hi = prefix.num_groups;  // the last group that starts at or before r
       while (hi - lo > 1) {
@@ -113,14 +114,16 @@ __global__ void __launch_bounds__(kCheckThreads) check_paged_kernel(
       }
       const int P = __ldg(prefix.prefix_lens + lo);
       if (P >= L) continue;  // nothing behind it (or a prefix that the other kernel refuses)
-      p0 = max(p0, P / block_size);
+      own = max(0, P);
+      p0 = max(p0, own / block_size);
     }
     const int np = (L + block_size - 1) / block_size;  // <= max_blocks: L <= max_seq_len
     for (int pg = p0 + lane; pg < np; pg += 32) {
       const int blk = __ldg(table + (size_t)r * max_blocks + pg);
       bad = bad || blk < 0 || blk >= num_blocks;
       if (blk >= 0 && blk < num_blocks)
-        bad = bad || bad_scales(fp8, blk, block_size, min(block_size, L - pg * block_size));
+        bad = bad || bad_scales(fp8, blk, block_size, max(0, own - pg * block_size),
+                                min(block_size, L - pg * block_size));
     }
   }
   finish_check(bad, &bad_s, cu_q, num_reqs + 1, cu_out, status);
@@ -167,7 +170,7 @@ __global__ void __launch_bounds__(kCheckThreads) check_groups_kernel(
       const int blk = __ldg(table + (size_t)a * max_blocks + pg);
       bad = bad || blk < 0 || blk >= num_blocks;
       if (blk >= 0 && blk < num_blocks && pg >= from)
-        bad = bad || bad_scales(fp8, blk, block_size, min(block_size, P - pg * block_size));
+        bad = bad || bad_scales(fp8, blk, block_size, 0, min(block_size, P - pg * block_size));
     }
   }
   if (bad) atomicOr(&bad_s, 1);

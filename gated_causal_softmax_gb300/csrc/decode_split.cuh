@@ -466,14 +466,16 @@ __global__ void __launch_bounds__(kThreads, 3)
           o[u][3] *= a1;
         }
       }
-      // V scales multiply the probabilities after the row sum; slots >= L get scale 0, and
-      // their value bytes are never multiplied (NaN allowed there)
+      // V scales multiply the probabilities after the row sum; slots that are not this call's get
+      // scale 0, and their value bytes are never multiplied (NaN allowed there): those at or past
+      // seq_len, and below the first key the ones of a prefix that is read elsewhere
+      auto foreign = [&](int c) { return tk[c] >= L || (SH && tk[c] < start); };
 #pragma unroll
       for (int c = 0; c < 4; ++c) vs[c] *= KVF == 0 ? kPScale : 1.f;
       if (!inner) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (tk[c] >= L) vs[c] = 0.f;
+          if (foreign(c)) vs[c] = 0.f;
       }
       if constexpr (KVF == 0) {
         uint32_t pa[4];
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         pa[2] = pack_f16x2(pr[0][2] * vs[2], pr[0][3] * vs[3]);
         pa[3] = pack_f16x2(pr[1][2] * vs[2], pr[1][3] * vs[3]);
         // value fragments: dims 16g .. 16g + 15 (16-B unit g) of slots 2tq, 2tq+1, 2tq+8, 2tq+9;
-        // slots at or past seq_len are zero (NaN allowed in their bytes)
+        // foreign slots are zero
         uint4 vr[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (!inner) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (tk[c] >= L) vr[c] = make_uint4(0, 0, 0, 0);
+            if (foreign(c)) vr[c] = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -523,13 +525,13 @@ __global__ void __launch_bounds__(kThreads, 3)
         pa[2] = pack_bf16x2(pr[0][2] * vs[2], pr[0][3] * vs[3]);
         pa[3] = pack_bf16x2(pr[1][2] * vs[2], pr[1][3] * vs[3]);
         // values of rows 2tq, 2tq+1, 2tq+8, 2tq+9 (tk[0..3]), dims 16g .. 16g + 15 (32 B each);
-        // rows at or past seq_len are zero (NaN allowed in their bytes)
+        // foreign rows are zero
         uint32_t rw[4][8];
 #pragma unroll
         for (int rr = 0; rr < 4; ++rr) {
           const int row = 2 * tq + (rr & 1) + 8 * (rr >> 1);
           uint4 a = lds128(st + C::KB + row * 256 + 32 * g), b = lds128(st + C::KB + row * 256 + 32 * g + 16);
-          if (!inner && tk[rr] >= L) a = b = make_uint4(0, 0, 0, 0);
+          if (!inner && foreign(rr)) a = b = make_uint4(0, 0, 0, 0);
           rw[rr][0] = a.x; rw[rr][1] = a.y; rw[rr][2] = a.z; rw[rr][3] = a.w;
           rw[rr][4] = b.x; rw[rr][5] = b.y; rw[rr][6] = b.z; rw[rr][7] = b.w;
         }

@@ -8,9 +8,11 @@ from test_decode_shared import Shared
 # rows that stand inside the prefix, in front of its last block too; prefixes that end inside a block
 CASES = {
     "gates": ([(160, [(1, 0), (3, 0), (2, 50), (4, 2), (4, 3)])], 16, 2, dict(features=True)),
-    "gates_odd": ([(157, [(1, 0), (4, 2), (1, 30)]), (97, [(2, 1), (4, 1), (4, 0)])], 32, 2, dict(features=True, block=32)),
+    "gates_odd": ([(157, [(1, 0), (4, 2), (1, 30)]), (97, [(2, 1), (4, 1), (4, 0)])], 32, 2,
+                  dict(features=True, block=32)),
     "gates_group8": ([(162, [(1, 9), (4, 1), (3, 0)]), (0, [(1, 3)])], 8, 1, dict(features=True)),
-    "gates_bf16": ([(129, [(1, 0), (4, 2), (4, 130)])], 16, 2, dict(features=True, kv_format="bf16", block=64, nhd=True)),
+    "gates_bf16": ([(129, [(1, 0), (4, 2), (4, 130)])], 16, 2,
+                   dict(features=True, kv_format="bf16", block=64, nhd=True)),
     "window": ([(301, [(1, 20), (4, 2), (3, 9)])], 16, 2, dict(features=True, window=60)),
     "plain": ([(333, [(1, 20), (2, 40), (1, 1)]), (20, [(1, 400), (1, 0)])], 16, 2, {}),
     "drafts": ([(203, [(4, 4), (4, 60), (3, 3)])], 32, 2, dict(block=128, nhd=True)),
@@ -82,5 +84,33 @@ def test_checked_mode_reads_what_the_call_reads(gcs_lib, name):
                 vs[int(c.t["block_table"][0, 0]), :, 0] = 300.0
                 assert torch.equal(c.run(gcs_lib, block_table=table, v_scale=vs), whole)
                 assert gcs_lib.get_device_status() == 0
+    finally:
+        gcs_lib.set_device_checks(False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_own_copies_of_the_last_block_without_the_prefix(gcs_lib, name):
+    """A request's own copy of the block that the prefix fills in part: its slots below the prefix's length may
+    hold NaN keys, values, scales and gates."""
+    groups, hq, hkv, kw = CASES[name]
+    c = Shared(groups, hq, hkv, **kw)
+    whole = c.run(gcs_lib)
+    table, bs, some = c.dc.block_table, c.dc.k_cache.shape[2], False
+    for r, p in followers(c):
+        if p % bs and c.lens[r] > p:
+            blk, some = int(table[r, p // bs]), True
+            for key in ("k_cache", "v_cache"):
+                c.t[key][blk, :, :p % bs] = float("nan") if c.t[key].dtype == torch.bfloat16 else 0x7F
+            for t in (c.t["k_scale"], c.t["v_scale"], c.opt["g_cache"]):
+                if t is not None and t.dim() == 3:
+                    t[blk, :, :p % bs] = float("nan")
+    assert some or name in ("gates",)
+    assert torch.equal(c.run(gcs_lib), whole)
+    c.check(gcs_lib, whole)
+    gcs_lib.set_device_checks(True)
+    try:  # nor does checked mode look there
+        assert torch.equal(c.run(gcs_lib), whole)
+        assert gcs_lib.get_device_status() == 0
     finally:
         gcs_lib.set_device_checks(False)
