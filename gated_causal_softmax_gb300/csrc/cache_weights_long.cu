@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
           next_see[k] = -1;
           next[k] = make_float2(neg_inf(), 0.f);
           if (n < nt && i < nrow && t < ql) {
-            next[k] = __ldg(p.rows + (size_t)(rq.q0 + t) * p.hq + kvh * G + i % G);
+            // written while this kernel may already run: not by the read-only path
+            next[k] = p.rows[(size_t)(rq.q0 + t) * p.hq + kvh * G + i % G];
             next_see[k] = L - ql + t;
           }
         }

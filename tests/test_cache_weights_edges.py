@@ -1,0 +1,32 @@
+"""Weights of cached tokens: rows that add nothing, and calls that follow one another."""
+import numpy as np
+import pytest
+import torch
+
+from test_cache_weights import CASES, Case
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sums", [False, True], ids=["summed", "given"])
+@pytest.mark.parametrize("name", ["drafts", "chunk", "window_chunk", "bf16_d256_chunk", "gates_group7_chunk",
+                                  "long_chunk"])
+def test_calls_behind_one_another_in_one_workspace(gcs_lib, name, sums):
+    """The rows' constants of the call before are in the workspace when the next one starts, kernel beside
+    kernel: each call takes its own."""
+    lens, qls, hq, hkv, d, kw = CASES[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    rng = np.random.default_rng(7)
+    calls = []
+    for _ in range(3):
+        lse = torch.from_numpy(rng.uniform(3, 9, (hq, sum(qls))).astype(np.float32)).cuda()
+        q = torch.from_numpy(rng.normal(size=(sum(qls), hq, d))).to(torch.bfloat16).cuda()
+        calls.append(dict(q=q, decay=0.0, **(dict(lse=lse) if sums else {})))
+    want = [torch.from_numpy(c.run(gcs_lib, **kw)).cuda() for kw in calls]
+    ws = torch.empty((64 << 20,), dtype=torch.uint8, device="cuda")
+    got = [torch.from_numpy(c.w).cuda() for _ in range(30)]
+    for i, w in enumerate(got):
+        gcs_lib.attn_cache_weights(w_cache=w, workspace=ws, **{**c.t, **calls[i % 3]})
+    torch.cuda.synchronize()
+    assert gcs_lib.get_device_status() == 0
+    for i, w in enumerate(got):
+        assert torch.equal(w, want[i % 3]), i
