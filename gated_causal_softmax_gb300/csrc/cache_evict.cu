@@ -49,7 +49,7 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 template <bool HELD, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 3) cache_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint4 keys[];
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(16) uint32_t hist[kBins];  // read by four
   __shared__ uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
   __shared__ uint2 few[kFew];  // (key, position)
   __shared__ uint32_t few_n;
