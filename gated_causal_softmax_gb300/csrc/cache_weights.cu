@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
           if (p.lse) {
             const float lse = __ldg(p.lse + (size_t)(kvh * G + head) * p.total_q + q0 + t);
             if (lse != neg_inf()) z = lse * kLog2e;
+            else row_g[i] = 0.f;  // adds nothing, whatever its elements and its gate are
           } else {
             float m = neg_inf(), l = 0.f;
             const int first = p.window > 0 ? max(0, L - ql + t - p.window + 1) / p.seg_len : 0;
@@ -213,7 +214,10 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const WeightsPa
       const int row = row0 + nt * 8 + (ln >> 2), t = row / G, head = row - t * G;
       const int dim = c * 64 + (BF16 ? (s >> 1) * 32 + (ln & 3) * 8 + (s & 1) * 4 : (ln & 3) * 16 + s * 4);
       uint2 v = make_uint2(0, 0);
-      if (row < nrows)
+      // a row without a sum is one of zeros
+      const bool valid = row < nrows && !(WRITE && p.lse &&
+                                          __ldg(p.lse + (size_t)(kvh * G + head) * p.total_q + q0 + t) == neg_inf());
+      if (valid)
         v = __ldg(reinterpret_cast<const uint2*>(p.q + (size_t)(q0 + t) * p.q_ts + (size_t)(kvh * G + head) * p.q_hs + dim));
       if (!BF16) v = make_uint2(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y));
       qf[i] = v;

@@ -479,7 +479,7 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
  * hkv with hq % hkv == 0, fp8 or bf16 caches.  With an fp8 cache q is rounded to f16, as in the
  * attention calls (|q| <= 65504).
  * lse: fp32 [hq, total_q] natural log, as attn_fwd gives it, or NULL: summed here first, which reads
- * the keys once more; a row whose lse is -inf adds nothing.  decay: finite.
+ * the keys once more; a row whose lse is -inf adds nothing, whatever its elements are.  decay: finite.
  * Every sum has a fixed order: repeated calls give the same bits.  The workspace (256-byte aligned)
  * holds the sums' parts (none with lse); calls that may run at the same time need one each. */
 size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse);

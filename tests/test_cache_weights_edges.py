@@ -30,3 +30,21 @@ def test_calls_behind_one_another_in_one_workspace(gcs_lib, name, sums):
     assert gcs_lib.get_device_status() == 0
     for i, w in enumerate(got):
         assert torch.equal(w, want[i % 3]), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["drafts", "bf16", "chunk", "gates_window", "window_chunk", "bf16_d256_chunk",
+                                  "gates_group7_chunk", "d512_chunk"])
+def test_rows_without_a_sum_may_hold_anything(gcs_lib, name):
+    """A given lse of -inf: the row adds nothing, whatever its elements (a padded row's, say) are."""
+    lens, qls, hq, hkv, d, kw = CASES[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    lse = torch.from_numpy(np.random.default_rng(3).uniform(3, 9, (hq, sum(qls))).astype(np.float32)).cuda()
+    lse[:, 1::2] = float("-inf")
+    want = c.run(gcs_lib, lse=lse)
+    assert np.isfinite(want).all()
+    for x in (float("nan"), float("inf"), -3e38):
+        q = c.t["q"].clone()
+        q[1::2] = x
+        assert np.array_equal(c.run(gcs_lib, lse=lse, q=q), want), x
+    assert gcs_lib.get_device_status() == 0
