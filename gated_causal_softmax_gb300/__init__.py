@@ -213,8 +213,9 @@ class CacheArgs(ctypes.Structure):
         ("kv_stride_slot", _i64),
         ("k_stride", Strides),
         ("v_stride", Strides),
+        ("first_lens", _vp),
     ]
-    _pack = struct.Struct("@iPiiPPi4P7iP7q").pack
+    _pack = struct.Struct("@iPiiPPi4P7iP7qP").pack
 
 
 class SelectArgs(ctypes.Structure):
@@ -891,7 +892,7 @@ def cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_row
         _vector(seq_lens, _I32, "seq_lens", (num_reqs,), dev),
         _vector(block_table, _I32, "block_table", block_table.shape, dev), max_blocks, k_cache.data_ptr(),
         v_cache.data_ptr(), ks, vs, nb, bs, hkv if hq is None else hq, hkv, d, kv_format, scale_mode,
-        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), cs[0], cs[1], cs[2], *k_stride, *v_stride))
+        _vector(g_cache, _F32, "g_cache", (nb, hq, bs), dev), cs[0], cs[1], cs[2], *k_stride, *v_stride, 0))
 
 
 def _packed_shape(rows, k_cache):
@@ -1049,8 +1050,10 @@ def attn_cache_select(w_cache, block_table, seq_lens, max_seq_len, budgets, max_
     """Chooses the cached tokens that stay: of each request min(budgets[r], seq_lens[r], max_keep),
     for every kv head on its own: the last `recent`, the first first_lens[r], then the largest weights
     in w_cache fp32 [num_blocks, hkv, block_size] (equal ones: the lowest position).  budgets,
-    first_lens int32 [R].  Returns kept int32 [R, hkv, max_keep] (ascending positions, -1 behind
-    them) and kept_lens int32 [R]."""
+    first_lens int32 [R].  Requests that share a prefix's blocks have it within first_lens, and
+    budgets (and max_keep) of first_lens + recent or more: the last tokens go before the first.
+    Returns kept int32 [R, hkv, max_keep] (ascending positions, -1 behind them) and kept_lens
+    int32 [R]."""
     dev = _current_device()
     if w_cache is None or w_cache.dim() != 3:
         raise ValueError("w_cache must be [num_blocks, num_kv_heads, block_size]")
@@ -1074,11 +1077,15 @@ def attn_cache_select(w_cache, block_table, seq_lens, max_seq_len, budgets, max_
 
 
 def attn_cache_compact(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, kept, kept_lens, g_cache=None,
-                       w_cache=None) -> None:
+                       w_cache=None, first_lens=None) -> None:
     """Moves the kept tokens of every request and kv head to the front of its pages, in place: cached
     position i takes what position kept[r, h, i] >= i holds (K, V, per-token scales, and the gates and
     weights where given), i < kept_lens[r].  kept int32 [R, hkv, max_keep], as attn_cache_select gives
-    it.  kept_lens are the seq_lens of the calls after it."""
+    it.  kept_lens are the seq_lens of the calls after it.  first_lens int32 [R]: the first tokens,
+    whose places are not written (a prefix whose blocks other requests share must be among them; no
+    other block may be in two requests' tables).  A request whose kept tokens do not begin with them all, as
+    after a choice with a budget below first_lens + recent, is left out and recorded in the device
+    status."""
     dev = _current_device()
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, 1, 1, None, g_cache, dev,
                    rows=False)
@@ -1089,4 +1096,5 @@ def attn_cache_compact(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     kp = _vector(kept, _I32, "kept", (num_reqs, hkv, max_keep), dev)
     lp = _vector(kept_lens, _I32, "kept_lens", (num_reqs,), dev)
     wp = _vector(w_cache, _F32, "w_cache", (nb, hkv, bs), dev)
+    a.first_lens = _vector(first_lens, _I32, "first_lens", (num_reqs,), dev)
     _check(load().attn_cache_compact(a, kp, lp, max_keep, wp, _raw_stream(dev)), "attn_cache_compact")

@@ -1622,7 +1622,8 @@ int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32
   b.k_stride = b.v_stride = gcs_strides{0, 0};
   const int st = check_cache(&b);
   if (st != GCS_OK) return st;
-  if (!kept || !kept_lens || max_keep < 1 || !aligned4(kept) || !aligned4(kept_lens) || !aligned4(w_cache))
+  if (!kept || !kept_lens || max_keep < 1 || !aligned4(kept) || !aligned4(kept_lens) || !aligned4(w_cache) ||
+      !aligned4(a->first_lens))
     return GCS_ERR_INVALID_ARG;
   // positions, and the grid of up to 8 blocks a (request, kv head) and eight vectors
   if (max_keep > 1 << 30 || (double)a->num_reqs * a->hkv > 268435455.0 || a->hq / a->hkv > 1 << 18)
@@ -1636,7 +1637,8 @@ int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32
   const TSpan none = tspan(Span{0, 0});
   const size_t R = (size_t)a->num_reqs, rows = (size_t)a->num_blocks * a->hkv * a->block_size;
   const TSpan ks = per_token ? cs.ks : none, vs = per_token ? cs.vs : none, w = tspan(span(w_cache, rows * 4));
-  const TSpan ins[] = {cs.table, cs.lens, tspan(span(kept, R * a->hkv * max_keep * 4)), tspan(span(kept_lens, R * 4))};
+  const TSpan ins[] = {cs.table, cs.lens, tspan(span(kept, R * a->hkv * max_keep * 4)), tspan(span(kept_lens, R * 4)),
+                       tspan(span(a->first_lens, R * 4))};
   // K against V was checked above
   const TSpan outs_k[] = {cs.k, ks, vs, cs.g, w}, outs_v[] = {cs.v, ks, vs, cs.g, w};
   if (outputs_overlap(outs_k, ins) || outputs_overlap(outs_v, ins)) return GCS_ERR_INVALID_ARG;
@@ -1648,6 +1650,7 @@ int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32
   p.block_table = a->block_table;
   p.kept = kept;
   p.kept_lens = kept_lens;
+  p.first_lens = a->first_lens;
   p.max_blocks = c.max_blocks;
   p.num_blocks = c.num_blocks;
   p.block_size = c.block_size;

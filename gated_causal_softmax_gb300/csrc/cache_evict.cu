@@ -398,12 +398,23 @@ __global__ void __launch_bounds__(kMoveThreads, 3) cache_move_kernel(const MoveP
     if (tid == 0) record_bad(p.status);
     return;
   }
+  // The first tokens stay where they are: a request that would move others to their places moves none at all.
+  const int first = p.first_lens ? max(0, __ldg(p.first_lens + r)) : 0, stay = min(first, n);
+  if (stay > 0) {
+    bool other = false;  // ascending positions are 0, 1, .. up to the one that is its own index
+    for (int k = tid; k < p.hkv; k += kMoveThreads)
+      other = other || __ldg(p.kept + ((size_t)r * p.hkv + k) * p.max_keep + stay - 1) != stay - 1;
+    if (__syncthreads_or(other)) {  // the same for all blocks of the request
+      if (tid == 0) record_bad(p.status);
+      return;
+    }
+  }
   const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
   const int32_t* kept = p.kept + (size_t)row * p.max_keep;
   // Source of target i (from kept, read ahead): block and slot, -1 where there is nothing to move.
   auto source = [&](int i, int src) -> Target {
     if (i >= n || src == i) return Target{-1, 0};
-    if (src < i || src >= L) {
+    if (src < i || src >= L || i < first) {
       record_bad(p.status);
       return Target{-1, 0};
     }

@@ -336,6 +336,7 @@ cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s);
 struct MoveParams {
   int num_reqs, hkv, group;
   const int32_t *seq_lens, *block_table, *kept, *kept_lens;
+  const int32_t* first_lens;      // [num_reqs] first tokens, whose places are not written, or null: 0
   int max_blocks, num_blocks, block_size, log2_block, max_keep;
   long long capacity;             // max_blocks * block_size
   uint8_t *k_cache, *v_cache;

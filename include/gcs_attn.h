@@ -289,8 +289,8 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
  * same for all of them and are read through the block table of the group's first request.  A
  * request's own table is read from there on (from the start of the cache block that holds position
  * prefix_lens[g]; the last, partly shared block may be each request's own copy): its entries before
- * that, and such a copy's slots before that position, are not looked at.  A query row may stand inside the prefix (prefix_lens[g] up to the seq_len).
- * A group may be one request or none, a prefix 0.
+ * that, and such a copy's slots before that position, are not looked at.  A query row may stand
+ * inside the prefix (prefix_lens[g] up to the seq_len).  A group may be one request or none, a prefix 0.
  * Everything of attn_decode_paged is supported (formats, groups of 16 or 8 heads, block sizes,
  * strides, q_len 1..4, gates, window, sink), except: segment_len is that of the tokens behind the
  * prefixes, 0 lets the library choose; and no kernel events are recorded (they stay armed).
@@ -420,6 +420,8 @@ typedef struct {
   float* g_cache;              /* fp32 [num_blocks, hq, block_size], or NULL              */
   int64_t kv_stride_block, kv_stride_head, kv_stride_slot;  /* as in gcs_decode_args      */
   gcs_strides k_stride, v_stride;  /* layouts of the packed k and v                       */
+  const int32_t* first_lens;   /* attn_cache_compact: device int32 [num_reqs], or NULL: 0; the
+                                  other calls do not look at it                           */
 } gcs_cache_args;
 
 /* Workspace bytes of the two append calls (256-byte aligned; 0 without g_cache and for short
@@ -457,7 +459,10 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
  *     place in the text: attn_cache_append_rope then takes the positions from the caller, and a
  *     window counts cached tokens.  Cumulative gates stay as they are: their differences
  *     are still the sums of the log gates between two tokens.
- *   - blocks whose tokens all stay where they are (a shared prefix within first_lens) are not written.
+ *   - blocks whose tokens all stay where they are are not written.  Where requests share the blocks of a
+ *     prefix, first_lens covers it in all three calls, and each request's budget (and max_keep) is at least
+ *     first_lens + recent, or its seq_len: the choice takes the last tokens before the first ones, and
+ *     with less they would go to the prefix's places.  attn_cache_compact leaves such a request out.
  * w_cache is fp32 [num_blocks, hkv, block_size], contiguous and 16-byte aligned, like the scales.
  * Like the cache calls, these check every index that they take from a device array, in every
  * mode: a request whose lengths do not fit (cu_q not sorted within 0 .. total_q, q_len above
@@ -514,10 +519,15 @@ int attn_cache_select(const gcs_select_args* a, int32_t* kept, int32_t* kept_len
  * query heads, with w_cache the weights (NULL: left).  In place; every source is read before it is
  * overwritten.  Needs kept[i] >= i (ascending positions are): an entry below i or at or past
  * seq_lens[r] is left out and recorded, and so is a request with kept_lens outside 0 ..
- * min(seq_len, max_keep).  Slots from kept_lens[r] on are left as they were.
+ * min(seq_len, max_keep).  a->first_lens: the places of each request's first tokens are not written: a
+ * request that would move others there (some kv head's kept does not begin with 0, 1, ..,
+ * min(first_lens, kept_lens) - 1) is left out as a whole and recorded, and its cache is as it was; with
+ * positions that do not ascend the entries for these places are.  Slots from kept_lens[r] on are left
+ * as they were.
  * a: the cache, its index arrays and hq (with gates); a->seq_lens are the lengths before the
  * move; cu_rows, total_rows, max_rows, k_stride and v_stride are not looked at.  No block
- * that is written may belong to another request.  No workspace. */
+ * that is written may belong to another request: where a prefix's blocks do, first_lens covers them.
+ * No workspace. */
 int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32_t* kept_lens, int max_keep,
                        float* w_cache, gcs_stream_t stream);
 
