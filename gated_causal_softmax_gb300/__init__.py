@@ -1052,6 +1052,7 @@ def attn_cache_select(w_cache, block_table, seq_lens, max_seq_len, budgets, max_
     in w_cache fp32 [num_blocks, hkv, block_size] (equal ones: the lowest position).  budgets,
     first_lens int32 [R].  Requests that share a prefix's blocks have it within first_lens, and
     budgets (and max_keep) of first_lens + recent or more: the last tokens go before the first.
+    With gates in the cache recent is 1 or more: the next append runs on from the last token's.
     Returns kept int32 [R, hkv, max_keep] (ascending positions, -1 behind them) and kept_lens
     int32 [R]."""
     dev = _current_device()
@@ -1085,7 +1086,8 @@ def attn_cache_compact(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     whose places are not written (a prefix whose blocks other requests share must be among them; no
     other block may be in two requests' tables).  A request whose kept tokens do not begin with them all, as
     after a choice with a budget below first_lens + recent, is left out and recorded in the device
-    status."""
+    status.  With g_cache every kv head's last token has to stay, for the next append runs on from its
+    gates (checked mode leaves out and records requests where it does not)."""
     dev = _current_device()
     a = cache_args(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, 1, 1, None, g_cache, dev,
                    rows=False)

@@ -1665,6 +1665,7 @@ int attn_cache_compact(const gcs_cache_args* a, const int32_t* kept, const int32
   p.v_scale = per_token ? c.v_scale : nullptr;
   p.g_cache = c.g_cache;
   p.w_cache = w_cache;
+  p.last_stays = c.g_cache && device_checks_on() ? 1 : 0;
   p.status = device_status_ptr();
   if (!p.status) return GCS_ERR_CUDA;
   return cuda_status(launch_cache_move(p, reinterpret_cast<cudaStream_t>(stream)));

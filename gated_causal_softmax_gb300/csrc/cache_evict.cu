@@ -409,6 +409,15 @@ __global__ void __launch_bounds__(kMoveThreads, 3) cache_move_kernel(const MoveP
       return;
     }
   }
+  if (p.last_stays && n > 0) {  // what is appended next runs on from the last token's gates
+    bool gone = false;
+    for (int k = tid; k < p.hkv; k += kMoveThreads)
+      gone = gone || __ldg(p.kept + ((size_t)r * p.hkv + k) * p.max_keep + n - 1) != L - 1;
+    if (__syncthreads_or(gone)) {
+      if (tid == 0) record_bad(p.status);
+      return;
+    }
+  }
   const int32_t* table = p.block_table + (size_t)r * p.max_blocks;
   const int32_t* kept = p.kept + (size_t)row * p.max_keep;
   // Source of target i (from kept, read ahead): block and slot, -1 where there is nothing to move.

@@ -344,6 +344,7 @@ struct MoveParams {
   int log2_units;                 // log2 of the 16-byte pieces of a row
   float *k_scale, *v_scale;       // per token, or null
   float *g_cache, *w_cache;       // or null
+  int last_stays;                 // checked mode with gates: a request whose last token goes is left out
   int* status;
 };
 cudaError_t launch_cache_move(const MoveParams& p, cudaStream_t s);

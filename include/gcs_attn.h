@@ -459,15 +459,20 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
  *     place in the text: attn_cache_append_rope then takes the positions from the caller, and a
  *     window counts cached tokens.  Cumulative gates stay as they are: their differences
  *     are still the sums of the log gates between two tokens.
+ *   - with gates, every kv head's last token has to stay (recent >= 1): the next append runs on from the
+ *     gates of the cached position in front of it, and the log gates of tokens between that one and the
+ *     end would be missing from all later tokens.  In checked mode attn_cache_compact with g_cache leaves
+ *     out a request of which some kv head keeps tokens but not the last, and records it.
  *   - blocks whose tokens all stay where they are are not written.  Where requests share the blocks of a
  *     prefix, first_lens covers it in all three calls, and each request's budget (and max_keep) is at least
  *     first_lens + recent, or its seq_len: the choice takes the last tokens before the first ones, and
  *     with less they would go to the prefix's places.  attn_cache_compact leaves such a request out.
  * w_cache is fp32 [num_blocks, hkv, block_size], contiguous and 16-byte aligned, like the scales.
  * Like the cache calls, these check every index that they take from a device array, in every
- * mode: a request whose lengths do not fit (cu_q not sorted within 0 .. total_q, q_len above
- * max_q_len or seq_len, seq_len above max_seq_len or the table) is left out, a key whose block-table entry is
- * not in [0, num_blocks) is left out, and GCS_ERR_INVALID_ARG is recorded in the device status word.
+ * mode (checked mode adds only what is said above): a request whose lengths do not fit (cu_q not
+ * sorted within 0 .. total_q, q_len above max_q_len or seq_len, seq_len above max_seq_len or the table)
+ * is left out, a key whose block-table entry is not in [0, num_blocks) is left out, and
+ * GCS_ERR_INVALID_ARG is recorded in the device status word.
  *
  * Weights.  With the scores s of attn_decode_paged (scale, causal mask at the end of the context,
  * and gates, window and sink where given), for every cached token j of a request and every kv head:

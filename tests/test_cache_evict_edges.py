@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import oracle
+from helpers import DECODE_RTOL, assert_close, f64
 from test_cache_evict import Moved, i32
 
 
@@ -126,3 +127,84 @@ def test_binding_refuses_wrong_first_lens(monkeypatch):
     for bad in (i(3), z(2), torch.zeros(2, dtype=torch.int32), OnGpu(torch.zeros(2, dtype=torch.int32), 1)):
         with pytest.raises(ValueError):
             gcs.attn_cache_compact(**good, first_lens=bad)
+
+
+def step_after_eviction(gcs, kv_format, recent):
+    """Prompts with gates written by the append, 40 tokens a kv head kept, three more tokens appended one by one
+    and decoded over what is left: (output, float64 over the cached keys and values with the text's own gates)."""
+    hq, hkv, d, bs, lens, keep, more = 16, 2, 128, 16, [150, 97], 40, 3
+    gen = torch.Generator().manual_seed(2)
+    rnd = lambda *s: torch.randn(s, generator=gen)
+    rows = lambda n, h: rnd(n, h, d).to(torch.bfloat16).cuda()
+    gates = [-torch.rand((n + more, hq), generator=gen) * 0.02 for n in lens]
+    for x, n in zip(gates, lens):
+        x[n - 5:n] = -1.0  # what is lost with the last tokens
+    nb, pages = 20, 10
+    bt = torch.randperm(nb, generator=gen).to(torch.int32).view(2, pages)
+    tab = bt.cuda()
+    dt = torch.bfloat16 if kv_format == "bf16" else torch.uint8
+    kc, vc = (torch.zeros((nb, hkv, bs, d), dtype=dt, device="cuda") for _ in range(2))
+    ks = vs = None
+    if kv_format != "bf16":
+        ks, vs = (torch.zeros((nb, hkv, bs), device="cuda") for _ in range(2))
+    g, w = torch.zeros((nb, hq, bs), device="cuda"), torch.zeros((nb, hkv, bs), device="cuda")
+    cache = (kc, vc, ks, vs, tab)
+    n = sum(lens)
+    gcs.attn_cache_append(rows(n, hkv), rows(n, hkv), *cache, i32(lens), i32([0, lens[0], n]), max(lens),
+                          log_gate=torch.cat([x[:m] for x, m in zip(gates, lens)]).cuda(), g_cache=g)
+    gcs.attn_cache_weights(rows(2, hq), kc, ks, tab, i32(lens), i32([0, 1, 2]), 1, max(lens), w, 0.0, g_cache=g)
+    for r, n in enumerate(lens):
+        for j in range(n - 8, n):  # light ones
+            w[int(bt[r, j // bs]), :, j % bs] = 0.0
+    kept, kept_lens = gcs.attn_cache_select(w, tab, i32(lens), max(lens), i32([keep] * 2), keep, recent=recent)
+    gcs.attn_cache_compact(*cache, i32(lens), kept, kept_lens, g_cache=g, w_cache=w)
+    cu = i32([0, 1, 2])
+    for i in range(more):
+        now = kept_lens + 1 + i
+        gcs.attn_cache_append(rows(2, hkv), rows(2, hkv), *cache, now, cu, 1,
+                              log_gate=torch.stack([x[m + i] for x, m in zip(gates, lens)]).cuda(), g_cache=g)
+    q = rows(2, hq)
+    out = gcs.attn_decode_paged(q, *cache, now, cu, 1, keep + more, g_cache=g)
+    torch.cuda.synchronize()
+    text = np.zeros((nb, hq, bs))  # the text's cumulative gates of what each place holds
+    for r, m in enumerate(lens):
+        total = gates[r].double().cumsum(0).numpy()
+        for h in range(hq):
+            at = np.concatenate([kept[r, h // (hq // hkv)].cpu().numpy(), m + np.arange(more)])
+            for i, pos in enumerate(at):
+                text[int(bt[r, i // bs]), h, i % bs] = total[pos, h]
+    num = lambda t: t.float().cpu().numpy() if kv_format == "bf16" else t.cpu().numpy()
+    opt = lambda t: None if t is None else t.double().cpu().numpy()
+    want = oracle.decode_paged(f64(q), num(kc), num(vc), opt(ks), opt(vs), bt.numpy(), now.cpu().numpy(),
+                               cu.cpu().numpy(), 1 / d**0.5, g_cache=text)
+    return out, want
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("recent", [1, 4])
+@pytest.mark.parametrize("kv_format", ["fp8", "bf16"])
+def test_gates_run_on_after_an_eviction(gcs_lib, kv_format, recent):
+    out, want = step_after_eviction(gcs_lib, kv_format, recent)
+    assert gcs_lib.get_device_status() == 0
+    assert_close("decode", out, want, DECODE_RTOL)
+
+
+@pytest.mark.gpu
+def test_checked_mode_wants_the_last_token_with_gates(gcs_lib):
+    """A request of which one kv head drops its last token is left out as a whole; without gates, and where
+    nothing is kept, it may."""
+    lens, keep = [300, 90, 50, 70], [60, 30, 0, 70]
+    last = lambda rng, L, n: np.sort(np.append(rng.permutation(L - 1)[:n - 1], L - 1)) if n else np.arange(0)
+    for gates in (True, False):
+        c = Moved(lens, keep, 4, 2, 64, gates=gates, chosen=last)
+        c.kept[0, 1, 59] = 298  # one token in front of the last
+        before = c.arrays()
+        gcs_lib.set_device_checks(True)
+        try:
+            c.run(gcs_lib)
+            assert gcs_lib.get_device_status() == (1 if gates else 0)
+        finally:
+            gcs_lib.set_device_checks(False)
+        if gates:
+            c.kept[0, :, :60] = np.arange(60)
+        c.check(gcs_lib, before)
