@@ -1464,7 +1464,8 @@ struct WeightsPlan {
   bool wide = false;  // the long form
   int seg_len = 0, segs = 0;
   size_t part = 0, rows = 0;  // bytes of the sums' parts; long form: of the rows' constants
-  size_t ws = 0;              // + long form, fp8: the queries in f16
+  bool queries = false;       // long form: fp8 (in f16) or given sums (rows without one as zeros): a copy of the queries
+  size_t ws = 0;              // + that copy
 };
 static bool plan_weights(const gcs_decode_args* a, bool with_lse, WeightsPlan* pl) {
   const int sms = current_sms();
@@ -1478,7 +1479,8 @@ static bool plan_weights(const gcs_decode_args* a, bool with_lse, WeightsPlan* p
   pl->segs = (a->max_seq_len + pl->seg_len - 1) / pl->seg_len;
   pl->part = with_lse ? 0 : round_up(pl->segs * rows * sizeof(float2));
   pl->rows = pl->wide ? round_up(rows * sizeof(float2)) : 0;
-  pl->ws = pl->part + pl->rows + (pl->wide && a->kv_format != GCS_KV_BF16 ? round_up(rows * a->d * 2) : 0);
+  pl->queries = pl->wide && (a->kv_format != GCS_KV_BF16 || with_lse);
+  pl->ws = pl->part + pl->rows + (pl->queries ? round_up(rows * a->d * 2) : 0);
   return true;
 }
 
@@ -1557,15 +1559,15 @@ int attn_cache_weights(const gcs_decode_args* a, const float* lse, const int32_t
   if (pl.wide) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.rows = reinterpret_cast<float2*>(ws + pl.part);
-    p.q16 = reinterpret_cast<uint16_t*>(ws + pl.part + pl.rows);
+    p.q16 = pl.queries ? reinterpret_cast<uint16_t*>(ws + pl.part + pl.rows) : nullptr;
     const bool bf16 = a->kv_format == GCS_KV_BF16;
     WeightsMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     const Layout packed{(long long)a->hq * a->d, a->d};
     if (bf16 && !make_page_map_bf16(&maps.k, a->k_cache, a->num_blocks, a->hkv, a->block_size, a->d, cl))
       return GCS_ERR_CUDA;
-    if (!make_query_map(&maps.q, bf16 ? static_cast<const void*>(a->q) : p.q16, !bf16, a->d, a->hq, a->total_q,
-                        bf16 ? lq : packed, p.group, 128 / p.group))
+    if (!make_query_map(&maps.q, p.q16 ? p.q16 : a->q, !bf16, a->d, a->hq, a->total_q, p.q16 ? packed : lq, p.group,
+                        128 / p.group))
       return GCS_ERR_CUDA;
     return cuda_status(launch_cache_weights_long(p, maps, reinterpret_cast<cudaStream_t>(stream)));
   }

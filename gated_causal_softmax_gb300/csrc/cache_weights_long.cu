@@ -7,7 +7,8 @@
 //   rows kernel      joins a row's partials and the sink: b = -lse (log2 units), beside its gate.
 //   weights kernel   S^T = K Q^T: keys on the lanes, so a key's weight, the sum over rows of
 //                    2^(scale s + b), stays in its thread too; the query tiles stream by.
-// Neither kernel moves data between threads, and nothing but (max, sum) leaves the SM.
+// Neither kernel moves data between threads until the four groups of lanes that share a row or a key join
+// their parts at its end, and nothing but (max, sum) leaves the SM.
 //
 // Both kernels are one engine: NA resident operand tiles of 128 rows x d (two, one at d 512) in tensor
 // memory, streamed tiles of 128 rows x d in a shared-memory ring of 64-dim stages, and accumulators of
@@ -107,15 +108,13 @@ __device__ __forceinline__ int block_of(const WeightsParams& p, const int32_t* t
   return -1;
 }
 
-// WRITE false: the sums kernel, true: the weights kernel.  NCH: d / 64.  SOME (weights, bf16): a query row may
-// add nothing whatever its elements are, so it is masked (an fp8 cache's are zeros by then); without it the
-// other calls' tiles keep their shorter test (4 x 1024 rows of an fp8 cache 2384 us with it, 2362 without).
-template <bool BF16, int NCH, bool WRITE, bool SOME>
+// WRITE false: the sums kernel, true: the weights kernel.  NCH: d / 64.
+template <bool BF16, int NCH, bool WRITE>
 __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
     weights_long_kernel(const __grid_constant__ CUtensorMap tm, const WeightsParams p) {
   using C = Cfg<NCH>;
   constexpr int NA = C::NA, NST = C::NST, kThreads = kThreadsOf<!BF16 && !WRITE>;
-  // Each kernel of a call may run beside the one before it: the sums need nothing of the queries in f16, the
+  // Each kernel of a call may run beside the one before it: the sums need nothing of the queries' copy, the
   // weights wait for the rows' constants (behind the sums) once their keys are in place.
   WaitAtEnd at_end;
   grid_release();
@@ -173,8 +172,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
   uint64_t* drain = aux_empty + C::NAUX;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  // [NAUX] sums: pages of a key tile that are not there; weights, SOME: whether rows of a query tile add nothing
-  uint32_t* left_out = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 8);
+  uint32_t* bad_pages = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 8);  // [NAUX] pages of a key tile that are not there
   const Abort ab{abort_flag, p.status};
   constexpr bool kCopied = BF16 || WRITE;  // the streamed tiles come by tensor copies
   if (threadIdx.x == 0) {
@@ -394,7 +392,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
           if (n < nt && i < nrow && t < ql) {
             // written while this kernel may already run: not by the read-only path
             next[k] = p.rows[(size_t)(rq.q0 + t) * p.hq + kvh * G + i % G];
-            next_see[k] = SOME && next[k].x == neg_inf() ? -1 : L - ql + t;
+            next_see[k] = L - ql + t;
           }
         }
       };
@@ -414,14 +412,6 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
           ax[i] = v[k].x;
           ax[kTile + i] = v[k].y;
           reinterpret_cast<int*>(ax)[2 * kTile + i] = see[k];
-        }
-        if (SOME) {  // (rows that a tile has past its tokens are masked by their number)
-          const int rows = min(nrow, (ql - (b_lo + n) * ntok) * G);
-          bool none = false;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) none = none || (lane + 32 * k < rows && see[k] < 0);
-          none = __any_sync(0xffffffffu, none);
-          if (lane == 0) left_out[a] = none;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&aux_full[a]);
@@ -454,7 +444,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
         }
         *reinterpret_cast<float4*>(ax + 4 * lane) = make_float4(v.x * sl2, v.y * sl2, v.z * sl2, v.w * sl2);
         const uint32_t bad = __reduce_or_sync(0xffffffffu, blk < 0 && pos < L ? 1u << (lane >> 2) : 0u);
-        if (lane == 0) left_out[a] = bad;
+        if (lane == 0) bad_pages[a] = bad;
         __syncwarp();
         if (lane == 0) mbar_arrive(&aux_full[a]);
       }
@@ -515,7 +505,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
         const uint32_t tS = tmem + lane_off + kAccCol + slot * kTile;
         if constexpr (!WRITE) {
           const int j0 = key0 + (b_lo + n) * kTile;
-          const uint32_t bad = left_out[a];
+          const uint32_t bad = bad_pages[a];
           const int first_t = a0 + x * ntok, last_t = min(first_t + ntok, ql) - 1;
           const bool need_mask = j0 + kTile - 1 > L - ql + first_t || bad != 0 || (W > 0 && j0 <= L - ql + last_t - W);
           const float4* g4 = reinterpret_cast<const float4*>(ax + 3 * kTile + head * kGateRow);
@@ -588,8 +578,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
         } else {
           const int t0 = (b_lo + n) * ntok;
           const int j_lo = a0 + x * kTile, j_hi = j_lo + kTile - 1;
-          const bool need_mask = t0 + ntok > ql || j_hi > L - ql + t0 || (SOME && left_out[a]) ||
-                                 (W > 0 && j_lo <= L - ql + t0 + ntok - 1 - W);
+          const bool need_mask = t0 + ntok > ql || j_hi > L - ql + t0 || (W > 0 && j_lo <= L - ql + t0 + ntok - 1 - W);
           const float4* b4 = reinterpret_cast<const float4*>(ax);
           const float4* gi4 = reinterpret_cast<const float4*>(ax + kTile);
           const int* see = reinterpret_cast<const int*>(ax) + 2 * kTile;
@@ -682,7 +671,7 @@ __global__ void __launch_bounds__(kThreadsOf<!BF16 && !WRITE>, 1)
       }
     }
   } else if (!kCopied) {
-    // ---------------------------------------------------------- e4m3 -> f16 stages (warps 12-15)
+    // ---------------------------------------------------------- e4m3 -> f16 stages (warps 20-23)
     // thread c takes the 16-byte piece c & 3 of keys 32 i + c / 4; two chunks are on their way
     // while one is converted
     const int c = threadIdx.x - (4 + kEpiWarps) * 32, piece = c & 3, row = c >> 2;
@@ -798,9 +787,11 @@ __global__ void __launch_bounds__(256) weights_rows_kernel(const WeightsParams p
   }
 }
 
-// The queries in f16, [total_q, hq, d]; a row without a sum (given -inf) is zeros: it adds nothing, whatever
-// its elements are.
-__global__ void __launch_bounds__(256) queries_f16_kernel(const WeightsParams p) {
+// The queries as the weights kernel streams them, [total_q, hq, d]: in f16 for an fp8 cache, and with given sums
+// zeros for a row without one (-inf), which adds nothing whatever its elements are.  (Masked by the tile
+// instead, over a bf16 cache 4 x 1024 rows took 1864 us and 8 x 33 of 256 dims 286, unmasked 1800 and 266.)
+template <bool BF16>
+__global__ void __launch_bounds__(256) queries_kernel(const WeightsParams p) {
   grid_release();
   const int units = p.d / 8;
   const long long n = (long long)p.total_q * p.hq * units;
@@ -808,16 +799,16 @@ __global__ void __launch_bounds__(256) queries_f16_kernel(const WeightsParams p)
     const long long row = i / units, t = row / p.hq, h = row % p.hq;
     uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_ts + h * p.q_hs) + i % units);
     if (p.lse && __ldg(p.lse + h * p.total_q + t) == neg_inf()) v = make_uint4(0, 0, 0, 0);
-    reinterpret_cast<uint4*>(p.q16)[i] =
-        make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+    if (!BF16) v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+    reinterpret_cast<uint4*>(p.q16)[i] = v;
   }
 }
 
-template <bool BF16, int NCH, bool WRITE, bool SOME>
+template <bool BF16, int NCH, bool WRITE>
 cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, bool beside, cudaStream_t s) {
   using C = Cfg<NCH>;
-  auto kern = weights_long_kernel<BF16, NCH, WRITE, SOME>;
-  cudaError_t e = allow_smem<weights_long_kernel<BF16, NCH, WRITE, SOME>>(C::SMEM);
+  auto kern = weights_long_kernel<BF16, NCH, WRITE>;
+  cudaError_t e = allow_smem<weights_long_kernel<BF16, NCH, WRITE>>(C::SMEM);
   if (e != cudaSuccess) return e;
   const int per = WRITE ? C::NA * kTile : C::NA * (kTile / p.group);
   const int n = WRITE ? (p.max_seq_len + per - 1) / per : (p.max_q_len + per - 1) / per * p.segs;
@@ -829,8 +820,8 @@ cudaError_t launch_t(const WeightsParams& p, const CUtensorMap& map, bool beside
 template <bool BF16, int NCH>
 cudaError_t launch_d(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
   cudaError_t e;
-  bool beside = !BF16;  // behind the queries in f16
-  if (!p.lse && (e = launch_t<BF16, NCH, false, false>(p, maps.k, beside, s)) != cudaSuccess) return e;
+  bool beside = !BF16 || p.lse;  // behind the queries' kernel
+  if (!p.lse && (e = launch_t<BF16, NCH, false>(p, maps.k, beside, s)) != cudaSuccess) return e;
   beside = beside || !p.lse;
   const long long rows = (long long)p.max_q_len * p.hq;
   const dim3 grid((unsigned)std::min(1024LL, (rows + 255) / 256), p.num_reqs);
@@ -840,9 +831,7 @@ cudaError_t launch_d(const WeightsParams& p, const WeightsMaps& maps, cudaStream
     weights_rows_kernel<<<grid, 256, 0, s>>>(p);
     e = cudaGetLastError();
   }
-  if (e != cudaSuccess) return e;
-  return BF16 && p.lse ? launch_t<BF16, NCH, true, BF16>(p, maps.q, true, s)
-                       : launch_t<BF16, NCH, true, false>(p, maps.q, true, s);
+  return e != cudaSuccess ? e : launch_t<BF16, NCH, true>(p, maps.q, true, s);
 }
 template <bool BF16>
 cudaError_t launch_f(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
@@ -868,11 +857,16 @@ int cache_weights_long_segment(int max_seq_len, int max_q_len, int group, int d,
 }
 
 cudaError_t launch_cache_weights_long(const WeightsParams& p, const WeightsMaps& maps, cudaStream_t s) {
-  if (p.format == kCacheBf16) return launch_f<true>(p, maps, s);
-  const long long units = (long long)p.total_q * p.hq * (p.d / 8);
-  queries_f16_kernel<<<(unsigned)std::min(4096LL, (units + 255) / 256), 256, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_f<false>(p, maps, s);
+  const bool bf16 = p.format == kCacheBf16;
+  if (p.q16) {
+    const long long units = (long long)p.total_q * p.hq * (p.d / 8);
+    const unsigned blocks = (unsigned)std::min(4096LL, (units + 255) / 256);
+    if (bf16) queries_kernel<true><<<blocks, 256, 0, s>>>(p);
+    else queries_kernel<false><<<blocks, 256, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return bf16 ? launch_f<true>(p, maps, s) : launch_f<false>(p, maps, s);
 }
 
 }  // namespace gcs

@@ -305,11 +305,11 @@ struct WeightsParams {
   int seg_len, segs;              // context segments
   int kv_head_inner;              // as in DecodeParams
   float2* rows;                   // long form: [total_q][hq] (-lse in log2 units, own gate)
-  uint16_t* q16;                  // long form, fp8: the queries in f16, [total_q, hq, d]
+  uint16_t* q16;                  // long form, fp8 or given sums: the queries as they are streamed, [total_q, hq, d]
   int* status;
 };
 // The long form's maps.  k (bf16 caches): {dim, slot, kv head, block}, box 64 dims of a page; q: {dim, head,
-// token} of the queries (bf16 caches) or of q16, box 64 dims x the heads of a kv head x 128 / heads tokens.
+// token} of q16 (null: of the queries), box 64 dims x the heads of a kv head x 128 / heads tokens.
 struct WeightsMaps {
   CUtensorMap k, q;
 };

@@ -297,8 +297,10 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
  * Preconditions on the device's arrays, beside those of attn_decode_paged: cu_groups[0] == 0,
  * cu_groups[num_groups] == num_reqs, sorted; prefix_lens[g] <= max_prefix_len and the seq_len of
  * every request of the group; seq_len - prefix_lens[g] <= max_suffix_len; at most
- * max_group_q query rows a group; the first request's table holds the prefix's blocks, whatever the window.
- * Checked mode checks them; where one fails the call's kernels see an empty batch. */
+ * max_group_q query rows a group; the first request's table holds the prefix's blocks, whatever the
+ * window.  Checked mode checks them; where one fails the call's kernels see an empty batch.
+ * The prefix's values are finite, also those that a row does not see for its window or because it
+ * stands in front of them: 128 tokens at a time they are multiplied by 0. */
 typedef struct {
   int num_groups;              /* >= 1                                                    */
   const int32_t* cu_groups;    /* device int32 [num_groups + 1]                          */
@@ -491,7 +493,8 @@ int attn_cache_gather(const gcs_cache_args* a, void* k, void* v, float* log_gate
  * lse: fp32 [hq, total_q] natural log, as attn_fwd gives it, or NULL: summed here first, which reads
  * the keys once more; a row whose lse is -inf adds nothing, whatever its elements are.  decay: finite.
  * Every sum has a fixed order: repeated calls give the same bits.  The workspace (256-byte aligned)
- * holds the sums' parts (none with lse); calls that may run at the same time need one each. */
+ * holds the sums' parts (none with lse) and, for many rows, their constants and mostly a copy of the
+ * queries; calls that may run at the same time need one each. */
 size_t attn_cache_weights_workspace(const gcs_decode_args* a, int with_lse);
 int attn_cache_weights(const gcs_decode_args* a, const float* lse, const int32_t* first_lens, float decay,
                        float* w_cache, void* workspace, size_t workspace_bytes, gcs_stream_t stream);
