@@ -48,3 +48,22 @@ def test_rows_without_a_sum_may_hold_anything(gcs_lib, name):
         q[1::2] = x
         assert np.array_equal(c.run(gcs_lib, lse=lse, q=q), want), x
     assert gcs_lib.get_device_status() == 0
+
+
+WIDE_GROUPS = {  # gates with more heads a kv head than the tiles of many rows hold
+    "group_17": ([200, 90], [70, 90], 17, 1, 64, dict(features=True)),
+    "group_40_window": ([130, 33], [20, 33], 40, 1, 128, dict(features=True, window=50, block=32)),
+    "group_128_bf16": ([90], [3], 128, 1, 64, dict(features=True, kv_format="bf16")),
+    "group_140": ([150], [2], 140, 1, 128, dict(features=True)),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("decay", [1.0, 0.5])
+@pytest.mark.parametrize("name", sorted(WIDE_GROUPS))
+def test_gates_of_wide_groups(gcs_lib, name, decay):
+    lens, qls, hq, hkv, d, kw = WIDE_GROUPS[name]
+    c = Case(lens, qls, hq, hkv, d, **kw)
+    got = c.run(gcs_lib, decay=decay)
+    assert gcs_lib.get_device_status() == 0
+    c.check(got, decay)
