@@ -592,9 +592,10 @@ cudaError_t launch_cache_select(const SelectParams& p, cudaStream_t s) {
   if (!sms) return cudaErrorInvalidDevice;
   // Blocks: up to two and a half an SM, of a thousand keys or more each; a wider cluster waits longer at each
   // of its steps than its shorter slices save (64 rows of 32K keys: 4 blocks a row 20.2 us, 8 29.0, 1 26.3;
-  // 192 of 16K: 1 21.0, 2 24.2; 16 of 4K: 4 15.3, 1 21.6). Slices past 28K keys leave an SM one block at a
-  // time, past kMaxSlice they are read again at each step: halved however many the rows (256 rows of 32K: 2
-  // blocks 40.0, 1 44.0; of 100K: 4 92.9, 2 129.5).
+  // 192 of 16K: 1 21.0, 2 24.2; 16 of 4K: 4 15.3, 1 21.6). Slices past about 26K keys leave an SM one block at
+  // a time, past kMaxSlice they are read again at each step: from 28K on they are halved however many the rows
+  // (256 rows of 32K: 2 blocks 40.0, 1 44.0; of 100K: 4 92.9, 2 129.5; of 27K, below that border, 1 43.6 and 2
+  // 43.5, 512 rows 82.5 and 68.2).
   const long long rows = (long long)p.num_reqs * p.hkv;
   int cs = 1;
   while (cs < 16 &&

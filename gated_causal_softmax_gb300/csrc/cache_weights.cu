@@ -421,6 +421,11 @@ cudaError_t launch_t(const WeightsParams& p, cudaStream_t s) {
   kern<<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
+// Blocks of 8 rows a walk takes: 2 for up to 16 rows of a kv head, 8 for more.  Eight take so many registers that
+// an SM holds one block, and 48 rows cost what 64 do, or more (a walk that is not full is masked throughout).  64
+// requests of 16K tokens, 4 kv heads of 128, fp8, with 2 and with 8: 16 rows 215 and 731 us, 32 rows 386 (two
+// walks) and 731, 48 rows 562 and 732, 64 rows 738 and 526; bf16 366 and 864, 686 and 863, 1006 and 864, 1327
+// and 668.  So the border lies too low for 17 to 48 rows; four blocks have not been built.
 template <bool BF16, int D>
 cudaError_t launch_d(const WeightsParams& p, cudaStream_t s) {
   return (long long)p.max_q_len * p.group <= 16 ? launch_t<BF16, D, 2>(p, s) : launch_t<BF16, D, 8>(p, s);
@@ -433,7 +438,8 @@ cudaError_t launch_f(const WeightsParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// Context segments: enough blocks for about eight an SM, of 256 to 4096 keys (a block spends a few microseconds before its first products: 64 requests up to 32K with 1024, 2048, 4096: 349, 298, 283 us).
+// Context segments: enough blocks for about eight an SM, of 256 to 4096 keys (a block spends a few microseconds
+// before its first products: 64 requests up to 32K with 1024, 2048, 4096: 349, 298, 283 us, since then 237).
 int cache_weights_segment(int max_seq_len, long long units, int sms) {
   const long long want = (8LL * sms + units - 1) / units;
   long long len = (max_seq_len + want - 1) / want;

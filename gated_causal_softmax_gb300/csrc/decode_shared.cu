@@ -16,7 +16,7 @@
 // Warp roles (768 threads):
 //   warp 0        tensor copies: fp8: tiles of codes; bf16: the operand tiles, 64 dims x 16 slots each
 //   warp 1        tcgen05 issuer: S_x = Q_x K^T and O_x += P_x V (P in TMEM)
-//   warps 2-3     per-key vectors of the tiles in turn (scales, gates), up to four tiles ahead
+//   warps 2-3     per-key vectors of the tiles in turn (scales, gates), up to four tiles ahead (two with gates)
 //   warps 4-19    softmax of tiles A and B, two threads a row with half of a tile's keys each (a tile's next
 //                 products wait for its softmax, so its length counts; the halves agree on a row's maximum
 //                 by shared memory)
