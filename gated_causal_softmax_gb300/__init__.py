@@ -673,7 +673,8 @@ def attn_decode_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table,
                              segment_len=0, out=None, workspace=None, g_cache=None, sink=None, window=0):
     """attn_decode_paged for requests that share a prefix, which is read once for each group of
     them: cu_groups int32 [groups + 1], the first request of each group and the end; prefix_lens
-    int32 [groups], its shared tokens (read through the block table of the group's first request).
+    int32 [groups], its shared tokens (read through the block table of the group's first request;
+    the other calls read them through each request's own).
     Host bounds: max_group_q on the query rows of a group, max_prefix_len on the prefixes,
     max_suffix_len on the tokens behind them.  segment_len: of those, 0 = the library's choice."""
     L = load()

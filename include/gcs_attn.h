@@ -289,8 +289,10 @@ int attn_prefill_paged(const gcs_decode_args* a, void* out, void* workspace, siz
  * same for all of them and are read through the block table of the group's first request.  A
  * request's own table is read from there on (from the start of the cache block that holds position
  * prefix_lens[g]; the last, partly shared block may be each request's own copy): its entries before
- * that, and such a copy's slots before that position, are not looked at.  A query row may stand
- * inside the prefix (prefix_lens[g] up to the seq_len).  A group may be one request or none, a prefix 0.
+ * that, and such a copy's slots before that position, are not looked at (by this call: the others,
+ * the cache calls among them, know no groups and read every position through the request's own
+ * table).  A query row may stand inside the prefix (prefix_lens[g] up to the seq_len).  A group may be
+ * one request or none, a prefix 0.
  * Everything of attn_decode_paged is supported (formats, groups of 16 or 8 heads, block sizes,
  * strides, q_len 1..4, gates, window, sink), except: segment_len is that of the tokens behind the
  * prefixes, 0 lets the library choose; and no kernel events are recorded (they stay armed).
